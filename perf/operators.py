@@ -33,30 +33,30 @@ def listed():
 
     return [
         # one decode step of 32 sequences: the new tokens' queries, at far positions (latency)
-        rope("rotate q, decode", 32, 64, first=131000),
+        rope("rotate q decode", 32, 64, first=131000),
         # the queries of a 32K prefill, taken out of a q|k|v projection; interleaved pairs, half the head rotated,
         # positions scaled to a longer context
-        rope("rotate q, prefill 32K", 32768, 32, layout="interleaved", rot=64, scaling="yarn", factor=4.0, gap=2048),
+        rope("rotate q prefill 32K", 32768, 32, layout="interleaved", rot=64, scaling="yarn", factor=4.0, gap=2048),
         # the attention's fp32 dq of a 64K training step, rotated back
-        rope("rotate dq back, 64K", 65536, 32, dtype="fp32", inverse=True),
+        rope("rotate dq back 64K", 65536, 32, dtype="fp32", inverse=True),
         # one decode step of 32 sequences: a token's K and V into pages that are partly filled (latency)
-        cache("append K V, decode", "kv", batch=32, ctx=2000, even=False, lens=3),
+        cache("append K V decode", "kv", batch=32, ctx=2000, even=False, lens=3),
         # the K and V of a 32K prefill into an empty cache
-        cache("append K V, prefill 32K", "kv", rows=32768),
+        cache("append K V prefill 32K", "kv", rows=32768),
         # the proxy keys of ragged chunks, kept in bf16 for the prefill and in NVFP4 for the decode steps after it
-        cache("append proxy K, chunks", "pk", batch=5, rows=7000, ctx=5000, even=False, lens=5, rot=32),
+        cache("append proxy K chunks", "pk", batch=5, rows=7000, ctx=5000, even=False, lens=5, rot=32),
         # the gradient pages of a 64K training step back to rows, with the rotation's transpose
-        cache("append backward, 64K", "bwd", rows=65536),
+        cache("append backward 64K", "bwd", rows=65536),
         # a single user's decode step at 131072 keys
-        attn("attend, decode 1", ctx=131071),
+        attn("attend decode 1", ctx=131071),
         # a serving batch's decode step
-        attn("attend, decode 32", batch=32, ctx=32767),
+        attn("attend decode 32", batch=32, ctx=32767),
         # a small ragged decode batch, sixteen query heads a KV head
-        attn("attend, decode ragged", batch=7, ctx=5000, even=False, lens=11, hq=32, hkv=2, hp=2, topk=5),
+        attn("attend decode ragged", batch=7, ctx=5000, even=False, lens=11, hq=32, hkv=2, hp=2, topk=5),
         # chunks of a mixed batch on top of what their sequences hold already; three query heads a KV head
-        attn("attend, chunks ragged", batch=6, rows=700, ctx=9000, even=False, lens=13, hq=12, hkv=4, hp=4, topk=9),
+        attn("attend chunks ragged", batch=6, rows=700, ctx=9000, even=False, lens=13, hq=12, hkv=4, hp=4, topk=9),
         # the 32K prefill
-        attn("attend, prefill 32K", rows=32768, hq=32),
+        attn("attend prefill 32K", rows=32768, hq=32),
     ]
 
 
