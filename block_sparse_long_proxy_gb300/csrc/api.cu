@@ -75,11 +75,20 @@ bool encode_tensor_map(void* map, int rank, const void* base, const uint64_t* di
   return r == CUDA_SUCCESS;
 }
 
+bool rows_disjoint_or_same(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t n,
+                           int64_t width) {
+  const intptr_t a = reinterpret_cast<intptr_t>(x), b = reinterpret_cast<intptr_t>(y);
+  if (a == b) return x_stride == y_stride || n <= 1;
+  if (a + (n - 1) * x_stride + width <= b || b + (n - 1) * y_stride + width <= a) return true;
+  if (x_stride != y_stride || n <= 1) return false;
+  const int64_t off = ((b - a) % x_stride + x_stride) % x_stride;  // columns of one wider array
+  return off >= width && off + width <= x_stride;
+}
+
 }  // namespace msa
 
 using namespace msa;
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 namespace msa {
@@ -138,8 +147,25 @@ __global__ void nan_scan_pages_kernel(const T* __restrict__ pool, const int32_t*
   }
 }
 
-// n elements of `elem` bytes (4: fp32, 2: bf16, 1: e4m3) of an array, when
-// the plan was created under MSA_CHECKS; otherwise nothing.
+// rows of `width` bf16 values at a stride
+__global__ void nan_scan_strided_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t width, int64_t stride,
+                                        uint32_t* err) {
+  bool bad = false;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int64_t i = threadIdx.x; i < width; i += blockDim.x) bad |= nan_bits(x[r * stride + i]);
+  if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(err, kErrNonFinite);
+}
+
+}  // namespace
+
+msa_status scan_strided(const msa_plan_s* p, const void* x, int64_t rows, int64_t width, int64_t stride,
+                        cudaStream_t st) {
+  if (!p->checks || rows <= 0) return MSA_OK;
+  const int grid = static_cast<int>(std::min<int64_t>(int64_t(p->num_sms) * 8, rows));
+  nan_scan_strided_kernel<<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(x), rows, width, stride, p->err_d);
+  return cuda_check(cudaGetLastError(), "MSA_CHECKS: scan launch");
+}
+
 msa_status scan_rows(const msa_plan_s* p, const void* x, int64_t n, int elem, cudaStream_t st) {
   if (!p->checks || x == nullptr || n <= 0) return MSA_OK;
   const int grid = static_cast<int>(std::min<int64_t>(int64_t(p->num_sms) * 8, (n + 255) / 256));
@@ -151,6 +177,8 @@ msa_status scan_rows(const msa_plan_s* p, const void* x, int64_t n, int elem, cu
     nan_scan_kernel<uint8_t><<<grid, 256, 0, st>>>(static_cast<const uint8_t*>(x), n, p->err_d);
   return cuda_check(cudaGetLastError(), "MSA_CHECKS: scan launch");
 }
+
+namespace {
 
 // The referenced pages of a pool, per_page elements of `elem` bytes each.
 msa_status scan_pages(const msa_plan_s* p, const void* pool, const int32_t* kv_indices, int64_t per_page, int elem,
@@ -206,7 +234,7 @@ msa_status msa_plan(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batc
   if (topk < 1 || topk > 1024) return set_error(MSA_ERR_INVALID_ARG, "msa_plan: topk must be in [1, 1024]");
   if (num_pages < 1 || num_pages > (int64_t(1) << 24))
     return set_error(MSA_ERR_INVALID_ARG, "msa_plan: num_pages out of range");
-  if (kv_dtype != MSA_KV_BF16 && kv_dtype != MSA_KV_FP8_E4M3)
+  if (kv_dtype != MSA_KV_BF16 && kv_dtype != MSA_KV_FP8_E4M3 && kv_dtype != MSA_KV_FP8_E4M3_BLOCK)
     return set_error(MSA_ERR_INVALID_ARG, "msa_plan: unknown kv_dtype");
   if (flags != 0) return set_error(MSA_ERR_INVALID_ARG, "msa_plan: flags must be 0");
 
@@ -277,6 +305,7 @@ msa_status msa_plan(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batc
   proxy_plan_tables(p, aux);
   attn_plan_tables(p, aux);
   bwd_plan_tables(p, aux);
+  append_plan_tables(p, aux);
 
   // device block: tiles | nvp | error word | aux tables | decode partials |
   // backward scratch | fused top-k counters and candidates
@@ -418,7 +447,8 @@ msa_status msa_sparse_attn(msa_plan_t plan, const void* q, const void* k_pages, 
     return set_error(MSA_ERR_INVALID_ARG, "msa_sparse_attn: NULL argument");
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
     return set_error(MSA_ERR_INVALID_ARG, "msa_sparse_attn: q, k_pages, v_pages, out must be 16-byte aligned");
-  const bool fp8 = plan->kv_dtype == MSA_KV_FP8_E4M3;
+  if (plan->kv_dtype == MSA_KV_FP8_E4M3_BLOCK) return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: block scales");
+  const bool fp8 = plan->kv_dtype != MSA_KV_BF16;
   if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
     return set_error(MSA_ERR_INVALID_ARG, "msa_sparse_attn: k_scale/v_scale must be given exactly for FP8 K/V");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

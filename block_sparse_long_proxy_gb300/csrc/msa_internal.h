@@ -83,6 +83,8 @@ struct msa_plan_s {
   int32_t n_proxy_attn_units = 0;
   int64_t heavy_tiles_off = 0;       // tile ids, most cached blocks first (the backward's dq order)
   int32_t n_page_entries = 0;        // sum over sequences of ceil(kv_len / 128)
+  int64_t append_units_off = 0;      // cache appends: one unit per page that gets rows
+  int32_t n_append_units = 0;
   void* bwd_d = nullptr;             // backward scratch (D, proxy LSE, inverse index)
 };
 
@@ -110,11 +112,23 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 
 msa_status set_error(msa_status s, const char* fmt, ...);
 msa_status cuda_check(cudaError_t e, const char* what);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// n rows of `width` bytes at x and at y share no byte, or are the same rows
+bool rows_disjoint_or_same(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t n,
+                           int64_t width);
+
+// MSA_CHECKS: n elements of `elem` bytes (4: fp32, 2: bf16, 1: e4m3) of an
+// array, or rows of bf16 at a stride in elements, when the plan was created
+// with it; otherwise nothing.
+msa_status scan_rows(const msa_plan_s* p, const void* x, int64_t n, int elem, cudaStream_t st);
+msa_status scan_strided(const msa_plan_s* p, const void* x, int64_t rows, int64_t width, int64_t stride,
+                        cudaStream_t st);
 
 // ---- plan-time tables (host), appended to the plan's aux array ----
 void proxy_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
 void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
 void bwd_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
+void append_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
 size_t bwd_scratch_bytes(const msa_plan_s* p);
 size_t fused_topk_scratch_bytes(const msa_plan_s* p);  // 0 when msa_proxy_topk is unsupported
 size_t fused_topk_counter_bytes(const msa_plan_s* p);  // leading part that starts at zero

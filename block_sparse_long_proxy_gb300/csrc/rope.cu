@@ -1,0 +1,162 @@
+// Rotary positions: the rotation of query and key heads by their positions,
+// and its transpose for the gradients.
+//
+//   pair (a, b) of a head, angle t = 2 pi turns_i position:
+//   a' = m (a cos t - b sin t),  b' = m (b cos t + a sin t)
+// Dims from rotary_dim on are copied.  The inverse rotates by -t with the
+// same factor m: it is the transpose of the forward map, so it takes the
+// gradient of the rotated heads to the gradient of the heads.
+//
+// Bound by HBM: every element is read and written once and costs three
+// multiply-adds.  A thread takes 16 values of a head (both members of eight
+// pairs) and works down the heads of its row, so that the eight sincospif of
+// a thread serve several heads.
+#include <math.h>
+
+#include <algorithm>
+#include <new>
+
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_kernel(const __grid_constant__ RopeTable tab, const T* x, int64_t x_stride, const int32_t* __restrict__ pos,
+                int64_t n_rows, int32_t heads, int32_t d, bool inverse, int32_t heads_per_thread, T* out,
+                int64_t out_stride) {
+  pdl_wait();
+  const int chunks = d / 16, rows = kRopeThreads / chunks;
+  const int c = threadIdx.x % chunks, r = threadIdx.x / chunks;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + r;
+  if (r >= rows || row >= n_rows) return;
+  const RopeChunk ch = rope_chunk(tab, c);
+  if (!ch.rotated && x == out) return;  // in place: nothing changes
+  float cs[8], sn[8];
+  if (ch.rotated) rope_angles(tab, c, pos[row], inverse, cs, sn);
+  const int h0 = blockIdx.y * heads_per_thread, h1 = min(heads, h0 + heads_per_thread);
+  const T* xr = x + row * x_stride;
+  T* orow = out + row * out_stride;
+#pragma unroll 2
+  for (int h = h0; h < h1; ++h) {
+    float v[16];
+    load8(xr + h * d + ch.lo, v);
+    load8(xr + h * d + ch.hi, v + 8);
+    if (ch.rotated) rope_rotate(tab.interleaved != 0, cs, sn, v);
+    store8(orow + h * d + ch.lo, v);
+    store8(orow + h * d + ch.hi, v + 8);
+  }
+}
+
+template <typename T>
+msa_status launch_rope(const RopeTable& tab, const void* x, int64_t xs, const int32_t* pos, int64_t n_rows,
+                       int32_t heads, int32_t d, bool inverse, void* out, int64_t os, int num_sms, cudaStream_t st) {
+  const int rows = kRopeThreads / (d / 16);
+  const int64_t gx = (n_rows + rows - 1) / rows;
+  if (gx > 0x7FFFFFFF) return set_error(MSA_ERR_INVALID_ARG, "msa_rope_apply: too many rows");
+  // heads per thread: the angles are shared by more heads the more rows there
+  // are to fill the GPU with
+  const int64_t fill = static_cast<int64_t>(num_sms) * 16;
+  const int hpt = static_cast<int>(std::clamp<int64_t>(gx * heads / fill, 1, std::min(heads, 8)));
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((heads + hpt - 1) / hpt));
+  return cuda_check(launch_pdl(rope_kernel<T>, grid, dim3(kRopeThreads), 0, st, tab, static_cast<const T*>(x), xs,
+                               pos, n_rows, heads, d, inverse, hpt, static_cast<T*>(out), os),
+                    "msa_rope_apply: launch");
+}
+
+}  // namespace
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+msa_status msa_rope_create(int32_t rotary_dim, msa_rope_layout layout, double base, msa_rope_scaling scaling,
+                           double factor, int32_t original_len, double beta_fast, double beta_slow, msa_rope_t* out) {
+  const char* fn = "msa_rope_create";
+  if (!out) return set_error(MSA_ERR_INVALID_ARG, "%s: out is NULL", fn);
+  *out = nullptr;
+  if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > 2 * kMaxRopePairs)
+    return set_error(MSA_ERR_UNSUPPORTED, "%s: rotary_dim must be a multiple of 16 in [16, %d]", fn,
+                     2 * kMaxRopePairs);
+  if (layout != MSA_ROPE_HALF && layout != MSA_ROPE_INTERLEAVED)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: unknown layout", fn);
+  if (!(base > 1.0) || !isfinite(base)) return set_error(MSA_ERR_INVALID_ARG, "%s: base must be above 1", fn);
+  if (scaling < MSA_ROPE_NONE || scaling > MSA_ROPE_YARN)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: unknown scaling", fn);
+  if (scaling != MSA_ROPE_NONE && (!(factor >= 1.0) || !isfinite(factor)))
+    return set_error(MSA_ERR_INVALID_ARG, "%s: factor must be at least 1", fn);
+  if (scaling == MSA_ROPE_YARN &&
+      (original_len < 1 || !(beta_fast >= beta_slow) || !(beta_slow > 0.0) || !isfinite(beta_fast)))
+    return set_error(MSA_ERR_INVALID_ARG, "%s: YaRN needs original_len >= 1 and beta_fast >= beta_slow > 0", fn);
+  auto* r = new (std::nothrow) msa_rope_s();
+  if (!r) return set_error(MSA_ERR_NO_MEMORY, "%s: out of host memory", fn);
+  const double two_pi = 6.283185307179586476925;
+  const int pairs = rotary_dim / 2;
+  if (scaling == MSA_ROPE_NTK) base *= pow(factor, static_cast<double>(rotary_dim) / (rotary_dim - 2));
+  // YaRN: pairs that turn more than beta_fast times over the original length
+  // keep their frequency, those below beta_slow are interpolated, a linear
+  // ramp over the pair index joins them
+  double lo = 0.0, width = 1.0;
+  if (scaling == MSA_ROPE_YARN) {
+    auto dim = [&](double beta) { return rotary_dim * log(original_len / (two_pi * beta)) / (2.0 * log(base)); };
+    lo = floor(dim(beta_fast));
+    width = std::max(ceil(dim(beta_slow)) - lo, 1e-3);
+  }
+  for (int i = 0; i < pairs; ++i) {
+    double turns = pow(base, -2.0 * i / rotary_dim) / two_pi;
+    if (scaling == MSA_ROPE_LINEAR) turns /= factor;
+    if (scaling == MSA_ROPE_YARN) {
+      const double ramp = std::clamp((i - lo) / width, 0.0, 1.0);
+      turns = turns * (1.0 - ramp) + turns / factor * ramp;
+    }
+    r->table.turns[i] = static_cast<uint64_t>(ldexp(turns, 64));  // turns <= 1 / (2 pi)
+  }
+  r->table.mscale = scaling == MSA_ROPE_YARN && factor > 1.0 ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.f;
+  r->table.rot = rotary_dim;
+  r->table.interleaved = layout == MSA_ROPE_INTERLEAVED;
+  *out = r;
+  return MSA_OK;
+}
+
+void msa_rope_destroy(msa_rope_t rope) { delete rope; }
+
+msa_status msa_rope_apply(msa_rope_t rope, const void* x, int64_t x_row_stride, const int32_t* positions,
+                          int64_t n_rows, int32_t heads, int32_t head_dim, msa_dtype dtype, int32_t inverse,
+                          void* out, int64_t out_row_stride, msa_stream_t stream) {
+  const char* fn = "msa_rope_apply";
+  if (!rope) return set_error(MSA_ERR_INVALID_ARG, "%s: NULL argument", fn);
+  if (n_rows < 0 || heads < 1 || heads > 65535 || head_dim < 16)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: sizes out of range", fn);
+  if (dtype != MSA_BF16 && dtype != MSA_F32) return set_error(MSA_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  if (head_dim % 16 != 0 || head_dim > 256)
+    return set_error(MSA_ERR_UNSUPPORTED, "%s: head_dim must be a multiple of 16 up to 256", fn);
+  if (rope->table.rot > head_dim)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: rotary_dim %d above head_dim %d", fn, rope->table.rot, head_dim);
+  if (n_rows == 0) return MSA_OK;
+  if (!x || !positions || !out) return set_error(MSA_ERR_INVALID_ARG, "%s: NULL argument", fn);
+  const int64_t es = dtype == MSA_BF16 ? 2 : 4, width = int64_t(heads) * head_dim;
+  if (x_row_stride < width || out_row_stride < width || x_row_stride > (int64_t(1) << 40) ||
+      out_row_stride > (int64_t(1) << 40))
+    return set_error(MSA_ERR_INVALID_ARG, "%s: row strides must be at least heads * head_dim", fn);
+  if (!aligned16(x) || !aligned16(out) || x_row_stride * es % 16 != 0 || out_row_stride * es % 16 != 0)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: rows must start on 16-byte boundaries", fn);
+  if (!rows_disjoint_or_same(x, x_row_stride * es, out, out_row_stride * es, n_rows, width * es))
+    return set_error(MSA_ERR_INVALID_ARG, "%s: out overlaps x without being x itself", fn);
+  int dev = 0, sms = 0;
+  msa_status s = cuda_check(cudaGetDevice(&dev), "msa_rope_apply: cudaGetDevice");
+  if (s == MSA_OK)
+    s = cuda_check(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "msa_rope_apply: SM count");
+  if (s != MSA_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == MSA_BF16 ? launch_rope<__nv_bfloat16>(rope->table, x, x_row_stride, positions, n_rows, heads,
+                                                        head_dim, inverse != 0, out, out_row_stride, sms, st)
+                           : launch_rope<float>(rope->table, x, x_row_stride, positions, n_rows, heads, head_dim,
+                                                inverse != 0, out, out_row_stride, sms, st);
+}
+
+}  // extern "C"

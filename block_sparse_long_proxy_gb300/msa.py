@@ -25,11 +25,14 @@ _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _u32 = ctypes.c_uint32
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_CUDA",
           4: "MSA_ERR_NO_MEMORY", 5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_DEVICE_CHECK",
           7: "MSA_ERR_NONFINITE"}
-KV_BF16, KV_FP8_E4M3 = 0, 1
+KV_BF16, KV_FP8_E4M3, KV_FP8_E4M3_BLOCK = 0, 1, 2
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 # Every symbol include/msa.h declares, with its ctypes signature.
 SIGNATURES = {
@@ -48,6 +51,12 @@ SIGNATURES = {
     "msa_sparse_attn_bwd": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _f32, _p, _p, _p, _p, _p, _p]),
     "msa_sparse_decode_noalloc": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _i64,
                                          _p, _p, _p, _p]),
+    "msa_rope_create": (_i32, [_i32, _i32, _f64, _i32, _f64, _i32, _f64, _f64, _p]),
+    "msa_rope_destroy": (None, [_p]),
+    "msa_rope_apply": (_i32, [_p, _p, _i64, _p, _i64, _i32, _i32, _i32, _i32, _p, _i64, _p]),
+    "msa_kv_append": (_i32, [_p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p]),
+    "msa_pk_append": (_i32, [_p, _p, _p, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _p]),
+    "msa_append_bwd": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p]),
     "msa_check_errors": (_i32, [_p, _p]),
     "msa_selftest_wait_timeout": (_i32, [_p]),
     "msa_test_fail_plan_allocs": (None, [_i32]),
@@ -88,6 +97,21 @@ def _need(t, dtype, shape, name):
         raise ValueError("%s: shape %s, want %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s: must be a contiguous CUDA tensor" % name)
+
+
+def _need_rows(t, dtype, shape, name):
+    """_need for rows at a stride: the heads of a row dense, the rows anywhere
+    apart (a slice of a fused projection)."""
+    if t.dtype != dtype:
+        raise TypeError("%s: dtype %s, want %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: shape %s, want %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_cuda or (t.numel() and t.stride()[1:] != (shape[2], 1) and not t[0].is_contiguous()):
+        raise ValueError("%s: must be a CUDA tensor with dense rows" % name)
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
 
 
 def version():
@@ -158,6 +182,44 @@ def sparse_decode_noalloc(q, k_pages, v_pages, kv_lens, kv_indptr, kv_indices, k
     return out, lse
 
 
+class Rope:
+    """Rotary frequencies (msa_rope_create): rotary_dim dims of a head turn in
+    pairs, (i, i + rotary_dim/2) for "half" and (2i, 2i + 1) for
+    "interleaved"; scaling "none", "linear", "ntk" or "yarn" by factor."""
+
+    def __init__(self, rotary_dim, layout="half", base=10000.0, scaling="none", factor=1.0, original_len=0,
+                 beta_fast=32.0, beta_slow=1.0):
+        self.rotary_dim = int(rotary_dim)
+        h = ctypes.c_void_p()
+        _check(_lib.msa_rope_create(self.rotary_dim, ROPE_LAYOUTS[layout], float(base), ROPE_SCALINGS[scaling],
+                                    float(factor), int(original_len), float(beta_fast), float(beta_slow),
+                                    ctypes.byref(h)), "msa_rope_create")
+        self._h = h
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            _lib.msa_rope_destroy(h)
+            self._h = None
+
+    def apply(self, x, positions, out=None, inverse=False, stream=None):
+        """x [rows, heads, head_dim] (bf16 or fp32, rows at a stride) rotated by
+        int32 positions [rows], or back with inverse=True, which is the
+        gradient (msa_rope_apply).  out may be x."""
+        if x.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("x: dtype %s, want bfloat16 or float32" % x.dtype)
+        n, heads, d = x.shape
+        _need_rows(x, x.dtype, (n, heads, d), "x")
+        _need(positions, torch.int32, (n,), "positions")
+        if out is None:
+            out = torch.empty((n, heads, d), dtype=x.dtype, device=x.device)
+        _need_rows(out, x.dtype, (n, heads, d), "out")
+        _check(_lib.msa_rope_apply(self._h, _ptr(x), _row_stride(x), _ptr(positions), n, heads, d,
+                                   int(x.dtype == torch.float32), int(inverse), _ptr(out), _row_stride(out),
+                                   _stream(stream)), "msa_rope_apply")
+        return out
+
+
 class Plan:
     """A validated batch shape with its device tables (msa_plan)."""
 
@@ -172,7 +234,7 @@ class Plan:
                                                                   head_dim, proxy_head_dim, topk)
         self.num_pages = int(num_pages)
         self.kv_dtype = kv_dtype
-        code = {"bf16": KV_BF16, "e4m3": KV_FP8_E4M3}[kv_dtype]
+        code = {"bf16": KV_BF16, "e4m3": KV_FP8_E4M3, "e4m3_block": KV_FP8_E4M3_BLOCK}[kv_dtype]
         h = ctypes.c_void_p()
         _check(_lib.msa_plan(qa, ka, b, num_qo_heads, num_kv_heads, num_proxy_heads, head_dim, proxy_head_dim,
                              page_size, topk, self.num_pages, code, 0, _stream(stream), ctypes.byref(h)),
@@ -193,6 +255,73 @@ class Plan:
         if h is not None and h.value:
             _lib.msa_plan_destroy(h)
             self._h = None
+
+    def _need_scales(self, k_scale, v_scale):
+        if self.kv_dtype != "bf16":
+            shape = (self.hkv,) if self.kv_dtype == "e4m3" else (self.num_pages, self.hkv)
+            _need(k_scale, torch.float32, shape, "k_scale")
+            _need(v_scale, torch.float32, shape, "v_scale")
+
+    # -- the cache
+    def kv_append(self, k, v, k_pages, v_pages, kv_indices, k_scale=None, v_scale=None, rope=None, positions=None,
+                  stream=None):
+        """The batch's new K and V rows [total_q, Hkv, d] bf16 into the cache
+        (msa_kv_append), K rotated by `rope` at int32 positions [total_q], or at
+        its key positions; quantised by the plan's kv_dtype."""
+        _need_rows(k, torch.bfloat16, (self.total_q, self.hkv, self.d), "k")
+        _need_rows(v, torch.bfloat16, (self.total_q, self.hkv, self.d), "v")
+        kvt = torch.bfloat16 if self.kv_dtype == "bf16" else torch.float8_e4m3fn
+        _need(k_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "k_pages")
+        _need(v_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "v_pages")
+        _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
+        self._need_scales(k_scale, v_scale)
+        if positions is not None:
+            _need(positions, torch.int32, (self.total_q,), "positions")
+        _check(_lib.msa_kv_append(self._h, rope and rope._h, _ptr(positions), _ptr(k), _row_stride(k), _ptr(v),
+                                  _row_stride(v), _ptr(kv_indices), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                  _ptr(v_scale), _stream(stream)), "msa_kv_append")
+
+    def pk_append(self, pk, kv_indices, pk_pages=None, pk_pages_e4m3=None, pk_scale=None, pk_codes=None,
+                  pk_block_scales=None, pk_global_scale=None, rope=None, positions=None, stream=None):
+        """The batch's new proxy K rows [total_q, 1, dp] bf16 into the pools given
+        (msa_pk_append): bf16, e4m3 with pk_scale, NVFP4 with its scales."""
+        pool = (self.num_pages, 1, 128)
+        _need_rows(pk, torch.bfloat16, (self.total_q, 1, self.dp), "pk")
+        _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
+        for t, dtype, shape, name in (
+                (pk_pages, torch.bfloat16, pool + (self.dp,), "pk_pages"),
+                (pk_pages_e4m3, torch.float8_e4m3fn, pool + (self.dp,), "pk_pages_e4m3"),
+                (pk_scale, torch.float32, (1,), "pk_scale"),
+                (pk_codes, torch.uint8, pool + (self.dp // 2,), "pk_codes"),
+                (pk_block_scales, torch.float8_e4m3fn, pool + (self.dp // 16,), "pk_block_scales"),
+                (pk_global_scale, torch.float32, (1,), "pk_global_scale"),
+                (positions, torch.int32, (self.total_q,), "positions")):
+            if t is not None:
+                _need(t, dtype, shape, name)
+        _check(_lib.msa_pk_append(self._h, rope and rope._h, _ptr(positions), _ptr(pk), _row_stride(pk),
+                                  _ptr(kv_indices), _ptr(pk_pages), _ptr(pk_pages_e4m3), _ptr(pk_scale),
+                                  _ptr(pk_codes), _ptr(pk_block_scales), _ptr(pk_global_scale), _stream(stream)),
+               "msa_pk_append")
+
+    def append_bwd(self, kv_indices, dk_pages=None, dv_pages=None, dpk_pages=None, k_rope=None, pk_rope=None,
+                   positions=None, stream=None):
+        """Gradients of the appended rows from the gradient pages of
+        sparse_attn_bwd (msa_append_bwd): (dk, dv [total_q, Hkv, d], dpk
+        [total_q, 1, dp]) fp32, None where no pages are given."""
+        _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
+        if positions is not None:
+            _need(positions, torch.int32, (self.total_q,), "positions")
+        rows = []
+        for pages, heads, d, name in ((dk_pages, self.hkv, self.d, "dk_pages"), (dv_pages, self.hkv, self.d, "dv_pages"),
+                                      (dpk_pages, 1, self.dp, "dpk_pages")):
+            if pages is not None:
+                _need(pages, torch.float32, (self.num_pages, heads, 128, d), name)
+            rows.append(None if pages is None else torch.empty((self.total_q, heads, d), dtype=torch.float32,
+                                                               device=pages.device))
+        _check(_lib.msa_append_bwd(self._h, k_rope and k_rope._h, pk_rope and pk_rope._h, _ptr(positions),
+                                   _ptr(kv_indices), _ptr(dk_pages), _ptr(dv_pages), _ptr(dpk_pages),
+                                   *(_ptr(r) for r in rows), _stream(stream)), "msa_append_bwd")
+        return tuple(rows)
 
     # -- stage 1
     def proxy_maxscore(self, pq, pk_pages, kv_indices, out=None, stream=None):
@@ -263,9 +392,7 @@ class Plan:
         _need(v_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "v_pages")
         _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
         _need(kv_block_indexes, torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes")
-        if self.kv_dtype != "bf16":
-            _need(k_scale, torch.float32, (self.hkv,), "k_scale")
-            _need(v_scale, torch.float32, (self.hkv,), "v_scale")
+        self._need_scales(k_scale, v_scale)
         if out is None:
             out = torch.empty_like(q)
         _need(out, torch.bfloat16, tuple(q.shape), "out")

@@ -82,10 +82,29 @@ typedef enum {
 
 typedef enum {
   MSA_KV_BF16 = 0,           /* K/V pages are bfloat16 */
-  MSA_KV_FP8_E4M3 = 1        /* K/V pages are OCP e4m3 with one fp32 scale per KV head */
+  MSA_KV_FP8_E4M3 = 1,       /* K/V pages are OCP e4m3 with one fp32 scale per KV head */
+  MSA_KV_FP8_E4M3_BLOCK = 2  /* K/V pages are OCP e4m3 with one fp32 scale per (page, KV head) */
 } msa_kv_dtype;
 
+typedef enum {
+  MSA_BF16 = 0,
+  MSA_F32 = 1
+} msa_dtype;
+
+typedef enum {
+  MSA_ROPE_HALF = 0,         /* pairs (i, i + rotary_dim / 2) */
+  MSA_ROPE_INTERLEAVED = 1   /* pairs (2 i, 2 i + 1) */
+} msa_rope_layout;
+
+typedef enum {
+  MSA_ROPE_NONE = 0,
+  MSA_ROPE_LINEAR = 1,       /* positions divided by the factor */
+  MSA_ROPE_NTK = 2,          /* base * factor^(rotary_dim / (rotary_dim - 2)) */
+  MSA_ROPE_YARN = 3          /* by parts, with the factor on the rotated values */
+} msa_rope_scaling;
+
 typedef struct msa_plan_s* msa_plan_t;
+typedef struct msa_rope_s* msa_rope_t;
 
 /*
  * msa_plan -- validate a batch shape and build the device tables every
@@ -279,9 +298,18 @@ msa_status msa_proxy_topk(msa_plan_t plan, const void* pq, const void* pk_pages,
  *                    sees no key of its selection gets out = 0 and
  *                    lse = -inf (a row of only -1 included); decode
  *                    selections must hold the diagonal (last) block.
- *  k_scale, v_scale  fp32 [Hkv] for FP8 K/V, NULL for bf16.
+ *  k_scale, v_scale  fp32 [Hkv] for MSA_KV_FP8_E4M3, fp32 [num_pages, Hkv]
+ *                    for MSA_KV_FP8_E4M3_BLOCK, NULL for bf16.
  *  out               bf16 [total_q, Hq, d] (output).
  *  lse               fp32 [total_q, Hq] (output) or NULL.
+ * MSA_KV_FP8_E4M3_BLOCK: s uses k * k_scale[page, g] and V is v *
+ * v_scale[page, g] of the page that holds the key; head_dim 128, and at
+ * decode at most 16 query heads per proxy head.  Scales are taken as lying in
+ * [2^-40, 2^40] (others, zero and NaN among them, count as the nearer end).
+ * Slots of a sequence's last page behind its last key may hold any bytes.  At
+ * decode, too, a row that sees no key of its selection gets out = 0 and
+ * lse = -inf.
+ *
  * Decode batches (every qo_len == 1) run a split-K kernel whose partial
  * results live in the plan's workspace: two calls on one plan must not
  * overlap in time (issue them on one stream, or order the streams).
@@ -373,6 +401,133 @@ msa_status msa_sparse_decode_noalloc(const void* q, const void* k_pages, const v
                                      int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
                                      int32_t topk, int64_t num_pages, void* out, float* lse,
                                      uint32_t* err_word, msa_stream_t stream);
+
+/*
+ * msa_rope_create -- a table of rotary frequencies, for msa_rope_apply and the
+ * cache appends.  Pair i of rotary_dim / 2 turns by
+ *   f_i = base^(-2 i / rotary_dim)
+ * radians a position, and `scaling` stretches that to contexts `factor` times
+ * as long:
+ *   MSA_ROPE_LINEAR  f_i / factor;
+ *   MSA_ROPE_NTK     base * factor^(rotary_dim / (rotary_dim - 2)) for base;
+ *   MSA_ROPE_YARN    with D(b) = rotary_dim ln(original_len / (2 pi b)) /
+ *                    (2 ln base), lo = floor D(beta_fast), hi = ceil
+ *                    D(beta_slow) and the ramp r_i = clamp((i - lo) /
+ *                    (hi - lo), 0, 1):  (1 - r_i) f_i + r_i f_i / factor,
+ *                    and the rotated values are multiplied by m = 0.1 ln
+ *                    factor + 1 (m = 1 otherwise).
+ *
+ *  rotary_dim    a multiple of 16 in [16, 256].
+ *  base          above 1.
+ *  factor        at least 1; read unless scaling is MSA_ROPE_NONE.
+ *  original_len, beta_fast, beta_slow   read for MSA_ROPE_YARN only.
+ *  out           receives the handle; release with msa_rope_destroy.
+ * Host memory only: the handle serves every device and stream, and calls that
+ * were given it keep no reference to it (they copy the table at the launch).
+ * Angles are exact to fp32 at every int32 position: the phase is an integer
+ * product modulo one turn.
+ */
+msa_status msa_rope_create(int32_t rotary_dim, msa_rope_layout layout, double base, msa_rope_scaling scaling,
+                           double factor, int32_t original_len, double beta_fast, double beta_slow,
+                           msa_rope_t* out);
+
+void msa_rope_destroy(msa_rope_t rope);
+
+/*
+ * msa_rope_apply -- rotary positions: with t = f_i * positions[row] and (a, b)
+ * pair i of a head,  a' = m (a cos t - b sin t),  b' = m (b cos t + a sin t);
+ * dims from rotary_dim on are copied.  With inverse != 0 the rotation is by
+ * -t (and still times m): the transpose, which takes the gradient of the
+ * rotated heads to that of the heads.  Computed in fp32, rounded once.
+ *
+ *  x             bf16 or fp32 [n_rows, heads, head_dim]; rows x_row_stride
+ *                elements apart, heads dense within a row (a slice of a fused
+ *                projection's rows serves).
+ *  positions     int32 [n_rows], any values.
+ *  n_rows        >= 0 (0: nothing is done).
+ *  head_dim      a multiple of 16 up to 256, at least rotary_dim.
+ *  out           as x, rows out_row_stride elements apart; x itself (in
+ *                place) or memory that shares no row with it.
+ * Rows must start on 16-byte boundaries (MSA_ERR_INVALID_ARG otherwise).
+ */
+msa_status msa_rope_apply(msa_rope_t rope, const void* x, int64_t x_row_stride, const int32_t* positions,
+                          int64_t n_rows, int32_t heads, int32_t head_dim, msa_dtype dtype, int32_t inverse,
+                          void* out, int64_t out_row_stride, msa_stream_t stream);
+
+/*
+ * msa_kv_append -- writes a batch's new K and V rows into the paged cache that
+ * msa_sparse_attn reads: row r of a sequence, at key position kv_len - qo_len
+ * + r, goes to slot position % 128 of the page of its block.  K is rotated
+ * first when a rope is given.
+ *
+ *  rope          NULL: K is written as it is.
+ *  positions     int32 [total_q] for the rotation, or NULL for the key
+ *                positions.
+ *  k, v          bf16 [total_q, Hkv, d], rows k_row_stride / v_row_stride
+ *                elements apart, each starting on a 16-byte boundary.
+ *  kv_indices    int32 page table.  Pages that get rows must be named once
+ *                (a shared prefix ends on a page boundary).
+ *  k_pages, v_pages, k_scale, v_scale   the cache, by the plan's kv_dtype:
+ *    MSA_KV_BF16            bf16(x); no scales.
+ *    MSA_KV_FP8_E4M3        e4m3(x / scale[head]); scale fp32 [Hkv] is read.
+ *    MSA_KV_FP8_E4M3_BLOCK  e4m3(x / s), s = scale[page, head], fp32
+ *        [num_pages, Hkv], is written: the least power of two s in [2^-40,
+ *        2^40] with |x| <= 448 s for the page's new rows (infinities aside),
+ *        and not below the page's scale (rounded up to a power of two) when
+ *        the rows go behind others on a partly filled page.  Where that
+ *        raises the scale, the slots before the new rows are converted to it.
+ *        A page whose first slot is written starts anew, whatever scale it
+ *        had.  A partly filled page whose scale is not in (0, 2^40] raises
+ *        MSA_ERR_DEVICE_CHECK and its old slots keep their bytes.
+ *    e4m3 conversions are to nearest, ties to even, saturating at +-448.
+ * Other slots of the pages keep their contents.  A page id outside the pool is
+ * reported (MSA_ERR_DEVICE_CHECK) and its rows are dropped.  One launch; the
+ * call uses no workspace of the plan, and appending the same rows again gives
+ * the same cache.
+ */
+msa_status msa_kv_append(msa_plan_t plan, msa_rope_t rope, const int32_t* positions, const void* k,
+                         int64_t k_row_stride, const void* v, int64_t v_row_stride, const int32_t* kv_indices,
+                         void* k_pages, void* v_pages, float* k_scale, float* v_scale, msa_stream_t stream);
+
+/*
+ * msa_pk_append -- writes a batch's new proxy K rows, as msa_kv_append does K,
+ * into any of the three pools that the proxy passes read (one at least; a
+ * prefill scans bf16, the decode steps after it e4m3 or NVFP4).
+ *
+ *  pk              bf16 [total_q, dp], rows pk_row_stride elements apart.
+ *  pk_pages        bf16 [num_pages, 1, 128, dp], or NULL.
+ *  pk_pages_e4m3   e4m3(x / pk_scale[0]), or NULL with pk_scale NULL.
+ *  pk_codes, pk_block_scales, pk_global_scale   NVFP4 as
+ *                  msa_proxy_maxscore_nvfp4 reads it, or all NULL: the block
+ *                  scale is e4m3(amax / (6 g)) over 16 dims, g the global
+ *                  scale (read, > 0), and a code e2m1(x / (block scale * g)),
+ *                  both to nearest with ties to even, saturating; codes of a
+ *                  block whose scale is 0 are 0.
+ * rope, positions, kv_indices, errors: as msa_kv_append.
+ */
+msa_status msa_pk_append(msa_plan_t plan, msa_rope_t rope, const int32_t* positions, const void* pk,
+                         int64_t pk_row_stride, const int32_t* kv_indices, void* pk_pages, void* pk_pages_e4m3,
+                         const float* pk_scale, void* pk_codes, void* pk_block_scales, const float* pk_global_scale,
+                         msa_stream_t stream);
+
+/*
+ * msa_append_bwd -- the backward of msa_kv_append and msa_pk_append on bf16
+ * plans: the gradients of the new rows out of the gradient pages that
+ * msa_sparse_attn_bwd wrote, dK and dpk rotated back (see msa_rope_apply,
+ * inverse).
+ *
+ *  k_rope, pk_rope, positions   as given to the appends (NULL where they were).
+ *  dk_pages, dv_pages   fp32 [num_pages, Hkv, 128, d];  dpk_pages fp32
+ *                       [num_pages, 1, 128, dp].
+ *  dk, dv               fp32 [total_q, Hkv, d];  dpk fp32 [total_q, dp]
+ *                       (outputs, overwritten).
+ * Each of the three is left out with both its pointers NULL.  All must be
+ * 16-byte aligned.  Rows of a page id outside the pool are zero, and
+ * reported.
+ */
+msa_status msa_append_bwd(msa_plan_t plan, msa_rope_t k_rope, msa_rope_t pk_rope, const int32_t* positions,
+                          const int32_t* kv_indices, const float* dk_pages, const float* dv_pages,
+                          const float* dpk_pages, float* dk, float* dv, float* dpk, msa_stream_t stream);
 
 /*
  * msa_check_errors -- waits for `stream`, then reads and clears the plan's

@@ -456,3 +456,116 @@ def kl_objective(pq, pk, q_bits, k_bits, kv_indices, kv_block_indexes, qo_lens, 
                 terms = np.where(p_main > 0, p_main * (np.log(p_main) - log_pp), 0.0)
             total += kl_weight * terms.sum()
     return total
+
+
+# ---------------------------------------------------------------------------
+# rotary positions and the paged-cache appends
+# ---------------------------------------------------------------------------
+
+def rope_freqs(rot: int, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0):
+    """Radians a position of each of the rot/2 pairs, and the factor on the
+    rotated values: base^(-2i/rot), divided by the factor (linear), with
+    base * factor^(rot/(rot-2)) (ntk), or joined from both by a linear ramp over
+    the pair index between the pairs that turn beta_fast and beta_slow times
+    over original_len positions (yarn)."""
+    i = np.arange(rot // 2, dtype=np.float64)
+    if scaling == "ntk":
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-2.0 * i / rot)
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling != "yarn":
+        return f, 1.0
+
+    def pair_turning(times):
+        return rot * math.log(original_len / (2 * math.pi * times)) / (2 * math.log(base))
+    lo, hi = math.floor(pair_turning(beta_fast)), math.ceil(pair_turning(beta_slow))
+    ramp = np.clip((i - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+    return (1.0 - ramp) * f + ramp * f / factor, 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+
+
+def rope(x, positions, rot: int, layout="half", inverse=False, **scaling):
+    """x [n, heads, d] with pairs (i, i + rot/2) or (2i, 2i + 1) of every head
+    rotated by freq_i * position (times the factor); inverse: the transpose."""
+    x = np.array(x, dtype=np.float64)
+    f, m = rope_freqs(rot, **scaling)
+    turns = np.asarray(positions, dtype=np.float64)[:, None] * (f / (2 * math.pi))[None]
+    t = (turns - np.floor(turns)) * 2 * math.pi * (-1.0 if inverse else 1.0)
+    c, s = m * np.cos(t)[:, None], m * np.sin(t)[:, None]
+    lo, hi = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
+    a, b = x[..., lo].copy(), x[..., hi].copy()
+    x[..., lo], x[..., hi] = a * c - b * s, b * c + a * s
+    return x
+
+
+def _nearest_code(x, magnitudes):
+    """Index of the magnitude nearest to each |x|; on a border the even one."""
+    mags = np.asarray(magnitudes, dtype=np.float64)
+    borders = (mags[1:] + mags[:-1]) / 2
+    a = np.abs(x)
+    up, down = np.searchsorted(borders, a, side="right"), np.searchsorted(borders, a, side="left")
+    return np.where(up % 2 == 0, up, down)
+
+
+def to_e4m3(x):
+    """e4m3 codes (uint8) of x: to nearest, ties to even, saturating; NaN 0x7f."""
+    x = np.asarray(x, dtype=np.float64)
+    mags = e4m3_to_f64(np.arange(127, dtype=np.uint8))
+    code = np.where(np.isnan(x), 0x7F, _nearest_code(np.where(np.isnan(x), 0.0, x), mags))
+    return (code | (np.signbit(x).astype(np.int64) << 7)).astype(np.uint8)
+
+
+def to_nvfp4(x, global_scale):
+    """(code bytes [..., d/2], block scale codes [..., d/16]) of x [..., d]:
+    e4m3 scale amax/(6 g) of 16 dims, e2m1 codes of x/(scale g)."""
+    x = np.asarray(x, dtype=np.float64)
+    g = float(global_scale)
+    blk = x.reshape(*x.shape[:-1], -1, 16)
+    sc = to_e4m3(np.abs(blk).max(-1) / (6 * g))
+    by = (e4m3_to_f64(sc) * g)[..., None]
+    with np.errstate(divide="ignore", invalid="ignore"):
+        y = np.where(by > 0, blk / by, 0.0)
+    code = _nearest_code(y, [0, 0.5, 1, 1.5, 2, 3, 4, 6]) | (np.signbit(blk) & (by > 0)).astype(np.int64) << 3
+    code = code.reshape(x.shape).astype(np.uint8)
+    return code[..., 0::2] | (code[..., 1::2] << 4), sc
+
+
+def block_scale(amax):
+    """The least power of two s in [2^-40, 2^40] with amax <= 448 s."""
+    e = -40
+    while e < 40 and amax > 448.0 * 2.0 ** e:
+        e += 1
+    return 2.0 ** e
+
+
+def kv_append(x, pages, kv_indices, qo_lens, kv_lens, kind, scale=None):
+    """Rows x [total_q, H, d] (float64, K already rotated) into a copy of pages
+    [P, H, 128, d] (bf16: float64 values; e4m3: codes): (pages, scale).  kind
+    "bf16" stores x itself (unrounded), "e4m3" codes of x / scale[h],
+    "e4m3_block" codes with scale [P, H], page by page."""
+    pages = np.array(pages)
+    scale = None if scale is None else np.array(scale, dtype=np.float64)
+    indptr, r = kv_indptr(kv_lens), 0
+    for s, (q, k) in enumerate(zip(qo_lens, kv_lens)):
+        pos = k - q
+        while pos < k:
+            slot = pos % PAGE
+            n = min(k - pos, PAGE - slot)
+            page = int(kv_indices[indptr[s] + pos // PAGE])
+            rows = x[r:r + n].transpose(1, 0, 2)
+            for h in range(x.shape[1]):
+                if kind == "bf16":
+                    pages[page, h, slot:slot + n] = rows[h]
+                    continue
+                by = scale[h] if kind == "e4m3" else None
+                if by is None:
+                    fin = np.abs(rows[h][np.isfinite(rows[h])])
+                    by = block_scale(fin.max() if fin.size else 0.0)
+                    if slot > 0:
+                        by = max(by, 2.0 ** math.ceil(math.log2(scale[page, h])))
+                        old = e4m3_to_f64(pages[page, h, :slot])
+                        pages[page, h, :slot] = to_e4m3(old * (scale[page, h] / by))
+                    scale[page, h] = by
+                pages[page, h, slot:slot + n] = to_e4m3(rows[h] / by)
+            pos, r = pos + n, r + n
+    return pages, scale
