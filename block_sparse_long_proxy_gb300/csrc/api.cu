@@ -447,7 +447,6 @@ msa_status msa_sparse_attn(msa_plan_t plan, const void* q, const void* k_pages, 
     return set_error(MSA_ERR_INVALID_ARG, "msa_sparse_attn: NULL argument");
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
     return set_error(MSA_ERR_INVALID_ARG, "msa_sparse_attn: q, k_pages, v_pages, out must be 16-byte aligned");
-  if (plan->kv_dtype == MSA_KV_FP8_E4M3_BLOCK) return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: block scales");
   const bool fp8 = plan->kv_dtype != MSA_KV_BF16;
   if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
     return set_error(MSA_ERR_INVALID_ARG, "msa_sparse_attn: k_scale/v_scale must be given exactly for FP8 K/V");

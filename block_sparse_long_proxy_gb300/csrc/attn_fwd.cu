@@ -41,6 +41,12 @@
 // Rounding: Q to f16 is exact for |q| in [2^-14, 65504] (smaller values
 // lose at most 2^-25, larger ones saturate) and P is rounded to f16 instead
 // of bf16.
+//
+// kBlk: one scale for each (page, KV head) instead (BlockScale in
+// msa_internal.h).  The softmax warps read a block's two scales a block ahead,
+// from the row the block's list entry already names, and take them into the
+// multiply-add that scales the logits; the converters write zeros for V rows
+// behind the sequence's last key, whose bytes were never written.
 #include "msa_internal.h"
 #include "ptx.cuh"
 
@@ -81,7 +87,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 // out-of-range entries dropped) and row[cap] (their first K/V tensor-map
 // row), cap >= topk.
 struct UnitHdr {
-  int32_t n, nh, h0, q_begin, rows, pos0, g, pad[9];
+  int32_t n, nh, h0, q_begin, rows, pos0, g, kv_len, pad[8];
 };
 constexpr int kListSlots = 2;
 constexpr int kHdrInts = 16;
@@ -117,7 +123,7 @@ struct AttnSmem {
 // barrier's phase comes from a running count (per head for the S / P / O
 // barriers), and Q is released right after a unit's last QK so the next
 // unit's Q load overlaps the tail of the current one.
-template <int D, bool kOneKvHead, bool kFp8, bool kStageO>
+template <int D, bool kOneKvHead, bool kFp8, bool kStageO, bool kBlk = false>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap o_map,
@@ -136,6 +142,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   using L = AttnSmem<D, kStageO, kOneKvHead ? 2 : 1>;
   constexpr int kChunks = D / 64;
   static_assert(!kFp8 || (D == 128 && !kOneKvHead), "FP8 K/V: head_dim 128, main attention");
+  static_assert(!kBlk || kFp8, "block scales come with FP8 K/V");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem + L::kQOff;
@@ -304,6 +311,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ls.rows = tl.rows;
         ls.pos0 = tl.pos0;
         ls.g = u.g / kv_div;
+        ls.kv_len = tl.kv_len;
       }
       __syncwarp();
       if (lane == 0) {
@@ -461,12 +469,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int n = ok ? ls.n : 0, nh = ok ? ls.nh : 0;
       const int rows = ls.rows, pos0 = ls.pos0;
       // FP8: the scores are q . k_code, scaled by k_scale of the unit's KV head
-      const float sl2 = kFp8 ? scale_log2 * k_scale[ls.g] : scale_log2;
+      float sl2 = kFp8 && !kBlk ? scale_log2 * k_scale[ls.g] : scale_log2;
+      float log2_vs = 0.f, inv_vs = 1.f, ks_next = 1.f, vs_next = 1.f;
+      if (kBlk && ok && n > 0) {
+        ks_next = k_scale[lrow(k)[0] >> 7];
+        vs_next = v_scale[lrow(k)[0] >> 7];
+      }
       const bool active = ok && h < nh;
       const bool row_ok = r < rows;
       const int qpos = pos0 + r;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; active && ok && i < n; ++i) {
+        if (kBlk) {
+          const BlockScale bs = block_scale_of(ks_next, vs_next);
+          sl2 = scale_log2 * bs.ks, log2_vs = bs.log2_vs, inv_vs = bs.inv_vs;
+          if (i + 1 < n) {
+            ks_next = k_scale[lrow(k)[i + 1] >> 7];
+            vs_next = v_scale[lrow(k)[i + 1] >> 7];
+          }
+        }
         if (!(ok = mbar_wait_inl(s_full + h, (ch + i) & 1, err))) break;
         tc_fence_after();
         uint32_t sv[128];
@@ -497,16 +518,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // lazy rescaling: the reference max moves only when the row max grows
         // by more than 2^8, so probabilities stay below 256 and O is rescaled
         // rarely
-        const float mx2 = mx * sl2;
+        const float mx2 = kBlk ? fmaf(mx, sl2, log2_vs) : mx * sl2;
         const float m_new = mx2 > m + 8.f ? mx2 : m;
         const float m_use = m_new == -INFINITY ? 0.f : m_new;
         const float alpha = m_new == m ? 1.f : ex2_approx(m - m_use);
+        const float shift = kBlk ? log2_vs - m_use : -m_use;
         float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
         uint32_t pk[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
           float x0, x1;
-          ffma2(x0, x1, __uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]), sl2, -m_use);
+          ffma2(x0, x1, __uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]), sl2, shift);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
           if (c & 1)
             fadd2(sum2, sum3, p0, p1);
@@ -518,7 +540,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         sum1 += sum3;
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_st16(s_addr + c * 16, pk + c * 16);
-        l = l * alpha + (sum0 + sum1);
+        l = l * alpha + (kBlk ? (sum0 + sum1) * inv_vs : sum0 + sum1);
         // rescale O_h (written by P.V of the previous block, already complete
         // because the S_h MMA of this block was issued after it)
         // (P_h.V of the previous block is complete: the MMA thread issued
@@ -591,7 +613,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool active = ok && st.active != 0;
         const bool unit_ok = ok && st.ok != 0;
         const float m = st.m[r], l = st.l[r];
-        const float o_scale = kFp8 ? v_scale[st.g] : 1.f;
+        const float o_scale = kFp8 && !kBlk ? v_scale[st.g] : 1.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(stat_empty + h * 2 + b);
         if (!active) {
@@ -675,7 +697,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // f16 units, and the only f16 units that land in that upper half are the
     // same row's, so no other thread's codes are overwritten.
     const int ct = threadIdx.x - 32 * (kSoftWarps + 2);
-    auto expand = [&](uint8_t* buf) {  // buf: one ring stage, 2 chunks x [128 rows][128 B] of f16
+    auto expand = [&](uint8_t* buf, int rows) {  // buf: one ring stage, 2 chunks x [128 rows][128 B] of f16
 #pragma unroll 1
       for (int rr = 0; rr < 2; ++rr) {
         const int r = ct + 64 * rr, sw = r & 7;
@@ -683,6 +705,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         uint4 u[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) u[c] = *reinterpret_cast<const uint4*>(raw + ((c ^ sw) << 4));
+        if (kBlk && r >= rows) {  // behind the sequence's last key
+#pragma unroll
+          for (int c = 0; c < 8; ++c) u[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {  // codes of d in [16c, 16c + 16) -> two f16 units
           uint4 lo, hi;
@@ -708,9 +734,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       ok = mbar_wait_inl(list_full + k % kListSlots, (k / kListSlots) & 1, err);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-      const int n = ls.n, nh = ls.nh;
+      const int n = ls.n, nh = ls.nh, kv_len = ls.kv_len;
+      const int32_t* const ls_j = lj(k);
       __syncwarp();
-      if (lane == 0) mbar_arrive(list_empty + k % kListSlots);
+      if (!kBlk && lane == 0) mbar_arrive(list_empty + k % kListSlots);
       // Q of the unit's heads, bf16 -> f16 in place
       if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait_inl(q_full, k & 1, err)))) break;
       for (int hh = 0; hh < nh; ++hh) {
@@ -731,12 +758,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int i = 0; i < n; ++i, ++kv_it) {
         const int s = kv_it % kStages;
         if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait_inl(raw_full + s, (kv_it / kStages) & 1, err)))) break;
-        expand(k_s + s * L::kTileBytes);
-        expand(v_s + s * L::kTileBytes);
+        expand(k_s + s * L::kTileBytes, 128);
+        expand(v_s + s * L::kTileBytes, kBlk ? kv_len - ls_j[i] * 128 : 128);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(kv_full + s);
       }
+      if (kBlk && lane == 0) mbar_arrive(list_empty + k % kListSlots);  // read up to here
     }
   } else {
     setmaxnreg_dec<kWg2Regs>();  // warps 10-11 without FP8 K/V: idle
@@ -800,7 +828,7 @@ cudaError_t check_launch_regs(K kern) {
   return a.numRegs == kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
-template <int D, bool kOneKvHead, bool kFp8>
+template <int D, bool kOneKvHead, bool kFp8, bool kBlk = false>
 cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& qm, const CUtensorMap& km,
                                 const CUtensorMap& vm, const CUtensorMap& om, int32_t topk, const AttnUnit* units,
                                 int32_t n_units, const TileInfo* tiles, const int32_t* idx,
@@ -811,7 +839,7 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
   if constexpr (kFp8) {
     const int staged = AttnSmem<D, true, kOneKvHead ? 2 : 1>::bytes(cap) + 1024;
     if (staged <= kMaxSmem) {
-      auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, true>;
+      auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, true, kBlk>;
       if (const cudaError_t e = check_launch_regs(kern)) return e;
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, staged);
       return launch_pdl(kern, grid, dim3(kAttnThreads), staged, st, qm, km, vm, om, cap, units, n_units,
@@ -820,7 +848,7 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
     }
   }
   const int plain = AttnSmem<D, false, kOneKvHead ? 2 : 1>::bytes(kMaxTopk) + 1024;
-  auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false>;
+  auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false, kBlk>;
   if (const cudaError_t e = check_launch_regs(kern)) return e;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plain);
   return launch_pdl(kern, grid, dim3(kAttnThreads), plain, st, qm, km, vm, om, cap, units, n_units, tiles, idx,
@@ -841,7 +869,7 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
                                const int32_t* kv_indices, const int32_t* idx, const float* k_scale,
                                const float* v_scale, void* out, float* lse, cudaStream_t st) {
   if (p->topk > kMaxTopk) return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: topk above 1024");
-  const bool fp8 = p->kv_dtype == MSA_KV_FP8_E4M3;
+  const bool fp8 = p->kv_dtype != MSA_KV_BF16;
   if (fp8 && p->d != 128)
     return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: FP8 K/V prefill needs head_dim 128");
   CUtensorMap qm, km, vm, om;
@@ -860,7 +888,11 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
   const dim3 grid(std::min(p->n_attn_units, p->num_sms));  // persistent: one CTA per SM
   const int kv_div = p->hp / p->hkv;
   cudaError_t e;
-  if (fp8)
+  if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK)
+    e = launch_attn_variant<128, false, true, true>(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units,
+                                                    p->tiles_d, idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp,
+                                                    kv_div, scale_log2, k_scale, v_scale, p->err_d);
+  else if (fp8)
     e = launch_attn_variant<128, false, true>(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units, p->tiles_d,
                                               idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp, kv_div, scale_log2,
                                               k_scale, v_scale, p->err_d);

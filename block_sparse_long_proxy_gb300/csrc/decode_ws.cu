@@ -17,6 +17,13 @@
 //   S^T = K . q^T     M = kKeys keys, N = 8 heads, K = d (e4m3 -> f16 in registers)
 //   O^T += V^T . P^T  M = d,  N = 8 heads, K = kKeys keys (P^T by movmatrix)
 // with d permuted so that every shared-memory read is one conflict-free word.
+//
+// kBlk: one scale for each (page, KV head) (BlockScale in msa_internal.h).  A
+// unit lies in one page, so its scales are three numbers a warp broadcasts
+// with the unit; they cost one fused add and one multiply a unit and thread.
+// Units wholly behind the query position are not loaded, and V rows behind it
+// are zeroed in shared memory (their bytes were never written, and 0 * NaN
+// would reach the output).
 #include "msa_internal.h"
 #include "ptx.cuh"
 
@@ -55,6 +62,7 @@ __device__ __forceinline__ uint32_t swz(int row, int col) {
   return row * 128 + ((((col >> 4) ^ row) & 7) << 4) + (col & 15);
 }
 
+template <bool kBlk>
 __global__ void __launch_bounds__(kWsThreads, 2)
     decode_ws_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                      const __nv_bfloat16* __restrict__ q, const TileInfo* __restrict__ tiles,
@@ -88,6 +96,8 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   const int n_units = kParts * topk;
   const int my_n = n_units > warp ? (n_units - warp + kWsWarps - 1) / kWsWarps : 0;
   int ukey = -1, urow = 0;
+  BlockScale ubs{};
+  const int qpos = tl.pos0;
   if (lane < my_n) {
     const int u = warp + lane * kWsWarps;
     const int j = idx[static_cast<int64_t>(row) * topk + u / kParts];
@@ -101,6 +111,11 @@ __global__ void __launch_bounds__(kWsThreads, 2)
       }
       ukey = j * 128 + (u % kParts) * kKeys;
       urow = static_cast<int>((page * hkv + kvh) * 128 + (u % kParts) * kKeys);
+      if (kBlk) {
+        ubs = block_scale_of(k_scale[page * hkv + kvh], v_scale[page * hkv + kvh]);
+        ubs.ks *= scale_log2;
+        if (ukey > qpos) ukey = -1;
+      }
     }
   }
   // compact the valid units to the low lanes (padding slots load nothing)
@@ -117,6 +132,9 @@ __global__ void __launch_bounds__(kWsThreads, 2)
     const int r2 = __shfl_sync(0xFFFFFFFFu, urow, src);
     ukey = k2;
     urow = r2;
+    if (kBlk)
+      ubs = {__shfl_sync(0xFFFFFFFFu, ubs.ks, src), __shfl_sync(0xFFFFFFFFu, ubs.log2_vs, src),
+             __shfl_sync(0xFFFFFFFFu, ubs.inv_vs, src)};
   }
 
   // q^T fragments: head gi of the group, d = 16 kc + 4 t4 + {0,1} | {2,3}
@@ -137,8 +155,8 @@ __global__ void __launch_bounds__(kWsThreads, 2)
       }
     }
   }
-  const float sl2 = scale_log2 * k_scale[kvh];
-  const int qpos = tl.pos0;
+  float sl2 = kBlk ? 0.f : scale_log2 * k_scale[kvh];
+  float log2_vs = 0.f, inv_vs = 1.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, oacc[8][4];
 #pragma unroll
   for (int md = 0; md < 8; ++md) oacc[md][0] = oacc[md][1] = oacc[md][2] = oacc[md][3] = 0.f;
@@ -159,8 +177,18 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   for (int i = 0; ok && i < n_valid; ++i) {
     issue(i + kStg - 1);  // the stage it fills was released at the end of unit i - 1
     const int key0 = __shfl_sync(0xFFFFFFFFu, ukey, i);
+    if (kBlk) {
+      sl2 = __shfl_sync(0xFFFFFFFFu, ubs.ks, i);
+      log2_vs = __shfl_sync(0xFFFFFFFFu, ubs.log2_vs, i);
+      inv_vs = __shfl_sync(0xFFFFFFFFu, ubs.inv_vs, i);
+    }
     if (!(ok = mbar_wait(bar + i % kStg, (i / kStg) & 1, err))) break;
     const uint32_t kb = smem_u32(buf + (i % kStg) * kStageBytes), vb = kb + kPartBytes;
+    if (kBlk && key0 + kKeys - 1 > qpos) {  // the unit with the query's own key
+      for (int r = qpos + 1 - key0; r < kKeys; ++r) sts32(vb + r * 128 + 4 * lane, 0u);
+      fence_async_shared();  // before the next load overwrites the stage
+      __syncwarp();
+    }
 
     // S^T for the unit's keys
     float sacc[kMT][4];
@@ -179,13 +207,14 @@ __global__ void __launch_bounds__(kWsThreads, 2)
     }
     // keys past the query position (and past kv_len) are masked; log2 domain
     const int kpos0 = key0 + gi;
+    auto scaled = [&](float x) { return kBlk ? fmaf(x, sl2, log2_vs) : x * sl2; };
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
       const bool va = kpos0 + 16 * mt <= qpos, vb2 = kpos0 + 16 * mt + 8 <= qpos;
-      sacc[mt][0] = va ? sacc[mt][0] * sl2 : -INFINITY;
-      sacc[mt][1] = va ? sacc[mt][1] * sl2 : -INFINITY;
-      sacc[mt][2] = vb2 ? sacc[mt][2] * sl2 : -INFINITY;
-      sacc[mt][3] = vb2 ? sacc[mt][3] * sl2 : -INFINITY;
+      sacc[mt][0] = va ? scaled(sacc[mt][0]) : -INFINITY;
+      sacc[mt][1] = va ? scaled(sacc[mt][1]) : -INFINITY;
+      sacc[mt][2] = vb2 ? scaled(sacc[mt][2]) : -INFINITY;
+      sacc[mt][3] = vb2 ? scaled(sacc[mt][3]) : -INFINITY;
     }
     uint32_t pb[kMT][2];
     float alpha[2];
@@ -208,7 +237,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
         sacc[mt][2 + c] = ex2_approx(sacc[mt][2 + c] - m_use);
         sum += sacc[mt][c] + sacc[mt][2 + c];
       }
-      l[c] = l[c] * alpha[c] + sum;
+      l[c] = l[c] * alpha[c] + (kBlk ? sum * inv_vs : sum);
     }
 #pragma unroll
     for (int md = 0; md < 8; ++md) {
@@ -268,7 +297,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
     }
   }
   __syncthreads();
-  const float vs = v_scale[kvh];
+  const float vs = kBlk ? 1.f : v_scale[kvh];
   for (int e = threadIdx.x; e < G * kD; e += kWsThreads) {
     const int h = e / kD, d = e % kD;
     float mm = -INFINITY;
@@ -306,8 +335,9 @@ msa_status launch_attn_decode_ws(const msa_plan_s* p, const void* q, const void*
       !encode_tensor_map(&vm, 2, v_pages, dims, str, box, 0, 128))
     return set_error(MSA_ERR_CUDA, "msa_sparse_attn: tensor map encoding failed");
   const int smem = WsSmem::kBytes + 1024;
-  cudaFuncSetAttribute(decode_ws_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return cuda_check(launch_pdl(decode_ws_kernel, dim3(p->n_tiles * p->hp), dim3(kWsThreads), smem, st, km, vm,
+  auto kern = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK ? decode_ws_kernel<true> : decode_ws_kernel<false>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return cuda_check(launch_pdl(kern, dim3(p->n_tiles * p->hp), dim3(kWsThreads), smem, st, km, vm,
                                 static_cast<const __nv_bfloat16*>(q), p->tiles_d, idx, kv_indices, p->num_pages,
                                 k_scale, v_scale, static_cast<__nv_bfloat16*>(out), lse, p->hq, p->hp,
                                 p->hp / p->hkv, p->topk, 1.4426950408889634f / sqrtf(static_cast<float>(kD)),

@@ -35,6 +35,23 @@ static_assert(sizeof(TileInfo) == 32, "TileInfo is uploaded as raw bytes");
 enum : uint32_t { kErrDeviceCheck = 1u, kErrTimeout = 2u, kErrNonFinite = 4u };
 
 #ifdef __CUDACC__
+// What a block-scaled e4m3 cache does to the softmax of one block: the logit
+// of a key in the log2 domain is t = s_code * ks * scale_log2, its value
+// v_code * vs.  The weights are kept as w = 2^(t + log2 vs - M), M the running
+// maximum of t + log2 vs, so that O += w . v_code needs no scale, and the sum
+// of probabilities is the sum of w / vs.  An f16 w is then as precise for a
+// block of small values as for one of large ones, whichever holds the mass of
+// the softmax.  Scales are kept in [2^-40, 2^40]: sums of w / vs stay far
+// inside fp32 (and a page with scale 0 or NaN has neither logits nor values).
+struct BlockScale {
+  float ks, log2_vs, inv_vs;
+};
+__device__ __forceinline__ float clamp_scale(float s) { return fminf(fmaxf(s, 0x1p-40f), 0x1p40f); }
+__device__ __forceinline__ BlockScale block_scale_of(float ks, float vs) {
+  vs = clamp_scale(vs);
+  return {clamp_scale(ks), log2f(vs), 1.f / vs};
+}
+
 // Order-preserving 32-bit key of a block score for the top-k selection:
 // -0.0 is folded onto +0.0, and -inf maps to 0, which no finite score maps
 // to (0 marks "not a candidate").

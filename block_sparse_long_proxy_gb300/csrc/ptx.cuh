@@ -377,6 +377,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // Named barrier `id` over n threads that also returns the AND of p over them.
 __device__ __forceinline__ bool bar_sync_and(int id, int n, bool p) {
   uint32_t r;

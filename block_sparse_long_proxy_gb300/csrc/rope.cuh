@@ -68,11 +68,15 @@ __device__ __forceinline__ void rope_rotate(bool interleaved, const float (&cs)[
                                             float (&x)[16]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    float& p = interleaved ? x[2 * e] : x[e];
-    float& q = interleaved ? x[2 * e + 1] : x[8 + e];
-    const float a = p, b = q;
-    p = a * cs[e] - b * sn[e];
-    q = b * cs[e] + a * sn[e];
+    if (interleaved) {
+      const float p = x[2 * e], q = x[2 * e + 1];
+      x[2 * e] = p * cs[e] - q * sn[e];
+      x[2 * e + 1] = q * cs[e] + p * sn[e];
+    } else {
+      const float p = x[e], q = x[8 + e];
+      x[e] = p * cs[e] - q * sn[e];
+      x[8 + e] = q * cs[e] + p * sn[e];
+    }
   }
 }
 

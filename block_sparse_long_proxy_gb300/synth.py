@@ -6,7 +6,8 @@ fp64 oracle (the oracle reads the identical bf16 / e4m3 bytes).
 
 Layouts (shared contract, see include/msa.h):
   q, dout        [total_q, Hq, d]          bf16
-  k_pages,v_pages[P, Hkv, 128, d]          bf16, or e4m3 with k_scale/v_scale [Hkv] fp32
+  k_pages,v_pages[P, Hkv, 128, d]          bf16, or e4m3 with k_scale/v_scale [Hkv] fp32,
+                                             or e4m3 with k_scale/v_scale [P, Hkv] ("e4m3_block")
   pk_pages_e4m3 [P, 1, 128, dp], pk_scale [1]  e4m3 proxy K (e4m3 cases only)
   pk_fp4_codes [P, 1, 128, dp/2] uint8, pk_fp4_scales [P, 1, 128, dp/16] e4m3,
   pk_fp4_global [1]                          NVFP4 proxy K (e4m3 cases only)
@@ -34,7 +35,7 @@ class Case:
     hp: int
     dp: int
     topk: int
-    kv_dtype: str = "bf16"          # "bf16" or "e4m3"
+    kv_dtype: str = "bf16"          # "bf16", "e4m3" or "e4m3_block"
     page_perm_seed: int | None = None  # None: identity page table
     planted: bool = False
     seed: int = 0
@@ -139,6 +140,19 @@ def make_inputs(case: Case, device="cpu", with_dout=False):
     if case.kv_dtype == "bf16":
         out["k_pages"] = k.to(torch.bfloat16)
         out["v_pages"] = v.to(torch.bfloat16)
+    elif case.kv_dtype == "e4m3_block":
+        # pages of different sizes, codes with one power-of-two scale for each
+        # (page, KV head); any bytes behind a sequence's last key, NaN among them
+        spread = torch.exp2(2.0 * _randn((2, n_pages, case.hkv), gen, dev)).clamp(2.0 ** -6, 2.0 ** 6)
+        for name, x, sp in (("k", k, spread[0].sqrt()), ("v", v, spread[1])):
+            x = x * sp[..., None, None]
+            scale = torch.exp2(torch.ceil(torch.log2(x.abs().amax(dim=(2, 3)) / 448.0)))
+            codes = (x / scale[..., None, None]).to(torch.float8_e4m3fn)
+            base = 0
+            for kl in case.kv_lens:
+                base += (kl + PAGE - 1) // PAGE
+                codes.view(torch.uint8)[int(table[base - 1]), :, (kl - 1) % PAGE + 1:] = 0x7F
+            out[name + "_pages"], out[name + "_scale"] = codes, scale.contiguous()
     else:
         # e4m3 codes with one fp32 scale per KV head: scale = amax / 448
         ks = k.abs().amax(dim=(0, 2, 3)) / 448.0

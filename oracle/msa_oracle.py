@@ -282,8 +282,8 @@ def sparse_attention(q_bits, k_bits, v_bits, kv_indices, kv_block_indexes, qo_le
     head p = h // (Hq/Hp), R8): softmax over the keys of the blocks
     kv_block_indexes[t, p, :] that are visible to i of q.k_g/sqrt(d),
     O = P.V_g, LSE = ln sum exp.  Hp is kv_block_indexes.shape[1].  bf16
-    K/V, or e4m3 K/V with per-KV-head scales when k_scale/v_scale are given.
-    Returns (O, LSE) in float64; rows of tiles not in tile_ids are NaN."""
+    K/V, or e4m3 K/V when k_scale/v_scale are given: [Hkv], or [P, Hkv] for
+    a scale of each (page, KV head).  Returns (O, LSE) in float64; rows of tiles not in tile_ids are NaN."""
     fp8 = k_scale is not None
     q_bits, k_bits, v_bits = np.asarray(q_bits), np.asarray(k_bits), np.asarray(v_bits)
     tiles = tiles_of(qo_lens, kv_lens)
@@ -308,7 +308,11 @@ def sparse_attention(q_bits, k_bits, v_bits, kv_indices, kv_block_indexes, qo_le
             ks = _selected_keys(tl, kv_block_indexes[ti, h // msa_grp])
             kmat = _decode_kv(kseq[ks, g, :], fp8)
             vmat = _decode_kv(vseq[ks, g, :], fp8)
-            if fp8:
+            if fp8 and np.ndim(k_scale) == 2:        # one scale for each (page, KV head)
+                page = np.asarray(kv_indices)[indptr[tl.seq] + ks // PAGE]
+                kmat = kmat * np.asarray(k_scale, dtype=np.float64)[page, g][:, None]
+                vmat = vmat * np.asarray(v_scale, dtype=np.float64)[page, g][:, None]
+            elif fp8:
                 kmat = kmat * float(k_scale[g])
                 vmat = vmat * float(v_scale[g])
             s = qt[:, h, :] @ kmat.T / math.sqrt(d)
