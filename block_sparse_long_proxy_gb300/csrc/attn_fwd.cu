@@ -176,7 +176,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* ost_free = ost_ready + 1;      // the TMA store has read it
   uint64_t* stat_full = ost_free + 1;      // [head * 2 + buffer]
   uint64_t* stat_empty = stat_full + 4;    // [head * 2 + buffer]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stat_empty + 4);
+  // FP8: K and V of a block travel apart, kv_full / kv_empty / raw_full being
+  // one half's (a block's K is read for the last time by S_1 = Q_1 K^T, a whole
+  // step before P_1 V reads its V, and each half has to be loaded and then
+  // expanded within the time from its release to its next use)
+  uint64_t* k_full = kv_full;              // [kStages]
+  uint64_t* k_empty = stat_empty + 4;      // [kStages]
+  uint64_t* v_full = k_empty + kStages;    // [kStages]
+  uint64_t* v_empty = kv_empty;            // [kStages]
+  uint64_t* raw_v_full = v_full + kStages; // [kStages]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_v_full + kStages);
   UnitStats* const stats = reinterpret_cast<UnitStats*>(smem + L::kStatOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -190,6 +199,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(kv_full + s, kFp8 ? kConvWarps : 1);
       mbar_init(kv_empty + s, 1);
       mbar_init(raw_full + s, 1);
+      mbar_init(k_empty + s, 1);
+      mbar_init(v_full + s, kConvWarps);
+      mbar_init(raw_v_full + s, 1);
     }
     mbar_init(q_ready, kConvWarps);
     mbar_init(ost_ready, 4);  // the four epilogue warps
@@ -325,14 +337,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         for (int i = 0; ok && i < n; ++i, ++kv_it) {
           const int s = kv_it % kStages;
-          if (!(ok = mbar_wait_inl(kv_empty + s, ((kv_it / kStages) & 1) ^ 1, err))) break;
           const int row = ls_row[i];
           if (kFp8) {  // e4m3 codes into the upper half of the stage; the converters expand them
-            mbar_expect_tx(raw_full + s, 2 * 16384);
+            const uint32_t par = ((kv_it / kStages) & 1) ^ 1;
+            if (!(ok = mbar_wait_inl(k_empty + s, par, err))) break;
+            mbar_expect_tx(raw_full + s, 16384);
             tma_load_2d(k_s + s * L::kTileBytes + 16384, &k_map, raw_full + s, 0, row);
-            tma_load_2d(v_s + s * L::kTileBytes + 16384, &v_map, raw_full + s, 0, row);
+            if (!(ok = mbar_wait_inl(v_empty + s, par, err))) break;
+            mbar_expect_tx(raw_v_full + s, 16384);
+            tma_load_2d(v_s + s * L::kTileBytes + 16384, &v_map, raw_v_full + s, 0, row);
             continue;
           }
+          if (!(ok = mbar_wait_inl(kv_empty + s, ((kv_it / kStages) & 1) ^ 1, err))) break;
           // a one-head pool's keys are its values: one load serves both, and
           // a paired unit's second head reads its own block from the V region
           const bool pair = kOneKvHead && u.nh == 2;
@@ -405,6 +421,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc_fence_after();
         qk(0, kv_it & 1);
         if (two) qk(1, kv_it & 1);
+        if (kFp8) mma_commit(k_empty + (kv_it & 1));
         if (n == 1) mma_commit(q_empty);  // the unit's last QK is issued
         for (int i = 0; i < n; ++i) {
           const int it = kv_it + i;
@@ -416,6 +433,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // epilogue must have read it (the QKs above already overlap it)
           if (i == 0 && k > 0 && !(ok = mbar_wait_inl(o_free, (k - 1) & 1, err))) break;
           if (i == 0 && k > 0 && !two && !(ok = mbar_wait_inl(o_free + 1, (k - 1) & 1, err))) break;
+          if (kFp8 && !(ok = mbar_wait_inl(v_full + s, (it >> 1) & 1, err))) break;
           tc_fence_after();
           pv(0, s, i > 0);
           if (!two) mma_commit(kv_empty + s);
@@ -423,6 +441,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!(ok = mbar_wait_inl(kv_full + s1, ((it + 1) >> 1) & 1, err))) break;
             tc_fence_after();
             qk(0, s1);
+            if (kFp8 && !two) mma_commit(k_empty + s1);
             if (!two && i + 1 == n - 1) mma_commit(q_empty);
           } else {
             mma_commit(o_done);
@@ -436,6 +455,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           mma_commit(kv_empty + s);
           if (more) {
             qk(1, s1);
+            if (kFp8) mma_commit(k_empty + s1);
             if (i + 1 == n - 1) mma_commit(q_empty);
           } else {
             mma_commit(o_done + 1);
@@ -759,10 +779,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int s = kv_it % kStages;
         if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait_inl(raw_full + s, (kv_it / kStages) & 1, err)))) break;
         expand(k_s + s * L::kTileBytes, 128);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + s);
+        if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait_inl(raw_v_full + s, (kv_it / kStages) & 1, err)))) break;
         expand(v_s + s * L::kTileBytes, kBlk ? kv_len - ls_j[i] * 128 : 128);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(kv_full + s);
+        if (lane == 0) mbar_arrive(v_full + s);
       }
       if (kBlk && lane == 0) mbar_arrive(list_empty + k % kListSlots);  // read up to here
     }
