@@ -19,12 +19,6 @@
 // (tile, group) row, giving one partial per row segment.  A second kernel
 // merges the (at most a few) segments of each row, applies v_scale and
 // writes out and lse.
-//
-// kBlk: one scale for each (page, KV head) (BlockScale in msa_internal.h): the
-// producer's lanes fetch a unit's scales beside its page id, and they travel
-// with the stage as the block index does.  V rows behind the query position
-// are zeroed in shared memory (their bytes were never written, and 0 * NaN
-// would reach the output).
 #include "msa_internal.h"
 #include "ptx.cuh"
 
@@ -46,7 +40,7 @@ static_assert(kRounds == 1 || kRounds == 2 || kRounds == 4, "a merge slice holds
 static_assert(kMT >= 1 && kKeysW % 16 == 0, "consumer warps take whole 16-key m-tiles");
 constexpr int kDThreads = 32 * (kCWarps + 1);
 constexpr int kDStages = 3;
-constexpr int kBlkBytes = 128 * kD;     // bytes of one e4m3 K (or V) block
+constexpr int kBlk = 128 * kD;          // bytes of one e4m3 K (or V) block
 
 // byte offset of (row, byte col) in a 128-row x 128-byte tile written by TMA
 // with 128-byte swizzle: the 16-byte chunk index is XORed with row % 8.
@@ -68,17 +62,16 @@ __device__ __forceinline__ int range_owner(int u, int U, int C) {
 template <int NT>
 struct DecodeSmem {
   static constexpr int kRingOff = 0;
-  static constexpr int kScratchOff = kDStages * 2 * kBlkBytes;
+  static constexpr int kScratchOff = kDStages * 2 * kBlk;
   // per-warp merge scratch, one slice of d at a time: [warp][head slot][kDR + 2]
   static constexpr int kScratchFloats = kCWarps * 8 * NT * (kDR + 2);
   static constexpr int kBarOff = kScratchOff + kScratchFloats * 4;
   static constexpr int kStageJOff = kBarOff + 8 * 2 * kDStages;
-  static constexpr int kStageSOff = kStageJOff + 4 * kDStages;  // BlockScale a stage
-  static constexpr int kFlagOff = kStageSOff + 12 * kDStages;
+  static constexpr int kFlagOff = kStageJOff + 4 * kDStages;
   static constexpr int kBytes = kFlagOff + 4;
 };
 
-template <int NT, bool kBlk = false>  // n-tiles of 8 heads: group size G <= 8*NT
+template <int NT>  // n-tiles of 8 heads: group size G <= 8*NT
 __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
     decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const __nv_bfloat16* __restrict__ q, const TileInfo* __restrict__ tiles,
@@ -102,7 +95,6 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* empty = full + kDStages;
   volatile int32_t* stage_j = reinterpret_cast<int32_t*>(smem + L::kStageJOff);
-  volatile float* stage_s = reinterpret_cast<float*>(smem + L::kStageSOff);
   volatile int32_t* merge_flag = reinterpret_cast<int32_t*>(smem + L::kFlagOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,7 +124,6 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
     for (int base = ub; ok && base < ue; base += 32) {
       const int u = base + lane;
       int j = -1, row_off = 0;
-      BlockScale bs{};
       if (u < ue) {
         const int row = u / topk;
         const int t = row / hsel, g = row % hsel;
@@ -149,32 +140,22 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
             page = 0;
           }
           row_off = static_cast<int>((page * hkv + g / kv_div) * 128);
-          if (kBlk) bs = block_scale_of(k_scale[row_off >> 7], v_scale[row_off >> 7]);
         }
       }
       const int n = min(32, ue - base);
       for (int k = 0; k < n; ++k, ++i) {
         const int jk = __shfl_sync(0xFFFFFFFFu, j, k);
         const int rk = __shfl_sync(0xFFFFFFFFu, row_off, k);
-        BlockScale sk{};
-        if (kBlk)
-          sk = {__shfl_sync(0xFFFFFFFFu, bs.ks, k), __shfl_sync(0xFFFFFFFFu, bs.log2_vs, k),
-                __shfl_sync(0xFFFFFFFFu, bs.inv_vs, k)};
         if (lane == 0) {
           const int s = i % kDStages;
           if (!(ok = mbar_wait(empty + s, ((i / kDStages) & 1) ^ 1, err))) {
             // leave the loop below too
           } else {
             stage_j[s] = jk;
-            if (kBlk) {
-              stage_s[3 * s] = sk.ks;
-              stage_s[3 * s + 1] = sk.log2_vs;
-              stage_s[3 * s + 2] = sk.inv_vs;
-            }
             if (jk >= 0) {
-              mbar_expect_tx(full + s, 2 * kBlkBytes);
-              tma_load_2d(ring + s * 2 * kBlkBytes, &k_map, full + s, 0, rk);
-              tma_load_2d(ring + s * 2 * kBlkBytes + kBlkBytes, &v_map, full + s, 0, rk);
+              mbar_expect_tx(full + s, 2 * kBlk);
+              tma_load_2d(ring + s * 2 * kBlk, &k_map, full + s, 0, rk);
+              tma_load_2d(ring + s * 2 * kBlk + kBlk, &v_map, full + s, 0, rk);
             } else {
               mbar_arrive(full + s);
             }
@@ -250,7 +231,7 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
         if (whole) {  // this CTA holds the whole row: write the result directly
           const int t = row / hsel, g = row % hsel;
           const int64_t orow = static_cast<int64_t>(tiles[t].q_begin) * hq + g * G + h;
-          out[orow * kD + kHalf * rnd + d] = __float2bfloat16_rn(Lsum > 0.f ? o / Lsum * (kBlk ? 1.f : v_scale[g / kv_div]) : 0.f);
+          out[orow * kD + kHalf * rnd + d] = __float2bfloat16_rn(Lsum > 0.f ? o / Lsum * v_scale[g / kv_div] : 0.f);
           if (d == 0 && rnd == 0 && lse != nullptr)
             lse[orow] = Lsum > 0.f ? (mm + log2f(Lsum)) * 0.69314718055994531f : -INFINITY;
         } else {
@@ -288,7 +269,7 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
       // (m, l and O of each head) are independent and issue together.
       __threadfence();
       const int t = row / hsel, g = row % hsel;
-      const float vs = kBlk ? 1.f : v_scale[g / kv_div];
+      const float vs = v_scale[g / kv_div];
       const int64_t q_row = tiles[t].q_begin;
       for (int d = threadIdx.x; d < kD; d += 32 * kCWarps)
 #pragma unroll 1
@@ -345,7 +326,7 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
       }
       const TileInfo tl = tiles[t];
       qpos = tl.pos0;
-      if (!kBlk) sl2 = scale_log2 * k_scale[g / kv_div];
+      sl2 = scale_log2 * k_scale[g / kv_div];
       // q^T fragments: head n = gi + 8nt of the group, d = 16kc + 4t4 + {0,1} | {2,3}
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -374,20 +355,8 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
       if (lane == 0) mbar_arrive(empty + s);
       continue;
     }
-    const uint32_t kb = smem_u32(ring + s * 2 * kBlkBytes);
-    const uint32_t vb = kb + kBlkBytes;
-    float log2_vs = 0.f, inv_vs = 1.f;
-    if (kBlk) {
-      sl2 = scale_log2 * stage_s[3 * s];
-      log2_vs = stage_s[3 * s + 1];
-      inv_vs = stage_s[3 * s + 2];
-      const int key0 = j * 128 + kKeysW * w;  // this warp's first key
-      if (key0 + kKeysW - 1 > qpos) {
-        for (int r = max(qpos + 1 - key0, 0); r < kKeysW; ++r) sts32(vb + (kKeysW * w + r) * 128 + 4 * lane, 0u);
-        fence_async_shared();  // before the next load overwrites the stage
-        __syncwarp();
-      }
-    }
+    const uint32_t kb = smem_u32(ring + s * 2 * kBlk);
+    const uint32_t vb = kb + kBlk;
 
     // S^T for this warp's 32 keys
     float sacc[kMT][NT][4];
@@ -410,16 +379,15 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
     }
     // mask keys past the query position, scale into the log2 domain
     const int kpos0 = j * 128 + kKeysW * w + gi;
-    auto scaled = [&](float x) { return kBlk ? fmaf(x, sl2, log2_vs) : x * sl2; };
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
       const bool va = kpos0 + 16 * mt <= qpos, vb2 = kpos0 + 16 * mt + 8 <= qpos;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        sacc[mt][nt][0] = va ? scaled(sacc[mt][nt][0]) : -INFINITY;
-        sacc[mt][nt][1] = va ? scaled(sacc[mt][nt][1]) : -INFINITY;
-        sacc[mt][nt][2] = vb2 ? scaled(sacc[mt][nt][2]) : -INFINITY;
-        sacc[mt][nt][3] = vb2 ? scaled(sacc[mt][nt][3]) : -INFINITY;
+        sacc[mt][nt][0] = va ? sacc[mt][nt][0] * sl2 : -INFINITY;
+        sacc[mt][nt][1] = va ? sacc[mt][nt][1] * sl2 : -INFINITY;
+        sacc[mt][nt][2] = vb2 ? sacc[mt][nt][2] * sl2 : -INFINITY;
+        sacc[mt][nt][3] = vb2 ? sacc[mt][nt][3] * sl2 : -INFINITY;
       }
     }
     // online softmax per head column
@@ -446,7 +414,7 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
           sacc[mt][nt][2 + c] = ex2_approx(sacc[mt][nt][2 + c] - m_use);
           sum += sacc[mt][nt][c] + sacc[mt][nt][2 + c];
         }
-        l[nt][c] = l[nt][c] * alpha[c] + (kBlk ? sum * inv_vs : sum);
+        l[nt][c] = l[nt][c] * alpha[c] + sum;
       }
 #pragma unroll
       for (int md = 0; md < 8; ++md) {
@@ -534,14 +502,20 @@ msa_status launch_attn_decode(const msa_plan_s* p, const void* q, const void* k_
   auto* o_ptr = static_cast<__nv_bfloat16*>(out);
   const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(kD));
   const auto* qq = static_cast<const __nv_bfloat16*>(q);
-  const bool blk = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK;
-  const auto kern = G <= 8 ? (blk ? decode_kernel<1, true> : decode_kernel<1>)
-                           : (blk ? decode_kernel<2, true> : decode_kernel<2>);
-  const int smem = (G <= 8 ? DecodeSmem<1>::kBytes : DecodeSmem<2>::kBytes) + 1024;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kDThreads), smem, st, km, vm, qq, p->tiles_d, idx, kv_indices,
-                                   p->num_pages, k_scale, v_scale, part_o, part_ml, row_cnt, o_ptr, lse, n_units,
-                                   p->hq, p->hp, kv_div, p->topk, scale_log2, p->err_d);
+  cudaError_t e;
+  if (G <= 8) {
+    const int smem = DecodeSmem<1>::kBytes + 1024;
+    cudaFuncSetAttribute(decode_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = launch_pdl(decode_kernel<1>, dim3(grid), dim3(kDThreads), smem, st, km, vm, qq, p->tiles_d, idx, kv_indices,
+                   p->num_pages, k_scale, v_scale, part_o, part_ml, row_cnt, o_ptr, lse, n_units, p->hq, p->hp, kv_div,
+                   p->topk, scale_log2, p->err_d);
+  } else {
+    const int smem = DecodeSmem<2>::kBytes + 1024;
+    cudaFuncSetAttribute(decode_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = launch_pdl(decode_kernel<2>, dim3(grid), dim3(kDThreads), smem, st, km, vm, qq, p->tiles_d, idx, kv_indices,
+                   p->num_pages, k_scale, v_scale, part_o, part_ml, row_cnt, o_ptr, lse, n_units, p->hq, p->hp, kv_div,
+                   p->topk, scale_log2, p->err_d);
+  }
   return cuda_check(e, "msa_sparse_attn: decode launch");
 }
 

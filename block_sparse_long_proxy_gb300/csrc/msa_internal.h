@@ -111,20 +111,29 @@ namespace msa {
 // scheduled while the previous kernel in the stream drains, which hides the
 // launch gap between the short kernels of a decode step; the kernel must
 // call pdl_wait() (ptx.cuh) before it touches global memory.
+// cluster: CTAs per cluster (the grid's x a multiple of it).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       Args&&... args) {
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, int cluster, dim3 block, size_t smem,
+                               cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                       Args&&... args) {
+  return launch_pdl_cluster(kernel, grid, 1, block, smem, st, static_cast<Args&&>(args)...);
 }
 
 msa_status set_error(msa_status s, const char* fmt, ...);
@@ -198,7 +207,7 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
                                const void* v_pages, const int32_t* kv_indices, const int32_t* idx,
                                const float* k_scale, const float* v_scale, void* out, float* lse,
                                cudaStream_t st);
-// one CTA per (sequence, group) row with warp-private half-block streams
+// one CTA or cluster per (sequence, group) row with warp-private streams
 // (decode_ws.cu); used by launch_attn_decode when decode_ws_applies(p)
 bool decode_ws_applies(const msa_plan_s* p);
 msa_status launch_attn_decode_ws(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,

@@ -81,33 +81,45 @@ def _check(status, where):
         raise MsaError(status, where)
 
 
+_current_device = torch._C._cuda_getDevice
+
+# The checks and conversions below run several times a call, and a decode step's
+# kernels are as short as they are: what passes is decided in one expression.
+
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(_current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, dtype, shape, name):
+    if t.dtype is dtype and t.shape == shape and t.get_device() == _current_device() and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError("%s: dtype %s, want %s" % (name, t.dtype, dtype))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s: shape %s, want %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s: must be a contiguous CUDA tensor" % name)
+    if not t.is_cuda or not t.is_contiguous() or t.get_device() != _current_device():
+        raise ValueError("%s: must be a contiguous CUDA tensor on the current device" % name)
 
 
 def _need_rows(t, dtype, shape, name):
     """_need for rows at a stride: the heads of a row dense, the rows anywhere
     apart (a slice of a fused projection)."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == _current_device()
+            and t.stride()[1:] == (shape[2], 1)):
+        return
     if t.dtype != dtype:
         raise TypeError("%s: dtype %s, want %s" % (name, t.dtype, dtype))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s: shape %s, want %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_cuda or (t.numel() and t.stride()[1:] != (shape[2], 1) and not t[0].is_contiguous()):
-        raise ValueError("%s: must be a CUDA tensor with dense rows" % name)
+    if (not t.is_cuda or t.get_device() != _current_device()
+            or (t.numel() and t.stride()[1:] != (shape[2], 1) and not t[0].is_contiguous())):
+        raise ValueError("%s: must be a CUDA tensor with dense rows on the current device" % name)
 
 
 def _row_stride(t):
