@@ -25,6 +25,7 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kKvThreads = 512;
 constexpr int kMinExp = -40, kMaxExp = 40;
 
 struct AppendUnit {
@@ -62,115 +63,188 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t v, float f) {
   return e4m3x4(x.x * f, x.y * f, y.x * f, y.y * f);
 }
 
-// K (blockIdx.z 0, rotated) or V (1) of one page and one KV head.
-template <int D, msa_kv_dtype KIND>
-__global__ void __launch_bounds__(kThreads)
-    kv_append_kernel(const __grid_constant__ RopeTable tab, const AppendUnit* __restrict__ units,
-                     const __nv_bfloat16* __restrict__ k, int64_t k_stride, const __nv_bfloat16* __restrict__ v,
-                     int64_t v_stride, const int32_t* __restrict__ positions, const int32_t* __restrict__ kv_indices,
-                     int64_t num_pages, void* __restrict__ k_pages, void* __restrict__ v_pages, float* k_scale,
-                     float* v_scale, int32_t hkv, uint32_t* err) {
-  pdl_wait();
-  constexpr int kChunks = D / 16, kRows = kThreads / kChunks, kPasses = 128 / kRows;
-  const AppendUnit u = units[blockIdx.x];
-  const int h = blockIdx.y;
-  const bool is_v = blockIdx.z == 1;
-  const int64_t page = kv_indices[u.entry];
-  if (page < 0 || page >= num_pages) {
-    if (threadIdx.x == 0) atomicOr(err, kErrDeviceCheck);
-    return;
-  }
+// K (blockIdx.z 0, rotated) or V (1) of one page, KV heads
+// blockIdx.y * heads_per_cta on.
+//
+// Bound by HBM for long appends.  A thread holds 16 values of one row, or of
+// two, from the load through the rotation and the page's amax to the codes: the
+// rows are read once.  The cos and sin of the page's rows go into shared
+// memory and serve all heads of the CTA (with eight angles computed for every
+// 16 values the call took 67 us, half of it issuing instructions), and the
+// next head's rows are on their way while this one's amax is reduced.  32768 rows, 8 heads, d
+// 128 (201 MB): 40.2 us, 5.0 TB/s.
+enum RopeKind { kPlain, kHalf, kInterleaved };
+
+struct KvAppendArgs {
+  const AppendUnit* units;
+  const __nv_bfloat16* x[2];  // K, V
+  int64_t stride[2];
+  void* pages[2];
+  float* scale[2];
+  const int32_t* positions;
+  const int32_t* kv_indices;
+  int64_t num_pages;
+  int32_t hkv, heads_per_cta;
+  uint32_t* err;
+};
+
+template <int D, msa_kv_dtype KIND, RopeKind ROPE>
+__device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendArgs& a, int which) {
+  constexpr int kChunks = D / 16, kRows = kKvThreads / kChunks, kPasses = 128 / kRows;
+  extern __shared__ float4 angles[];  // [row][4][kChunks]: (cos, sin) of pairs 2 j and 2 j + 1 of a chunk
+  __shared__ uint32_t warp_max[2][kKvThreads / 32];
+  const AppendUnit u = a.units[blockIdx.x];
+  const int64_t page = a.kv_indices[u.entry];
   const int slot0 = u.slot0_n & 0xFF, n = u.slot0_n >> 8;
   const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
-  RopeChunk ch = rope_chunk(tab, c);
-  if (is_v || !ch.rotated) ch = {16 * c, 16 * c + 8, false};
-  const __nv_bfloat16* src = (is_v ? v + u.row * v_stride : k + u.row * k_stride) + h * D;
-  const int64_t stride = is_v ? v_stride : k_stride;
-  const int64_t head_row = (page * hkv + h) * 128;  // first row of the (page, head) in the pool
-
-  float x[kPasses][16];
-  float amax = 0.f;
+  RopeChunk ch{16 * c, 16 * c + 8, false};
+  if (ROPE != kPlain) ch = rope_chunk(tab, c);
+  const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.hkv, h0 + a.heads_per_cta);
+  const __nv_bfloat16* src[kPasses];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int i = p * kRows + r0;
-    if (i < n) {
-      load8(src + i * stride + ch.lo, x[p]);
-      load8(src + i * stride + ch.hi, x[p] + 8);
-      if (ch.rotated) {
-        float cs[8], sn[8];
-        rope_angles(tab, c, positions ? positions[u.row + i] : u.pos + i, false, cs, sn);
-        rope_rotate(tab.interleaved != 0, cs, sn, x[p]);
-      }
-      if (KIND == MSA_KV_FP8_E4M3_BLOCK) {
+  for (int p = 0; p < kPasses; ++p) src[p] = a.x[which] + (u.row + p * kRows + r0) * a.stride[which];
+  uint4 raw[kPasses][2];
+  auto load = [&](int h) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float a = fabsf(x[p][e]);
-          if (a <= 3.4028234e38f) amax = fmaxf(amax, a);  // infinities saturate, they set no scale
-        }
+    for (int p = 0; p < kPasses; ++p)
+      if (p * kRows + r0 < n) {
+        const __nv_bfloat16* at = src[p] + h * D;
+        raw[p][0] = *reinterpret_cast<const uint4*>(at + ch.lo);
+        raw[p][1] = *reinterpret_cast<const uint4*>(at + ch.hi);
       }
-    }
+  };
+  load(h0);
+  if (page < 0 || page >= a.num_pages) {
+    if (threadIdx.x == 0) atomicOr(a.err, kErrDeviceCheck);
+    return;
   }
-  if (KIND == MSA_KV_BF16) {
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? v_pages : k_pages) + (head_row + slot0) * D;
+  if (ROPE != kPlain && ch.rotated) {
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
       const int i = p * kRows + r0;
       if (i < n) {
-        store8(dst + i * D + ch.lo, x[p]);
-        store8(dst + i * D + ch.hi, x[p] + 8);
+        float cs[8], sn[8];
+        rope_angles(tab, c, a.positions ? a.positions[u.row + i] : u.pos + i, false, cs, sn);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          angles[(i * 4 + j) * kChunks + c] = make_float4(cs[2 * j], sn[2 * j], cs[2 * j + 1], sn[2 * j + 1]);
       }
     }
-    return;
-  }
-  uint8_t* pool = static_cast<uint8_t*>(is_v ? v_pages : k_pages) + head_row * D;
-  float* scales = is_v ? v_scale : k_scale;
-  float by = 1.f;  // the codes are x * by (block) or x / by (one scale a head)
-  if (KIND == MSA_KV_FP8_E4M3_BLOCK) {
-    __shared__ float warp_max[kThreads / 32];
+  }  // every thread reads back what it wrote
+  for (int h = h0; h < h1; ++h) {
+    float x[kPasses][16];
+    float amax = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
-    __syncthreads();
+    for (int p = 0; p < kPasses; ++p) {
+      const int i = p * kRows + r0;
+      if (i < n) {
+        unpack8(raw[p][0], x[p]);
+        unpack8(raw[p][1], x[p] + 8);
+        if (ROPE != kPlain && ch.rotated) {
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, warp_max[w]);
-    int e = block_exp(amax);
-    float* sp = scales + page * hkv + h;
-    if (slot0 > 0) {  // rows came before: the scale only grows
-      const float old = *sp;
-      if (!(old > 0.f && old <= pow2(kMaxExp))) {  // never written: the old slots keep their bytes
-        if (threadIdx.x == 0) atomicOr(err, kErrDeviceCheck);
-      } else {
-        // another writer's scale need not be a power of two: round it up to one
-        const uint32_t ou = __float_as_uint(old);
-        e = max(e, static_cast<int>(ou >> 23) - 127 + ((ou & 0x7FFFFFu) != 0u ? 1 : 0));
-        const float f = old * pow2(-e);
-        if (f != 1.f) {
-          uint4* q = reinterpret_cast<uint4*>(pool);
-          for (int i = threadIdx.x; i < slot0 * (D / 16); i += kThreads) {
-            uint4 w = q[i];
-            w.x = rescale4(w.x, f), w.y = rescale4(w.y, f), w.z = rescale4(w.z, f), w.w = rescale4(w.w, f);
-            q[i] = w;
+          for (int j = 0; j < 4; ++j)
+            rope_rotate2(ROPE == kInterleaved, j, angles[(i * 4 + j) * kChunks + c], x[p]);
+        }
+        if (KIND == MSA_KV_FP8_E4M3_BLOCK) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) amax = fmax3(amax, fabsf(x[p][e]), fabsf(x[p][e + 1]));  // NaN is passed over
+        }
+      }
+    }
+    if (h + 1 < h1) load(h + 1);
+    const int64_t head_row = (page * a.hkv + h) * 128;  // first row of the (page, head) in the pool
+    if (KIND == MSA_KV_BF16) {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.pages[which]) + (head_row + slot0) * D;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int i = p * kRows + r0;
+        if (i < n) {
+          store8(dst + i * D + ch.lo, x[p]);
+          store8(dst + i * D + ch.hi, x[p] + 8);
+        }
+      }
+      continue;
+    }
+    uint8_t* pool = static_cast<uint8_t*>(a.pages[which]) + head_row * D;
+    float by;  // the codes are x * by (block) or x / by (one scale a head)
+    if (KIND == MSA_KV_FP8_E4M3_BLOCK) {
+      float* sp = a.scale[which] + page * a.hkv + h;
+      const float old = slot0 > 0 ? *sp : 0.f;  // rows came before: the scale only grows
+      // one barrier a head: the buffers alternate
+      auto cta_max = [&](float m, int buf) {  // of values >= 0, whose bits order as they do
+        const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
+        if ((threadIdx.x & 31) == 0) warp_max[buf][threadIdx.x >> 5] = w;
+        __syncthreads();
+        return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, warp_max[buf][threadIdx.x % (kKvThreads / 32)]));
+      };
+      amax = cta_max(amax, h & 1);
+      if (amax == INFINITY) {  // infinities saturate, they set no scale
+        float fin = 0.f;
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p)
+          if (p * kRows + r0 < n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (fabsf(x[p][e]) < INFINITY) fin = fmaxf(fin, fabsf(x[p][e]));
+        __syncthreads();
+        amax = cta_max(fin, h & 1);
+      }
+      int e = block_exp(amax);
+      if (slot0 > 0) {
+        if (!(old > 0.f && old <= pow2(kMaxExp))) {  // never written: the old slots keep their bytes
+          if (threadIdx.x == 0) atomicOr(a.err, kErrDeviceCheck);
+        } else {
+          // another writer's scale need not be a power of two: round it up to one
+          const uint32_t ou = __float_as_uint(old);
+          e = max(e, static_cast<int>(ou >> 23) - 127 + ((ou & 0x7FFFFFu) != 0u ? 1 : 0));
+          const float f = old * pow2(-e);
+          if (f != 1.f) {
+            uint4* q = reinterpret_cast<uint4*>(pool);
+            for (int i = threadIdx.x; i < slot0 * (D / 16); i += kKvThreads) {
+              uint4 w = q[i];
+              w.x = rescale4(w.x, f), w.y = rescale4(w.y, f), w.z = rescale4(w.z, f), w.w = rescale4(w.w, f);
+              q[i] = w;
+            }
           }
         }
       }
-      __syncthreads();  // every thread has read the old scale
+      if (threadIdx.x == 0) *sp = pow2(e);  // every thread read the old one before the barrier
+      by = pow2(-e);
+    } else {
+      by = a.scale[which][h];
     }
-    if (threadIdx.x == 0) *sp = pow2(e);
-    by = pow2(-e);
-  } else {
-    by = scales[h];
-  }
-  uint8_t* dst = pool + slot0 * D;
+    uint8_t* dst = pool + slot0 * D;
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int i = p * kRows + r0;
-    if (i < n) {
+    for (int p = 0; p < kPasses; ++p) {
+      const int i = p * kRows + r0;
+      if (i < n) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[p][e] = KIND == MSA_KV_FP8_E4M3_BLOCK ? x[p][e] * by : __fdiv_rn(x[p][e], by);
-      *reinterpret_cast<uint2*>(dst + i * D + ch.lo) = e4m3x8(x[p]);
-      *reinterpret_cast<uint2*>(dst + i * D + ch.hi) = e4m3x8(x[p] + 8);
+        for (int e = 0; e < 16; e += 2) {
+          if (KIND == MSA_KV_FP8_E4M3_BLOCK) {
+            fmul2v(x[p][e], x[p][e + 1], x[p][e], x[p][e + 1], by, by);
+          } else {
+            x[p][e] = __fdiv_rn(x[p][e], by);
+            x[p][e + 1] = __fdiv_rn(x[p][e + 1], by);
+          }
+        }
+        *reinterpret_cast<uint2*>(dst + i * D + ch.lo) = e4m3x8(x[p]);
+        *reinterpret_cast<uint2*>(dst + i * D + ch.hi) = e4m3x8(x[p] + 8);
+      }
     }
   }
+}
+
+template <int D, msa_kv_dtype KIND>
+__global__ void __launch_bounds__(kKvThreads, 2)
+    kv_append_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ KvAppendArgs a) {
+  pdl_wait();
+  // one body for each way of rotating: what differs is which values pair up
+  if (blockIdx.z == 1 || tab.rot == 0)
+    kv_append<D, KIND, kPlain>(tab, a, blockIdx.z);
+  else if (tab.interleaved)
+    kv_append<D, KIND, kInterleaved>(tab, a, 0);
+  else
+    kv_append<D, KIND, kHalf>(tab, a, 0);
 }
 
 // Proxy K rows of one page, to any of three pools.
@@ -372,9 +446,17 @@ msa_status check_rows(const char* fn, const char* name, const void* x, int64_t s
   return MSA_OK;
 }
 
-template <int D, msa_kv_dtype KIND, typename... A>
-cudaError_t launch_kv(const msa_plan_s* p, cudaStream_t st, A... a) {
-  return launch_pdl(kv_append_kernel<D, KIND>, dim3(p->n_append_units, p->hkv, 2), dim3(kThreads), 0, st, a...);
+template <int D, msa_kv_dtype KIND>
+cudaError_t launch_kv(const msa_plan_s* p, const RopeTable& tab, KvAppendArgs a, cudaStream_t st) {
+  // heads a CTA: the angles are shared while three CTAs are left for an SM
+  // (32768 rows, 8 heads, d 128: 4 heads a CTA 42.7 us, 8 40.2)
+  int hpc = 1;
+  while (hpc < 8 && int64_t(p->n_append_units) * ((p->hkv + 2 * hpc - 1) / (2 * hpc)) * 2 >= 3 * p->num_sms) hpc *= 2;
+  a.heads_per_cta = hpc;
+  auto kern = kv_append_kernel<D, KIND>;
+  const int smem = (p->decode ? 1 : 128) * D * 4;  // (cos, sin) of D / 2 pairs of a page's rows
+  if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  return launch_pdl(kern, dim3(p->n_append_units, (p->hkv + hpc - 1) / hpc, 2), dim3(kKvThreads), smem, st, tab, a);
 }
 
 }  // namespace
@@ -423,24 +505,24 @@ msa_status msa_kv_append(msa_plan_t plan, msa_rope_t rope, const int32_t* positi
   if (k_pages == v_pages || (fp8 && k_scale == v_scale && plan->kv_dtype == MSA_KV_FP8_E4M3_BLOCK))
     return set_error(MSA_ERR_INVALID_ARG, "%s: K and V need pools and scales of their own", fn);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  auto run = [&](auto launch) {
-    return launch(plan, st, table_of(rope), reinterpret_cast<const AppendUnit*>(plan->aux_d + plan->append_units_off),
-                  static_cast<const __nv_bfloat16*>(k), k_row_stride, static_cast<const __nv_bfloat16*>(v),
-                  v_row_stride, positions, kv_indices, plan->num_pages, k_pages, v_pages, k_scale, v_scale, plan->hkv,
-                  plan->err_d);
-  };
+  const KvAppendArgs a{reinterpret_cast<const AppendUnit*>(plan->aux_d + plan->append_units_off),
+                       {static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v)},
+                       {k_row_stride, v_row_stride},
+                       {k_pages, v_pages},
+                       {k_scale, v_scale},
+                       positions,
+                       kv_indices,
+                       plan->num_pages,
+                       plan->hkv,
+                       1,
+                       plan->err_d};
   const bool d128 = plan->d == 128;
-  cudaError_t e;
-  if (plan->kv_dtype == MSA_KV_BF16)
-    e = run([&](auto... a) { return d128 ? launch_kv<128, MSA_KV_BF16>(a...) : launch_kv<64, MSA_KV_BF16>(a...); });
-  else if (plan->kv_dtype == MSA_KV_FP8_E4M3)
-    e = run([&](auto... a) {
-      return d128 ? launch_kv<128, MSA_KV_FP8_E4M3>(a...) : launch_kv<64, MSA_KV_FP8_E4M3>(a...);
-    });
-  else
-    e = run([&](auto... a) {
-      return d128 ? launch_kv<128, MSA_KV_FP8_E4M3_BLOCK>(a...) : launch_kv<64, MSA_KV_FP8_E4M3_BLOCK>(a...);
-    });
+  const auto launch =
+      plan->kv_dtype == MSA_KV_BF16       ? (d128 ? launch_kv<128, MSA_KV_BF16> : launch_kv<64, MSA_KV_BF16>)
+      : plan->kv_dtype == MSA_KV_FP8_E4M3 ? (d128 ? launch_kv<128, MSA_KV_FP8_E4M3> : launch_kv<64, MSA_KV_FP8_E4M3>)
+                                          : (d128 ? launch_kv<128, MSA_KV_FP8_E4M3_BLOCK>
+                                                  : launch_kv<64, MSA_KV_FP8_E4M3_BLOCK>);
+  const cudaError_t e = launch(plan, table_of(rope), a, st);
   s = cuda_check(e, "msa_kv_append: launch");
   if (s == MSA_OK) s = scan_strided(plan, k, plan->total_q, width, k_row_stride, st);
   if (s == MSA_OK) s = scan_strided(plan, v, plan->total_q, width, v_row_stride, st);

