@@ -43,10 +43,12 @@
 // of bf16.
 //
 // kBlk: one scale for each (page, KV head) instead (BlockScale in
-// msa_internal.h).  The softmax warps read a block's two scales a block ahead,
-// from the row the block's list entry already names, and take them into the
-// multiply-add that scales the logits; the converters write zeros for V rows
-// behind the sequence's last key, whose bytes were never written.
+// msa_internal.h).  The producer's lanes fetch them beside the page ids, at
+// least 32 blocks ahead, into a ring that the softmax warps read, one pair a
+// block, into the multiply-add that scales the logits (fetched and converted
+// by the softmax warps themselves they cost 130 us of 965 at S=32768).  The
+// converters write zeros for V rows behind the sequence's last key, whose
+// bytes were never written.
 #include "msa_internal.h"
 #include "ptx.cuh"
 
@@ -90,6 +92,7 @@ struct UnitHdr {
   int32_t n, nh, h0, q_begin, rows, pos0, g, kv_len, pad[8];
 };
 constexpr int kListSlots = 2;
+constexpr int kScaleRing = 128;  // blocks; written up to 64 ahead of the one being loaded
 constexpr int kHdrInts = 16;
 
 // A head's row statistics at the end of a unit, from the softmax warps to
@@ -103,7 +106,7 @@ struct UnitStats {
 // (kStageO: one 64-column box of a head's bf16 O tile, for the TMA stores of
 // full tiles), barriers, the units' row statistics, then the two list slots,
 // whose size follows topk.
-template <int D, bool kStageO, int kLists = 1>
+template <int D, bool kStageO, int kLists = 1, bool kBlk = false>
 struct AttnSmem {
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows x D bf16, in D/64 swizzled chunks of 16 KB
   static constexpr int kQOff = 0;
@@ -113,7 +116,8 @@ struct AttnSmem {
   static constexpr int kOChunkBytes = 128 * 64 * 2;  // 64 columns of 128 rows
   static constexpr int kBarOff = kOOff + (kStageO ? kOChunkBytes : 0);
   static constexpr int kStatOff = kBarOff + 8 * 64;
-  static constexpr int kListOff = kStatOff + 4 * static_cast<int>(sizeof(UnitStats));
+  static constexpr int kScaleOff = kStatOff + 4 * static_cast<int>(sizeof(UnitStats));
+  static constexpr int kListOff = kScaleOff + (kBlk ? 8 * kScaleRing : 0);
   static __host__ __device__ constexpr int slot_ints(int cap) { return kHdrInts + 2 * kLists * cap; }
   static __host__ __device__ constexpr int bytes(int cap) { return kListOff + kListSlots * slot_ints(cap) * 4; }
 };
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int hkv = hsel / kv_div;
   // a one-head K/V pool (the backward's proxy softmax) pairs two proxy heads
   // per unit, each over its own blocks: one (j, row) list per head
-  using L = AttnSmem<D, kStageO, kOneKvHead ? 2 : 1>;
+  using L = AttnSmem<D, kStageO, kOneKvHead ? 2 : 1, kBlk>;
   constexpr int kChunks = D / 64;
   static_assert(!kFp8 || (D == 128 && !kOneKvHead), "FP8 K/V: head_dim 128, main attention");
   static_assert(!kBlk || kFp8, "block scales come with FP8 K/V");
@@ -187,6 +191,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* raw_v_full = v_full + kStages; // [kStages]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_v_full + kStages);
   UnitStats* const stats = reinterpret_cast<UnitStats*>(smem + L::kStatOff);
+  // kBlk: (k_scale * scale_log2, log2 v_scale) of the running block count's block
+  float2* const scale_ring = reinterpret_cast<float2*>(smem + L::kScaleOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -238,6 +244,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     setmaxnreg_dec<kWg2Regs>();
     int kv_it = 0;
     bool ok = true;
+    auto put_scale = [&](int it, int row) {
+      const BlockScale b = block_scale_of(k_scale[row >> 7], v_scale[row >> 7]);
+      scale_ring[it % kScaleRing] = make_float2(b.ks * scale_log2, b.log2_vs);
+    };
     for (int k = 0, ui = blockIdx.x; ok && ui < n_units; ++k, ui += gridDim.x) {
       UnitHdr& ls = lhdr(k);
       int32_t* const ls_j = lj(k);
@@ -272,6 +282,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int o = n + __popc(m & ((1u << lane) - 1u));
           ls_j[o] = j;
           ls_row[o] = row;
+          if (kBlk && o < 64) put_scale(kv_it + o, row);
         }
         n += __popc(m);
       }
@@ -335,7 +346,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int c = 0; c < kChunks; ++c)
               tma_load_3d(q_s + h * L::kTileBytes + c * 16384, &q_map, q_full, c * 64, u.h0 + h, tl.q_begin);
         }
-        for (int i = 0; ok && i < n; ++i, ++kv_it) {
+      }
+      constexpr int kStep = kBlk ? 32 : 1 << 30;  // kBlk: the lanes come together every 32 blocks to fetch scales
+      for (int i0 = 0; i0 < n; i0 += kStep) {
+        if (kBlk && i0 > 0) {
+          if (i0 + 32 + lane < n) put_scale(kv_it + 32 + lane, ls_row[i0 + 32 + lane]);
+          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+          __syncwarp();
+        }
+        const int i1 = kBlk ? min(n, i0 + kStep) : n;
+        for (int i = i0; lane == 0 && ok && i < i1; ++i, ++kv_it) {
           const int s = kv_it % kStages;
           const int row = ls_row[i];
           if (kFp8) {  // e4m3 codes into the upper half of the stage; the converters expand them
@@ -360,6 +380,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int c = 0; c < kChunks; ++c)
               tma_load_2d(v_s + s * L::kTileBytes + c * 16384, &v_map, kv_full + s, c * 64, row1);
         }
+        if (kBlk && lane != 0) kv_it += i1 - i0;
+        if (!kBlk) break;
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
     }
@@ -480,6 +502,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t s_addr = tmem + lane_base + h * 128;
     const uint32_t o_addr = tmem + lane_base + 256 + h * D;
     int ch = 0;  // blocks of head h so far
+    int kv_it = 0;  // blocks of either so far
     bool ok = true;
     for (int k = 0, ui = blockIdx.x; ui < n_units; ++k, ui += gridDim.x) {
       const UnitHdr& ls = lhdr(k);
@@ -490,26 +513,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int rows = ls.rows, pos0 = ls.pos0;
       // FP8: the scores are q . k_code, scaled by k_scale of the unit's KV head
       float sl2 = kFp8 && !kBlk ? scale_log2 * k_scale[ls.g] : scale_log2;
-      float log2_vs = 0.f, inv_vs = 1.f, ks_next = 1.f, vs_next = 1.f;
-      if (kBlk && ok && n > 0) {
-        ks_next = k_scale[lrow(k)[0] >> 7];
-        vs_next = v_scale[lrow(k)[0] >> 7];
-      }
+      float log2_vs = 0.f, inv_vs = 1.f;
       const bool active = ok && h < nh;
       const bool row_ok = r < rows;
       const int qpos = pos0 + r;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; active && ok && i < n; ++i) {
-        if (kBlk) {
-          const BlockScale bs = block_scale_of(ks_next, vs_next);
-          sl2 = scale_log2 * bs.ks, log2_vs = bs.log2_vs, inv_vs = bs.inv_vs;
-          if (i + 1 < n) {
-            ks_next = k_scale[lrow(k)[i + 1] >> 7];
-            vs_next = v_scale[lrow(k)[i + 1] >> 7];
-          }
-        }
         if (!(ok = mbar_wait_inl(s_full + h, (ch + i) & 1, err))) break;
         tc_fence_after();
+        if (kBlk) {
+          const float2 sc = scale_ring[(kv_it + i) % kScaleRing];
+          sl2 = sc.x, log2_vs = sc.y, inv_vs = ex2_approx(-sc.y);
+        }
         uint32_t sv[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, sv + c * 32);
@@ -600,6 +615,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         st.g = ls.g;
       }
       if (h < nh) ch += n;
+      kv_it += n;
       // the list slot may be refilled (every warp arrives once per unit, active or not)
       tc_fence_before();
       __syncwarp();
@@ -861,7 +877,7 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
                                 const float* v_scale, uint32_t* err) {
   const int cap = (topk + 3) & ~3;
   if constexpr (kFp8) {
-    const int staged = AttnSmem<D, true, kOneKvHead ? 2 : 1>::bytes(cap) + 1024;
+    const int staged = AttnSmem<D, true, kOneKvHead ? 2 : 1, kBlk>::bytes(cap) + 1024;
     if (staged <= kMaxSmem) {
       auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, true, kBlk>;
       if (const cudaError_t e = check_launch_regs(kern)) return e;
@@ -871,7 +887,7 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
                         v_scale, err);
     }
   }
-  const int plain = AttnSmem<D, false, kOneKvHead ? 2 : 1>::bytes(kMaxTopk) + 1024;
+  const int plain = AttnSmem<D, false, kOneKvHead ? 2 : 1, kBlk>::bytes(kMaxTopk) + 1024;
   auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false, kBlk>;
   if (const cudaError_t e = check_launch_regs(kern)) return e;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plain);
