@@ -469,7 +469,7 @@ int decode_grid_rows(int rows, int topk, int num_sms, int G) {
 }  // namespace
 
 size_t decode_partial_floats(const msa_plan_s* p) {
-  if (!p->decode) return 0;
+  if (!p->decode || p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK) return 0;  // those rows merge inside a cluster
   // rows are (sequence, proxy head): one block set each
   const size_t units = static_cast<size_t>(p->n_tiles) * p->hp * p->topk;
   const size_t g = p->hq / p->hp;
