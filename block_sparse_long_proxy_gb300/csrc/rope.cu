@@ -8,10 +8,13 @@
 // gradient of the rotated heads to the gradient of the heads.
 //
 // Bound by HBM: every element is read and written once and costs three
-// multiply-adds.  A thread takes 16 values of a head (both members of eight
-// pairs) and works down the heads of its row, so that the eight angles of
-// a thread serve several heads.  fp32, 65536 rows x 32 heads of 128 (2.15 GB):
-// 317 us, 6.8 TB/s; bf16, 32768 x 32 (0.54 GB): 90 us, 5.9 TB/s.
+// multiply-adds.  A CTA takes the rows' memory in order (a row is its heads, one
+// after the other), with the cos and sin of its rows in shared memory, computed
+// once for all heads; a thread rotates 16 values at a time (both members of
+// eight pairs) and has the loads of kBatch such chunks in flight before the
+// first store, which the compiler cannot move them across.
+// bf16, 32768 rows x 32 heads of 128 (0.54 GB): 81 us, 6.6 TB/s (a copy of as much takes 82); fp32, 65536 x 32
+// (2.1 GB): 309 us, 6.9 TB/s.
 #include <math.h>
 
 #include <algorithm>
@@ -24,50 +27,87 @@ namespace msa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeSmem = 16384;  // bytes of angles a CTA at most
 
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeTable tab, const T* x, int64_t x_stride, const int32_t* __restrict__ pos,
-                int64_t n_rows, int32_t heads, int32_t d, bool inverse, int32_t heads_per_thread, T* out,
+                int64_t n_rows, int32_t heads, int32_t d, bool inverse, int32_t cta_rows, int32_t cta_heads, T* out,
                 int64_t out_stride) {
   pdl_wait();
-  const int chunks = d / 16, rows = kRopeThreads / chunks;
-  const int c = threadIdx.x % chunks, r = threadIdx.x / chunks;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + r;
-  if (r >= rows || row >= n_rows) return;
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+  extern __shared__ float4 angles[];  // [row][4][rot / 16]: (cos, sin) of pairs 2 j and 2 j + 1 of a chunk
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * cta_rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(cta_rows), n_rows - row0));
+  const int h0 = blockIdx.y * cta_heads, nh = min(cta_heads, heads - h0);
+  // thread: chunk c of the (row, head) items j, j + step, ...
+  const int chunks = d / 16, step = kRopeThreads / chunks, turning = tab.rot / 16;
+  const int c = threadIdx.x % chunks, j = threadIdx.x / chunks;
   const RopeChunk ch = rope_chunk(tab, c);
-  if (!ch.rotated && x == out) return;  // in place: nothing changes
-  float cs[8], sn[8];
-  if (ch.rotated) rope_angles(tab, c, pos[row], inverse, cs, sn);
-  const int h0 = blockIdx.y * heads_per_thread, h1 = min(heads, h0 + heads_per_thread);
-  const T* xr = x + row * x_stride;
-  T* orow = out + row * out_stride;
-#pragma unroll 2
-  for (int h = h0; h < h1; ++h) {
-    float v[16];
-    load8(xr + h * d + ch.lo, v);
-    load8(xr + h * d + ch.hi, v + 8);
-    if (ch.rotated) rope_rotate(INTERLEAVED, cs, sn, v);
-    store8(orow + h * d + ch.lo, v);
-    store8(orow + h * d + ch.hi, v + 8);
+  const int n = j < step && (ch.rotated || x != out) ? rows * nh : 0;  // in place: the unrotated stay
+  const T* xr = x + row0 * x_stride + h0 * d;
+  T* orow = out + row0 * out_stride + h0 * d;
+  const int step_r = step / nh, step_h = step % nh;
+  int r = j / nh, h = j % nh;  // of item i
+  bool first = true;
+  for (int i = j; i < n || first; i += kBatch * step) {
+    Raw16<T> raw[kBatch];
+    int rr[kBatch], hh[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      rr[b] = r, hh[b] = h;
+      if (i + b * step < n) raw[b].load(xr + r * x_stride + h * d + ch.lo, xr + r * x_stride + h * d + ch.hi);
+      r += step_r, h += step_h;
+      if (h >= nh) h -= nh, ++r;
+    }
+    if (first) {  // while the first loads are on their way
+      for (int a = threadIdx.x; a < rows * turning; a += kRopeThreads) {
+        const int ar = a / turning, ac = a % turning;
+        float cs[8], sn[8];
+        rope_angles(tab, ac, pos[row0 + ar], inverse, cs, sn);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          angles[(ar * 4 + k) * turning + ac] = make_float4(cs[2 * k], sn[2 * k], cs[2 * k + 1], sn[2 * k + 1]);
+      }
+      __syncthreads();
+      first = false;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (i + b * step >= n) break;
+      float v[16];
+      raw[b].unpack(v);
+      if (ch.rotated) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rope_rotate2(INTERLEAVED, k, angles[(rr[b] * 4 + k) * turning + c], v);
+      }
+      T* o = orow + rr[b] * out_stride + hh[b] * d;
+      store8(o + ch.lo, v);
+      store8(o + ch.hi, v + 8);
+    }
   }
 }
 
 template <typename T>
 msa_status launch_rope(const RopeTable& tab, const void* x, int64_t xs, const int32_t* pos, int64_t n_rows,
                        int32_t heads, int32_t d, bool inverse, void* out, int64_t os, int num_sms, cudaStream_t st) {
-  const int rows = kRopeThreads / (d / 16);
-  const int64_t gx = (n_rows + rows - 1) / rows;
+  // a CTA's items: kItems chunks a thread (512 bytes read), of whole rows where
+  // a row has no more; fewer where that leaves SMs without a CTA.  bf16, 32768
+  // rows x 32 heads: 4 items 88 us, 8 83, 16 81, 32 86; fp32, 65536 x 32: 4 304,
+  // 8 309, 16 316, 32 325.  4096 x 8: a CTA an SM 5.2 us, 4 an SM 6.8
+  const int64_t chunks = d / 16, total = n_rows * heads * chunks;
+  constexpr int kItems = 32 / sizeof(T);
+  const int64_t per = std::clamp<int64_t>(total / num_sms, kRopeThreads, kItems * kRopeThreads) / chunks;
+  const int cta_heads = static_cast<int>(std::min<int64_t>(heads, per));
+  const int cta_rows = static_cast<int>(
+      std::clamp<int64_t>(per / heads, 1, std::min<int64_t>(n_rows, kRopeSmem / (tab.rot * 4))));
+  const int64_t gx = (n_rows + cta_rows - 1) / cta_rows;
   if (gx > 0x7FFFFFFF) return set_error(MSA_ERR_INVALID_ARG, "msa_rope_apply: too many rows");
-  // heads per thread: the angles are shared by more heads the more rows there
-  // are to give every SM two CTAs (4096 rows x 8 heads of 128: 1 head a
-  // thread 6.6 us, 4 4.3; 32768 x 32: 1 157, 4 94, 8 90, 16 91)
-  const int64_t fill = static_cast<int64_t>(num_sms) * 2;
-  const int hpt = static_cast<int>(std::clamp<int64_t>(gx * heads / fill, 1, std::min(heads, 8)));
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((heads + hpt - 1) / hpt));
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((heads + cta_heads - 1) / cta_heads));
   const auto kern = tab.interleaved ? rope_kernel<T, true> : rope_kernel<T, false>;
-  return cuda_check(launch_pdl(kern, grid, dim3(kRopeThreads), 0, st, tab, static_cast<const T*>(x), xs,
-                               pos, n_rows, heads, d, inverse, hpt, static_cast<T*>(out), os),
+  return cuda_check(launch_pdl(kern, grid, dim3(kRopeThreads), size_t(cta_rows) * tab.rot * 4, st, tab,
+                               static_cast<const T*>(x), xs, pos, n_rows, heads, d, inverse, cta_rows, cta_heads,
+                               static_cast<T*>(out), os),
                     "msa_rope_apply: launch");
 }
 

@@ -148,6 +148,34 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// A chunk's two runs of 8 values as they come from memory.
+template <typename T>
+struct Raw16;
+template <>
+struct Raw16<__nv_bfloat16> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* lo, const __nv_bfloat16* hi) {
+    a = *reinterpret_cast<const uint4*>(lo);
+    b = *reinterpret_cast<const uint4*>(hi);
+  }
+  __device__ __forceinline__ void unpack(float (&x)[16]) const {
+    unpack8(a, x);
+    unpack8(b, x + 8);
+  }
+};
+template <>
+struct Raw16<float> {
+  float v[16];
+  __device__ __forceinline__ void load(const float* lo, const float* hi) {
+    load8(lo, v);
+    load8(hi, v + 8);
+  }
+  __device__ __forceinline__ void unpack(float (&x)[16]) const {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = v[e];
+  }
+};
+
 #endif  // __CUDACC__
 
 }  // namespace msa

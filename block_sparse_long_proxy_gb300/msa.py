@@ -225,7 +225,8 @@ class Rope:
         _need(positions, torch.int32, (n,), "positions")
         if out is None:
             out = torch.empty((n, heads, d), dtype=x.dtype, device=x.device)
-        _need_rows(out, x.dtype, (n, heads, d), "out")
+        else:
+            _need_rows(out, x.dtype, (n, heads, d), "out")
         _check(_lib.msa_rope_apply(self._h, _ptr(x), _row_stride(x), _ptr(positions), n, heads, d,
                                    int(x.dtype == torch.float32), int(inverse), _ptr(out), _row_stride(out),
                                    _stream(stream)), "msa_rope_apply")
@@ -407,11 +408,12 @@ class Plan:
         self._need_scales(k_scale, v_scale)
         if out is None:
             out = torch.empty_like(q)
-        _need(out, torch.bfloat16, tuple(q.shape), "out")
-        if lse is None and want_lse:
-            lse = torch.empty((self.total_q, self.hq), dtype=torch.float32, device=q.device)
+        else:
+            _need(out, torch.bfloat16, (self.total_q, self.hq, self.d), "out")
         if lse is not None:
             _need(lse, torch.float32, (self.total_q, self.hq), "lse")
+        elif want_lse:
+            lse = torch.empty((self.total_q, self.hq), dtype=torch.float32, device=q.device)
         _check(_lib.msa_sparse_attn(self._h, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_indices),
                                     _ptr(kv_block_indexes), _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse),
                                     _stream(stream)), "msa_sparse_attn")
