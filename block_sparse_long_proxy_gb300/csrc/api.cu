@@ -460,8 +460,10 @@ msa_status msa_sparse_attn(msa_plan_t plan, const void* q, const void* k_pages, 
   const int kv_elem = fp8 ? 1 : 2;
   const int64_t per_page = int64_t(plan->hkv) * 128 * plan->d;
   if (s == MSA_OK) s = scan_rows(plan, q, rows * plan->d, 2, st);
-  if (s == MSA_OK) s = scan_pages(plan, k_pages, kv_indices, per_page, kv_elem, st);
-  if (s == MSA_OK) s = scan_pages(plan, v_pages, kv_indices, per_page, kv_elem, st);
+  if (plan->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) {  // whose unwritten slots may hold any bytes
+    if (s == MSA_OK) s = scan_pages(plan, k_pages, kv_indices, per_page, kv_elem, st);
+    if (s == MSA_OK) s = scan_pages(plan, v_pages, kv_indices, per_page, kv_elem, st);
+  }
   if (s == MSA_OK) s = scan_rows(plan, out, rows * plan->d, 2, st);
   if (s == MSA_OK) s = scan_rows(plan, lse, rows, 4, st);
   return s;

@@ -147,8 +147,8 @@ msa_status msa_rope_create(int32_t rotary_dim, msa_rope_layout layout, double ba
   double lo = 0.0, width = 1.0;
   if (scaling == MSA_ROPE_YARN) {
     auto dim = [&](double beta) { return rotary_dim * log(original_len / (two_pi * beta)) / (2.0 * log(base)); };
-    lo = floor(dim(beta_fast));
-    width = std::max(ceil(dim(beta_slow)) - lo, 1e-3);
+    lo = std::max(floor(dim(beta_fast)), 0.0);
+    width = std::max(std::min(ceil(dim(beta_slow)), rotary_dim - 1.0) - lo, 1e-3);
   }
   for (int i = 0; i < pairs; ++i) {
     double turns = pow(base, -2.0 * i / rotary_dim) / two_pi;

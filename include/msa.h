@@ -50,9 +50,12 @@
  *    created while the environment variable MSA_CHECKS is set (to anything
  *    but "0") adds, after each of its calls, scans of that call's
  *    floating-point inputs (the query-side arrays q, pq, dout, and the pages
- *    of k/v/pk that kv_indices names; bf16 or e4m3, not the NVFP4 codes) and
- *    outputs (max_score, out, lse, dq, dpq; not dk/dv/dpk, whose unreferenced
- *    pages keep the caller's contents), and raises MSA_ERR_NONFINITE in the
+ *    of k/v/pk that kv_indices names; bf16 or e4m3, not the NVFP4 codes, nor
+ *    MSA_KV_FP8_E4M3_BLOCK pages, whose unwritten slots may hold any bytes;
+ *    the new rows of the appends) and
+ *    outputs (max_score, out, lse, dq, dpq, the rows of msa_append_bwd; not
+ *    the pages of dk/dv/dpk and of the caches, of which those not referenced
+ *    keep the caller's contents), and raises MSA_ERR_NONFINITE in the
  *    error word when one holds a NaN.  -inf in max_score and lse is a
  *    defined value (no visible key) and is not flagged.  Each scan is one
  *    read of its array.
@@ -411,9 +414,9 @@ msa_status msa_sparse_decode_noalloc(const void* q, const void* k_pages, const v
  *   MSA_ROPE_LINEAR  f_i / factor;
  *   MSA_ROPE_NTK     base * factor^(rotary_dim / (rotary_dim - 2)) for base;
  *   MSA_ROPE_YARN    with D(b) = rotary_dim ln(original_len / (2 pi b)) /
- *                    (2 ln base), lo = floor D(beta_fast), hi = ceil
- *                    D(beta_slow) and the ramp r_i = clamp((i - lo) /
- *                    (hi - lo), 0, 1):  (1 - r_i) f_i + r_i f_i / factor,
+ *                    (2 ln base), lo = max(floor D(beta_fast), 0), hi =
+ *                    min(ceil D(beta_slow), rotary_dim - 1) and the ramp
+ *                    r_i = clamp((i - lo) / (hi - lo), 0, 1):  (1 - r_i) f_i + r_i f_i / factor,
  *                    and the rotated values are multiplied by m = 0.1 ln
  *                    factor + 1 (m = 1 otherwise).
  *

@@ -483,7 +483,8 @@ def rope_freqs(rot: int, base=10000.0, scaling="none", factor=1.0, original_len=
 
     def pair_turning(times):
         return rot * math.log(original_len / (2 * math.pi * times)) / (2 * math.log(base))
-    lo, hi = math.floor(pair_turning(beta_fast)), math.ceil(pair_turning(beta_slow))
+    lo = max(math.floor(pair_turning(beta_fast)), 0)
+    hi = min(math.ceil(pair_turning(beta_slow)), rot - 1)
     ramp = np.clip((i - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
     return (1.0 - ramp) * f + ramp * f / factor, 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
 

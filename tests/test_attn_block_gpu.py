@@ -222,6 +222,35 @@ def test_refusals(cuda_dev):
     assert e.value.status == 6
 
 
+def test_checks_mode(cuda_dev, monkeypatch):
+    """MSA_CHECKS: bytes behind a sequence's last key raise nothing; a NaN among
+    the new rows of an append, or in the queries, does."""
+    from block_sparse_long_proxy_gb300 import msa
+    monkeypatch.setenv("MSA_CHECKS", "1")
+    for qo in ([1] * 2, [150, 3]):
+        case = _case("checks", qo, [300, 129], 8, 2, 2, 3)
+        inp = synth.make_inputs(case, device=cuda_dev)
+        plan = make_plan(case, inp)
+        idx = random_idx(case, np.random.default_rng(0))
+        _attend(case, inp, idx, cuda_dev, plan)
+        k = torch.zeros((sum(qo), 2, 128), device=cuda_dev).bfloat16()
+        args = (inp["k_pages"], inp["v_pages"], inp["kv_indices"])
+        plan.kv_append(k, k, *args, k_scale=inp["k_scale"], v_scale=inp["v_scale"])
+        plan.check_errors()
+        bad = k.clone()
+        bad[-1, 1, 77] = float("nan")
+        for pair in ((bad, k), (k, bad)):
+            plan.kv_append(*pair, *args, k_scale=inp["k_scale"], v_scale=inp["v_scale"])
+            with pytest.raises(msa.MsaError) as e:
+                plan.check_errors()
+            assert e.value.status == 7
+        plan.kv_append(k, k, *args, k_scale=inp["k_scale"], v_scale=inp["v_scale"])
+        inp["q"][0, 0, 0] = float("nan")
+        with pytest.raises(msa.MsaError) as e:
+            _attend(case, inp, idx, cuda_dev, plan)
+        assert e.value.status == 7
+
+
 def test_captured_decode_step(cuda_dev):
     """Append and attend captured in one graph, replayed over new inputs."""
     case = _case("graph", [1] * 4, [300, 129, 1000, 77], 16, 2, 2, 3, page_perm_seed=3)
