@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // per unit, each over its own blocks: one (j, row) list per head
   using L = AttnSmem<D, kStageO, kOneKvHead ? 2 : 1, kBlk>;
   constexpr int kChunks = D / 64;
-  static_assert(!kFp8 || (D == 128 && !kOneKvHead), "FP8 K/V: head_dim 128, main attention");
+  static_assert(!kFp8 || ((D == 128 || kBlk) && !kOneKvHead), "FP8 K/V: head_dim 128 or block scales, main attention");
   static_assert(!kBlk || kFp8, "block scales come with FP8 K/V");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* v_full = k_empty + kStages;    // [kStages]
   uint64_t* v_empty = kv_empty;            // [kStages]
   uint64_t* raw_v_full = v_full + kStages; // [kStages]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_v_full + kStages);
+  uint64_t* conv_read = raw_v_full + kStages;  // head_dim 64: both converter warps hold a half's codes
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(conv_read + 1);
   UnitStats* const stats = reinterpret_cast<UnitStats*>(smem + L::kStatOff);
   // kBlk: (k_scale * scale_log2, log2 v_scale) of the running block count's block
   float2* const scale_ring = reinterpret_cast<float2*>(smem + L::kScaleOff);
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(raw_v_full + s, 1);
     }
     mbar_init(q_ready, kConvWarps);
+    mbar_init(conv_read, kConvWarps);
     mbar_init(ost_ready, 4);  // the four epilogue warps
     mbar_init(ost_free, 1);
     for (int i = 0; i < 4; ++i) {
@@ -361,11 +363,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (kFp8) {  // e4m3 codes into the upper half of the stage; the converters expand them
             const uint32_t par = ((kv_it / kStages) & 1) ^ 1;
             if (!(ok = mbar_wait_inl(k_empty + s, par, err))) break;
-            mbar_expect_tx(raw_full + s, 16384);
-            tma_load_2d(k_s + s * L::kTileBytes + 16384, &k_map, raw_full + s, 0, row);
+            mbar_expect_tx(raw_full + s, L::kTileBytes / 2);
+            tma_load_2d(k_s + s * L::kTileBytes + L::kTileBytes / 2, &k_map, raw_full + s, 0, row);
             if (!(ok = mbar_wait_inl(v_empty + s, par, err))) break;
-            mbar_expect_tx(raw_v_full + s, 16384);
-            tma_load_2d(v_s + s * L::kTileBytes + 16384, &v_map, raw_v_full + s, 0, row);
+            mbar_expect_tx(raw_v_full + s, L::kTileBytes / 2);
+            tma_load_2d(v_s + s * L::kTileBytes + L::kTileBytes / 2, &v_map, raw_v_full + s, 0, row);
             continue;
           }
           if (!(ok = mbar_wait_inl(kv_empty + s, ((kv_it / kStages) & 1) ^ 1, err))) break;
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // f16 units, and the only f16 units that land in that upper half are the
     // same row's, so no other thread's codes are overwritten.
     const int ct = threadIdx.x - 32 * (kSoftWarps + 2);
-    auto expand = [&](uint8_t* buf, int rows) {  // buf: one ring stage, 2 chunks x [128 rows][128 B] of f16
+    auto expand128 = [&](uint8_t* buf, int rows) {  // buf: one ring stage, 2 chunks x [128 rows][128 B] of f16
 #pragma unroll 1
       for (int rr = 0; rr < 2; ++rr) {
         const int r = ct + 64 * rr, sw = r & 7;
@@ -762,6 +764,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           *reinterpret_cast<uint4*>(dst + (((u0 + 1) ^ sw) << 4)) = hi;
         }
       }
+    };
+    // head_dim 64: a stage is one chunk of 64 f16 columns, its upper half the
+    // 64-byte rows of codes, and the f16 rows from 64 on land on other rows'
+    // codes: both warps have read all of them before either writes (a bounded
+    // wait, so that one warp's timeout ends the other's too).
+    uint32_t halves = 0;
+    auto expand64 = [&](uint8_t* buf, int rows) {
+      uint4 u[2][4];
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int r = ct + 64 * rr;
+        const uint8_t* raw = buf + 8192 + r * 64;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          u[rr][c] = *reinterpret_cast<const uint4*>(raw + ((c ^ ((r >> 1) & 3)) << 4));
+          if (r >= rows) u[rr][c] = make_uint4(0u, 0u, 0u, 0u);  // behind the sequence's last key
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(conv_read);
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_inl(conv_read, halves++ & 1, err))) return false;
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int r = ct + 64 * rr, sw = r & 7;
+        uint8_t* dst = buf + r * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 v = u[rr][c];
+          *reinterpret_cast<uint4*>(dst + (((2 * c) ^ sw) << 4)) =
+              make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
+                         e4m3x2_to_f16x2(v.y >> 16));
+          *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ sw) << 4)) =
+              make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
+                         e4m3x2_to_f16x2(v.w >> 16));
+        }
+      }
+      return true;
+    };
+    auto expand = [&](uint8_t* buf, int rows) {
+      if constexpr (D == 64) return expand64(buf, rows);
+      expand128(buf, rows);
+      return true;
     };
     int kv_it = 0;
     bool ok = true;
@@ -794,12 +838,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int i = 0; i < n; ++i, ++kv_it) {
         const int s = kv_it % kStages;
         if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait_inl(raw_full + s, (kv_it / kStages) & 1, err)))) break;
-        expand(k_s + s * L::kTileBytes, 128);
+        if (!(ok = expand(k_s + s * L::kTileBytes, 128))) break;
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full + s);
         if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait_inl(raw_v_full + s, (kv_it / kStages) & 1, err)))) break;
-        expand(v_s + s * L::kTileBytes, kBlk ? kv_len - ls_j[i] * 128 : 128);
+        if (!(ok = expand(v_s + s * L::kTileBytes, kBlk ? kv_len - ls_j[i] * 128 : 128))) break;
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full + s);
@@ -943,17 +987,18 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
                                const float* v_scale, void* out, float* lse, cudaStream_t st) {
   if (p->topk > kMaxTopk) return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: topk above 1024");
   const bool fp8 = p->kv_dtype != MSA_KV_BF16;
-  if (fp8 && p->d != 128)
+  if (p->kv_dtype == MSA_KV_FP8_E4M3 && p->d != 128)
     return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: FP8 K/V prefill needs head_dim 128");
   CUtensorMap qm, km, vm, om;
   const int kv_elem = fp8 ? 1 : 2;
   const uint64_t kdims[2] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->num_pages) * p->hkv * 128};
   const uint64_t kstr[1] = {static_cast<uint64_t>(p->d) * kv_elem};
-  // bf16: 64-column boxes (128 B rows); e4m3: whole 128-byte rows of codes
-  const uint32_t kbox[2] = {fp8 ? 128u : 64u, 128};
+  // bf16: 64-column boxes (128 B rows); e4m3: whole rows of codes
+  const uint32_t kbox[2] = {fp8 ? static_cast<uint32_t>(p->d) : 64u, 128};
+  const int kswz = fp8 ? p->d : 128;
   if (!rows_map(&qm, q, p->d, p->hq, p->total_q) || !rows_map(&om, out, p->d, p->hq, p->total_q) ||
-      !encode_tensor_map(&km, 2, k_pages, kdims, kstr, kbox, fp8 ? 0 : 1, 128) ||
-      !encode_tensor_map(&vm, 2, v_pages, kdims, kstr, kbox, fp8 ? 0 : 1, 128))
+      !encode_tensor_map(&km, 2, k_pages, kdims, kstr, kbox, fp8 ? 0 : 1, kswz) ||
+      !encode_tensor_map(&vm, 2, v_pages, kdims, kstr, kbox, fp8 ? 0 : 1, kswz))
     return set_error(MSA_ERR_CUDA, "msa_sparse_attn: tensor map encoding failed");
   const AttnUnit* units = reinterpret_cast<const AttnUnit*>(p->aux_d + p->attn_units_off);
   const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(p->d));
@@ -961,11 +1006,12 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
   const dim3 grid(std::min(p->n_attn_units, p->num_sms));  // persistent: one CTA per SM
   const int kv_div = p->hp / p->hkv;
   cudaError_t e;
-  if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK)
-    e = launch_attn_variant<128, false, true, true>(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units,
-                                                    p->tiles_d, idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp,
-                                                    kv_div, scale_log2, k_scale, v_scale, p->err_d);
-  else if (fp8)
+  if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK) {
+    const auto launch = p->d == 128 ? launch_attn_variant<128, false, true, true>
+                                    : launch_attn_variant<64, false, true, true>;
+    e = launch(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units, p->tiles_d, idx, kv_indices, p->num_pages, o,
+               lse, p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d);
+  } else if (fp8)
     e = launch_attn_variant<128, false, true>(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units, p->tiles_d,
                                               idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp, kv_div, scale_log2,
                                               k_scale, v_scale, p->err_d);

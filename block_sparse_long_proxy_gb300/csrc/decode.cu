@@ -479,7 +479,8 @@ size_t decode_partial_floats(const msa_plan_s* p) {
 msa_status launch_attn_decode(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,
                               const int32_t* kv_indices, const int32_t* idx, const float* k_scale,
                               const float* v_scale, void* out, float* lse, cudaStream_t st) {
-  if (p->d != kD) return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: FP8 decode needs head_dim 128");
+  if (p->d != kD && p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK)
+    return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: FP8 decode needs head_dim 128");
   if (p->hq / p->hp > 16)
     return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: FP8 decode needs at most 16 query heads per proxy head");
   if (decode_ws_applies(p))

@@ -42,7 +42,6 @@
 namespace msa {
 namespace {
 
-constexpr int kD = 128;
 // a unit is kKeys keys of one selected block (K and V), streamed by one warp
 // through a private buffer; kWsWarps warps per CTA, two CTAs per SM.
 // Measured at 32 x 131072 (keys, stages, warps): (64,1,6) 29.9 us,
@@ -52,14 +51,15 @@ constexpr int kKeys = 32;
 constexpr int kWsWarps = 8;
 constexpr int kWsThreads = 32 * kWsWarps;
 constexpr int kParts = 128 / kKeys;             // units per block
-constexpr int kPartBytes = kKeys * kD;          // K (or V) bytes of one unit
-constexpr int kBufBytes = 2 * kPartBytes;       // one warp's buffer: K part | V part
 constexpr int kMT = kKeys / 16;                 // 16-key m-tiles of a unit
 constexpr int kMaxStaticTopk = (32 * kWsWarps) / kParts;
 
-template <int NT>
+template <int D, int NT>
 struct WsSmem {
   static constexpr int kHeads = 8 * NT;
+  static constexpr int kPartBytes = kKeys * D;      // K (or V) bytes of one unit
+  static constexpr int kBufBytes = 2 * kPartBytes;  // one warp's buffer: K part | V part
+  static constexpr int kD = D;
   static_assert(kBufBytes >= kHeads * kD * 4, "a warp's O fits its buffer");
   static constexpr int kBufOff = 0;
   static constexpr int kCtaOff = kWsWarps * kBufBytes;            // the CTA's merged O, for its cluster
@@ -68,10 +68,13 @@ struct WsSmem {
   static constexpr int kBytes = kBarOff + 16 * kWsWarps;
 };
 
-// byte offset of (row, byte col) in a tile of 128-byte rows written by TMA
-// with 128-byte swizzle: the 16-byte chunk index is XORed with row % 8.
+// byte offset of (row, byte col) in a tile of D-byte rows written by TMA with
+// D-byte swizzle: within a 128-byte line the 16-byte chunk index is XORed with
+// the line's (D = 128) or the line pair's (D = 64) number.
+template <int D>
 __device__ __forceinline__ uint32_t swz(int row, int col) {
-  return row * 128 + ((((col >> 4) ^ row) & 7) << 4) + (col & 15);
+  if (D == 128) return row * 128 + ((((col >> 4) ^ row) & 7) << 4) + (col & 15);
+  return row * 64 + ((((col >> 4) ^ (row >> 1)) & 3) << 4) + (col & 15);
 }
 
 // Merge of n states (m, l, O) of one head and four dims: stable in the log2
@@ -81,7 +84,7 @@ struct Merged {
   float4 o;
 };
 
-template <bool kBlk, int NT>
+template <bool kBlk, int kD, int NT>
 __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
     decode_ws_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                      const __nv_bfloat16* __restrict__ q, const TileInfo* __restrict__ tiles,
@@ -90,7 +93,8 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int32_t hq, int32_t hsel,
                      int32_t kv_div, int32_t topk, int32_t cs, float scale_log2, uint32_t* err) {
   pdl_wait();
-  using L = WsSmem<NT>;
+  using L = WsSmem<kD, NT>;
+  constexpr int kPartBytes = L::kPartBytes, kBufBytes = L::kBufBytes, kMD = kD / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -184,13 +188,13 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   }
   float sl2 = kBlk ? 0.f : scale_log2 * k_scale[kvh];
   float log2_vs = 0.f, inv_vs = 1.f;
-  float m[NT][2], l[NT][2], oacc[8][NT][4];
+  float m[NT][2], l[NT][2], oacc[kMD][NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt][0] = m[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-    for (int md = 0; md < 8; ++md) oacc[md][nt][0] = oacc[md][nt][1] = oacc[md][nt][2] = oacc[md][nt][3] = 0.f;
+    for (int md = 0; md < kMD; ++md) oacc[md][nt][0] = oacc[md][nt][1] = oacc[md][nt][2] = oacc[md][nt][3] = 0.f;
   }
   const uint32_t kb = smem_u32(buf), vb = kb + kPartBytes;
   bool ok = true;
@@ -226,8 +230,8 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
         for (int nt = 0; nt < NT; ++nt) sacc[mt][nt][0] = sacc[mt][nt][1] = sacc[mt][nt][2] = sacc[mt][nt][3] = 0.f;
 #pragma unroll
         for (int kc = 0; kc < kD / 16; ++kc) {
-          const uint32_t wa = lds32(kb + swz(ra, kc * 16 + 4 * t4));
-          const uint32_t wb = lds32(kb + swz(rb, kc * 16 + 4 * t4));
+          const uint32_t wa = lds32(kb + swz<kD>(ra, kc * 16 + 4 * t4));
+          const uint32_t wb = lds32(kb + swz<kD>(rb, kc * 16 + 4 * t4));
           const uint32_t a0 = e4m3x2_to_f16x2(wa), a1 = e4m3x2_to_f16x2(wb);
           const uint32_t a2 = e4m3x2_to_f16x2(wa >> 16), a3 = e4m3x2_to_f16x2(wb >> 16);
 #pragma unroll
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
           l[nt][c] = l[nt][c] * alpha[c] + (kBlk ? sum * inv_vs : sum);
         }
 #pragma unroll
-        for (int md = 0; md < 8; ++md) {
+        for (int md = 0; md < kMD; ++md) {
           oacc[md][nt][0] *= alpha[0];
           oacc[md][nt][2] *= alpha[0];
           oacc[md][nt][1] *= alpha[1];
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
       }
       if (!(ok = mbar_wait(bar_v, phase, err))) break;
       if (kBlk && key0 + kKeys - 1 > qpos) {  // the unit with the query's own key
-        for (int r = qpos + 1 - key0; r < kKeys; ++r) sts32(vb + r * 128 + 4 * lane, 0u);
+        for (int w = (qpos + 1 - key0) * (kD / 4) + lane; w < kKeys * (kD / 4); w += 32) sts32(vb + 4 * w, 0u);
         fence_async_shared();  // before the next load overwrites the buffer
         __syncwarp();
       }
@@ -301,8 +305,8 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
 #pragma unroll
         for (int qg = 0; qg < kD / 32; ++qg) {
           const int col = 32 * qg + 4 * gi;
-          const uint32_t w0 = lds32(vb + swz(r0, col)), w1 = lds32(vb + swz(r0 + 1, col));
-          const uint32_t w2 = lds32(vb + swz(r0 + 8, col)), w3 = lds32(vb + swz(r0 + 9, col));
+          const uint32_t w0 = lds32(vb + swz<kD>(r0, col)), w1 = lds32(vb + swz<kD>(r0 + 1, col));
+          const uint32_t w2 = lds32(vb + swz<kD>(r0 + 8, col)), w3 = lds32(vb + swz<kD>(r0 + 9, col));
           const uint32_t x01 = prmt(w0, w1, 0x5140), x23 = prmt(w2, w3, 0x5140);
           const uint32_t y01 = prmt(w0, w1, 0x7362), y23 = prmt(w2, w3, 0x7362);
           const uint32_t a0 = e4m3x2_to_f16x2(x01), a1 = e4m3x2_to_f16x2(x01 >> 16);
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
       const int h = 8 * nt + 2 * t4 + c;
       if (gi == 0) ml[warp * L::kHeads + h] = make_float2(ok ? m[nt][c] : -INFINITY, l[nt][c]);
 #pragma unroll
-      for (int md = 0; md < 8; ++md) {
+      for (int md = 0; md < kMD; ++md) {
         const int d0 = 32 * (md >> 1) + 4 * gi + 2 * (md & 1);
         *reinterpret_cast<float2*>(sc + h * kD + d0) = make_float2(oacc[md][nt][c], oacc[md][nt][2 + c]);
       }
@@ -393,18 +397,18 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   cluster_sync();  // nobody leaves while its state may be read
 }
 
-template <bool kBlk, int NT>
+template <bool kBlk, int D, int NT>
 cudaError_t launch_ws(const msa_plan_s* p, int cs, cudaStream_t st, const CUtensorMap& km, const CUtensorMap& vm,
                       const void* q, const int32_t* kv_indices, const int32_t* idx, const float* k_scale,
                       const float* v_scale, void* out, float* lse) {
-  auto kern = decode_ws_kernel<kBlk, NT>;
-  const int smem = WsSmem<NT>::kBytes + 1024;
+  auto kern = decode_ws_kernel<kBlk, D, NT>;
+  const int smem = WsSmem<D, NT>::kBytes + 1024;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (cs > 8) cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return launch_pdl_cluster(kern, dim3(p->n_tiles * p->hp * cs), cs, dim3(kWsThreads), smem, st, km, vm,
                             static_cast<const __nv_bfloat16*>(q), p->tiles_d, idx, kv_indices, p->num_pages, k_scale,
                             v_scale, static_cast<__nv_bfloat16*>(out), lse, p->hq, p->hp, p->hp / p->hkv, p->topk, cs,
-                            1.4426950408889634f / sqrtf(static_cast<float>(kD)), p->err_d);
+                            1.4426950408889634f / sqrtf(static_cast<float>(D)), p->err_d);
 }
 
 // CTAs a row: one for an SM at most, with a unit for every warp; clusters of
@@ -433,23 +437,23 @@ int row_cluster(const msa_plan_s* p) {
 
 bool decode_ws_applies(const msa_plan_s* p) {
   if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK) return true;
-  return p->n_tiles * p->hp >= p->num_sms && p->hq / p->hp <= 8 && p->topk <= kMaxStaticTopk && p->d == kD;
+  return p->n_tiles * p->hp >= p->num_sms && p->hq / p->hp <= 8 && p->topk <= kMaxStaticTopk && p->d == 128;
 }
 
 msa_status launch_attn_decode_ws(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,
                                  const int32_t* kv_indices, const int32_t* idx, const float* k_scale,
                                  const float* v_scale, void* out, float* lse, cudaStream_t st) {
   CUtensorMap km, vm;
-  const uint64_t dims[2] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(p->num_pages) * p->hkv * 128};
-  const uint64_t str[1] = {static_cast<uint64_t>(kD)};
-  const uint32_t box[2] = {static_cast<uint32_t>(kD), static_cast<uint32_t>(kKeys)};
-  if (!encode_tensor_map(&km, 2, k_pages, dims, str, box, 0, 128) ||
-      !encode_tensor_map(&vm, 2, v_pages, dims, str, box, 0, 128))
+  const uint64_t dims[2] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->num_pages) * p->hkv * 128};
+  const uint64_t str[1] = {static_cast<uint64_t>(p->d)};
+  const uint32_t box[2] = {static_cast<uint32_t>(p->d), static_cast<uint32_t>(kKeys)};
+  if (!encode_tensor_map(&km, 2, k_pages, dims, str, box, 0, p->d) ||
+      !encode_tensor_map(&vm, 2, v_pages, dims, str, box, 0, p->d))
     return set_error(MSA_ERR_CUDA, "msa_sparse_attn: tensor map encoding failed");
   const bool wide = p->hq / p->hp > 8;
-  const auto launch = p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK ? launch_ws<false, 1>
-                      : wide                               ? launch_ws<true, 2>
-                                                           : launch_ws<true, 1>;
+  const auto launch = p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK ? launch_ws<false, 128, 1>
+                      : p->d == 128 ? (wide ? launch_ws<true, 128, 2> : launch_ws<true, 128, 1>)
+                                    : (wide ? launch_ws<true, 64, 2> : launch_ws<true, 64, 1>);
   const int cs = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK ? row_cluster(p) : 1;
   return cuda_check(launch(p, cs, st, km, vm, q, kv_indices, idx, k_scale, v_scale, out, lse),
                     "msa_sparse_attn: decode launch");

@@ -306,7 +306,7 @@ msa_status msa_proxy_topk(msa_plan_t plan, const void* pq, const void* pk_pages,
  *  out               bf16 [total_q, Hq, d] (output).
  *  lse               fp32 [total_q, Hq] (output) or NULL.
  * MSA_KV_FP8_E4M3_BLOCK: s uses k * k_scale[page, g] and V is v *
- * v_scale[page, g] of the page that holds the key; head_dim 128, and at
+ * v_scale[page, g] of the page that holds the key; head_dim 64 or 128, and at
  * decode at most 16 query heads per proxy head.  Scales are taken as lying in
  * [2^-40, 2^40] (others, zero and NaN among them, count as the nearer end).
  * Slots of a sequence's last page behind its last key may hold any bytes.  At

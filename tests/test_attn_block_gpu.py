@@ -19,8 +19,8 @@ from tests.gpu_cases import compare_out, irregular_idx, make_plan, random_idx
 pytestmark = pytest.mark.gpu
 
 
-def _case(name, qo, kv, hq, hkv, hp, topk, **kw):
-    return synth.Case(name, qo, kv, hq, hkv, 128, hp, 64, topk, kv_dtype="e4m3_block", **kw)
+def _case(name, qo, kv, hq, hkv, hp, topk, d=128, **kw):
+    return synth.Case(name, qo, kv, hq, hkv, d, hp, 64, topk, kv_dtype="e4m3_block", **kw)
 
 
 def _attend(case, inp, idx, dev, plan=None):
@@ -76,6 +76,16 @@ CASES = [
     _case("no queries mid-batch", [300, 0, 129], [300, 500, 129], 8, 2, 2, 3, page_perm_seed=6),
     _case("topk 1024", [2048], [2048], 4, 1, 1, 1024, page_perm_seed=7),
     _case("40 blocks", [5120], [5120], 8, 2, 2, 16, page_perm_seed=11),
+    # head_dim 64
+    _case("d64 decode one key", [1], [1], 8, 1, 1, 4, d=64),
+    _case("d64 decode ragged", [1] * 5, [700, 129, 128, 33, 5000], 16, 2, 2, 4, d=64, page_perm_seed=2, extra_pages=3),
+    _case("d64 decode G=16", [1] * 3, [2048, 777, 95], 32, 2, 2, 5, d=64, page_perm_seed=6),
+    _case("d64 decode rows>=SMs", [1] * 40, _LENS, 32, 4, 4, 12, d=64, page_perm_seed=10),
+    _case("d64 decode topk 200", [1] * 2, [30000, 3000], 3, 1, 1, 200, d=64, page_perm_seed=12),
+    _case("d64 ragged chunks", [300, 77, 128, 129, 2], [300, 1000, 128, 500, 260], 8, 2, 2, 3, d=64, page_perm_seed=3),
+    _case("d64 G=3", [200], [333], 6, 2, 2, 2, d=64, page_perm_seed=1),
+    _case("d64 topk 1024", [2048], [2048], 4, 1, 1, 1024, d=64, page_perm_seed=7),
+    _case("d64 two block sets a head", [2560], [2600], 16, 2, 4, 9, d=64, page_perm_seed=1),
 ]
 
 
@@ -206,7 +216,7 @@ def test_refusals(cuda_dev):
     pages = (inp["q"], inp["k_pages"], inp["v_pages"], inp["kv_indices"], idx)
     with pytest.raises(ValueError):
         plan.sparse_attn(*pages, k_scale=inp["k_scale"][0], v_scale=inp["v_scale"][0])
-    for d, hq, qo in ((64, 8, 1), (64, 8, 2), (128, 34, 1)):
+    for d, hq, qo in ((64, 34, 1), (128, 34, 1)):
         c = synth.Case("x", [qo], [200], hq, 2, d, 2, 32, 2, kv_dtype="e4m3_block")
         i = synth.make_inputs(c, device=cuda_dev)
         with pytest.raises(msa.MsaError) as e:
