@@ -49,6 +49,10 @@
 // by the softmax warps themselves they cost 130 us of 965 at S=32768).  The
 // converters write zeros for V rows behind the sequence's last key, whose
 // bytes were never written.
+//
+// kSplit (kBlk, few units): the CTAs of a cluster take a part of one unit's
+// blocks each, leave their O, m and l in shared memory (where the rings were)
+// and merge a share of the rows each over distributed shared memory.
 #include "msa_internal.h"
 #include "ptx.cuh"
 
@@ -127,7 +131,7 @@ struct AttnSmem {
 // barrier's phase comes from a running count (per head for the S / P / O
 // barriers), and Q is released right after a unit's last QK so the next
 // unit's Q load overlaps the tail of the current one.
-template <int D, bool kOneKvHead, bool kFp8, bool kStageO, bool kBlk = false>
+template <int D, bool kOneKvHead, bool kFp8, bool kStageO, bool kBlk = false, bool kSplit = false>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap o_map,
@@ -136,8 +140,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int32_t* __restrict__ kv_indices, int64_t num_pages, __nv_bfloat16* __restrict__ out,
                     float* __restrict__ lse, int32_t hq, int32_t hsel, int32_t kv_div, int32_t topk,
                     float scale_log2, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
-                    uint32_t* err) {
+                    int32_t parts, uint32_t* err) {
   pdl_wait();
+  // kSplit (few units): a unit's blocks are shared out over the `parts` CTAs of
+  // a cluster, which do nothing else and merge at the end
+  const int part = kSplit ? blockIdx.x % parts : 0;
+  auto first_unit = [&]() -> int { return kSplit ? blockIdx.x / parts : blockIdx.x; };
   // hsel block sets (proxy heads) per tile; a unit's u.g is its proxy head,
   // whose blocks are read from KV head u.g / kv_div of hsel / kv_div
   const int hkv = hsel / kv_div;
@@ -147,12 +155,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr int kChunks = D / 64;
   static_assert(!kFp8 || ((D == 128 || kBlk) && !kOneKvHead), "FP8 K/V: head_dim 128 or block scales, main attention");
   static_assert(!kBlk || kFp8, "block scales come with FP8 K/V");
+  static_assert(!kSplit || (kBlk && !kStageO), "split units: block scales, O through the merge");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem + L::kQOff;
   uint8_t* k_s = smem + L::kKOff;
   uint8_t* v_s = smem + L::kVOff;
   int32_t* const list_base = reinterpret_cast<int32_t*>(smem + L::kListOff);
+  // A part's O_h: rows of D floats where the K (h = 0) or V ring was, their
+  // 16-byte chunks spread over the banks by row.  P_0.V of the unit's last
+  // block is issued after its last Q K^T, and P_1.V after that: the K ring is
+  // free once O_0 is done, the V ring once O_1 is.
+  auto part_o = [](uint8_t* base, int h, int r, int chunk) -> uint4& {
+    return reinterpret_cast<uint4*>(base + (h == 0 ? L::kKOff : L::kVOff))[r * (D / 4) + (chunk ^ (r & (D / 4 - 1)))];
+  };
   // the staged layout sizes the list slots by topk; the other keeps them at
   // the compile-time maximum (constant offsets in the issue loops)
   const int cap = kStageO ? list_cap : kMaxTopk;
@@ -250,7 +266,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const BlockScale b = block_scale_of(k_scale[row >> 7], v_scale[row >> 7]);
       scale_ring[it % kScaleRing] = make_float2(b.ks * scale_log2, b.log2_vs);
     };
-    for (int k = 0, ui = blockIdx.x; ok && ui < n_units; ++k, ui += gridDim.x) {
+    for (int k = 0, ui = first_unit(); ok && ui < n_units; ++k, ui += kSplit ? n_units : gridDim.x) {
       UnitHdr& ls = lhdr(k);
       int32_t* const ls_j = lj(k);
       int32_t* const ls_row = lrow(k);
@@ -263,6 +279,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!ok) break;
       // the unit's blocks: padding skipped, entries past the tile's valid
       // blocks dropped and reported, pages checked against the pool
+      int first = 0, count = topk;  // of the valid blocks, this part's
+      if (kSplit) {
+        int total = 0;
+        for (int b = 0; b < topk; b += 32) {
+          const int j = b + lane < topk ? sel[b + lane] : -1;
+          total += __popc(__ballot_sync(0xFFFFFFFFu, j >= 0 && j < tl.nvp));
+        }
+        first = total * part / parts;
+        count = total * (part + 1) / parts - first;
+      }
       int n = 0;
       for (int b = 0; b < topk; b += 32) {
         const int kk = b + lane;
@@ -281,13 +307,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, valid);
         if (valid) {
-          const int o = n + __popc(m & ((1u << lane) - 1u));
-          ls_j[o] = j;
-          ls_row[o] = row;
-          if (kBlk && o < 64) put_scale(kv_it + o, row);
+          const int o = n + __popc(m & ((1u << lane) - 1u)) - first;
+          if (!kSplit || (o >= 0 && o < count)) {
+            ls_j[o] = j;
+            ls_row[o] = row;
+            if (kBlk && o < 64) put_scale(kv_it + o, row);
+          }
         }
         n += __popc(m);
       }
+      if (kSplit) n = count;
       const bool pair = kOneKvHead && u.nh == 2;
       if (pair) {
         // the second proxy head's own blocks (selection row g + 1); the
@@ -424,7 +453,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       };
       int kv_it = 0, ch0 = 0, ch1 = 0;
       bool ok = true;
-      for (int k = 0, ui = blockIdx.x; ok && ui < n_units; ++k, ui += gridDim.x) {
+      for (int k = 0, ui = first_unit(); ok && ui < n_units; ++k, ui += kSplit ? n_units : gridDim.x) {
         if (!(ok = mbar_wait_inl(list_full + k % kListSlots, (k / kListSlots) & 1, err))) break;
         const int n = lhdr(k).n;
         const bool two = lhdr(k).nh == 2;
@@ -506,7 +535,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int ch = 0;  // blocks of head h so far
     int kv_it = 0;  // blocks of either so far
     bool ok = true;
-    for (int k = 0, ui = blockIdx.x; ui < n_units; ++k, ui += gridDim.x) {
+    for (int k = 0, ui = first_unit(); ui < n_units; ++k, ui += kSplit ? n_units : gridDim.x) {
       const UnitHdr& ls = lhdr(k);
       const int32_t* const ls_j = kOneKvHead && h == 1 ? lj1(k) : lj(k);  // a paired unit's heads: own blocks
       if (ok) ok = mbar_wait_inl(list_full + k % kListSlots, (k / kListSlots) & 1, err);
@@ -640,7 +669,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int od0 = 0, od1 = 0;  // units with blocks of head 0 / head 1 so far
     int ost_uses = 0;      // 64-column boxes staged so far
     bool ok = true;
-    for (int k = 0, ui = blockIdx.x; ui < n_units; ++k, ui += gridDim.x) {
+    for (int k = 0, ui = first_unit(); ui < n_units; ++k, ui += kSplit ? n_units : gridDim.x) {
       const int b = k & 1;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -685,6 +714,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free + h);
           }
+          if (kSplit) {  // a part's O as it is, for the merge
+#pragma unroll
+            for (int e = 0; e < 8; ++e) part_o(smem, h, r, 8 * c + e) = *reinterpret_cast<const uint4*>(ov + 4 * e);
+            continue;
+          }
           // staged: one 64-column box at a time, once the previous box's
           // store has read the buffer
           if (staged && (c & 1) == 0 && ost_uses > 0 && ok) ok = mbar_wait_inl(ost_free, (ost_uses - 1) & 1, err);
@@ -721,7 +755,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ++ost_uses;
           }
         }
-        if (unit_ok && row_ok && lse != nullptr)
+        if (!kSplit && unit_ok && row_ok && lse != nullptr)
           lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
     }
@@ -809,7 +843,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
     int kv_it = 0;
     bool ok = true;
-    for (int k = 0, ui = blockIdx.x; ok && ui < n_units; ++k, ui += gridDim.x) {
+    for (int k = 0, ui = first_unit(); ok && ui < n_units; ++k, ui += kSplit ? n_units : gridDim.x) {
       const UnitHdr& ls = lhdr(k);
       ok = mbar_wait_inl(list_full + k % kListSlots, (k / kListSlots) & 1, err);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -857,6 +891,62 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
+  if constexpr (kSplit) {
+    cluster_sync();  // every part's O, m and l are in its shared memory
+    if (warp < kSoftWarps) {
+      // Part p merges rows p, p + parts, ... of the unit: first every row's
+      // weights (where Q was), then its O, a chunk of all parts at a time.
+      constexpr int kThreads = 32 * kSoftWarps, kMost = 8;
+      const AttnUnit u = units[first_unit()];
+      const TileInfo tl = tiles[u.tile];
+      const int mine = (tl.rows - part + parts - 1) / parts;  // rows 1..128, parts <= 8
+      float* const wts = reinterpret_cast<float*>(q_s);       // [head * mine + row][kMost]
+      for (int e = threadIdx.x; e < u.nh * mine; e += kThreads) {
+        const int h = e >= mine, r = part + (e - h * mine) * parts;
+        const uint32_t m_at = smem_u32(&stats[2 * h].m[r]), l_at = smem_u32(&stats[2 * h].l[r]);
+        float m[kMost], l[kMost], mm = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int p = 0; p < kMost; ++p)
+          if (p < parts) m[p] = ld_cluster_f1(m_at, p), l[p] = ld_cluster_f1(l_at, p);
+#pragma unroll
+        for (int p = 0; p < kMost; ++p)
+          if (p < parts) mm = fmaxf(mm, m[p]);
+#pragma unroll
+        for (int p = 0; p < kMost; ++p)
+          if (p < parts) {
+            m[p] = m[p] == -INFINITY ? 0.f : ex2_approx(m[p] - mm);
+            sum += l[p] * m[p];
+          }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int p = 0; p < kMost; ++p)
+          if (p < parts) wts[e * kMost + p] = m[p] * inv;
+        if (lse != nullptr)
+          lse[static_cast<int64_t>(tl.q_begin + r) * hq + u.h0 + h] =
+              sum > 0.f ? (mm + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+#pragma unroll 1
+      for (int e = threadIdx.x; e < u.nh * mine * (D / 4); e += kThreads) {
+        const int item = e / (D / 4), chunk = e % (D / 4);
+        const int h = item >= mine, r = part + (item - h * mine) * parts;
+        const uint32_t at = smem_u32(&part_o(smem, h, r, chunk));
+        float4 op[kMost], o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < kMost; ++p)
+          if (p < parts) op[p] = ld_cluster_f4(at, p);
+#pragma unroll
+        for (int p = 0; p < kMost; ++p)
+          if (p < parts) {
+            const float w = wts[item * kMost + p];
+            o.x += op[p].x * w, o.y += op[p].y * w, o.z += op[p].z * w, o.w += op[p].w * w;
+          }
+        *reinterpret_cast<uint2*>(out + (static_cast<int64_t>(tl.q_begin + r) * hq + u.h0 + h) * D + 4 * chunk) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+      }
+    }
+    cluster_sync();  // nobody leaves while its part may be read
+  }
 }
 
 }  // namespace
@@ -895,15 +985,47 @@ static void balance_units(const msa_plan_s* p, std::vector<AttnUnit>& us) {
   us.swap(out);
 }
 
+// Heads a unit (returned) and CTAs a unit (p->attn_parts).
+//
+// Two heads share a block's K and V and overlap each other's softmax; with an
+// SM for every head, a head alone is done sooner (512 rows x 32 heads, topk 16:
+// e4m3 38.0 us in pairs, 32.6 alone; bf16 34.4, 28.8).  Block-scaled plans also
+// share a unit's blocks out over a cluster while each of its CTAs has an SM.  A
+// block step takes about 1.65 us for a head and 1.78 for two, a unit 6 besides
+// and the merge 3.  Clusters of 8 are not placed as densely as the SMs would
+// allow: 16 of them took two waves, 12 one.  Measured (us; heads a unit / parts):
+//   rows x heads, blocks     1/1    1/2    1/4    1/8    2/1    2/2    2/4
+//     128 x 32, 16          33.8   24.4  [17.9]  41.7   38.3   29.2   21.1
+//     512 x 32, 16          34.4   48.5   67.5    126   39.0  [30.1]  42.9
+//       2 x 64, 16          39.2   25.3   33.3   61.8   42.4   27.1  [20.0]
+//     300 x 4, 24           55.0   33.5   21.3  [16.4]  58.7   36.5   24.6
+//     700 x 12, 9           24.5  [20.0]  31.3   69.2   27.7   24.1   30.9
+//     100 x 8, 64            139   76.7   43.6  [27.3]   144   81.3   47.2
+static int unit_shape(msa_plan_s* p) {
+  const int grp = p->hq / p->hp;
+  p->attn_parts = 1;
+  if (p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) return int64_t(p->n_tiles) * p->hq <= p->num_sms ? 1 : 2;
+  int blocks = 1, best_heads = 2;
+  for (const TileInfo& t : p->tiles) blocks = std::max(blocks, std::min(t.nvp, p->topk));
+  double best = 1e30;
+  for (int heads = 2; heads >= 1; --heads)
+    for (int parts = 1; parts <= 8 && parts <= blocks; parts *= 2) {
+      const int64_t units = int64_t(p->n_tiles) * p->hp * ((grp + heads - 1) / heads);
+      if (parts > 1 && units * parts > (parts < 8 ? p->num_sms - 8 : p->num_sms * 2 / 3)) break;
+      const int64_t rounds = (units * parts + p->num_sms - 1) / p->num_sms;
+      double us = rounds * ((blocks + parts - 1) / parts * (heads == 2 ? 1.78 : 1.65) + 6) + (parts > 1 ? 3 : 0);
+      if (heads == 1 && rounds > 1) us *= 1.1;  // an odd head beside pairs fills the rounds better
+      if (us < best) best = us, best_heads = heads, p->attn_parts = parts;
+    }
+  return best_heads;
+}
+
 void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   // a unit: (tile, proxy head g, a pair of the query heads that use g's
   // blocks); with one proxy head per GQA group g is the group
   std::vector<AttnUnit> us;
   const int grp = p->hq / p->hp;
-  // two heads share a block's K and V and overlap each other's softmax; with
-  // an SM for every head, a head alone is done sooner (512 rows x 32 heads,
-  // topk 16: e4m3 38.0 us in pairs, 32.6 alone; bf16 34.4, 28.8)
-  const int pair = int64_t(p->n_tiles) * p->hq <= p->num_sms ? 1 : 2;
+  const int pair = unit_shape(p);
   for (int t = 0; t < p->n_tiles; ++t)
     for (int g = 0; g < p->hp; ++g)
       for (int h = 0; h < grp; h += pair) us.push_back(AttnUnit{t, g, g * grp + h, std::min(pair, grp - h)});
@@ -951,25 +1073,28 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
                                 int32_t n_units, const TileInfo* tiles, const int32_t* idx,
                                 const int32_t* kv_indices, int64_t num_pages, __nv_bfloat16* o, float* lse,
                                 int32_t hq, int32_t hsel, int32_t kv_div, float scale_log2, const float* k_scale,
-                                const float* v_scale, uint32_t* err) {
+                                const float* v_scale, uint32_t* err, int parts = 1) {
   const int cap = (topk + 3) & ~3;
   if constexpr (kFp8) {
     const int staged = AttnSmem<D, true, kOneKvHead ? 2 : 1, kBlk>::bytes(cap) + 1024;
-    if (staged <= kMaxSmem) {
+    if (staged <= kMaxSmem && parts == 1) {
       auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, true, kBlk>;
       if (const cudaError_t e = check_launch_regs(kern)) return e;
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, staged);
-      return launch_pdl(kern, grid, dim3(kAttnThreads), staged, st, qm, km, vm, om, cap, units, n_units,
-                        tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
-                        v_scale, err);
+      return launch_pdl_cluster(kern, grid, 1, dim3(kAttnThreads), staged, st, qm, km, vm, om, cap, units, n_units,
+                                tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
+                                v_scale, 1, err);
     }
   }
   const int plain = AttnSmem<D, false, kOneKvHead ? 2 : 1, kBlk>::bytes(kMaxTopk) + 1024;
   auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false, kBlk>;
+  if constexpr (kBlk)
+    if (parts > 1) kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false, true, true>;
   if (const cudaError_t e = check_launch_regs(kern)) return e;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plain);
-  return launch_pdl(kern, grid, dim3(kAttnThreads), plain, st, qm, km, vm, om, cap, units, n_units, tiles, idx,
-                    kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale, v_scale, err);
+  return launch_pdl_cluster(kern, grid, parts, dim3(kAttnThreads), plain, st, qm, km, vm, om, cap, units, n_units,
+                            tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
+                            v_scale, parts, err);
 }
 
 // [total_q, heads, D] bf16 rows as 3-D boxes of 64 columns x 1 head x 128 rows, 128-byte swizzle
@@ -1009,8 +1134,10 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
   if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK) {
     const auto launch = p->d == 128 ? launch_attn_variant<128, false, true, true>
                                     : launch_attn_variant<64, false, true, true>;
-    e = launch(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units, p->tiles_d, idx, kv_indices, p->num_pages, o,
-               lse, p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d);
+    const int parts = p->attn_parts;
+    e = launch(parts > 1 ? dim3(p->n_attn_units * parts) : grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units,
+               p->tiles_d, idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale,
+               p->err_d, parts);
   } else if (fp8)
     e = launch_attn_variant<128, false, true>(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units, p->tiles_d,
                                               idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp, kv_div, scale_log2,

@@ -392,7 +392,18 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
 // visible to all of them; and reads of another CTA's shared memory (addr: the
 // same variable's address in this CTA).
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f1(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
 }
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr, uint32_t rank) {
   float2 v;

@@ -76,7 +76,13 @@ CASES = [
     _case("no queries mid-batch", [300, 0, 129], [300, 500, 129], 8, 2, 2, 3, page_perm_seed=6),
     _case("topk 1024", [2048], [2048], 4, 1, 1, 1024, page_perm_seed=7),
     _case("40 blocks", [5120], [5120], 8, 2, 2, 16, page_perm_seed=11),
+    # a unit's blocks over clusters of 2, 4 and 8, rows of every part; more parts than some tiles have blocks
+    _case("parts 8", [300, 1], [9000, 60], 4, 1, 1, 24, page_perm_seed=3),
+    _case("parts 4", [5, 3, 128], [9000, 130, 2000], 12, 4, 4, 9, page_perm_seed=3),
+    _case("parts 2", [700], [9000], 12, 4, 4, 9, page_perm_seed=3),
+    _case("parts 8 topk 200", [100], [90000], 8, 1, 1, 200, page_perm_seed=3),
     # head_dim 64
+    _case("d64 parts 8", [130], [9000], 6, 1, 2, 24, d=64, page_perm_seed=3),
     _case("d64 decode one key", [1], [1], 8, 1, 1, 4, d=64),
     _case("d64 decode ragged", [1] * 5, [700, 129, 128, 33, 5000], 16, 2, 2, 4, d=64, page_perm_seed=2, extra_pages=3),
     _case("d64 decode G=16", [1] * 3, [2048, 777, 95], 32, 2, 2, 5, d=64, page_perm_seed=6),
