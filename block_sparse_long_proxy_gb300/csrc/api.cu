@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <exception>
 #include <mutex>
 
 #include "msa_internal.h"
@@ -208,6 +209,11 @@ msa_status scan_proxy(const msa_plan_s* p, msa_status s, const void* pq, const v
 }  // namespace
 }  // namespace msa
 
+static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batch, int32_t num_qo_heads,
+                            int32_t num_kv_heads, int32_t num_proxy_heads, int32_t head_dim, int32_t proxy_head_dim,
+                            int32_t page_size, int32_t topk, int64_t num_pages, msa_kv_dtype kv_dtype, uint32_t flags,
+                            msa_stream_t stream, msa_plan_t* out);
+
 extern "C" {
 
 const char* msa_last_error(void) { return g_last_error.c_str(); }
@@ -217,6 +223,20 @@ msa_status msa_plan(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batc
                     int32_t num_kv_heads, int32_t num_proxy_heads, int32_t head_dim, int32_t proxy_head_dim,
                     int32_t page_size, int32_t topk, int64_t num_pages, msa_kv_dtype kv_dtype, uint32_t flags,
                     msa_stream_t stream, msa_plan_t* out) {
+  try {
+    return make_plan(qo_lens, kv_lens, batch, num_qo_heads, num_kv_heads, num_proxy_heads, head_dim, proxy_head_dim,
+                     page_size, topk, num_pages, kv_dtype, flags, stream, out);
+  } catch (const std::exception&) {  // the host tables of a batch too large for memory
+    return set_error(MSA_ERR_NO_MEMORY, "msa_plan: out of host memory");
+  }
+}
+
+}  // extern "C"
+
+static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batch, int32_t num_qo_heads,
+                            int32_t num_kv_heads, int32_t num_proxy_heads, int32_t head_dim, int32_t proxy_head_dim,
+                            int32_t page_size, int32_t topk, int64_t num_pages, msa_kv_dtype kv_dtype, uint32_t flags,
+                            msa_stream_t stream, msa_plan_t* out) {
   if (!out) return set_error(MSA_ERR_INVALID_ARG, "msa_plan: out is NULL");
   *out = nullptr;
   if (batch < 1 || !qo_lens || !kv_lens) return set_error(MSA_ERR_INVALID_ARG, "msa_plan: empty batch");
@@ -361,6 +381,8 @@ msa_status msa_plan(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batc
   return MSA_OK;
 }
 
+extern "C" {
+
 void msa_plan_destroy(msa_plan_t plan) {
   if (!plan) return;
   if (plan->dev_block) cudaFree(plan->dev_block);
@@ -451,7 +473,10 @@ msa_status msa_sparse_attn(msa_plan_t plan, const void* q, const void* k_pages, 
   if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
     return set_error(MSA_ERR_INVALID_ARG, "msa_sparse_attn: k_scale/v_scale must be given exactly for FP8 K/V");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  msa_status s = fp8 && plan->decode
+  // rows of more than 16 heads over block-scaled pages go through the prefill
+  // kernel, as bf16 decode does
+  const bool wide = plan->kv_dtype == MSA_KV_FP8_E4M3_BLOCK && plan->hq / plan->hp > 16;
+  msa_status s = fp8 && plan->decode && !wide
                      ? launch_attn_decode(plan, q, k_pages, v_pages, kv_indices, kv_block_indexes, k_scale, v_scale,
                                           out, lse, st)
                      : launch_attn_prefill(plan, q, k_pages, v_pages, kv_indices, kv_block_indexes, k_scale, v_scale,

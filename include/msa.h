@@ -292,7 +292,8 @@ msa_status msa_proxy_topk(msa_plan_t plan, const void* pq, const void* pk_pages,
  *
  *  q                 bf16 [total_q, Hq, d].
  *  k_pages, v_pages  [num_pages, Hkv, 128, d], bf16 or e4m3 per the plan
- *                    (e4m3 prefill: head_dim 128; the MMAs run in f16, with
+ *                    (MSA_KV_FP8_E4M3: head_dim 128, at decode at most 16
+ *                    query heads per proxy head; the e4m3 MMAs run in f16, with
  *                    q rounded to f16, exact for |q| in [2^-14, 65504]).
  *  kv_indices        int32 page table.
  *  kv_block_indexes  int32 [num_tiles, Hp, topk], as msa_topk_select writes
@@ -306,12 +307,11 @@ msa_status msa_proxy_topk(msa_plan_t plan, const void* pq, const void* pk_pages,
  *  out               bf16 [total_q, Hq, d] (output).
  *  lse               fp32 [total_q, Hq] (output) or NULL.
  * MSA_KV_FP8_E4M3_BLOCK: s uses k * k_scale[page, g] and V is v *
- * v_scale[page, g] of the page that holds the key; head_dim 64 or 128, and at
- * decode at most 16 query heads per proxy head.  Scales are taken as lying in
+ * v_scale[page, g] of the page that holds the key.  Scales are taken as lying in
  * [2^-40, 2^40] (others, zero and NaN among them, count as the nearer end).
  * Slots of a sequence's last page behind its last key may hold any bytes.  At
  * decode, too, a row that sees no key of its selection gets out = 0 and
- * lse = -inf.
+ * lse = -inf.  These plans use no workspace: their calls may overlap.
  *
  * Decode batches (every qo_len == 1) run a split-K kernel whose partial
  * results live in the plan's workspace: two calls on one plan must not

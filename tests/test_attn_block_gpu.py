@@ -65,6 +65,8 @@ CASES = [
     _case("decode rows>=SMs", [1] * 20, _LENS[:20], 64, 8, 8, 8, page_perm_seed=9, extra_pages=5),
     _case("decode rows>=SMs G=4 padded", [1] * 40, _LENS, 16, 4, 4, 12, page_perm_seed=10),
     _case("decode rows>=SMs topk 80", [1] * 20, _LENS[:20], 64, 8, 8, 80, page_perm_seed=11),
+    _case("decode G=17", [1] * 3, [900, 1500, 33], 34, 2, 2, 6, page_perm_seed=7),
+    _case("decode G=40 d64", [1] * 2, [900, 77], 40, 1, 1, 3, d=64, page_perm_seed=7),
     _case("decode rows>=SMs G=16", [1] * 40, _LENS, 64, 4, 4, 5, page_perm_seed=13),
     # prefill
     _case("two rows", [2], [2], 4, 1, 1, 1),
@@ -117,6 +119,18 @@ def test_irregular_selections_and_empty_rows(cuda_dev, qo, rows):
     out, lse = _attend(case, inp, idx, cuda_dev)
     assert np.isneginf(lse.cpu().numpy()).any()
     _check(case, inp, idx, out, lse)
+
+
+def test_irregular_selections_in_parts(cuda_dev):
+    """The same with few units, whose blocks are shared out over clusters: parts
+    without a block, tiles without any."""
+    case = _case("irregular parts", [130, 3, 60], [2000, 3, 700], 8, 2, 2, 6, page_perm_seed=4)
+    inp = synth.make_inputs(case, device=cuda_dev)
+    for seed in (9, 10):
+        idx = irregular_idx(case, np.random.default_rng(seed))
+        out, lse = _attend(case, inp, idx, cuda_dev)
+        assert np.isneginf(lse.cpu().numpy()).any()
+        _check(case, inp, idx, out, lse)
 
 
 @pytest.mark.parametrize("batch", [1, 20])
@@ -222,14 +236,6 @@ def test_refusals(cuda_dev):
     pages = (inp["q"], inp["k_pages"], inp["v_pages"], inp["kv_indices"], idx)
     with pytest.raises(ValueError):
         plan.sparse_attn(*pages, k_scale=inp["k_scale"][0], v_scale=inp["v_scale"][0])
-    for d, hq, qo in ((64, 34, 1), (128, 34, 1)):
-        c = synth.Case("x", [qo], [200], hq, 2, d, 2, 32, 2, kv_dtype="e4m3_block")
-        i = synth.make_inputs(c, device=cuda_dev)
-        with pytest.raises(msa.MsaError) as e:
-            make_plan(c, i).sparse_attn(i["q"], i["k_pages"], i["v_pages"], i["kv_indices"],
-                                        torch.from_numpy(random_idx(c, np.random.default_rng(0))).to(cuda_dev),
-                                        k_scale=i["k_scale"], v_scale=i["v_scale"])
-        assert e.value.status == 2
     bad = inp["kv_indices"].clone()
     bad[0] = plan.num_pages
     plan.sparse_attn(inp["q"], inp["k_pages"], inp["v_pages"], bad, idx, k_scale=inp["k_scale"], v_scale=inp["v_scale"])
