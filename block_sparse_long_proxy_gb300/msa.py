@@ -107,23 +107,21 @@ def _need(t, dtype, shape, name):
         raise ValueError("%s: must be a contiguous CUDA tensor on the current device" % name)
 
 
-def _need_rows(t, dtype, shape, name):
+def _rows(t, dtype, shape, name):
     """_need for rows at a stride: the heads of a row dense, the rows anywhere
-    apart (a slice of a fused projection)."""
-    if (t.dtype is dtype and t.shape == shape and t.get_device() == _current_device()
-            and t.stride()[1:] == (shape[2], 1)):
-        return
+    apart (a slice of a fused projection).  Returns that stride."""
+    n, heads, d = shape
+    if t.dtype is dtype and t.shape == shape and t.get_device() == _current_device():
+        row, head, one = t.stride()
+        if one == 1 and (head == d or heads == 1):
+            return row if n > 1 else heads * d
     if t.dtype != dtype:
         raise TypeError("%s: dtype %s, want %s" % (name, t.dtype, dtype))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s: shape %s, want %s" % (name, tuple(t.shape), tuple(shape)))
-    if (not t.is_cuda or t.get_device() != _current_device()
-            or (t.numel() and t.stride()[1:] != (shape[2], 1) and not t[0].is_contiguous())):
-        raise ValueError("%s: must be a CUDA tensor with dense rows on the current device" % name)
-
-
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    if t.numel() == 0 and t.is_cuda:
+        return heads * d
+    raise ValueError("%s: must be a CUDA tensor with dense rows on the current device" % name)
 
 
 def version():
@@ -218,18 +216,19 @@ class Rope:
         """x [rows, heads, head_dim] (bf16 or fp32, rows at a stride) rotated by
         int32 positions [rows], or back with inverse=True, which is the
         gradient (msa_rope_apply).  out may be x."""
-        if x.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError("x: dtype %s, want bfloat16 or float32" % x.dtype)
-        n, heads, d = x.shape
-        _need_rows(x, x.dtype, (n, heads, d), "x")
+        dtype, shape = x.dtype, x.shape
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise TypeError("x: dtype %s, want bfloat16 or float32" % dtype)
+        n, heads, d = shape
+        x_stride = _rows(x, dtype, shape, "x")
         _need(positions, torch.int32, (n,), "positions")
         if out is None:
-            out = torch.empty((n, heads, d), dtype=x.dtype, device=x.device)
+            out, out_stride = torch.empty(shape, dtype=dtype, device=x.device), heads * d
         else:
-            _need_rows(out, x.dtype, (n, heads, d), "out")
-        _check(_lib.msa_rope_apply(self._h, _ptr(x), _row_stride(x), _ptr(positions), n, heads, d,
-                                   int(x.dtype == torch.float32), int(inverse), _ptr(out), _row_stride(out),
-                                   _stream(stream)), "msa_rope_apply")
+            out_stride = _rows(out, dtype, shape, "out")
+        _check(_lib.msa_rope_apply(self._h, x.data_ptr(), x_stride, positions.data_ptr(), n, heads, d,
+                                   dtype is torch.float32, inverse, out.data_ptr(), out_stride, _stream(stream)),
+               "msa_rope_apply")
         return out
 
 
@@ -281,8 +280,8 @@ class Plan:
         """The batch's new K and V rows [total_q, Hkv, d] bf16 into the cache
         (msa_kv_append), K rotated by `rope` at int32 positions [total_q], or at
         its key positions; quantised by the plan's kv_dtype."""
-        _need_rows(k, torch.bfloat16, (self.total_q, self.hkv, self.d), "k")
-        _need_rows(v, torch.bfloat16, (self.total_q, self.hkv, self.d), "v")
+        k_stride = _rows(k, torch.bfloat16, (self.total_q, self.hkv, self.d), "k")
+        v_stride = _rows(v, torch.bfloat16, (self.total_q, self.hkv, self.d), "v")
         kvt = torch.bfloat16 if self.kv_dtype == "bf16" else torch.float8_e4m3fn
         _need(k_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "k_pages")
         _need(v_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "v_pages")
@@ -290,16 +289,16 @@ class Plan:
         self._need_scales(k_scale, v_scale)
         if positions is not None:
             _need(positions, torch.int32, (self.total_q,), "positions")
-        _check(_lib.msa_kv_append(self._h, rope and rope._h, _ptr(positions), _ptr(k), _row_stride(k), _ptr(v),
-                                  _row_stride(v), _ptr(kv_indices), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                                  _ptr(v_scale), _stream(stream)), "msa_kv_append")
+        _check(_lib.msa_kv_append(self._h, rope and rope._h, _ptr(positions), k.data_ptr(), k_stride, v.data_ptr(),
+                                  v_stride, kv_indices.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                  _ptr(k_scale), _ptr(v_scale), _stream(stream)), "msa_kv_append")
 
     def pk_append(self, pk, kv_indices, pk_pages=None, pk_pages_e4m3=None, pk_scale=None, pk_codes=None,
                   pk_block_scales=None, pk_global_scale=None, rope=None, positions=None, stream=None):
         """The batch's new proxy K rows [total_q, 1, dp] bf16 into the pools given
         (msa_pk_append): bf16, e4m3 with pk_scale, NVFP4 with its scales."""
         pool = (self.num_pages, 1, 128)
-        _need_rows(pk, torch.bfloat16, (self.total_q, 1, self.dp), "pk")
+        pk_stride = _rows(pk, torch.bfloat16, (self.total_q, 1, self.dp), "pk")
         _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
         for t, dtype, shape, name in (
                 (pk_pages, torch.bfloat16, pool + (self.dp,), "pk_pages"),
@@ -311,7 +310,7 @@ class Plan:
                 (positions, torch.int32, (self.total_q,), "positions")):
             if t is not None:
                 _need(t, dtype, shape, name)
-        _check(_lib.msa_pk_append(self._h, rope and rope._h, _ptr(positions), _ptr(pk), _row_stride(pk),
+        _check(_lib.msa_pk_append(self._h, rope and rope._h, _ptr(positions), _ptr(pk), pk_stride,
                                   _ptr(kv_indices), _ptr(pk_pages), _ptr(pk_pages_e4m3), _ptr(pk_scale),
                                   _ptr(pk_codes), _ptr(pk_block_scales), _ptr(pk_global_scale), _stream(stream)),
                "msa_pk_append")
