@@ -73,7 +73,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t v, float f) {
 // memory and serve all heads of the CTA (with eight angles computed for every
 // 16 values the call took 67 us, half of it issuing instructions), and the
 // next head's rows are on their way while this one's amax is reduced.  32768 rows, 8 heads, d
-// 128 (201 MB): 40.2 us, 5.0 TB/s.
+// 128 (201 MB): 42.6 us, 4.7 TB/s (40.2 with the shorter angle polynomials, whose
+// last bits change a few codes).
 enum RopeKind { kPlain, kHalf, kInterleaved };
 
 struct KvAppendArgs {
@@ -92,7 +93,7 @@ struct KvAppendArgs {
 template <int D, msa_kv_dtype KIND, RopeKind ROPE>
 __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendArgs& a, int which) {
   constexpr int kChunks = D / 16, kRows = kKvThreads / kChunks, kPasses = 128 / kRows;
-  extern __shared__ float4 angles[];  // [row][4][kChunks]: (cos, sin) of pairs 2 j and 2 j + 1 of a chunk
+  extern __shared__ float4 angles[];  // [row][4][kChunks]: cos, cos, sin, sin of pairs 2 j and 2 j + 1 of a chunk
   __shared__ uint32_t warp_max[2][kKvThreads / 32];
   const AppendUnit u = a.units[blockIdx.x];
   const int64_t page = a.kv_indices[u.entry];
@@ -114,7 +115,7 @@ __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendAr
         raw[p][1] = *reinterpret_cast<const uint4*>(at + ch.hi);
       }
   };
-  load(h0);
+  if (ROPE == kPlain) load(h0);
   if (page < 0 || page >= a.num_pages) {
     if (threadIdx.x == 0) atomicOr(a.err, kErrDeviceCheck);
     return;
@@ -128,10 +129,11 @@ __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendAr
         rope_angles(tab, c, a.positions ? a.positions[u.row + i] : u.pos + i, false, cs, sn);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          angles[(i * 4 + j) * kChunks + c] = make_float4(cs[2 * j], sn[2 * j], cs[2 * j + 1], sn[2 * j + 1]);
+          angles[(i * 4 + j) * kChunks + c] = make_float4(cs[2 * j], cs[2 * j + 1], sn[2 * j], sn[2 * j + 1]);
       }
     }
   }  // every thread reads back what it wrote
+  if (ROPE != kPlain) load(h0);  // not before: the angles take the registers
   for (int h = h0; h < h1; ++h) {
     float x[kPasses][16];
     float amax = 0.f;
@@ -371,6 +373,11 @@ __global__ void __launch_bounds__(kPkThreads)
 
 // Gradient pages to rows: dK (rotated back), dV and dpk (rotated back).
 // blockIdx.y: KV heads of K, then of V, then the proxy head.
+//
+// Bound by HBM: 65536 rows, 8 heads of 128, dpk of 64 (1.1 GB) take 167 us, 6.6
+// TB/s.  Each CTA computes its own angles, by the shorter polynomials, as
+// nothing is quantised here; sharing them between heads, as the appends do,
+// costs the occupancy that keeps the loads coming (180-190 us).
 struct GradSet {
   const float* pages;
   float* rows;
@@ -410,7 +417,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (ch.rotated) {
       float cs[8], sn[8];
-      rope_angles(tab, c, positions ? positions[u.row + i] : u.pos + i, true, cs, sn);
+      rope_angles<false>(tab, c, positions ? positions[u.row + i] : u.pos + i, true, cs, sn);
       rope_rotate(tab.interleaved != 0, cs, sn, x);
     }
     float* dst = gs.rows + (static_cast<int64_t>(u.row + i) * gs.heads + h) * gs.d;
@@ -449,7 +456,7 @@ msa_status check_rows(const char* fn, const char* name, const void* x, int64_t s
 template <int D, msa_kv_dtype KIND>
 cudaError_t launch_kv(const msa_plan_s* p, const RopeTable& tab, KvAppendArgs a, cudaStream_t st) {
   // heads a CTA: the angles are shared while three CTAs are left for an SM
-  // (32768 rows, 8 heads, d 128: 4 heads a CTA 42.7 us, 8 40.2)
+  // (32768 rows, 8 heads, d 128, shorter angles: 4 heads a CTA 42.7 us, 8 40.2)
   int hpc = 1;
   while (hpc < 8 && int64_t(p->n_append_units) * ((p->hkv + 2 * hpc - 1) / (2 * hpc)) * 2 >= 3 * p->num_sms) hpc *= 2;
   a.heads_per_cta = hpc;

@@ -13,8 +13,8 @@
 // once for all heads; a thread rotates 16 values at a time (both members of
 // eight pairs) and has the loads of kBatch such chunks in flight before the
 // first store, which the compiler cannot move them across.
-// bf16, 32768 rows x 32 heads of 128 (0.54 GB): 81 us, 6.6 TB/s (a copy of as much takes 82); fp32, 65536 x 32
-// (2.1 GB): 309 us, 6.9 TB/s.
+// bf16, 32768 rows x 32 heads of 128 (0.54 GB): 85 us, 6.3 TB/s (a copy of as
+// much takes 82); fp32, 65536 x 32 (2.1 GB): 310 us, 6.9 TB/s.
 #include <math.h>
 
 #include <algorithm>
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kRopeThreads)
                 int64_t out_stride) {
   pdl_wait();
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
-  extern __shared__ float4 angles[];  // [row][4][rot / 16]: (cos, sin) of pairs 2 j and 2 j + 1 of a chunk
+  extern __shared__ float4 angles[];  // [row][4][rot / 16]: cos, cos, sin, sin of pairs 2 j and 2 j + 1 of a chunk
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * cta_rows;
   const int rows = static_cast<int>(min(static_cast<int64_t>(cta_rows), n_rows - row0));
   const int h0 = blockIdx.y * cta_heads, nh = min(cta_heads, heads - h0);
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         rope_angles(tab, ac, pos[row0 + ar], inverse, cs, sn);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          angles[(ar * 4 + k) * turning + ac] = make_float4(cs[2 * k], sn[2 * k], cs[2 * k + 1], sn[2 * k + 1]);
+          angles[(ar * 4 + k) * turning + ac] = make_float4(cs[2 * k], cs[2 * k + 1], sn[2 * k], sn[2 * k + 1]);
       }
       __syncthreads();
       first = false;
@@ -93,7 +93,7 @@ msa_status launch_rope(const RopeTable& tab, const void* x, int64_t xs, const in
                        int32_t heads, int32_t d, bool inverse, void* out, int64_t os, int num_sms, cudaStream_t st) {
   // a CTA's items: kItems chunks a thread (512 bytes read), of whole rows where
   // a row has no more; fewer where that leaves SMs without a CTA.  bf16, 32768
-  // rows x 32 heads: 4 items 88 us, 8 83, 16 81, 32 86; fp32, 65536 x 32: 4 304,
+  // rows x 32 heads (shorter angle polynomials): 4 items 88 us, 8 83, 16 81, 32 86; fp32, 65536 x 32: 4 304,
   // 8 309, 16 316, 32 325.  4096 x 8: a CTA an SM 5.2 us, 4 an SM 6.8
   const int64_t chunks = d / 16, total = n_rows * heads * chunks;
   constexpr int kItems = 32 / sizeof(T);
@@ -159,7 +159,9 @@ msa_status msa_rope_create(int32_t rotary_dim, msa_rope_layout layout, double ba
     }
     r->table.turns[i] = static_cast<uint64_t>(ldexp(turns, 64));  // turns <= 1 / (2 pi)
   }
-  r->table.mscale = scaling == MSA_ROPE_YARN && factor > 1.0 ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.f;
+  const double m = scaling == MSA_ROPE_YARN && factor > 1.0 ? 0.1 * log(factor) + 1.0 : 1.0;
+  r->table.mscale = static_cast<float>(m);
+  r->table.mscale_lo = static_cast<float>(m - static_cast<double>(r->table.mscale));
   r->table.rot = rotary_dim;
   r->table.interleaved = layout == MSA_ROPE_INTERLEAVED;
   *out = r;

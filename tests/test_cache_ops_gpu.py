@@ -104,6 +104,28 @@ def test_rope_in_place_slices_and_streams(cuda_dev):
     assert rope.apply(q0[:0], pos[:0]).shape == (0, 4, 64)
 
 
+@pytest.mark.parametrize("layout, inverse, scaling", [("half", False, {}), ("interleaved", True, {}),
+                                                      ("half", True, dict(scaling="yarn", factor=8.0, original_len=4096))])
+def test_rope_has_the_bits_of_elementwise_arithmetic(cuda_dev, layout, inverse, scaling):
+    """cos and sin from fp64, products and sums rounded in fp32: equal but where a
+    cosine (1 of 200) or a sine (1 of 40) is the other neighbour, and there by the
+    rounding of a value and of two products."""
+    n, rot = 4000, 64
+    gen = torch.Generator(device=cuda_dev).manual_seed(4)
+    x = torch.randn((n, 2, rot), generator=gen, device=cuda_dev)
+    pos = torch.randint(0, 200000, (n,), generator=gen, device=cuda_dev, dtype=torch.int32)
+    got = _rope(rot, layout, **scaling).apply(x, pos, inverse=inverse)
+    f, m = O.rope_freqs(rot, **scaling)
+    t = np.outer(pos.cpu().numpy(), f / (2 * np.pi))
+    t = (t - np.floor(t)) * 2 * np.pi
+    c, s = (torch.from_numpy((y * m).astype(np.float32)).to(cuda_dev)[:, None] for y in (np.cos(t), np.sin(t)))
+    s = -s if inverse else s
+    a, b = (x[..., :32], x[..., 32:]) if layout == "half" else (x[..., 0::2], x[..., 1::2])
+    p, q = a * c - b * s, b * c + a * s
+    want = torch.cat((p, q), -1) if layout == "half" else torch.stack((p, q), -1).flatten(-2)
+    assert (got != want).float().mean() <= 0.05 and (got - want).abs().max() <= 1e-6 * 5
+
+
 def test_rope_inverse_is_the_gradient(cuda_dev):
     """<rope(x), y> = <x, inverse(y)>, and central differences of it."""
     rope = _rope(64, "interleaved", scaling="yarn", factor=4.0, original_len=1024)
