@@ -38,13 +38,13 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 
 # dram bytes of one attention-forward launch at the 32K prefill workload from
 # an ncu capture, valid only for the kernel source it was taken on.
-# Captured on S=16384 (15424 selected tile-blocks: 245.7 MB read + 107.8 MB
+# Captured on S=16384 (15424 selected tile-blocks: 245.5 MB read + 107.8 MB
 # written) and scaled by selected tile-blocks to the S=32768 launch (31808).
 NCU_TRAFFIC = {
     # (DRAM bytes read + written) of one launch of the small S=16384 capture and the
     # (tile, group, block) selections it processed; scaled to a launch by selections.
-    "attn_fwd.cu": {"src": "61945f29ac0760d2", "bytes": 245654528 + 107804928, "sel": 15424},
-    "attn_fwd.cu:fp8": {"src": "61945f29ac0760d2", "bytes": 181007616 + 101192960, "sel": 15424},
+    "attn_fwd.cu": {"src": "e6fdb51d31a1ef54", "bytes": 245467648 + 107834368, "sel": 15424},
+    "attn_fwd.cu:fp8": {"src": "e6fdb51d31a1ef54", "bytes": 180965888 + 101286144, "sel": 15424},
 }
 
 

@@ -956,20 +956,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // least so far, and the last, partial round to the CTAs with the least of all
 // (which become the first columns).  A unit visits at most min(num_valid_pages,
 // topk) blocks; a block step of one head takes about 0.8 of one of two, and a
-// unit about a step besides.  160 units (6 ragged sequences, three heads a
-// group) on 152 SMs: 54 -> 44 us.
-static void balance_units(const msa_plan_s* p, std::vector<AttnUnit>& us) {
-  const int n = static_cast<int>(us.size()), grid = std::min(n, p->num_sms);
-  if (grid == 0) return;
+// unit about a step besides.  176 units (6 ragged sequences, three heads a
+// group) on 152 SMs: 54 -> 44 us.  The lightest n_split units stay at the end
+// for a launch of their own.
+static void balance_units(const msa_plan_s* p, std::vector<AttnUnit>& us, int n_split = 0) {
+  const int n = static_cast<int>(us.size()) - n_split, grid = std::min(n, p->num_sms);
   auto cost = [&](const AttnUnit& u) {
     return int64_t(std::min(p->tiles[u.tile].nvp, p->topk) + 1) * (u.nh == 2 ? 5 : 4);
   };
   std::stable_sort(us.begin(), us.end(), [&](const AttnUnit& a, const AttnUnit& b) { return cost(a) > cost(b); });
+  if (grid == 0) return;
   std::vector<int64_t> load(grid, 0);
   std::vector<int> col(grid);
   for (int c = 0; c < grid; ++c) col[c] = c;
-  std::vector<AttnUnit> out(us.size());
-  std::vector<int> place(us.size());  // column of each unit
+  std::vector<AttnUnit> out(us);
+  std::vector<int> place(n);  // column of each unit
   auto by_load = [&](int a, int b) { return load[a] < load[b]; };
   for (int base = 0; base < n; base += grid) {
     std::stable_sort(col.begin(), col.end(), by_load);
@@ -985,15 +986,18 @@ static void balance_units(const msa_plan_s* p, std::vector<AttnUnit>& us) {
   us.swap(out);
 }
 
-// Heads a unit (returned) and CTAs a unit (p->attn_parts).
+// Heads a unit (returned), units to split (p->attn_split) and the CTAs that
+// share each of those (p->attn_parts).
 //
 // Two heads share a block's K and V and overlap each other's softmax; with an
 // SM for every head, a head alone is done sooner (512 rows x 32 heads, topk 16:
 // e4m3 38.0 us in pairs, 32.6 alone; bf16 34.4, 28.8).  Block-scaled plans also
-// share a unit's blocks out over a cluster while each of its CTAs has an SM.  A
-// block step takes about 1.65 us for a head and 1.78 for two, a unit 6 besides
-// and the merge 3.  Clusters of 8 are not placed as densely as the SMs would
-// allow: 16 of them took two waves, 12 one.  Measured (us; heads a unit / parts):
+// share a unit's blocks out over a cluster while each of its CTAs has an SM: all
+// units, or those that a last, short round would be left with, in a launch of
+// their own.  A block step takes about 1.65 us for a head and 1.78 for two, a
+// unit 6 besides, the merge 3 and a second launch 10.  Clusters of 8 are not
+// placed as densely as the SMs would allow: 16 of them took two waves, 12 one.
+// Measured (us; heads a unit / parts):
 //   rows x heads, blocks     1/1    1/2    1/4    1/8    2/1    2/2    2/4
 //     128 x 32, 16          33.8   24.4  [17.9]  41.7   38.3   29.2   21.1
 //     512 x 32, 16          34.4   48.5   67.5    126   39.0  [30.1]  42.9
@@ -1001,22 +1005,29 @@ static void balance_units(const msa_plan_s* p, std::vector<AttnUnit>& us) {
 //     300 x 4, 24           55.0   33.5   21.3  [16.4]  58.7   36.5   24.6
 //     700 x 12, 9           24.5  [20.0]  31.3   69.2   27.7   24.1   30.9
 //     100 x 8, 64            139   76.7   43.6  [27.3]   144   81.3   47.2
+// 160 pairs on 152 SMs, the last 8 split: 16 blocks 84.5 -> 68.0, 64 292 -> 196.
 static int unit_shape(msa_plan_s* p) {
-  const int grp = p->hq / p->hp;
+  const int grp = p->hq / p->hp, sms = p->num_sms;
+  p->attn_split = 0;
   p->attn_parts = 1;
-  if (p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) return int64_t(p->n_tiles) * p->hq <= p->num_sms ? 1 : 2;
+  if (p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) return int64_t(p->n_tiles) * p->hq <= sms ? 1 : 2;
   int blocks = 1, best_heads = 2;
   for (const TileInfo& t : p->tiles) blocks = std::max(blocks, std::min(t.nvp, p->topk));
   double best = 1e30;
-  for (int heads = 2; heads >= 1; --heads)
-    for (int parts = 1; parts <= 8 && parts <= blocks; parts *= 2) {
-      const int64_t units = int64_t(p->n_tiles) * p->hp * ((grp + heads - 1) / heads);
-      if (parts > 1 && units * parts > (parts < 8 ? p->num_sms - 8 : p->num_sms * 2 / 3)) break;
-      const int64_t rounds = (units * parts + p->num_sms - 1) / p->num_sms;
-      double us = rounds * ((blocks + parts - 1) / parts * (heads == 2 ? 1.78 : 1.65) + 6) + (parts > 1 ? 3 : 0);
-      if (heads == 1 && rounds > 1) us *= 1.1;  // an odd head beside pairs fills the rounds better
-      if (us < best) best = us, best_heads = heads, p->attn_parts = parts;
-    }
+  for (int heads = 2; heads >= 1; --heads) {
+    const int64_t units = int64_t(p->n_tiles) * p->hp * ((grp + heads - 1) / heads), rounds = units / sms;
+    const double step = heads == 2 ? 1.78 : 1.65, unit = blocks * step + 6;
+    const int64_t rest = units - rounds * sms;
+    auto take = [&](double us, int64_t split, int parts) {
+      if (us >= best) return;
+      best = us, best_heads = heads, p->attn_split = static_cast<int32_t>(split), p->attn_parts = parts;
+    };
+    // an odd head beside pairs fills the rounds better than heads alone
+    take((rounds + (rest > 0)) * unit * (heads == 1 && units > sms ? 1.1 : 1.0), 0, 1);
+    for (int parts = 2; parts <= 8 && parts <= blocks && rest > 0; parts *= 2)
+      if (rest * parts <= (parts < 8 ? sms - 8 : sms * 2 / 3))
+        take(rounds * unit + (rounds > 0 ? 10 : 0) + (blocks + parts - 1) / parts * step + 9, rest, parts);
+  }
   return best_heads;
 }
 
@@ -1029,7 +1040,7 @@ void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   for (int t = 0; t < p->n_tiles; ++t)
     for (int g = 0; g < p->hp; ++g)
       for (int h = 0; h < grp; h += pair) us.push_back(AttnUnit{t, g, g * grp + h, std::min(pair, grp - h)});
-  balance_units(p, us);
+  balance_units(p, us, p->attn_split);
   p->attn_units_off = static_cast<int64_t>(aux.size());
   p->n_attn_units = static_cast<int32_t>(us.size());
   const int32_t* raw = reinterpret_cast<const int32_t*>(us.data());
@@ -1134,10 +1145,14 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
   if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK) {
     const auto launch = p->d == 128 ? launch_attn_variant<128, false, true, true>
                                     : launch_attn_variant<64, false, true, true>;
-    const int parts = p->attn_parts;
-    e = launch(parts > 1 ? dim3(p->n_attn_units * parts) : grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units,
-               p->tiles_d, idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale,
-               p->err_d, parts);
+    const int whole = p->n_attn_units - p->attn_split;
+    auto run = [&](int ctas, const AttnUnit* first, int n, int parts) {
+      return launch(dim3(ctas), st, qm, km, vm, om, p->topk, first, n, p->tiles_d, idx, kv_indices, p->num_pages, o, lse,
+                    p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d, parts);
+    };
+    e = whole > 0 ? run(std::min(whole, p->num_sms), units, whole, 1) : cudaSuccess;
+    if (e == cudaSuccess && p->attn_split > 0)
+      e = run(p->attn_split * p->attn_parts, units + whole, p->attn_split, p->attn_parts);
   } else if (fp8)
     e = launch_attn_variant<128, false, true>(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units, p->tiles_d,
                                               idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp, kv_div, scale_log2,

@@ -96,7 +96,8 @@ struct msa_plan_s {
   void* fused_topk_d = nullptr;      // msa_proxy_topk scratch: per-row counters, chunk candidates
   int64_t attn_units_off = 0;        // prefill attention work units
   int32_t n_attn_units = 0;
-  int32_t attn_parts = 1;            // CTAs that share a unit's blocks (block-scaled plans)
+  int32_t attn_split = 0;            // of them, the last ones that clusters share (block-scaled plans)
+  int32_t attn_parts = 1;            // CTAs that share each of those
   int64_t proxy_attn_units_off = 0;  // backward proxy softmax work units
   int32_t n_proxy_attn_units = 0;
   int64_t heavy_tiles_off = 0;       // tile ids, most cached blocks first (the backward's dq order)

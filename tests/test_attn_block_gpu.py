@@ -83,6 +83,9 @@ CASES = [
     _case("parts 4", [5, 3, 128], [9000, 130, 2000], 12, 4, 4, 9, page_perm_seed=3),
     _case("parts 2", [700], [9000], 12, 4, 4, 9, page_perm_seed=3),
     _case("parts 8 topk 200", [100], [90000], 8, 1, 1, 200, page_perm_seed=3),
+    # a short last round, split in a launch of its own
+    _case("split tail", [9, 20, 3, 31, 2, 17, 5, 26, 4, 12], [4000, 2100, 1700, 2500, 1999, 60, 1600, 3000, 1920, 130], 32,
+          8, 8, 14, page_perm_seed=3),
     # head_dim 64
     _case("d64 parts 8", [130], [9000], 6, 1, 2, 24, d=64, page_perm_seed=3),
     _case("d64 decode one key", [1], [1], 8, 1, 1, 4, d=64),
