@@ -56,6 +56,33 @@ __device__ __forceinline__ int block_exp(float amax) {
   return min(max(e, kMinExp), kMaxExp);
 }
 
+// x0 / s and x1 / s to nearest, given the nearest reciprocal of s: one residual
+// step on x * inv (Markstein 1990).  Quotients that saturate, infinities and NaN
+// are left as the product has them.
+__device__ __forceinline__ void quotient2(float& x0, float& x1, float s, float inv) {
+  const F2 x{x0, x1}, q = mul2(x, inv), r = fma2(fma2(q, -s, x), inv, q);
+  x0 = fabsf(q.x) < 512.f ? r.x : q.x;
+  x1 = fabsf(q.y) < 512.f ? r.y : q.y;
+}
+
+// Sixteen consecutive values as their even ones and their odd ones, and back:
+// interleaved pairs then rotate, and pack into bytes, as halves do.
+__device__ __forceinline__ void unpack_pairs(uint4 a, uint4 b, float (&x)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = __uint_as_float(w[i] << 16);
+    x[8 + i] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void pack_pairs(float (&x)[16]) {
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[2 * i] = x[i], y[2 * i + 1] = x[8 + i];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = y[i];
+}
+
 // four e4m3 codes times a factor, rounded to e4m3 again
 __device__ __forceinline__ uint32_t rescale4(uint32_t v, float f) {
   const uint32_t a = e4m3x2_to_f16x2(v), b = e4m3x2_to_f16x2(v >> 16);
@@ -141,12 +168,14 @@ __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendAr
     for (int p = 0; p < kPasses; ++p) {
       const int i = p * kRows + r0;
       if (i < n) {
-        unpack8(raw[p][0], x[p]);
-        unpack8(raw[p][1], x[p] + 8);
+        if (ROPE == kInterleaved)
+          unpack_pairs(raw[p][0], raw[p][1], x[p]);
+        else
+          unpack8(raw[p][0], x[p]), unpack8(raw[p][1], x[p] + 8);
         if (ROPE != kPlain && ch.rotated) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            rope_rotate2(ROPE == kInterleaved, j, angles[(i * 4 + j) * kChunks + c], x[p]);
+            rope_rotate2(false, j, angles[(i * 4 + j) * kChunks + c], x[p]);
         }
         if (KIND == MSA_KV_FP8_E4M3_BLOCK) {
 #pragma unroll
@@ -162,6 +191,7 @@ __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendAr
       for (int p = 0; p < kPasses; ++p) {
         const int i = p * kRows + r0;
         if (i < n) {
+          if (ROPE == kInterleaved) pack_pairs(x[p]);
           store8(dst + i * D + ch.lo, x[p]);
           store8(dst + i * D + ch.hi, x[p] + 8);
         }
@@ -169,7 +199,7 @@ __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendAr
       continue;
     }
     uint8_t* pool = static_cast<uint8_t*>(a.pages[which]) + head_row * D;
-    float by;  // the codes are x * by (block) or x / by (one scale a head)
+    float by, inv = 0.f;  // the codes are x * by (block) or x / by (one scale a head)
     if (KIND == MSA_KV_FP8_E4M3_BLOCK) {
       float* sp = a.scale[which] + page * a.hkv + h;
       const float old = slot0 > 0 ? *sp : 0.f;  // rows came before: the scale only grows
@@ -215,6 +245,7 @@ __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendAr
       by = pow2(-e);
     } else {
       by = a.scale[which][h];
+      inv = __frcp_rn(by);
     }
     uint8_t* dst = pool + slot0 * D;
 #pragma unroll
@@ -223,13 +254,12 @@ __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendAr
       if (i < n) {
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-          if (KIND == MSA_KV_FP8_E4M3_BLOCK) {
+          if (KIND == MSA_KV_FP8_E4M3_BLOCK)
             fmul2v(x[p][e], x[p][e + 1], x[p][e], x[p][e + 1], by, by);
-          } else {
-            x[p][e] = __fdiv_rn(x[p][e], by);
-            x[p][e + 1] = __fdiv_rn(x[p][e + 1], by);
-          }
+          else
+            quotient2(x[p][e], x[p][e + 1], by, inv);
         }
+        if (ROPE == kInterleaved) pack_pairs(x[p]);
         *reinterpret_cast<uint2*>(dst + i * D + ch.lo) = e4m3x8(x[p]);
         *reinterpret_cast<uint2*>(dst + i * D + ch.hi) = e4m3x8(x[p] + 8);
       }
@@ -346,9 +376,9 @@ __global__ void __launch_bounds__(kPkThreads)
       store8(&rows[r][ch.hi], x + 8);
     }
     if (pools.e4m3) {
-      const float scale = *pools.e4m3_scale;
+      const float scale = *pools.e4m3_scale, inv = __frcp_rn(scale);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = __fdiv_rn(x[e], scale);
+      for (int e = 0; e < 16; e += 2) quotient2(x[e], x[e + 1], scale, inv);
       *reinterpret_cast<uint2*>(pools.e4m3 + row * DP + ch.lo) = e4m3x8(x);
       *reinterpret_cast<uint2*>(pools.e4m3 + row * DP + ch.hi) = e4m3x8(x + 8);
     }
