@@ -93,7 +93,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 // out-of-range entries dropped) and row[cap] (their first K/V tensor-map
 // row), cap >= topk.
 struct UnitHdr {
-  int32_t n, nh, h0, q_begin, rows, pos0, g, kv_len, pad[8];
+  int32_t n, nh, h0, q_begin, rows, pos0, g, kv_len, h_end, pad[7];
 };
 constexpr int kListSlots = 2;
 constexpr int kScaleRing = 128;  // blocks; written up to 64 ahead of the one being loaded
@@ -102,7 +102,7 @@ constexpr int kHdrInts = 16;
 // A head's row statistics at the end of a unit, from the softmax warps to
 // the epilogue warps (two buffers per head, alternating by unit).
 struct UnitStats {
-  int32_t n, active, ok, h0, q_begin, rows, g, pad[9];
+  int32_t n, active, ok, h0, q_begin, rows, g, h_end, pad[8];
   float m[128], l[128];
 };
 
@@ -140,8 +140,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int32_t* __restrict__ kv_indices, int64_t num_pages, __nv_bfloat16* __restrict__ out,
                     float* __restrict__ lse, int32_t hq, int32_t hsel, int32_t kv_div, int32_t topk,
                     float scale_log2, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
-                    int32_t parts, uint32_t* err) {
+                    int32_t parts, int32_t pack_log2, uint32_t* err) {
   pdl_wait();
+  // kBlk: a tile of few rows has 2^lg heads side by side in the 128 rows of a
+  // product, row r being query row r >> lg of head r % 2^lg; "head" 0 and 1 of a
+  // unit are then such groups
+  const int lg = kBlk ? pack_log2 : 0;
   // kSplit (few units): a unit's blocks are shared out over the `parts` CTAs of
   // a cluster, which do nothing else and merge at the end
   const int part = kSplit ? blockIdx.x % parts : 0;
@@ -366,6 +370,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ls.pos0 = tl.pos0;
         ls.g = u.g / kv_div;
         ls.kv_len = tl.kv_len;
+        ls.h_end = (u.g + 1) * (hq / hsel);
       }
       __syncwarp();
       if (lane == 0) {
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           mbar_expect_tx(q_full, u.nh * L::kTileBytes);
           for (int h = 0; h < u.nh; ++h)
             for (int c = 0; c < kChunks; ++c)
-              tma_load_3d(q_s + h * L::kTileBytes + c * 16384, &q_map, q_full, c * 64, u.h0 + h, tl.q_begin);
+              tma_load_3d(q_s + h * L::kTileBytes + c * 16384, &q_map, q_full, c * 64, u.h0 + (h << lg), tl.q_begin);
         }
       }
       constexpr int kStep = kBlk ? 32 : 1 << 30;  // kBlk: the lanes come together every 32 blocks to fetch scales
@@ -546,8 +551,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       float sl2 = kFp8 && !kBlk ? scale_log2 * k_scale[ls.g] : scale_log2;
       float log2_vs = 0.f, inv_vs = 1.f;
       const bool active = ok && h < nh;
-      const bool row_ok = r < rows;
-      const int qpos = pos0 + r;
+      const bool row_ok = (r >> lg) < rows;
+      const int qpos = pos0 + (r >> lg);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; active && ok && i < n; ++i) {
         if (kBlk) {
@@ -644,6 +649,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         st.q_begin = ls.q_begin;
         st.rows = rows;
         st.g = ls.g;
+        st.h_end = ls.h_end;
       }
       if (h < nh) ch += n;
       kv_it += n;
@@ -676,7 +682,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const UnitStats& st = stats[h * 2 + b];
         if (ok) ok = mbar_wait_inl(stat_full + h * 2 + b, (k >> 1) & 1, err);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        const int n = st.n, rows = st.rows, q_begin = st.q_begin, h0 = st.h0;
+        const int n = st.n, rows = st.rows, q_begin = st.q_begin, h0 = st.h0, st_h_end = st.h_end;
         const bool active = ok && st.active != 0;
         const bool unit_ok = ok && st.ok != 0;
         const float m = st.m[r], l = st.l[r];
@@ -694,8 +700,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc_fence_after();
         const uint32_t o_addr = tmem + lane_base + 256 + h * D;
         const float inv_l = l > 0.f ? o_scale / l : 0.f;
-        const bool row_ok = r < rows;
-        const int64_t orow = static_cast<int64_t>(q_begin + r) * hq + h0 + h;
+        const int head = h0 + (h << lg) + (r & ((1 << lg) - 1));
+        const bool row_ok = (r >> lg) < rows && (!kBlk || head < st_h_end);
+        const int64_t orow = static_cast<int64_t>(q_begin + (r >> lg)) * hq + head;
         const bool staged = kStageO && rows == 128;
         uint8_t* const ob = smem + L::kOOff + r * 128;
         uint4* const dst = reinterpret_cast<uint4*>(out + orow * D);
@@ -899,7 +906,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       constexpr int kThreads = 32 * kSoftWarps, kMost = 8;
       const AttnUnit u = units[first_unit()];
       const TileInfo tl = tiles[u.tile];
-      const int mine = (tl.rows - part + parts - 1) / parts;  // rows 1..128, parts <= 8
+      const int mine = ((tl.rows << lg) - part + parts - 1) / parts;  // rows 1..128, parts <= 8
+      const int h_end = (u.g + 1) * (hq / hsel);
+      auto head_of = [&](int h, int r) { return u.h0 + (h << lg) + (r & ((1 << lg) - 1)); };
       float* const wts = reinterpret_cast<float*>(q_s);       // [head * mine + row][kMost]
       for (int e = threadIdx.x; e < u.nh * mine; e += kThreads) {
         const int h = e >= mine, r = part + (e - h * mine) * parts;
@@ -921,8 +930,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
         for (int p = 0; p < kMost; ++p)
           if (p < parts) wts[e * kMost + p] = m[p] * inv;
-        if (lse != nullptr)
-          lse[static_cast<int64_t>(tl.q_begin + r) * hq + u.h0 + h] =
+        if (lse != nullptr && head_of(h, r) < h_end)
+          lse[static_cast<int64_t>(tl.q_begin + (r >> lg)) * hq + head_of(h, r)] =
               sum > 0.f ? (mm + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
@@ -941,8 +950,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const float w = wts[item * kMost + p];
             o.x += op[p].x * w, o.y += op[p].y * w, o.z += op[p].z * w, o.w += op[p].w * w;
           }
-        *reinterpret_cast<uint2*>(out + (static_cast<int64_t>(tl.q_begin + r) * hq + u.h0 + h) * D + 4 * chunk) =
-            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        if (head_of(h, r) < h_end)
+          *reinterpret_cast<uint2*>(out + (static_cast<int64_t>(tl.q_begin + (r >> lg)) * hq + head_of(h, r)) * D +
+                                    4 * chunk) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
       }
     }
     cluster_sync();  // nobody leaves while its part may be read
@@ -1007,12 +1017,26 @@ static void balance_units(const msa_plan_s* p, std::vector<AttnUnit>& us, int n_
 //     100 x 8, 64            139   76.7   43.6  [27.3]   144   81.3   47.2
 // 160 pairs on 152 SMs, the last 8 split: 16 blocks 84.5 -> 68.0, 64 292 -> 196.
 static int unit_shape(msa_plan_s* p) {
-  const int grp = p->hq / p->hp, sms = p->num_sms;
-  p->attn_split = 0;
+  const int sms = p->num_sms;
+  int grp = p->hq / p->hp;
+  p->attn_split = p->attn_pack_log2 = 0;
   p->attn_parts = 1;
   if (p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) return int64_t(p->n_tiles) * p->hq <= sms ? 1 : 2;
-  int blocks = 1, best_heads = 2;
-  for (const TileInfo& t : p->tiles) blocks = std::max(blocks, std::min(t.nvp, p->topk));
+  int blocks = 1, rows = 1, best_heads = 2;
+  for (const TileInfo& t : p->tiles) {
+    blocks = std::max(blocks, std::min(t.nvp, p->topk));
+    rows = std::max(rows, t.rows);
+  }
+  // tiles of few rows: as many heads of a group side by side in the 128 M rows
+  // as fit, so a block step serves them all; otherwise most of each MMA and of
+  // each softmax row would be padding.  Measured (us), a head a tile -> packed:
+  //   32 x 4 rows, 64 / 8 heads, 16 blocks   274 -> 72.7
+  //   64 x 2 rows, 128 / 8 heads, 16 blocks 1037 -> 136
+  //   30 x 9 rows, 128 / 8 heads, 2 blocks   108 -> 22.1
+  //    1 x 4 rows, 64 / 8 heads, 16 blocks  20.3 -> 13.8
+  while (p->attn_pack_log2 < 4 && (rows << (p->attn_pack_log2 + 1)) <= 128 && (2 << p->attn_pack_log2) <= grp)
+    ++p->attn_pack_log2;
+  grp = (grp + (1 << p->attn_pack_log2) - 1) >> p->attn_pack_log2;
   double best = 1e30;
   for (int heads = 2; heads >= 1; --heads) {
     const int64_t units = int64_t(p->n_tiles) * p->hp * ((grp + heads - 1) / heads), rounds = units / sms;
@@ -1036,10 +1060,12 @@ void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   // blocks); with one proxy head per GQA group g is the group
   std::vector<AttnUnit> us;
   const int grp = p->hq / p->hp;
-  const int pair = unit_shape(p);
+  const int pair = unit_shape(p), lg = p->attn_pack_log2;
+  const int slots = (grp + (1 << lg) - 1) >> lg;  // heads, or groups of heads side by side
   for (int t = 0; t < p->n_tiles; ++t)
     for (int g = 0; g < p->hp; ++g)
-      for (int h = 0; h < grp; h += pair) us.push_back(AttnUnit{t, g, g * grp + h, std::min(pair, grp - h)});
+      for (int h = 0; h < slots; h += pair)
+        us.push_back(AttnUnit{t, g, g * grp + (h << lg), std::min(pair, slots - h)});
   balance_units(p, us, p->attn_split);
   p->attn_units_off = static_cast<int64_t>(aux.size());
   p->n_attn_units = static_cast<int32_t>(us.size());
@@ -1084,7 +1110,7 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
                                 int32_t n_units, const TileInfo* tiles, const int32_t* idx,
                                 const int32_t* kv_indices, int64_t num_pages, __nv_bfloat16* o, float* lse,
                                 int32_t hq, int32_t hsel, int32_t kv_div, float scale_log2, const float* k_scale,
-                                const float* v_scale, uint32_t* err, int parts = 1) {
+                                const float* v_scale, uint32_t* err, int parts = 1, int pack_log2 = 0) {
   const int cap = (topk + 3) & ~3;
   if constexpr (kFp8) {
     const int staged = AttnSmem<D, true, kOneKvHead ? 2 : 1, kBlk>::bytes(cap) + 1024;
@@ -1094,7 +1120,7 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, staged);
       return launch_pdl_cluster(kern, grid, 1, dim3(kAttnThreads), staged, st, qm, km, vm, om, cap, units, n_units,
                                 tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
-                                v_scale, 1, err);
+                                v_scale, 1, pack_log2, err);
     }
   }
   const int plain = AttnSmem<D, false, kOneKvHead ? 2 : 1, kBlk>::bytes(kMaxTopk) + 1024;
@@ -1105,14 +1131,15 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plain);
   return launch_pdl_cluster(kern, grid, parts, dim3(kAttnThreads), plain, st, qm, km, vm, om, cap, units, n_units,
                             tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
-                            v_scale, parts, err);
+                            v_scale, parts, pack_log2, err);
 }
 
 // [total_q, heads, D] bf16 rows as 3-D boxes of 64 columns x 1 head x 128 rows, 128-byte swizzle
-bool rows_map(CUtensorMap* m, const void* base, int d, int heads, int64_t total_q) {
+// (pack_log2: 2^pack_log2 heads x 128 / 2^pack_log2 rows)
+bool rows_map(CUtensorMap* m, const void* base, int d, int heads, int64_t total_q, int pack_log2 = 0) {
   const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(heads), static_cast<uint64_t>(total_q)};
   const uint64_t str[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(heads) * d * 2};
-  const uint32_t box[3] = {64, 1, 128};
+  const uint32_t box[3] = {64, 1u << pack_log2, 128u >> pack_log2};
   return encode_tensor_map(m, 3, base, dims, str, box, 1, 128);
 }
 
@@ -1132,7 +1159,7 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
   // bf16: 64-column boxes (128 B rows); e4m3: whole rows of codes
   const uint32_t kbox[2] = {fp8 ? static_cast<uint32_t>(p->d) : 64u, 128};
   const int kswz = fp8 ? p->d : 128;
-  if (!rows_map(&qm, q, p->d, p->hq, p->total_q) || !rows_map(&om, out, p->d, p->hq, p->total_q) ||
+  if (!rows_map(&qm, q, p->d, p->hq, p->total_q, p->attn_pack_log2) || !rows_map(&om, out, p->d, p->hq, p->total_q) ||
       !encode_tensor_map(&km, 2, k_pages, kdims, kstr, kbox, fp8 ? 0 : 1, kswz) ||
       !encode_tensor_map(&vm, 2, v_pages, kdims, kstr, kbox, fp8 ? 0 : 1, kswz))
     return set_error(MSA_ERR_CUDA, "msa_sparse_attn: tensor map encoding failed");
@@ -1148,7 +1175,7 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
     const int whole = p->n_attn_units - p->attn_split;
     auto run = [&](int ctas, const AttnUnit* first, int n, int parts) {
       return launch(dim3(ctas), st, qm, km, vm, om, p->topk, first, n, p->tiles_d, idx, kv_indices, p->num_pages, o, lse,
-                    p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d, parts);
+                    p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d, parts, p->attn_pack_log2);
     };
     e = whole > 0 ? run(std::min(whole, p->num_sms), units, whole, 1) : cudaSuccess;
     if (e == cudaSuccess && p->attn_split > 0)

@@ -84,8 +84,16 @@ CASES = [
     _case("parts 2", [700], [9000], 12, 4, 4, 9, page_perm_seed=3),
     _case("parts 8 topk 200", [100], [90000], 8, 1, 1, 200, page_perm_seed=3),
     # a short last round, split in a launch of its own
-    _case("split tail", [9, 20, 3, 31, 2, 17, 5, 26, 4, 12], [4000, 2100, 1700, 2500, 1999, 60, 1600, 3000, 1920, 130], 32,
+    _case("split tail", [9, 66, 3, 31, 2, 17, 5, 26, 4, 12], [4000, 2100, 1700, 2500, 1999, 60, 1600, 3000, 1920, 130], 32,
           8, 8, 14, page_perm_seed=3),
+    # tiles of few rows, several heads side by side: whole groups, odd ones, two sets a KV head, many units
+    _case("heads by 16", [2, 1, 8], [900, 1500, 33], 64, 2, 2, 5, page_perm_seed=7),
+    _case("heads by 8", [9, 16, 1, 5], [900, 1500, 133, 5], 16, 1, 1, 6, page_perm_seed=7),
+    _case("heads by 2, G=3", [33, 64], [900, 1500], 6, 2, 2, 4, page_perm_seed=7),
+    _case("heads by 4, G=6", [20, 32, 3], [900, 1500, 300], 12, 1, 2, 4, page_perm_seed=7),
+    _case("heads by 8, many units", [int(x) for x in np.random.default_rng(3).integers(1, 10, 40)],
+          [int(x) for x in np.random.default_rng(4).integers(10, 900, 40)], 72, 8, 8, 3, page_perm_seed=7),
+    _case("d64 heads by 4, G=5", [20, 32, 3], [900, 1500, 300], 5, 1, 1, 4, d=64, page_perm_seed=7),
     # head_dim 64
     _case("d64 parts 8", [130], [9000], 6, 1, 2, 24, d=64, page_perm_seed=3),
     _case("d64 decode one key", [1], [1], 8, 1, 1, 4, d=64),
