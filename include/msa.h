@@ -135,7 +135,8 @@ typedef struct msa_rope_s* msa_rope_t;
  *  topk              K >= 1 selected blocks per (tile, proxy head), the
  *                    diagonal block included.
  *  num_pages         physical pages in the K/V page pool (and the proxy K
- *                    pool, which shares page ids).
+ *                    pool, which shares page ids); at most 2^24, and so
+ *                    num_pages * Hkv with MSA_KV_FP8_E4M3_BLOCK.
  *  kv_dtype          element type of k_pages / v_pages.
  *  flags             reserved, pass 0.
  *  stream            stream for the one host->device copy of the tables.

@@ -158,3 +158,15 @@ def test_append_null_refusals(msa):
     assert f.msa_pk_append(None, None, None, None, 0, None, None, None, None, None, None, None, None) == INVALID
     assert f.msa_append_bwd(None, None, None, None, None, None, None, None, None, None, None, None) == INVALID
     f.msa_rope_destroy(None)
+
+
+@pytest.mark.parametrize("pages, hkv", [(2 ** 21 + 1, 8), (2 ** 24, 2), (2 ** 24 // 3 + 1, 3)])
+def test_block_plan_pool_within_32_bit_rows(msa, pages, hkv):
+    """K/V rows are addressed in 32 bits: a pool of more is refused (before any
+    device work)."""
+    with pytest.raises(msa.MsaError) as e:
+        one = (ctypes.c_int32 * 1)(1)
+        h = ctypes.c_void_p()
+        msa._check(msa._lib.msa_plan(one, one, 1, hkv, hkv, hkv, 64, 64, 128, 1, pages, msa.KV_FP8_E4M3_BLOCK, 0, None,
+                                     ctypes.byref(h)), "msa_plan")
+    assert e.value.status == INVALID
