@@ -315,6 +315,65 @@ def test_captured_decode_step(cuda_dev):
     plan.check_errors()
 
 
+def test_calls_overlap_on_two_streams(cuda_dev):
+    """Block-scaled calls use no workspace: two on one plan at once, each the
+    result of a call alone."""
+    for qo, kv in (([1] * 6, [3000, 129, 1000, 77, 2000, 512]), ([300, 5], [2000, 700]), ([4] * 6, [900] * 6)):
+        case = _case("overlap", qo, kv, 32, 2, 2, 12, page_perm_seed=3)
+        inp = synth.make_inputs(case, device=cuda_dev)
+        plan = make_plan(case, inp)
+        idx = torch.from_numpy(random_idx(case, np.random.default_rng(1))).to(cuda_dev)
+        kw = dict(k_scale=inp["k_scale"], v_scale=inp["v_scale"])
+        qs = [inp["q"], -inp["q"]]
+        alone = [plan.sparse_attn(q, inp["k_pages"], inp["v_pages"], inp["kv_indices"], idx, **kw) for q in qs]
+        outs = [[(torch.empty_like(q), torch.empty_like(alone[0][1])) for _ in range(8)] for q in qs]
+        streams = [torch.cuda.Stream() for _ in qs]
+        torch.cuda.synchronize()
+        for i in range(8):
+            for s, q, o in zip(streams, qs, outs):
+                plan.sparse_attn(q, inp["k_pages"], inp["v_pages"], inp["kv_indices"], idx, out=o[i][0], lse=o[i][1],
+                                 stream=s, **kw)
+        torch.cuda.synchronize()
+        plan.check_errors()
+        for a, o in zip(alone, outs):
+            assert all(torch.equal(a[0], x) and torch.equal(a[1], y) for x, y in o)
+
+
+@pytest.mark.parametrize("qo", [1, 60])
+def test_pages_beyond_4_gib(cuda_dev, qo):
+    """The last pages of pools of more than 2^32 bytes: append and attend as on
+    small pools, bit for bit, and the first pages stay as they were."""
+    kv, hkv, n = [500, 300], 8, 33000                     # 131072 bytes a page
+    table = torch.tensor([5, 2, 0, 6, 3, 1, 4], dtype=torch.int32, device=cuda_dev)
+    case = _case("far", [qo] * 2, kv, 32, hkv, hkv, 2)
+    gen = torch.Generator(device=cuda_dev).manual_seed(5)
+    codes = [torch.randint(0, 0x7F, (7, hkv, 128, 128), generator=gen, device=cuda_dev, dtype=torch.uint8) for _ in "kv"]
+    new = [torch.randn((2 * qo, hkv, 128), generator=gen, device=cuda_dev).bfloat16() for _ in "kv"]
+    q = torch.randn((2 * qo, 32, 128), generator=gen, device=cuda_dev).bfloat16()
+    idx = torch.from_numpy(random_idx(case, np.random.default_rng(1))).to(cuda_dev)
+    got = []
+    for pages in (7, n):
+        cache = dict(zip(("k_pages", "v_pages"), (torch.zeros((pages, hkv, 128, 128), dtype=torch.uint8, device=cuda_dev)
+                                                  for _ in "kv")))
+        cache.update(zip(("k_scale", "v_scale"), (torch.full((pages, hkv), 2.0 ** -6, device=cuda_dev) for _ in "kv")))
+        for name, c in zip(("k_pages", "v_pages"), codes):
+            cache[name][-7:] = c
+            cache[name] = cache[name].view(torch.float8_e4m3fn)
+        from block_sparse_long_proxy_gb300 import msa
+        plan = msa.Plan([qo] * 2, kv, 32, hkv, hkv, 128, 64, 2, pages, kv_dtype="e4m3_block")
+        kv_indices = table + (pages - 7)
+        plan.kv_append(*new, cache["k_pages"], cache["v_pages"], kv_indices, k_scale=cache["k_scale"],
+                       v_scale=cache["v_scale"])
+        got.append(plan.sparse_attn(q, cache["k_pages"], cache["v_pages"], kv_indices, idx, k_scale=cache["k_scale"],
+                                    v_scale=cache["v_scale"]))
+        plan.check_errors()
+        got[-1] += tuple(cache[name][-7:].view(torch.uint8).clone() for name in ("k_pages", "v_pages"))
+        if pages > 7:
+            assert not any(cache[name].view(torch.uint8)[:7].any().item() for name in ("k_pages", "v_pages"))
+        del cache
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_prefill_then_decode_over_the_quantised_cache(cuda_dev):
     """The calls as a server makes them: a ragged prefill and then decode steps,
     queries and keys rotated, K and V appended in e4m3 with block scales, proxy

@@ -429,6 +429,46 @@ def test_append_bwd(cuda_dev, lens):
     assert (got2[rows_of] == 0).all() and torch.equal(got2[~rows_of], got[0][~rows_of])
 
 
+@pytest.mark.parametrize("call", ["bf16", "proxy", "bwd"])
+def test_append_pages_beyond_4_gib(cuda_dev, call):
+    """The last pages of pools of more than 2^32 bytes, bit for bit as on small
+    pools; the first pages stay as they were."""
+    from block_sparse_long_proxy_gb300 import msa
+    hkv, n = 8, {"bf16": 17000, "proxy": 263000, "bwd": 8500}[call]
+    gen = torch.Generator(device=cuda_dev).manual_seed(5)
+    table = torch.tensor([4, 1, 0, 3], dtype=torch.int32, device=cuda_dev)   # of the last five pages
+    rope = msa.Rope(64)
+    got = []
+    for pages in (5, n):
+        plan = msa.Plan([200, 1], [300, 128], 8, hkv, hkv, 128, 64, 2, pages)
+        ids = table + (pages - 5)
+        gen.manual_seed(6)
+        rows = lambda h, d: torch.randn((201, h, d), generator=gen, device=cuda_dev).bfloat16()  # noqa: E731
+        zeros = lambda h, d, t: torch.zeros((pages, h, 128, d), dtype=t, device=cuda_dev)  # noqa: E731
+        if call == "bf16":
+            pools = [zeros(hkv, 128, torch.bfloat16) for _ in "kv"]
+            plan.kv_append(rows(hkv, 128), rows(hkv, 128), *pools, ids, rope=rope)
+        elif call == "proxy":
+            f8 = lambda d: zeros(1, d, torch.uint8).view(torch.float8_e4m3fn)  # noqa: E731
+            one = torch.full((1,), 0.01, device=cuda_dev)
+            pools = [zeros(1, 64, torch.bfloat16), f8(64), zeros(1, 32, torch.uint8), f8(4)]
+            plan.pk_append(rows(1, 64), ids, pk_pages=pools[0], pk_pages_e4m3=pools[1], pk_scale=one, pk_codes=pools[2],
+                           pk_block_scales=pools[3], pk_global_scale=one, rope=rope)
+        else:
+            pools = [zeros(hkv, 128, torch.float32) for _ in "kv"]
+            for x in pools:
+                x[-5:] = torch.randn((5, hkv, 128, 128), generator=gen, device=cuda_dev)
+            got.append(plan.append_bwd(ids, dk_pages=pools[0], dv_pages=pools[1], k_rope=rope)[:2])
+        plan.check_errors()
+        if call != "bwd":
+            got.append([x[-5:].view(torch.uint8).clone() for x in pools])
+            assert all(x.any().item() for x in got[-1])
+            if pages > 5:
+                assert not any(x.view(torch.uint8)[:5].any().item() for x in pools)
+        del pools
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_append_refusals(cuda_dev):
     msa = _msa()
     plan, table, gen, p = _setup([4], [4], 2, 64, 32, "e4m3_block", cuda_dev, 0)
