@@ -91,8 +91,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t v, float f) {
   return e4m3x4(x.x * f, x.y * f, y.x * f, y.y * f);
 }
 
-// K (blockIdx.z 0, rotated) or V (1) of one page, KV heads
-// blockIdx.y * heads_per_cta on.
+// K (which 0, rotated) or V (1) of one page, a few KV heads.
 //
 // Bound by HBM for long appends.  A thread holds 16 values of one row, or of
 // two, from the load through the rotation and the page's amax to the codes: the
@@ -100,8 +99,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t v, float f) {
 // memory and serve all heads of the CTA (with eight angles computed for every
 // 16 values the call took 67 us, half of it issuing instructions), and the
 // next head's rows are on their way while this one's amax is reduced.  32768 rows, 8 heads, d
-// 128 (201 MB): 42.6 us, 4.7 TB/s (40.2 with the shorter angle polynomials, whose
-// last bits change a few codes).
+// 128 (201 MB): 41.7 us, 4.8 TB/s (2.4 us less with the shorter angle polynomials,
+// whose last bits change a few codes).
 enum RopeKind { kPlain, kHalf, kInterleaved };
 
 struct KvAppendArgs {
@@ -113,22 +112,25 @@ struct KvAppendArgs {
   const int32_t* positions;
   const int32_t* kv_indices;
   int64_t num_pages;
-  int32_t hkv, heads_per_cta;
+  int32_t hkv;
+  int32_t heads_per_cta[2];  // K, V
+  int32_t groups[2];         // CTAs a unit that makes
+  int32_t k_ctas;            // those of K come first
   uint32_t* err;
 };
 
 template <int D, msa_kv_dtype KIND, RopeKind ROPE>
-__device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendArgs& a, int which) {
+__device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendArgs& a, int which, int cta) {
   constexpr int kChunks = D / 16, kRows = kKvThreads / kChunks, kPasses = 128 / kRows;
   extern __shared__ float4 angles[];  // [row][4][kChunks]: cos, cos, sin, sin of pairs 2 j and 2 j + 1 of a chunk
   __shared__ uint32_t warp_max[2][kKvThreads / 32];
-  const AppendUnit u = a.units[blockIdx.x];
+  const AppendUnit u = a.units[cta / a.groups[which]];
   const int64_t page = a.kv_indices[u.entry];
   const int slot0 = u.slot0_n & 0xFF, n = u.slot0_n >> 8;
   const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
   RopeChunk ch{16 * c, 16 * c + 8, false};
   if (ROPE != kPlain) ch = rope_chunk(tab, c);
-  const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.hkv, h0 + a.heads_per_cta);
+  const int h0 = cta % a.groups[which] * a.heads_per_cta[which], h1 = min(a.hkv, h0 + a.heads_per_cta[which]);
   const __nv_bfloat16* src[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) src[p] = a.x[which] + (u.row + p * kRows + r0) * a.stride[which];
@@ -272,12 +274,13 @@ __global__ void __launch_bounds__(kKvThreads, 2)
     kv_append_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ KvAppendArgs a) {
   pdl_wait();
   // one body for each way of rotating: what differs is which values pair up
-  if (blockIdx.z == 1 || tab.rot == 0)
-    kv_append<D, KIND, kPlain>(tab, a, blockIdx.z);
+  const int which = static_cast<int>(blockIdx.x) >= a.k_ctas, cta = blockIdx.x - which * a.k_ctas;
+  if (which == 1 || tab.rot == 0)
+    kv_append<D, KIND, kPlain>(tab, a, which, cta);
   else if (tab.interleaved)
-    kv_append<D, KIND, kInterleaved>(tab, a, 0);
+    kv_append<D, KIND, kInterleaved>(tab, a, 0, cta);
   else
-    kv_append<D, KIND, kHalf>(tab, a, 0);
+    kv_append<D, KIND, kHalf>(tab, a, 0, cta);
 }
 
 // Proxy K rows of one page, to any of three pools.
@@ -489,11 +492,18 @@ cudaError_t launch_kv(const msa_plan_s* p, const RopeTable& tab, KvAppendArgs a,
   // (32768 rows, 8 heads, d 128, shorter angles: 4 heads a CTA 42.7 us, 8 40.2)
   int hpc = 1;
   while (hpc < 8 && int64_t(p->n_append_units) * ((p->hkv + 2 * hpc - 1) / (2 * hpc)) * 2 >= 3 * p->num_sms) hpc *= 2;
-  a.heads_per_cta = hpc;
+  // V has no angles: smaller CTAs behind those of K fill the last round (8 heads a
+  // CTA for both 43.2 us, 4 for V 41.7, 2 41.7, 1 44.3; bf16 53.1, 49.3, 49.9, 50.6)
+  const int hpv = std::max(1, hpc / 2);
+  a.heads_per_cta[0] = hpc, a.heads_per_cta[1] = hpv;
+  a.groups[0] = (p->hkv + hpc - 1) / hpc, a.groups[1] = (p->hkv + hpv - 1) / hpv;
+  const int64_t ctas = int64_t(p->n_append_units) * (a.groups[0] + a.groups[1]);
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  a.k_ctas = p->n_append_units * a.groups[0];
   auto kern = kv_append_kernel<D, KIND>;
   const int smem = (p->decode ? 1 : 128) * D * 4;  // (cos, sin) of D / 2 pairs of a page's rows
   if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-  return launch_pdl(kern, dim3(p->n_append_units, (p->hkv + hpc - 1) / hpc, 2), dim3(kKvThreads), smem, st, tab, a);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kKvThreads), smem, st, tab, a);
 }
 
 }  // namespace
@@ -551,7 +561,9 @@ msa_status msa_kv_append(msa_plan_t plan, msa_rope_t rope, const int32_t* positi
                        kv_indices,
                        plan->num_pages,
                        plan->hkv,
-                       1,
+                       {1, 1},
+                       {1, 1},
+                       0,
                        plan->err_d};
   const bool d128 = plan->d == 128;
   const auto launch =
