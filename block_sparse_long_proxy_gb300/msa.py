@@ -107,6 +107,15 @@ def _need(t, dtype, shape, name):
         raise ValueError("%s: must be a contiguous CUDA tensor on the current device" % name)
 
 
+def _need_all(tensors, needs):
+    """_need of several tensors; needs: their (dtype, shape, name)."""
+    dev = _current_device()
+    for t, need in zip(tensors, needs):
+        dtype, shape, _ = need
+        if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+            _need(t, *need)
+
+
 def _rows(t, dtype, shape, name):
     """_need for rows at a stride: the heads of a row dense, the rows anywhere
     apart (a slice of a fused projection).  Returns that stride."""
@@ -261,6 +270,18 @@ class Plan:
         self._nvp_raw = nvp_ptr
         self.num_valid_pages = _device_view_int32(nvp_ptr, self.n_tiles, torch.cuda.current_device())
         self.num_valid_pages_host = None
+        # what sparse_attn and kv_append check of their tensors, made once
+        kvt = torch.bfloat16 if kv_dtype == "bf16" else torch.float8_e4m3fn
+        pool = (self.num_pages, self.hkv, 128, self.d)
+        self._rows_shape = (self.total_q, self.hkv, self.d)
+        self._q_shape, self._lse_shape = (self.total_q, self.hq, self.d), (self.total_q, self.hq)
+        self._cache_needs = ((torch.int32, (self.n_page_entries,), "kv_indices"), (kvt, pool, "k_pages"),
+                             (kvt, pool, "v_pages"))
+        if kv_dtype != "bf16":
+            shape = (self.hkv,) if kv_dtype == "e4m3" else (self.num_pages, self.hkv)
+            self._cache_needs += ((torch.float32, shape, "k_scale"), (torch.float32, shape, "v_scale"))
+        self._attn_needs = self._cache_needs + ((torch.bfloat16, self._q_shape, "q"), (
+            torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes"))
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -268,25 +289,16 @@ class Plan:
             _lib.msa_plan_destroy(h)
             self._h = None
 
-    def _need_scales(self, k_scale, v_scale):
-        if self.kv_dtype != "bf16":
-            shape = (self.hkv,) if self.kv_dtype == "e4m3" else (self.num_pages, self.hkv)
-            _need(k_scale, torch.float32, shape, "k_scale")
-            _need(v_scale, torch.float32, shape, "v_scale")
-
     # -- the cache
     def kv_append(self, k, v, k_pages, v_pages, kv_indices, k_scale=None, v_scale=None, rope=None, positions=None,
                   stream=None):
         """The batch's new K and V rows [total_q, Hkv, d] bf16 into the cache
         (msa_kv_append), K rotated by `rope` at int32 positions [total_q], or at
         its key positions; quantised by the plan's kv_dtype."""
-        k_stride = _rows(k, torch.bfloat16, (self.total_q, self.hkv, self.d), "k")
-        v_stride = _rows(v, torch.bfloat16, (self.total_q, self.hkv, self.d), "v")
-        kvt = torch.bfloat16 if self.kv_dtype == "bf16" else torch.float8_e4m3fn
-        _need(k_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "k_pages")
-        _need(v_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "v_pages")
-        _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
-        self._need_scales(k_scale, v_scale)
+        k_stride = _rows(k, torch.bfloat16, self._rows_shape, "k")
+        v_stride = _rows(v, torch.bfloat16, self._rows_shape, "v")
+        _need_all((kv_indices, k_pages, v_pages) if self.kv_dtype == "bf16" else
+                  (kv_indices, k_pages, v_pages, k_scale, v_scale), self._cache_needs)
         if positions is not None:
             _need(positions, torch.int32, (self.total_q,), "positions")
         _check(_lib.msa_kv_append(self._h, rope and rope._h, _ptr(positions), k.data_ptr(), k_stride, v.data_ptr(),
@@ -398,24 +410,19 @@ class Plan:
     # -- stage 3
     def sparse_attn(self, q, k_pages, v_pages, kv_indices, kv_block_indexes, k_scale=None, v_scale=None,
                     out=None, lse=None, want_lse=True, stream=None):
-        _need(q, torch.bfloat16, (self.total_q, self.hq, self.d), "q")
-        kvt = torch.bfloat16 if self.kv_dtype == "bf16" else torch.float8_e4m3fn
-        _need(k_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "k_pages")
-        _need(v_pages, kvt, (self.num_pages, self.hkv, 128, self.d), "v_pages")
-        _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
-        _need(kv_block_indexes, torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes")
-        self._need_scales(k_scale, v_scale)
+        _need_all((kv_indices, k_pages, v_pages, q, kv_block_indexes) if self.kv_dtype == "bf16" else
+                  (kv_indices, k_pages, v_pages, k_scale, v_scale, q, kv_block_indexes), self._attn_needs)
         if out is None:
             out = torch.empty_like(q)
         else:
-            _need(out, torch.bfloat16, (self.total_q, self.hq, self.d), "out")
+            _need(out, torch.bfloat16, self._q_shape, "out")
         if lse is not None:
-            _need(lse, torch.float32, (self.total_q, self.hq), "lse")
+            _need(lse, torch.float32, self._lse_shape, "lse")
         elif want_lse:
-            lse = torch.empty((self.total_q, self.hq), dtype=torch.float32, device=q.device)
-        _check(_lib.msa_sparse_attn(self._h, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_indices),
-                                    _ptr(kv_block_indexes), _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse),
-                                    _stream(stream)), "msa_sparse_attn")
+            lse = torch.empty(self._lse_shape, dtype=torch.float32, device=q.device)
+        _check(_lib.msa_sparse_attn(self._h, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                    kv_indices.data_ptr(), kv_block_indexes.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                                    out.data_ptr(), _ptr(lse), _stream(stream)), "msa_sparse_attn")
         return out, lse
 
     # -- training extension
