@@ -79,7 +79,16 @@ constexpr int kEpiRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kWg2Regs + 128 * kEpiRegs == kAttnThreads * kLaunchRegs, "register split");
 
 struct AttnUnit {
-  int32_t tile, g, h0, nh;
+  int32_t tile, g, h0;
+  int16_t nh, lg;
+};
+static_assert(sizeof(AttnUnit) == 16, "four words of the plan's aux array");
+
+// The queries' tensor maps: [lg] has boxes of 2^lg heads x 128 >> lg rows.
+constexpr int kMaxPack = 4;
+template <bool kBlk>
+struct QueryMaps {
+  CUtensorMap by_lg[kBlk ? kMaxPack + 1 : 1];
 };
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -93,7 +102,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 // out-of-range entries dropped) and row[cap] (their first K/V tensor-map
 // row), cap >= topk.
 struct UnitHdr {
-  int32_t n, nh, h0, q_begin, rows, pos0, g, kv_len, h_end, pad[7];
+  int32_t n, nh, h0, q_begin, rows, pos0, g, kv_len, h_end, lg, pad[6];
 };
 constexpr int kListSlots = 2;
 constexpr int kScaleRing = 128;  // blocks; written up to 64 ahead of the one being loaded
@@ -102,7 +111,7 @@ constexpr int kHdrInts = 16;
 // A head's row statistics at the end of a unit, from the softmax warps to
 // the epilogue warps (two buffers per head, alternating by unit).
 struct UnitStats {
-  int32_t n, active, ok, h0, q_begin, rows, g, h_end, pad[8];
+  int32_t n, active, ok, h0, q_begin, rows, g, h_end, lg, pad[7];
   float m[128], l[128];
 };
 
@@ -133,19 +142,18 @@ struct AttnSmem {
 // unit's Q load overlaps the tail of the current one.
 template <int D, bool kOneKvHead, bool kFp8, bool kStageO, bool kBlk = false, bool kSplit = false>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    attn_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+    attn_fwd_kernel(const __grid_constant__ QueryMaps<kBlk> q_maps, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap o_map,
                     int32_t list_cap, const AttnUnit* __restrict__ units, int32_t n_units,
                     const TileInfo* __restrict__ tiles, const int32_t* __restrict__ idx,
                     const int32_t* __restrict__ kv_indices, int64_t num_pages, __nv_bfloat16* __restrict__ out,
                     float* __restrict__ lse, int32_t hq, int32_t hsel, int32_t kv_div, int32_t topk,
                     float scale_log2, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
-                    int32_t parts, int32_t pack_log2, uint32_t* err) {
+                    int32_t parts, uint32_t* err) {
   pdl_wait();
-  // kBlk: a tile of few rows has 2^lg heads side by side in the 128 rows of a
-  // product, row r being query row r >> lg of head r % 2^lg; "head" 0 and 1 of a
-  // unit are then such groups
-  const int lg = kBlk ? pack_log2 : 0;
+  // kBlk: a unit of a tile of few rows has 2^lg heads side by side in the 128
+  // rows of a product, row r being query row r >> lg of head r % 2^lg; "head" 0
+  // and 1 of a unit are then such groups
   // kSplit (few units): a unit's blocks are shared out over the `parts` CTAs of
   // a cluster, which do nothing else and merge at the end
   const int part = kSplit ? blockIdx.x % parts : 0;
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    prefetch_tmap(&q_map);
+    if (!kBlk) prefetch_tmap(&q_maps.by_lg[0]);  // kBlk: the producer, which knows the unit's
     prefetch_tmap(&k_map);
     prefetch_tmap(&v_map);
     mbar_init(q_full, 1);
@@ -276,6 +284,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       int32_t* const ls_row = lrow(k);
       const AttnUnit u = units[ui];
       const TileInfo tl = tiles[u.tile];
+      const int lg = kBlk ? u.lg : 0;
+      if (kBlk && k == 0 && lane == 0) prefetch_tmap(&q_maps.by_lg[lg]);
       const int32_t* sel = idx + (static_cast<int64_t>(u.tile) * hsel + u.g) * topk;
       if (lane == 0) ok = mbar_wait_inl(list_empty + k % kListSlots, ((k / kListSlots) & 1) ^ 1, err);
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -371,6 +381,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ls.g = u.g / kv_div;
         ls.kv_len = tl.kv_len;
         ls.h_end = (u.g + 1) * (hq / hsel);
+        ls.lg = lg;
       }
       __syncwarp();
       if (lane == 0) {
@@ -380,7 +391,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           mbar_expect_tx(q_full, u.nh * L::kTileBytes);
           for (int h = 0; h < u.nh; ++h)
             for (int c = 0; c < kChunks; ++c)
-              tma_load_3d(q_s + h * L::kTileBytes + c * 16384, &q_map, q_full, c * 64, u.h0 + (h << lg), tl.q_begin);
+              tma_load_3d(q_s + h * L::kTileBytes + c * 16384, &q_maps.by_lg[lg], q_full, c * 64, u.h0 + (h << lg),
+                          tl.q_begin);
         }
       }
       constexpr int kStep = kBlk ? 32 : 1 << 30;  // kBlk: the lanes come together every 32 blocks to fetch scales
@@ -551,6 +563,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       float sl2 = kFp8 && !kBlk ? scale_log2 * k_scale[ls.g] : scale_log2;
       float log2_vs = 0.f, inv_vs = 1.f;
       const bool active = ok && h < nh;
+      const int lg = kBlk ? ls.lg : 0;
       const bool row_ok = (r >> lg) < rows;
       const int qpos = pos0 + (r >> lg);
       float m = -INFINITY, l = 0.f;
@@ -650,6 +663,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         st.rows = rows;
         st.g = ls.g;
         st.h_end = ls.h_end;
+        st.lg = lg;
       }
       if (h < nh) ch += n;
       kv_it += n;
@@ -683,6 +697,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (ok) ok = mbar_wait_inl(stat_full + h * 2 + b, (k >> 1) & 1, err);
         ok = __all_sync(0xFFFFFFFFu, ok);
         const int n = st.n, rows = st.rows, q_begin = st.q_begin, h0 = st.h0, st_h_end = st.h_end;
+        const int lg = kBlk ? st.lg : 0;
         const bool active = ok && st.active != 0;
         const bool unit_ok = ok && st.ok != 0;
         const float m = st.m[r], l = st.l[r];
@@ -906,6 +921,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       constexpr int kThreads = 32 * kSoftWarps, kMost = 8;
       const AttnUnit u = units[first_unit()];
       const TileInfo tl = tiles[u.tile];
+      const int lg = u.lg;
       const int mine = ((tl.rows << lg) - part + parts - 1) / parts;  // rows 1..128, parts <= 8
       const int h_end = (u.g + 1) * (hq / hsel);
       auto head_of = [&](int h, int r) { return u.h0 + (h << lg) + (r & ((1 << lg) - 1)); };
@@ -996,6 +1012,26 @@ static void balance_units(const msa_plan_s* p, std::vector<AttnUnit>& us, int n_
   us.swap(out);
 }
 
+// Tiles of few rows (block scales): log2 of the heads of a group that go side by
+// side into the 128 M rows, as many as fit, so that a block step serves them
+// all; otherwise most of each product and of each softmax row would be padding.
+// Measured (us), a head a tile -> packed:
+//   32 x 4 rows, 64 / 8 heads, 16 blocks   274 -> 72.7
+//   64 x 2 rows, 128 / 8 heads, 16 blocks 1037 -> 136
+//   30 x 9 rows, 128 / 8 heads, 2 blocks   108 -> 22.1
+//    1 x 4 rows, 64 / 8 heads, 16 blocks  20.3 -> 13.8
+// Each tile its own number, as decode rows beside a chunk want it (64 / 8 heads, 16 blocks):
+//   32 x 1 row + 512 rows                  308 -> 107
+//   64 x 1 row + 2048 rows                 637 -> 240
+//   12 x 1..400 rows, 32 / 4 heads         116 -> 84.9
+static int pack_of(const msa_plan_s* p, const TileInfo& t) {
+  int lg = 0;
+  if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK)
+    while (lg < kMaxPack && (t.rows << (lg + 1)) <= 128 && (2 << lg) <= p->hq / p->hp) ++lg;
+  return lg;
+}
+static int slots_of(int heads, int lg) { return (heads + (1 << lg) - 1) >> lg; }
+
 // Heads a unit (returned), units to split (p->attn_split) and the CTAs that
 // share each of those (p->attn_parts).
 //
@@ -1018,28 +1054,17 @@ static void balance_units(const msa_plan_s* p, std::vector<AttnUnit>& us, int n_
 // 160 pairs on 152 SMs, the last 8 split: 16 blocks 84.5 -> 68.0, 64 292 -> 196.
 static int unit_shape(msa_plan_s* p) {
   const int sms = p->num_sms;
-  int grp = p->hq / p->hp;
-  p->attn_split = p->attn_pack_log2 = 0;
+  const int grp = p->hq / p->hp;
+  p->attn_split = 0;
   p->attn_parts = 1;
   if (p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) return int64_t(p->n_tiles) * p->hq <= sms ? 1 : 2;
-  int blocks = 1, rows = 1, best_heads = 2;
-  for (const TileInfo& t : p->tiles) {
-    blocks = std::max(blocks, std::min(t.nvp, p->topk));
-    rows = std::max(rows, t.rows);
-  }
-  // tiles of few rows: as many heads of a group side by side in the 128 M rows
-  // as fit, so a block step serves them all; otherwise most of each MMA and of
-  // each softmax row would be padding.  Measured (us), a head a tile -> packed:
-  //   32 x 4 rows, 64 / 8 heads, 16 blocks   274 -> 72.7
-  //   64 x 2 rows, 128 / 8 heads, 16 blocks 1037 -> 136
-  //   30 x 9 rows, 128 / 8 heads, 2 blocks   108 -> 22.1
-  //    1 x 4 rows, 64 / 8 heads, 16 blocks  20.3 -> 13.8
-  while (p->attn_pack_log2 < 4 && (rows << (p->attn_pack_log2 + 1)) <= 128 && (2 << p->attn_pack_log2) <= grp)
-    ++p->attn_pack_log2;
-  grp = (grp + (1 << p->attn_pack_log2) - 1) >> p->attn_pack_log2;
+  int blocks = 1, best_heads = 2;
+  for (const TileInfo& t : p->tiles) blocks = std::max(blocks, std::min(t.nvp, p->topk));
   double best = 1e30;
   for (int heads = 2; heads >= 1; --heads) {
-    const int64_t units = int64_t(p->n_tiles) * p->hp * ((grp + heads - 1) / heads), rounds = units / sms;
+    int64_t units = 0;
+    for (const TileInfo& t : p->tiles) units += int64_t(p->hp) * ((slots_of(grp, pack_of(p, t)) + heads - 1) / heads);
+    const int64_t rounds = units / sms;
     const double step = heads == 2 ? 1.78 : 1.65, unit = blocks * step + 6;
     const int64_t rest = units - rounds * sms;
     auto take = [&](double us, int64_t split, int parts) {
@@ -1060,12 +1085,15 @@ void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   // blocks); with one proxy head per GQA group g is the group
   std::vector<AttnUnit> us;
   const int grp = p->hq / p->hp;
-  const int pair = unit_shape(p), lg = p->attn_pack_log2;
-  const int slots = (grp + (1 << lg) - 1) >> lg;  // heads, or groups of heads side by side
-  for (int t = 0; t < p->n_tiles; ++t)
+  const int pair = unit_shape(p);
+  for (int t = 0; t < p->n_tiles; ++t) {
+    const int lg = pack_of(p, p->tiles[t]), slots = slots_of(grp, lg);  // heads, or groups of heads side by side
+    p->attn_packs |= 1 << lg;
     for (int g = 0; g < p->hp; ++g)
       for (int h = 0; h < slots; h += pair)
-        us.push_back(AttnUnit{t, g, g * grp + (h << lg), std::min(pair, slots - h)});
+        us.push_back(AttnUnit{t, g, g * grp + (h << lg), static_cast<int16_t>(std::min(pair, slots - h)),
+                              static_cast<int16_t>(lg)});
+  }
   balance_units(p, us, p->attn_split);
   p->attn_units_off = static_cast<int64_t>(aux.size());
   p->n_attn_units = static_cast<int32_t>(us.size());
@@ -1076,7 +1104,7 @@ void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   // other's products)
   std::vector<AttnUnit> ps;
   for (int t = 0; t < p->n_tiles; ++t)
-    for (int g = 0; g < p->hp; g += 2) ps.push_back(AttnUnit{t, g, g, std::min(2, p->hp - g)});
+    for (int g = 0; g < p->hp; g += 2) ps.push_back(AttnUnit{t, g, g, static_cast<int16_t>(std::min(2, p->hp - g)), 0});
   balance_units(p, ps);
   p->proxy_attn_units_off = static_cast<int64_t>(aux.size());
   p->n_proxy_attn_units = static_cast<int32_t>(ps.size());
@@ -1105,12 +1133,12 @@ cudaError_t check_launch_regs(K kern) {
 }
 
 template <int D, bool kOneKvHead, bool kFp8, bool kBlk = false>
-cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& qm, const CUtensorMap& km,
+cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const QueryMaps<kBlk>& qm, const CUtensorMap& km,
                                 const CUtensorMap& vm, const CUtensorMap& om, int32_t topk, const AttnUnit* units,
                                 int32_t n_units, const TileInfo* tiles, const int32_t* idx,
                                 const int32_t* kv_indices, int64_t num_pages, __nv_bfloat16* o, float* lse,
                                 int32_t hq, int32_t hsel, int32_t kv_div, float scale_log2, const float* k_scale,
-                                const float* v_scale, uint32_t* err, int parts = 1, int pack_log2 = 0) {
+                                const float* v_scale, uint32_t* err, int parts = 1) {
   const int cap = (topk + 3) & ~3;
   if constexpr (kFp8) {
     const int staged = AttnSmem<D, true, kOneKvHead ? 2 : 1, kBlk>::bytes(cap) + 1024;
@@ -1120,7 +1148,7 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, staged);
       return launch_pdl_cluster(kern, grid, 1, dim3(kAttnThreads), staged, st, qm, km, vm, om, cap, units, n_units,
                                 tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
-                                v_scale, 1, pack_log2, err);
+                                v_scale, 1, err);
     }
   }
   const int plain = AttnSmem<D, false, kOneKvHead ? 2 : 1, kBlk>::bytes(kMaxTopk) + 1024;
@@ -1131,7 +1159,7 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const CUtensorMap& q
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plain);
   return launch_pdl_cluster(kern, grid, parts, dim3(kAttnThreads), plain, st, qm, km, vm, om, cap, units, n_units,
                             tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
-                            v_scale, parts, pack_log2, err);
+                            v_scale, parts, err);
 }
 
 // [total_q, heads, D] bf16 rows as 3-D boxes of 64 columns x 1 head x 128 rows, 128-byte swizzle
@@ -1152,14 +1180,20 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
   const bool fp8 = p->kv_dtype != MSA_KV_BF16;
   if (p->kv_dtype == MSA_KV_FP8_E4M3 && p->d != 128)
     return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn: FP8 K/V prefill needs head_dim 128");
-  CUtensorMap qm, km, vm, om;
+  QueryMaps<true> qms{};  // the launch copies those of packs no unit has, too
+  QueryMaps<false> qm;
+  CUtensorMap km, vm, om;
   const int kv_elem = fp8 ? 1 : 2;
   const uint64_t kdims[2] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->num_pages) * p->hkv * 128};
   const uint64_t kstr[1] = {static_cast<uint64_t>(p->d) * kv_elem};
   // bf16: 64-column boxes (128 B rows); e4m3: whole rows of codes
   const uint32_t kbox[2] = {fp8 ? static_cast<uint32_t>(p->d) : 64u, 128};
   const int kswz = fp8 ? p->d : 128;
-  if (!rows_map(&qm, q, p->d, p->hq, p->total_q, p->attn_pack_log2) || !rows_map(&om, out, p->d, p->hq, p->total_q) ||
+  const bool blk = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK;
+  bool maps = blk || rows_map(&qm.by_lg[0], q, p->d, p->hq, p->total_q);
+  for (int lg = 0; blk && lg <= kMaxPack; ++lg)
+    if (p->attn_packs >> lg & 1) maps = maps && rows_map(&qms.by_lg[lg], q, p->d, p->hq, p->total_q, lg);
+  if (!maps || !rows_map(&om, out, p->d, p->hq, p->total_q) ||
       !encode_tensor_map(&km, 2, k_pages, kdims, kstr, kbox, fp8 ? 0 : 1, kswz) ||
       !encode_tensor_map(&vm, 2, v_pages, kdims, kstr, kbox, fp8 ? 0 : 1, kswz))
     return set_error(MSA_ERR_CUDA, "msa_sparse_attn: tensor map encoding failed");
@@ -1169,13 +1203,13 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
   const dim3 grid(std::min(p->n_attn_units, p->num_sms));  // persistent: one CTA per SM
   const int kv_div = p->hp / p->hkv;
   cudaError_t e;
-  if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK) {
+  if (blk) {
     const auto launch = p->d == 128 ? launch_attn_variant<128, false, true, true>
                                     : launch_attn_variant<64, false, true, true>;
     const int whole = p->n_attn_units - p->attn_split;
     auto run = [&](int ctas, const AttnUnit* first, int n, int parts) {
-      return launch(dim3(ctas), st, qm, km, vm, om, p->topk, first, n, p->tiles_d, idx, kv_indices, p->num_pages, o, lse,
-                    p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d, parts, p->attn_pack_log2);
+      return launch(dim3(ctas), st, qms, km, vm, om, p->topk, first, n, p->tiles_d, idx, kv_indices, p->num_pages, o, lse,
+                    p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d, parts);
     };
     e = whole > 0 ? run(std::min(whole, p->num_sms), units, whole, 1) : cudaSuccess;
     if (e == cudaSuccess && p->attn_split > 0)
@@ -1204,14 +1238,15 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
 msa_status launch_proxy_softmax(const msa_plan_s* p, const void* pq, const void* pk_pages, const int32_t* kv_indices,
                                 const int32_t* idx, void* op, float* lse, cudaStream_t st) {
   if (p->topk > kMaxTopk) return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_bwd: topk above 1024");
-  CUtensorMap qm, km, om;
+  QueryMaps<false> qm;
+  CUtensorMap km, om;
   // pq and pk at dp = 32 are read as 64-column boxes whose upper half lies
   // past the tensor's edge: TMA fills it with zeros, so the dp = 64 kernel
   // computes the same scores and an Op whose columns [dp, 64) are zero
   const uint64_t kdims[2] = {static_cast<uint64_t>(p->dp), static_cast<uint64_t>(p->num_pages) * 128};
   const uint64_t kstr[1] = {static_cast<uint64_t>(p->dp) * 2};
   const uint32_t kbox[2] = {64, 128};
-  if (!rows_map(&qm, pq, p->dp, p->hp, p->total_q) || !rows_map(&om, op, 64, p->hp, p->total_q) ||
+  if (!rows_map(&qm.by_lg[0], pq, p->dp, p->hp, p->total_q) || !rows_map(&om, op, 64, p->hp, p->total_q) ||
       !encode_tensor_map(&km, 2, pk_pages, kdims, kstr, kbox, 1, 128))
     return set_error(MSA_ERR_CUDA, "msa_sparse_attn_bwd: tensor map encoding failed");
   const AttnUnit* units = reinterpret_cast<const AttnUnit*>(p->aux_d + p->proxy_attn_units_off);

@@ -98,7 +98,7 @@ struct msa_plan_s {
   int32_t n_attn_units = 0;
   int32_t attn_split = 0;            // of them, the last ones that clusters share (block-scaled plans)
   int32_t attn_parts = 1;            // CTAs that share each of those
-  int32_t attn_pack_log2 = 0;        // heads side by side in a tile (block-scaled plans, tiles of few rows)
+  uint32_t attn_packs = 0;           // bit lg: some tile has 2^lg heads side by side (block-scaled plans)
   int64_t proxy_attn_units_off = 0;  // backward proxy softmax work units
   int32_t n_proxy_attn_units = 0;
   int64_t heavy_tiles_off = 0;       // tile ids, most cached blocks first (the backward's dq order)

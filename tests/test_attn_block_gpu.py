@@ -94,6 +94,12 @@ CASES = [
     _case("heads by 8, many units", [int(x) for x in np.random.default_rng(3).integers(1, 10, 40)],
           [int(x) for x in np.random.default_rng(4).integers(10, 900, 40)], 72, 8, 8, 3, page_perm_seed=7),
     _case("d64 heads by 4, G=5", [20, 32, 3], [900, 1500, 300], 5, 1, 1, 4, d=64, page_perm_seed=7),
+    # decode rows beside a chunk, and tiles of several kinds of few rows
+    _case("mixed batch", [1] * 9 + [300, 1, 20, 64, 7], [900, 1, 2000, 129, 77, 500, 333, 128, 3000, 1100, 700, 20, 64, 900],
+          48, 4, 4, 6, page_perm_seed=7, extra_pages=2),
+    _case("mixed batch G=3, few units", [200, 1, 65, 4], [900, 700, 1500, 40], 3, 1, 1, 9, page_perm_seed=7),
+    _case("mixed batch two sets a head, many units", [1] * 30 + [700], _LENS[:30] + [1500], 64, 2, 4, 5, page_perm_seed=7),
+    _case("d64 mixed batch", [1] * 5 + [150, 33], [900, 1, 2000, 129, 77, 500, 333], 10, 2, 2, 6, d=64, page_perm_seed=7),
     # head_dim 64
     _case("d64 parts 8", [130], [9000], 6, 1, 2, 24, d=64, page_perm_seed=3),
     _case("d64 decode one key", [1], [1], 8, 1, 1, 4, d=64),
