@@ -1032,8 +1032,8 @@ static int pack_of(const msa_plan_s* p, const TileInfo& t) {
 }
 static int slots_of(int heads, int lg) { return (heads + (1 << lg) - 1) >> lg; }
 
-// Heads a unit (returned), units to split (p->attn_split) and the CTAs that
-// share each of those (p->attn_parts).
+// Heads a unit, the units to split, the CTAs that share each of those, and the
+// time that takes, estimated (block scales; us).  apart: without the tiles of one row.
 //
 // Two heads share a block's K and V and overlap each other's softmax; with an
 // SM for every head, a head alone is done sooner (512 rows x 32 heads, topk 16:
@@ -1052,24 +1052,29 @@ static int slots_of(int heads, int lg) { return (heads + (1 << lg) - 1) >> lg; }
 //     700 x 12, 9           24.5  [20.0]  31.3   69.2   27.7   24.1   30.9
 //     100 x 8, 64            139   76.7   43.6  [27.3]   144   81.3   47.2
 // 160 pairs on 152 SMs, the last 8 split: 16 blocks 84.5 -> 68.0, 64 292 -> 196.
-static int unit_shape(msa_plan_s* p) {
+struct UnitShape {
+  double us;
+  int heads;
+  int64_t split;
+  int parts;
+};
+static UnitShape unit_shape(const msa_plan_s* p, bool apart) {
   const int sms = p->num_sms;
   const int grp = p->hq / p->hp;
-  p->attn_split = 0;
-  p->attn_parts = 1;
-  if (p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) return int64_t(p->n_tiles) * p->hq <= sms ? 1 : 2;
-  int blocks = 1, best_heads = 2;
-  for (const TileInfo& t : p->tiles) blocks = std::max(blocks, std::min(t.nvp, p->topk));
-  double best = 1e30;
+  if (p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) return {0.0, int64_t(p->n_tiles) * p->hq <= sms ? 1 : 2, 0, 1};
+  int blocks = 1;
+  for (const TileInfo& t : p->tiles)
+    if (!(apart && t.rows == 1)) blocks = std::max(blocks, std::min(t.nvp, p->topk));
+  UnitShape best{1e30, 2, 0, 1};
   for (int heads = 2; heads >= 1; --heads) {
     int64_t units = 0;
-    for (const TileInfo& t : p->tiles) units += int64_t(p->hp) * ((slots_of(grp, pack_of(p, t)) + heads - 1) / heads);
+    for (const TileInfo& t : p->tiles)
+      if (!(apart && t.rows == 1)) units += int64_t(p->hp) * ((slots_of(grp, pack_of(p, t)) + heads - 1) / heads);
     const int64_t rounds = units / sms;
     const double step = heads == 2 ? 1.78 : 1.65, unit = blocks * step + 6;
     const int64_t rest = units - rounds * sms;
     auto take = [&](double us, int64_t split, int parts) {
-      if (us >= best) return;
-      best = us, best_heads = heads, p->attn_split = static_cast<int32_t>(split), p->attn_parts = parts;
+      if (us < best.us) best = {us, heads, split, parts};
     };
     // an odd head beside pairs fills the rounds better than heads alone
     take((rounds + (rest > 0)) * unit * (heads == 1 && units > sms ? 1.1 : 1.0), 0, 1);
@@ -1077,7 +1082,20 @@ static int unit_shape(msa_plan_s* p) {
       if (rest * parts <= (parts < 8 ? sms - 8 : sms * 2 / 3))
         take(rounds * unit + (rounds > 0 ? 10 : 0) + (blocks + parts - 1) / parts * step + 9, rest, parts);
   }
-  return best_heads;
+  return best;
+}
+
+// Estimated time of the decode kernel for a batch's tiles of one row: its ramp
+// and the K and V bytes at the rate it reaches (8 to 256 rows of 16 blocks: 6.9
+// to 25.9 us).  None: 0.
+static double rows_us(const msa_plan_s* p) {
+  int64_t bytes = 0, blocks = 0;
+  for (const TileInfo& t : p->tiles)
+    if (t.rows == 1) {
+      const int64_t n = std::min(t.nvp, p->topk);
+      bytes += n * p->hp * 2 * 128 * p->d, blocks = std::max(blocks, n);
+    }
+  return bytes > 0 ? 6 + bytes / 6.4e6 + 0.03 * blocks : 0.0;
 }
 
 void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
@@ -1085,8 +1103,29 @@ void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   // blocks); with one proxy head per GQA group g is the group
   std::vector<AttnUnit> us;
   const int grp = p->hq / p->hp;
-  const int pair = unit_shape(p);
+  UnitShape shape = unit_shape(p, false);
+  // a mixed batch (block scales): its tiles of one row in a launch of the decode
+  // kernel where that is done sooner (64 / 8 heads, 16 blocks, 32 rows beside a
+  // chunk of 512: 107 -> 69.3 us; 64 beside 2048: 240 -> 200)
+  std::vector<int32_t> row_tiles;
+  if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK && !p->decode && grp <= 16) {
+    const UnitShape rest = unit_shape(p, true);
+    const double rows = rows_us(p);
+    if (rows > 0 && rows + (rest.us > 0 ? rest.us + 2 : 0) < shape.us) {
+      shape = rest;
+      for (int t = 0; t < p->n_tiles; ++t)
+        if (p->tiles[t].rows == 1) row_tiles.push_back(t);
+    }
+  }
+  p->attn_split = static_cast<int32_t>(shape.split);
+  p->attn_parts = shape.parts;
+  p->row_tiles_off = static_cast<int64_t>(aux.size());
+  p->n_row_tiles = static_cast<int32_t>(row_tiles.size());
+  aux.insert(aux.end(), row_tiles.begin(), row_tiles.end());
+  aux.resize((aux.size() + 3) & ~size_t(3));  // the tables after it stay on 16 bytes
+  const int pair = shape.heads;
   for (int t = 0; t < p->n_tiles; ++t) {
+    if (p->n_row_tiles > 0 && p->tiles[t].rows == 1) continue;
     const int lg = pack_of(p, p->tiles[t]), slots = slots_of(grp, lg);  // heads, or groups of heads side by side
     p->attn_packs |= 1 << lg;
     for (int g = 0; g < p->hp; ++g)

@@ -88,7 +88,7 @@ template <bool kBlk, int kD, int NT>
 __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
     decode_ws_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                      const __nv_bfloat16* __restrict__ q, const TileInfo* __restrict__ tiles,
-                     const int32_t* __restrict__ idx, const int32_t* __restrict__ kv_indices, int64_t num_pages,
+                     const int32_t* __restrict__ tile_list, const int32_t* __restrict__ idx, const int32_t* __restrict__ kv_indices, int64_t num_pages,
                      const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int32_t hq, int32_t hsel,
                      int32_t kv_div, int32_t topk, int32_t cs, float scale_log2, uint32_t* err) {
@@ -99,9 +99,10 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // row = (sequence, proxy head g): the G = hq / hsel query heads of g over
-  // g's blocks of KV head g / kv_div; CTA `rank` of the row's cs
+  // g's blocks of KV head g / kv_div; CTA `rank` of the row's cs.  tile_list:
+  // the tiles of one row of a batch that has others too
   const int row = blockIdx.x / cs, rank = blockIdx.x % cs;
-  const int t = row / hsel, g = row % hsel;
+  const int g = row % hsel, t = kBlk && tile_list != nullptr ? tile_list[row / hsel] : row / hsel;
   const int G = hq / hsel;
   const int hkv = hsel / kv_div, kvh = g / kv_div;
   const TileInfo tl = tiles[t];
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
     ukey = -1;
     if (base + lane < my_n) {
       const int u = gw + (base + lane) * W;
-      const int j = idx[static_cast<int64_t>(row) * topk + u / kParts];
+      const int j = idx[(static_cast<int64_t>(t) * hsel + g) * topk + u / kParts];
       if (j >= tl.nvp) {
         atomicOr(err, kErrDeviceCheck);
       } else if (j >= 0) {
@@ -398,15 +399,15 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
 }
 
 template <bool kBlk, int D, int NT>
-cudaError_t launch_ws(const msa_plan_s* p, int cs, cudaStream_t st, const CUtensorMap& km, const CUtensorMap& vm,
+cudaError_t launch_ws(const msa_plan_s* p, int n_tiles, const int32_t* tile_list, int cs, cudaStream_t st, const CUtensorMap& km, const CUtensorMap& vm,
                       const void* q, const int32_t* kv_indices, const int32_t* idx, const float* k_scale,
                       const float* v_scale, void* out, float* lse) {
   auto kern = decode_ws_kernel<kBlk, D, NT>;
   const int smem = WsSmem<D, NT>::kBytes + 1024;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (cs > 8) cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return launch_pdl_cluster(kern, dim3(p->n_tiles * p->hp * cs), cs, dim3(kWsThreads), smem, st, km, vm,
-                            static_cast<const __nv_bfloat16*>(q), p->tiles_d, idx, kv_indices, p->num_pages, k_scale,
+  return launch_pdl_cluster(kern, dim3(n_tiles * p->hp * cs), cs, dim3(kWsThreads), smem, st, km, vm,
+                            static_cast<const __nv_bfloat16*>(q), p->tiles_d, tile_list, idx, kv_indices, p->num_pages, k_scale,
                             v_scale, static_cast<__nv_bfloat16*>(out), lse, p->hq, p->hp, p->hp / p->hkv, p->topk, cs,
                             1.4426950408889634f / sqrtf(static_cast<float>(D)), p->err_d);
 }
@@ -425,8 +426,8 @@ cudaError_t launch_ws(const msa_plan_s* p, int cs, cudaStream_t st, const CUtens
 //   64 rows, topk 16, G 16  27.3 | 16.4 [12.9] 19.9
 // Two CTAs of different clusters on one SM cost more than the second half of
 // the row's parallelism brings.
-int row_cluster(const msa_plan_s* p) {
-  const int rows = p->n_tiles * p->hp;
+int row_cluster(const msa_plan_s* p, int n_tiles) {
+  const int rows = n_tiles * p->hp;
   int cs = 1;
   while (cs < 16 && rows * cs * 2 <= p->num_sms && 2 * cs * kWsWarps <= kParts * p->topk && (cs < 8 || p->topk >= 128))
     cs *= 2;
@@ -443,6 +444,8 @@ bool decode_ws_applies(const msa_plan_s* p) {
 msa_status launch_attn_decode_ws(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,
                                  const int32_t* kv_indices, const int32_t* idx, const float* k_scale,
                                  const float* v_scale, void* out, float* lse, cudaStream_t st) {
+  const int32_t* tile_list = p->n_row_tiles > 0 ? p->aux_d + p->row_tiles_off : nullptr;
+  const int n_tiles = tile_list ? p->n_row_tiles : p->n_tiles;
   CUtensorMap km, vm;
   const uint64_t dims[2] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->num_pages) * p->hkv * 128};
   const uint64_t str[1] = {static_cast<uint64_t>(p->d)};
@@ -454,8 +457,8 @@ msa_status launch_attn_decode_ws(const msa_plan_s* p, const void* q, const void*
   const auto launch = p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK ? launch_ws<false, 128, 1>
                       : p->d == 128 ? (wide ? launch_ws<true, 128, 2> : launch_ws<true, 128, 1>)
                                     : (wide ? launch_ws<true, 64, 2> : launch_ws<true, 64, 1>);
-  const int cs = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK ? row_cluster(p) : 1;
-  return cuda_check(launch(p, cs, st, km, vm, q, kv_indices, idx, k_scale, v_scale, out, lse),
+  const int cs = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK ? row_cluster(p, n_tiles) : 1;
+  return cuda_check(launch(p, n_tiles, tile_list, cs, st, km, vm, q, kv_indices, idx, k_scale, v_scale, out, lse),
                     "msa_sparse_attn: decode launch");
 }
 

@@ -99,6 +99,8 @@ CASES = [
           48, 4, 4, 6, page_perm_seed=7, extra_pages=2),
     _case("mixed batch G=3, few units", [200, 1, 65, 4], [900, 700, 1500, 40], 3, 1, 1, 9, page_perm_seed=7),
     _case("mixed batch two sets a head, many units", [1] * 30 + [700], _LENS[:30] + [1500], 64, 2, 4, 5, page_perm_seed=7),
+    _case("mixed batch, rows alone", [1, 0, 1, 1], [900, 300, 77, 2000], 16, 2, 2, 6, page_perm_seed=7),
+    _case("mixed batch G=16, many rows", [1] * 39 + [40], _LENS[:39] + [90], 64, 4, 4, 9, page_perm_seed=7),
     _case("d64 mixed batch", [1] * 5 + [150, 33], [900, 1, 2000, 129, 77, 500, 333], 10, 2, 2, 6, d=64, page_perm_seed=7),
     # head_dim 64
     _case("d64 parts 8", [130], [9000], 6, 1, 2, 24, d=64, page_perm_seed=3),
