@@ -1033,16 +1033,18 @@ static int pack_of(const msa_plan_s* p, const TileInfo& t) {
 static int slots_of(int heads, int lg) { return (heads + (1 << lg) - 1) >> lg; }
 
 // Heads a unit, the units to split, the CTAs that share each of those, and the
-// time that takes, estimated (block scales; us).  apart: without the tiles of one row.
+// time that takes, estimated (block scales; us), without the tiles of `apart` rows or
+// fewer.
 //
 // Two heads share a block's K and V and overlap each other's softmax; with an
 // SM for every head, a head alone is done sooner (512 rows x 32 heads, topk 16:
 // e4m3 38.0 us in pairs, 32.6 alone; bf16 34.4, 28.8).  Block-scaled plans also
 // share a unit's blocks out over a cluster while each of its CTAs has an SM: all
 // units, or those that a last, short round would be left with, in a launch of
-// their own.  A block step takes about 1.65 us for a head and 1.78 for two, a
+// their own.  A block step takes about 1.65 us for a head and 1.78 for two (0.35
+// more where no other unit reads the same blocks, which then come from HBM), a
 // unit 6 besides, the merge 3 and a second launch 10.  Clusters of 8 are not
-// placed as densely as the SMs would allow: 16 of them took two waves, 12 one.
+// placed as densely as the SMs would allow: 15 run at once.
 // Measured (us; heads a unit / parts):
 //   rows x heads, blocks     1/1    1/2    1/4    1/8    2/1    2/2    2/4
 //     128 x 32, 16          33.8   24.4  [17.9]  41.7   38.3   29.2   21.1
@@ -1058,20 +1060,23 @@ struct UnitShape {
   int64_t split;
   int parts;
 };
-static UnitShape unit_shape(const msa_plan_s* p, bool apart) {
+static UnitShape unit_shape(const msa_plan_s* p, int apart) {
   const int sms = p->num_sms;
   const int grp = p->hq / p->hp;
   if (p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK) return {0.0, int64_t(p->n_tiles) * p->hq <= sms ? 1 : 2, 0, 1};
   int blocks = 1;
   for (const TileInfo& t : p->tiles)
-    if (!(apart && t.rows == 1)) blocks = std::max(blocks, std::min(t.nvp, p->topk));
+    if (t.rows > apart) blocks = std::max(blocks, std::min(t.nvp, p->topk));
   UnitShape best{1e30, 2, 0, 1};
   for (int heads = 2; heads >= 1; --heads) {
-    int64_t units = 0;
+    int64_t units = 0, sets = 0;
     for (const TileInfo& t : p->tiles)
-      if (!(apart && t.rows == 1)) units += int64_t(p->hp) * ((slots_of(grp, pack_of(p, t)) + heads - 1) / heads);
+      if (t.rows > apart) {
+        units += int64_t(p->hp) * ((slots_of(grp, pack_of(p, t)) + heads - 1) / heads);
+        sets += p->hp;
+      }
     const int64_t rounds = units / sms;
-    const double step = heads == 2 ? 1.78 : 1.65, unit = blocks * step + 6;
+    const double step = (heads == 2 ? 1.78 : 1.65) + (units == sets ? 0.35 : 0.0), unit = blocks * step + 6;
     const int64_t rest = units - rounds * sms;
     auto take = [&](double us, int64_t split, int parts) {
       if (us < best.us) best = {us, heads, split, parts};
@@ -1079,23 +1084,26 @@ static UnitShape unit_shape(const msa_plan_s* p, bool apart) {
     // an odd head beside pairs fills the rounds better than heads alone
     take((rounds + (rest > 0)) * unit * (heads == 1 && units > sms ? 1.1 : 1.0), 0, 1);
     for (int parts = 2; parts <= 8 && parts <= blocks && rest > 0; parts *= 2)
-      if (rest * parts <= (parts < 8 ? sms - 8 : sms * 2 / 3))
+      if (rest * parts <= (parts < 8 ? sms - 8 : sms * 3 / 4))
         take(rounds * unit + (rounds > 0 ? 10 : 0) + (blocks + parts - 1) / parts * step + 9, rest, parts);
   }
   return best;
 }
 
-// Estimated time of the decode kernel for a batch's tiles of one row: its ramp
-// and the K and V bytes at the rate it reaches (8 to 256 rows of 16 blocks: 6.9
-// to 25.9 us).  None: 0.
-static double rows_us(const msa_plan_s* p) {
+// Estimated time of the decode kernel for a batch's tiles of `apart` rows or
+// fewer, in parts of up to 16 (row, head) columns: its ramp and the K and V bytes
+// at the rate it reaches with one tile of 8 columns or with two.  None: 0.
+static double rows_us(const msa_plan_s* p, int apart) {
+  const int grp = p->hq / p->hp, most = 16 / grp;
   int64_t bytes = 0, blocks = 0;
+  int columns = 0;
   for (const TileInfo& t : p->tiles)
-    if (t.rows == 1) {
+    if (t.rows <= apart) {
       const int64_t n = std::min(t.nvp, p->topk);
-      bytes += n * p->hp * 2 * 128 * p->d, blocks = std::max(blocks, n);
+      bytes += n * ((t.rows + most - 1) / most) * p->hp * 2 * 128 * p->d;
+      blocks = std::max(blocks, n), columns = std::max(columns, std::min(t.rows, most) * grp);
     }
-  return bytes > 0 ? 6 + bytes / 6.4e6 + 0.03 * blocks : 0.0;
+  return bytes > 0 ? 6 + bytes / (columns > 8 ? 4.7e6 : 6.4e6) + 0.03 * blocks : 0.0;
 }
 
 void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
@@ -1103,29 +1111,42 @@ void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   // blocks); with one proxy head per GQA group g is the group
   std::vector<AttnUnit> us;
   const int grp = p->hq / p->hp;
-  UnitShape shape = unit_shape(p, false);
-  // a mixed batch (block scales): its tiles of one row in a launch of the decode
-  // kernel where that is done sooner (64 / 8 heads, 16 blocks, 32 rows beside a
-  // chunk of 512: 107 -> 69.3 us; 64 beside 2048: 240 -> 200)
-  std::vector<int32_t> row_tiles;
-  if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK && !p->decode && grp <= 16) {
-    const UnitShape rest = unit_shape(p, true);
-    const double rows = rows_us(p);
-    if (rows > 0 && rows + (rest.us > 0 ? rest.us + 2 : 0) < shape.us) {
-      shape = rest;
-      for (int t = 0; t < p->n_tiles; ++t)
-        if (p->tiles[t].rows == 1) row_tiles.push_back(t);
+  UnitShape shape = unit_shape(p, 0);
+  // block scales: tiles of few rows in a launch of the decode kernel where that
+  // is done sooner.  Measured (us, 16 blocks; all as tiles -> so):
+  //   32 x 1 + 512 rows, 64 / 8 heads   107 -> 69.4      64 x 4, 32 / 8   136 -> 70.6
+  //   64 x 1 + 2048 rows, 64 / 8        240 -> 201       16 x 4, 32 / 8  39.9 -> 16.7
+  //   32 x 2 rows, 64 / 8              73.4 -> 35.5      16 x 8, 32 / 8  39.8 -> 31.7
+  //   32 x 4 rows, 64 / 8 (two parts)  73.2 -> 66.3       8 x 2, 64 / 8  25.9 -> 12.7
+  // and where it is not: 16 x 4 rows, 64 / 4 (four parts) 26.8, 31.0; 30 x 9 rows,
+  // 128 / 8, 2 blocks 21.9, 89; 4 x 1 + 128 rows, 16 / 2 17.4, 25.9.
+  const int most = 16 / grp;  // rows a part of those
+  int apart = 0;
+  std::vector<int32_t> parts;  // two words each
+  if (p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK && !p->decode && most > 0) {
+    double best = shape.us;
+    for (int rows = 1; rows <= 16; ++rows) {
+      const UnitShape rest = unit_shape(p, rows);
+      const double us = rows_us(p, rows) + (rest.us > 0 ? rest.us + 2 : 0);
+      if (us < best) best = us, apart = rows, shape = rest;
     }
+    for (int t = 0; t < p->n_tiles; ++t)
+      for (int r = 0; p->tiles[t].rows <= apart && r < p->tiles[t].rows; r += most) {
+        const int n = std::min(most, p->tiles[t].rows - r);
+        parts.insert(parts.end(), {t, r | n << 16});
+        p->row_part_heads = std::max(p->row_part_heads, n * grp);
+      }
   }
   p->attn_split = static_cast<int32_t>(shape.split);
   p->attn_parts = shape.parts;
-  p->row_tiles_off = static_cast<int64_t>(aux.size());
-  p->n_row_tiles = static_cast<int32_t>(row_tiles.size());
-  aux.insert(aux.end(), row_tiles.begin(), row_tiles.end());
-  aux.resize((aux.size() + 3) & ~size_t(3));  // the tables after it stay on 16 bytes
+  aux.resize((aux.size() + 3) & ~size_t(3));
+  p->row_parts_off = static_cast<int64_t>(aux.size());
+  p->n_row_parts = static_cast<int32_t>(parts.size() / 2);
+  aux.insert(aux.end(), parts.begin(), parts.end());
+  aux.resize((aux.size() + 3) & ~size_t(3));
   const int pair = shape.heads;
   for (int t = 0; t < p->n_tiles; ++t) {
-    if (p->n_row_tiles > 0 && p->tiles[t].rows == 1) continue;
+    if (p->tiles[t].rows <= apart) continue;
     const int lg = pack_of(p, p->tiles[t]), slots = slots_of(grp, lg);  // heads, or groups of heads side by side
     p->attn_packs |= 1 << lg;
     for (int g = 0; g < p->hp; ++g)

@@ -84,11 +84,11 @@ struct Merged {
   float4 o;
 };
 
-template <bool kBlk, int kD, int NT>
+template <bool kBlk, int kD, int NT, bool kFew>
 __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
     decode_ws_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                      const __nv_bfloat16* __restrict__ q, const TileInfo* __restrict__ tiles,
-                     const int32_t* __restrict__ tile_list, const int32_t* __restrict__ idx, const int32_t* __restrict__ kv_indices, int64_t num_pages,
+                     const int2* __restrict__ part_list, const int32_t* __restrict__ idx, const int32_t* __restrict__ kv_indices, int64_t num_pages,
                      const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int32_t hq, int32_t hsel,
                      int32_t kv_div, int32_t topk, int32_t cs, float scale_log2, uint32_t* err) {
@@ -99,13 +99,19 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // row = (sequence, proxy head g): the G = hq / hsel query heads of g over
-  // g's blocks of KV head g / kv_div; CTA `rank` of the row's cs.  tile_list:
-  // the tiles of one row of a batch that has others too
+  // g's blocks of KV head g / kv_div; CTA `rank` of the row's cs.  kFew: tiles of
+  // few rows of a batch that has others too, part_list[] = (tile, first row |
+  // rows << 16), rows * G <= 8 NT; "head" h is then head h % G of row h / G
   const int row = blockIdx.x / cs, rank = blockIdx.x % cs;
-  const int g = row % hsel, t = kBlk && tile_list != nullptr ? tile_list[row / hsel] : row / hsel;
-  const int G = hq / hsel;
+  const int g = row % hsel, G = hq / hsel;
+  int t = row / hsel, first = 0, H = G;
+  if (kFew) {
+    const int2 part = part_list[t];
+    t = part.x, first = part.y & 0xFFFF, H = G * (part.y >> 16);
+  }
   const int hkv = hsel / kv_div, kvh = g / kv_div;
   const TileInfo tl = tiles[t];
+  const int q_begin = tl.q_begin + first;
   uint8_t* buf = smem + L::kBufOff + warp * kBufBytes;
   uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + L::kBarOff) + 2 * warp;
   uint64_t* bar_v = bar_k + 1;
@@ -118,7 +124,10 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   }
   __syncwarp();
 
-  const int qpos = tl.pos0;
+  // of the first query row and of the last
+  const int qpos = tl.pos0 + first, last = kFew ? qpos + H / G - 1 : qpos;
+  auto row_of = [&](int h) { return kFew ? h / G : 0; };
+  auto head_of = [&](int h) { return kFew ? h % G : h; };
   const int n_units = kParts * topk;
   const int W = kWsWarps * cs, gw = rank * kWsWarps + warp;
   const int my_n = n_units > gw ? (n_units - gw + W - 1) / W : 0;
@@ -140,7 +149,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
         }
         ukey = j * 128 + (u % kParts) * kKeys;
         urow = static_cast<int>((page * hkv + kvh) * 128 + (u % kParts) * kKeys);
-        if (kBlk && ukey > qpos) ukey = -1;
+        if (kBlk && ukey > last) ukey = -1;
       }
     }
     // compact the valid units to the low lanes (padding slots load nothing)
@@ -173,10 +182,10 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int hl = gi + 8 * nt;
-    const __nv_bfloat16* qr = q + (static_cast<int64_t>(tl.q_begin) * hq + g * G + hl) * kD;
+    const __nv_bfloat16* qr = q + (static_cast<int64_t>(q_begin + row_of(hl)) * hq + g * G + head_of(hl)) * kD;
 #pragma unroll
     for (int kc = 0; kc < kD / 16; ++kc) {
-      if (hl < G) {
+      if (hl < H) {
         const uint2 v = *reinterpret_cast<const uint2*>(qr + kc * 16 + 4 * t4);
         const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
         const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
@@ -189,6 +198,11 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   }
   float sl2 = kBlk ? 0.f : scale_log2 * k_scale[kvh];
   float log2_vs = 0.f, inv_vs = 1.f;
+  int qp[NT][2];  // positions of this thread's columns
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) qp[nt][c] = qpos + row_of(8 * nt + 2 * t4 + c);
   float m[NT][2], l[NT][2], oacc[kMD][NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -246,13 +260,13 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
       auto scaled = [&](float x) { return kBlk ? fmaf(x, sl2, log2_vs) : x * sl2; };
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
-        const bool va = kpos0 + 16 * mt <= qpos, vb2 = kpos0 + 16 * mt + 8 <= qpos;
+        const int ka = kpos0 + 16 * mt, kb2 = ka + 8;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          sacc[mt][nt][0] = va ? scaled(sacc[mt][nt][0]) : -INFINITY;
-          sacc[mt][nt][1] = va ? scaled(sacc[mt][nt][1]) : -INFINITY;
-          sacc[mt][nt][2] = vb2 ? scaled(sacc[mt][nt][2]) : -INFINITY;
-          sacc[mt][nt][3] = vb2 ? scaled(sacc[mt][nt][3]) : -INFINITY;
+          sacc[mt][nt][0] = ka <= qp[nt][0] ? scaled(sacc[mt][nt][0]) : -INFINITY;
+          sacc[mt][nt][1] = ka <= qp[nt][1] ? scaled(sacc[mt][nt][1]) : -INFINITY;
+          sacc[mt][nt][2] = kb2 <= qp[nt][0] ? scaled(sacc[mt][nt][2]) : -INFINITY;
+          sacc[mt][nt][3] = kb2 <= qp[nt][1] ? scaled(sacc[mt][nt][3]) : -INFINITY;
         }
       }
       uint32_t pb[kMT][NT][2];
@@ -294,8 +308,8 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
         }
       }
       if (!(ok = mbar_wait(bar_v, phase, err))) break;
-      if (kBlk && key0 + kKeys - 1 > qpos) {  // the unit with the query's own key
-        for (int w = (qpos + 1 - key0) * (kD / 4) + lane; w < kKeys * (kD / 4); w += 32) sts32(vb + 4 * w, 0u);
+      if (kBlk && key0 + kKeys - 1 > last) {  // the unit with the last query's own key
+        for (int w = (last + 1 - key0) * (kD / 4) + lane; w < kKeys * (kD / 4); w += 32) sts32(vb + 4 * w, 0u);
         fence_async_shared();  // before the next load overwrites the buffer
         __syncwarp();
       }
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   };
   const float vs = kBlk ? 1.f : v_scale[kvh];
   auto write = [&](int h, int d4, const Merged& r) {
-    const int64_t orow = static_cast<int64_t>(tl.q_begin) * hq + g * G + h;
+    const int64_t orow = static_cast<int64_t>(q_begin + row_of(h)) * hq + g * G + head_of(h);
     auto norm = [&](float x) { return r.l > 0.f ? x / r.l * vs : 0.f; };
     const __nv_bfloat162 a = __floats2bfloat162_rn(norm(r.o.x), norm(r.o.y));
     const __nv_bfloat162 b = __floats2bfloat162_rn(norm(r.o.z), norm(r.o.w));
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   };
   float4* cta_o = reinterpret_cast<float4*>(smem + L::kCtaOff);
   float2* cta_ml = ml + kWsWarps * L::kHeads;
-  for (int e = threadIdx.x; e < G * (kD / 4); e += kWsThreads) {
+  for (int e = threadIdx.x; e < H * (kD / 4); e += kWsThreads) {
     const int h = e / (kD / 4), d4 = e % (kD / 4);
     const Merged r = merge(
         kWsWarps, [&](int w) { return ml[w * L::kHeads + h]; },
@@ -389,7 +403,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   }
   if (cs == 1) return;
   cluster_sync();  // the row's CTAs have written their states
-  for (int e = rank * kWsThreads + threadIdx.x; e < G * (kD / 4); e += cs * kWsThreads) {
+  for (int e = rank * kWsThreads + threadIdx.x; e < H * (kD / 4); e += cs * kWsThreads) {
     const int h = e / (kD / 4);
     write(h, e % (kD / 4), merge(
         cs, [&](int w) { return ld_cluster_f2(smem_u32(cta_ml + h), w); },
@@ -398,16 +412,16 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
   cluster_sync();  // nobody leaves while its state may be read
 }
 
-template <bool kBlk, int D, int NT>
-cudaError_t launch_ws(const msa_plan_s* p, int n_tiles, const int32_t* tile_list, int cs, cudaStream_t st, const CUtensorMap& km, const CUtensorMap& vm,
+template <bool kBlk, int D, int NT, bool kFew = false>
+cudaError_t launch_ws(const msa_plan_s* p, int n_tiles, const int2* part_list, int cs, cudaStream_t st, const CUtensorMap& km, const CUtensorMap& vm,
                       const void* q, const int32_t* kv_indices, const int32_t* idx, const float* k_scale,
                       const float* v_scale, void* out, float* lse) {
-  auto kern = decode_ws_kernel<kBlk, D, NT>;
+  auto kern = decode_ws_kernel<kBlk, D, NT, kFew>;
   const int smem = WsSmem<D, NT>::kBytes + 1024;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (cs > 8) cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return launch_pdl_cluster(kern, dim3(n_tiles * p->hp * cs), cs, dim3(kWsThreads), smem, st, km, vm,
-                            static_cast<const __nv_bfloat16*>(q), p->tiles_d, tile_list, idx, kv_indices, p->num_pages, k_scale,
+                            static_cast<const __nv_bfloat16*>(q), p->tiles_d, part_list, idx, kv_indices, p->num_pages, k_scale,
                             v_scale, static_cast<__nv_bfloat16*>(out), lse, p->hq, p->hp, p->hp / p->hkv, p->topk, cs,
                             1.4426950408889634f / sqrtf(static_cast<float>(D)), p->err_d);
 }
@@ -425,11 +439,16 @@ cudaError_t launch_ws(const msa_plan_s* p, int n_tiles, const int32_t* tile_list
 //    8 rows, topk 256    56.6 |  137  72  39  24 [21.3]
 //   64 rows, topk 16, G 16  27.3 | 16.4 [12.9] 19.9
 // Two CTAs of different clusters on one SM cost more than the second half of
-// the row's parallelism brings.
-int row_cluster(const msa_plan_s* p, int n_tiles) {
+// the row's parallelism brings.  Large clusters are not placed as densely as the
+// SMs would allow: with one CTA an SM (two head tiles) 15 of 8 and 7 of 16 run at
+// once (16 rows, G 16, topk 16: 8 CTAs a row 16.1 us, 4 9.4; 8 rows, topk 200: 16
+// 32.1, 8 23.2).
+int row_cluster(const msa_plan_s* p, int n_tiles, int ctas_per_sm) {
   const int rows = n_tiles * p->hp;
+  auto fits = [&](int cs) { return cs < 8 || rows <= (cs == 8 ? 14 : 7) * ctas_per_sm; };
   int cs = 1;
-  while (cs < 16 && rows * cs * 2 <= p->num_sms && 2 * cs * kWsWarps <= kParts * p->topk && (cs < 8 || p->topk >= 128))
+  while (cs < 16 && rows * cs * 2 <= p->num_sms && 2 * cs * kWsWarps <= kParts * p->topk &&
+         (cs < 8 || p->topk >= 128) && fits(2 * cs))
     cs *= 2;
   return cs;
 }
@@ -444,8 +463,8 @@ bool decode_ws_applies(const msa_plan_s* p) {
 msa_status launch_attn_decode_ws(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,
                                  const int32_t* kv_indices, const int32_t* idx, const float* k_scale,
                                  const float* v_scale, void* out, float* lse, cudaStream_t st) {
-  const int32_t* tile_list = p->n_row_tiles > 0 ? p->aux_d + p->row_tiles_off : nullptr;
-  const int n_tiles = tile_list ? p->n_row_tiles : p->n_tiles;
+  const int2* part_list = p->n_row_parts > 0 ? reinterpret_cast<const int2*>(p->aux_d + p->row_parts_off) : nullptr;
+  const int n_tiles = part_list ? p->n_row_parts : p->n_tiles;
   CUtensorMap km, vm;
   const uint64_t dims[2] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->num_pages) * p->hkv * 128};
   const uint64_t str[1] = {static_cast<uint64_t>(p->d)};
@@ -453,12 +472,15 @@ msa_status launch_attn_decode_ws(const msa_plan_s* p, const void* q, const void*
   if (!encode_tensor_map(&km, 2, k_pages, dims, str, box, 0, p->d) ||
       !encode_tensor_map(&vm, 2, v_pages, dims, str, box, 0, p->d))
     return set_error(MSA_ERR_CUDA, "msa_sparse_attn: tensor map encoding failed");
-  const bool wide = p->hq / p->hp > 8;
-  const auto launch = p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK ? launch_ws<false, 128, 1>
-                      : p->d == 128 ? (wide ? launch_ws<true, 128, 2> : launch_ws<true, 128, 1>)
-                                    : (wide ? launch_ws<true, 64, 2> : launch_ws<true, 64, 1>);
-  const int cs = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK ? row_cluster(p, n_tiles) : 1;
-  return cuda_check(launch(p, n_tiles, tile_list, cs, st, km, vm, q, kv_indices, idx, k_scale, v_scale, out, lse),
+  const bool wide = (part_list ? p->row_part_heads : p->hq / p->hp) > 8;
+  const auto launch =
+      p->kv_dtype != MSA_KV_FP8_E4M3_BLOCK ? launch_ws<false, 128, 1>
+      : part_list ? (p->d == 128 ? (wide ? launch_ws<true, 128, 2, true> : launch_ws<true, 128, 1, true>)
+                                 : (wide ? launch_ws<true, 64, 2, true> : launch_ws<true, 64, 1, true>))
+                  : (p->d == 128 ? (wide ? launch_ws<true, 128, 2> : launch_ws<true, 128, 1>)
+                                 : (wide ? launch_ws<true, 64, 2> : launch_ws<true, 64, 1>));
+  const int cs = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK ? row_cluster(p, n_tiles, wide ? 1 : 2) : 1;
+  return cuda_check(launch(p, n_tiles, part_list, cs, st, km, vm, q, kv_indices, idx, k_scale, v_scale, out, lse),
                     "msa_sparse_attn: decode launch");
 }
 

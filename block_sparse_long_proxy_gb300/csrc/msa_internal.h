@@ -98,8 +98,9 @@ struct msa_plan_s {
   int32_t n_attn_units = 0;
   int32_t attn_split = 0;            // of them, the last ones that clusters share (block-scaled plans)
   int32_t attn_parts = 1;            // CTAs that share each of those
-  int64_t row_tiles_off = 0;         // tiles of one row that the decode kernel takes in a mixed batch
-  int32_t n_row_tiles = 0;           // (block-scaled plans that are not decode batches)
+  int64_t row_parts_off = 0;         // tiles of few rows that the decode kernel takes, as (tile, first row |
+  int32_t n_row_parts = 0;           // rows << 16) (block-scaled plans that are not decode batches)
+  int32_t row_part_heads = 0;        // the most query heads of such a part, times its rows
   uint32_t attn_packs = 0;           // bit lg: some tile has 2^lg heads side by side (block-scaled plans)
   int64_t proxy_attn_units_off = 0;  // backward proxy softmax work units
   int32_t n_proxy_attn_units = 0;

@@ -101,6 +101,13 @@ CASES = [
     _case("mixed batch two sets a head, many units", [1] * 30 + [700], _LENS[:30] + [1500], 64, 2, 4, 5, page_perm_seed=7),
     _case("mixed batch, rows alone", [1, 0, 1, 1], [900, 300, 77, 2000], 16, 2, 2, 6, page_perm_seed=7),
     _case("mixed batch G=16, many rows", [1] * 39 + [40], _LENS[:39] + [90], 64, 4, 4, 9, page_perm_seed=7),
+    # tiles of few rows through the decode kernel, in parts of 16 (row, head) columns: one and several parts a tile
+    _case("few rows G=8", [2] * 18 + [1, 4, 3], _LENS[:18] + [1, 129, 1500], 64, 8, 8, 5, page_perm_seed=7),
+    _case("few rows G=3", [5] * 3 + [6, 2, 1], [900, 5, 133, 2000, 129, 70], 6, 2, 2, 6, page_perm_seed=7),
+    _case("few rows G=1", [16] * 3 + [130, 2], [900, 16, 133, 2000, 129], 4, 2, 4, 6, page_perm_seed=7),
+    _case("few rows G=16", [3] * 3 + [1], [900, 3, 133, 2000], 16, 1, 1, 6, page_perm_seed=7),
+    _case("few rows G=5 d64", [3] * 6 + [200], [900, 3, 133, 2000, 128, 130, 700], 10, 2, 2, 4, d=64, page_perm_seed=7),
+    _case("few rows topk 200", [4], [40000], 4, 1, 1, 200, page_perm_seed=7),
     _case("d64 mixed batch", [1] * 5 + [150, 33], [900, 1, 2000, 129, 77, 500, 333], 10, 2, 2, 6, d=64, page_perm_seed=7),
     # head_dim 64
     _case("d64 parts 8", [130], [9000], 6, 1, 2, 24, d=64, page_perm_seed=3),
