@@ -159,6 +159,20 @@ def test_irregular_selections_in_parts(cuda_dev):
         _check(case, inp, idx, out, lse)
 
 
+@pytest.mark.parametrize("hq, hkv, rows", [(64, 8, 2), (6, 2, 5), (8, 8, 16), (48, 4, 3)])
+def test_irregular_selections_few_rows(cuda_dev, hq, hkv, rows):
+    """Tiles of few rows, some crossing a page, whose selections leave rows of a
+    tile without a key."""
+    kv = [max(k, rows) for k in _LENS[:17]] + [129, 130, 256 + rows // 2]
+    case = _case("irregular few", [min(rows, 1 + i % rows) for i in range(20)], kv, hq, hkv, hkv, 6, page_perm_seed=4)
+    inp = synth.make_inputs(case, device=cuda_dev)
+    for seed in (9, 10):
+        idx = irregular_idx(case, np.random.default_rng(seed))
+        out, lse = _attend(case, inp, idx, cuda_dev)
+        assert np.isneginf(lse.cpu().numpy()).any()
+        _check(case, inp, idx, out, lse)
+
+
 @pytest.mark.parametrize("batch", [1, 20])
 @pytest.mark.parametrize("decode", [True, False])
 def test_scales_far_apart(cuda_dev, decode, batch):
