@@ -107,10 +107,13 @@ def _need(t, dtype, shape, name):
         raise ValueError("%s: must be a contiguous CUDA tensor on the current device" % name)
 
 
-def _need_all(tensors, needs):
-    """_need of several tensors; needs: their (dtype, shape, name)."""
+def _need_all(tensors, needs, optional=False):
+    """_need of several tensors, None passed over where `optional`; needs: their
+    (dtype, shape, name)."""
     dev = _current_device()
     for t, need in zip(tensors, needs):
+        if t is None and optional:
+            continue
         dtype, shape, _ = need
         if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
             _need(t, *need)
@@ -270,7 +273,7 @@ class Plan:
         self._nvp_raw = nvp_ptr
         self.num_valid_pages = _device_view_int32(nvp_ptr, self.n_tiles, torch.cuda.current_device())
         self.num_valid_pages_host = None
-        # what sparse_attn and kv_append check of their tensors, made once
+        # what the calls around a step check of their tensors, made once
         kvt = torch.bfloat16 if kv_dtype == "bf16" else torch.float8_e4m3fn
         pool = (self.num_pages, self.hkv, 128, self.d)
         self._rows_shape = (self.total_q, self.hkv, self.d)
@@ -280,6 +283,15 @@ class Plan:
         if kv_dtype != "bf16":
             shape = (self.hkv,) if kv_dtype == "e4m3" else (self.num_pages, self.hkv)
             self._cache_needs += ((torch.float32, shape, "k_scale"), (torch.float32, shape, "v_scale"))
+        pos, ppool = (torch.int32, (self.total_q,), "positions"), (self.num_pages, 1, 128)
+        self._pk_needs = ((torch.bfloat16, ppool + (self.dp,), "pk_pages"),
+                          (torch.float8_e4m3fn, ppool + (self.dp,), "pk_pages_e4m3"), (torch.float32, (1,), "pk_scale"),
+                          (torch.uint8, ppool + (self.dp // 2,), "pk_codes"),
+                          (torch.float8_e4m3fn, ppool + (self.dp // 16,), "pk_block_scales"),
+                          (torch.float32, (1,), "pk_global_scale"), pos, self._cache_needs[0])
+        self._pk_shape = (self.total_q, 1, self.dp)
+        self._grad_needs = ((torch.float32, pool, "dk_pages"), (torch.float32, pool, "dv_pages"),
+                            (torch.float32, ppool + (self.dp,), "dpk_pages"), pos, self._cache_needs[0])
         self._attn_needs = self._cache_needs + ((torch.bfloat16, self._q_shape, "q"), (
             torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes"))
 
@@ -309,21 +321,11 @@ class Plan:
                   pk_block_scales=None, pk_global_scale=None, rope=None, positions=None, stream=None):
         """The batch's new proxy K rows [total_q, 1, dp] bf16 into the pools given
         (msa_pk_append): bf16, e4m3 with pk_scale, NVFP4 with its scales."""
-        pool = (self.num_pages, 1, 128)
-        pk_stride = _rows(pk, torch.bfloat16, (self.total_q, 1, self.dp), "pk")
-        _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
-        for t, dtype, shape, name in (
-                (pk_pages, torch.bfloat16, pool + (self.dp,), "pk_pages"),
-                (pk_pages_e4m3, torch.float8_e4m3fn, pool + (self.dp,), "pk_pages_e4m3"),
-                (pk_scale, torch.float32, (1,), "pk_scale"),
-                (pk_codes, torch.uint8, pool + (self.dp // 2,), "pk_codes"),
-                (pk_block_scales, torch.float8_e4m3fn, pool + (self.dp // 16,), "pk_block_scales"),
-                (pk_global_scale, torch.float32, (1,), "pk_global_scale"),
-                (positions, torch.int32, (self.total_q,), "positions")):
-            if t is not None:
-                _need(t, dtype, shape, name)
-        _check(_lib.msa_pk_append(self._h, rope and rope._h, _ptr(positions), _ptr(pk), pk_stride,
-                                  _ptr(kv_indices), _ptr(pk_pages), _ptr(pk_pages_e4m3), _ptr(pk_scale),
+        pk_stride = _rows(pk, torch.bfloat16, self._pk_shape, "pk")
+        _need_all((pk_pages, pk_pages_e4m3, pk_scale, pk_codes, pk_block_scales, pk_global_scale, positions, kv_indices),
+                  self._pk_needs, optional=True)
+        _check(_lib.msa_pk_append(self._h, rope and rope._h, _ptr(positions), pk.data_ptr(), pk_stride,
+                                  kv_indices.data_ptr(), _ptr(pk_pages), _ptr(pk_pages_e4m3), _ptr(pk_scale),
                                   _ptr(pk_codes), _ptr(pk_block_scales), _ptr(pk_global_scale), _stream(stream)),
                "msa_pk_append")
 
@@ -332,20 +334,15 @@ class Plan:
         """Gradients of the appended rows from the gradient pages of
         sparse_attn_bwd (msa_append_bwd): (dk, dv [total_q, Hkv, d], dpk
         [total_q, 1, dp]) fp32, None where no pages are given."""
-        _need(kv_indices, torch.int32, (self.n_page_entries,), "kv_indices")
-        if positions is not None:
-            _need(positions, torch.int32, (self.total_q,), "positions")
-        rows = []
-        for pages, heads, d, name in ((dk_pages, self.hkv, self.d, "dk_pages"), (dv_pages, self.hkv, self.d, "dv_pages"),
-                                      (dpk_pages, 1, self.dp, "dpk_pages")):
-            if pages is not None:
-                _need(pages, torch.float32, (self.num_pages, heads, 128, d), name)
-            rows.append(None if pages is None else torch.empty((self.total_q, heads, d), dtype=torch.float32,
-                                                               device=pages.device))
+        _need_all((dk_pages, dv_pages, dpk_pages, positions, kv_indices), self._grad_needs, optional=True)
+        dev = kv_indices.device
+        dk, dv, dpk = (None if pages is None else torch.empty(shape, dtype=torch.float32, device=dev)
+                       for pages, shape in ((dk_pages, self._rows_shape), (dv_pages, self._rows_shape),
+                                            (dpk_pages, self._pk_shape)))
         _check(_lib.msa_append_bwd(self._h, k_rope and k_rope._h, pk_rope and pk_rope._h, _ptr(positions),
-                                   _ptr(kv_indices), _ptr(dk_pages), _ptr(dv_pages), _ptr(dpk_pages),
-                                   *(_ptr(r) for r in rows), _stream(stream)), "msa_append_bwd")
-        return tuple(rows)
+                                   kv_indices.data_ptr(), _ptr(dk_pages), _ptr(dv_pages), _ptr(dpk_pages), _ptr(dk),
+                                   _ptr(dv), _ptr(dpk), _stream(stream)), "msa_append_bwd")
+        return dk, dv, dpk
 
     # -- stage 1
     def proxy_maxscore(self, pq, pk_pages, kv_indices, out=None, stream=None):
