@@ -43,8 +43,8 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 NCU_TRAFFIC = {
     # (DRAM bytes read + written) of one launch of the small S=16384 capture and the
     # (tile, group, block) selections it processed; scaled to a launch by selections.
-    "attn_fwd.cu": {"src": "1d4231ba0160569e", "bytes": 245725440 + 108027392, "sel": 15424},
-    "attn_fwd.cu:fp8": {"src": "1d4231ba0160569e", "bytes": 180717056 + 101520640, "sel": 15424},
+    "attn_fwd.cu": {"src": "dfd07b8e3f3a76e5", "bytes": 246252032 + 107771136, "sel": 15424},
+    "attn_fwd.cu:fp8": {"src": "dfd07b8e3f3a76e5", "bytes": 180852736 + 100995584, "sel": 15424},
 }
 
 

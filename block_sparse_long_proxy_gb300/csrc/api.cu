@@ -482,10 +482,10 @@ msa_status msa_sparse_attn(msa_plan_t plan, const void* q, const void* k_pages, 
   const bool wide = plan->kv_dtype == MSA_KV_FP8_E4M3_BLOCK && plan->hq / plan->hp > 16;
   const bool decode = fp8 && plan->decode && !wide;
   msa_status s = MSA_OK;
-  if (decode || plan->n_row_parts > 0)
-    s = launch_attn_decode(plan, q, k_pages, v_pages, kv_indices, kv_block_indexes, k_scale, v_scale, out, lse, st);
-  if (s == MSA_OK && !decode && plan->n_attn_units > 0)
+  if (!decode && plan->n_attn_units > 0)
     s = launch_attn_prefill(plan, q, k_pages, v_pages, kv_indices, kv_block_indexes, k_scale, v_scale, out, lse, st);
+  if (s == MSA_OK && (decode || plan->n_row_parts > 0))
+    s = launch_attn_decode(plan, q, k_pages, v_pages, kv_indices, kv_block_indexes, k_scale, v_scale, out, lse, st);
   const int64_t rows = plan->total_q * plan->hq;
   const int kv_elem = fp8 ? 1 : 2;
   const int64_t per_page = int64_t(plan->hkv) * 128 * plan->d;

@@ -140,7 +140,7 @@ struct AttnSmem {
 // barrier's phase comes from a running count (per head for the S / P / O
 // barriers), and Q is released right after a unit's last QK so the next
 // unit's Q load overlaps the tail of the current one.
-template <int D, bool kOneKvHead, bool kFp8, bool kStageO, bool kBlk = false, bool kSplit = false>
+template <int D, bool kOneKvHead, bool kFp8, bool kStageO, bool kBlk = false, bool kSplit = false, bool kLead = false>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_fwd_kernel(const __grid_constant__ QueryMaps<kBlk> q_maps, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap o_map,
@@ -149,8 +149,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int32_t* __restrict__ kv_indices, int64_t num_pages, __nv_bfloat16* __restrict__ out,
                     float* __restrict__ lse, int32_t hq, int32_t hsel, int32_t kv_div, int32_t topk,
                     float scale_log2, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
-                    int32_t parts, uint32_t* err) {
-  pdl_wait();
+                    int32_t parts, uint32_t* err, int32_t chain) {
+  if (!kSplit || !(chain & kFollows)) pdl_wait();
+  // a variant of its own: the call alone costs the others 1 % (32K prefill 862 -> 870 us)
+  if (kLead || (kSplit && (chain & kLeads))) pdl_trigger();
   // kBlk: a unit of a tile of few rows has 2^lg heads side by side in the 128
   // rows of a product, row r being query row r >> lg of head r % 2^lg; "head" 0
   // and 1 of a unit are then such groups
@@ -972,6 +974,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     }
     cluster_sync();  // nobody leaves while its part may be read
+    if ((chain & kFollows) && threadIdx.x == 0) pdl_wait();
   }
 }
 
@@ -1043,7 +1046,7 @@ static int slots_of(int heads, int lg) { return (heads + (1 << lg) - 1) >> lg; }
 // units, or those that a last, short round would be left with, in a launch of
 // their own.  A block step takes about 1.65 us for a head and 1.78 for two (0.35
 // more where no other unit reads the same blocks, which then come from HBM), a
-// unit 6 besides, the merge 3 and a second launch 10.  Clusters of 8 are not
+// unit 6 besides, the merge 3 and a second launch 6.  Clusters of 8 are not
 // placed as densely as the SMs would allow: 15 run at once.
 // Measured (us; heads a unit / parts):
 //   rows x heads, blocks     1/1    1/2    1/4    1/8    2/1    2/2    2/4
@@ -1085,7 +1088,7 @@ static UnitShape unit_shape(const msa_plan_s* p, int apart) {
     take((rounds + (rest > 0)) * unit * (heads == 1 && units > sms ? 1.1 : 1.0), 0, 1);
     for (int parts = 2; parts <= 8 && parts <= blocks && rest > 0; parts *= 2)
       if (rest * parts <= (parts < 8 ? sms - 8 : sms * 3 / 4))
-        take(rounds * unit + (rounds > 0 ? 10 : 0) + (blocks + parts - 1) / parts * step + 9, rest, parts);
+        take(rounds * unit + (rounds > 0 ? 6 : 0) + (blocks + parts - 1) / parts * step + 9, rest, parts);
   }
   return best;
 }
@@ -1114,12 +1117,14 @@ void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   UnitShape shape = unit_shape(p, 0);
   // block scales: tiles of few rows in a launch of the decode kernel where that
   // is done sooner.  Measured (us, 16 blocks; all as tiles -> so):
-  //   32 x 1 + 512 rows, 64 / 8 heads   107 -> 69.4      64 x 4, 32 / 8   136 -> 70.6
-  //   64 x 1 + 2048 rows, 64 / 8        240 -> 201       16 x 4, 32 / 8  39.9 -> 16.7
+  //   32 x 1 + 512 rows, 64 / 8 heads   107 -> 66.0      64 x 4, 32 / 8   136 -> 70.6
+  //   64 x 1 + 2048 rows, 64 / 8        240 -> 203       16 x 4, 32 / 8  39.9 -> 16.7
   //   32 x 2 rows, 64 / 8              73.4 -> 35.5      16 x 8, 32 / 8  39.8 -> 31.7
   //   32 x 4 rows, 64 / 8 (two parts)  73.2 -> 66.3       8 x 2, 64 / 8  25.9 -> 12.7
   // and where it is not: 16 x 4 rows, 64 / 4 (four parts) 26.8, 31.0; 30 x 9 rows,
-  // 128 / 8, 2 blocks 21.9, 89; 4 x 1 + 128 rows, 16 / 2 17.4, 25.9.
+  // 128 / 8, 2 blocks 21.9, 89; 4 x 1 + 128 rows, 16 / 2 17.4, 25.9.  That launch
+  // comes last and starts as the others' SMs fall idle (kFollows): 6 ragged chunks,
+  // 12 / 4 heads, 9 blocks, 40.9 -> 32.5 us.
   const int most = 16 / grp;  // rows a part of those
   int apart = 0;
   std::vector<int32_t> parts;  // two words each
@@ -1198,28 +1203,34 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const QueryMaps<kBlk
                                 int32_t n_units, const TileInfo* tiles, const int32_t* idx,
                                 const int32_t* kv_indices, int64_t num_pages, __nv_bfloat16* o, float* lse,
                                 int32_t hq, int32_t hsel, int32_t kv_div, float scale_log2, const float* k_scale,
-                                const float* v_scale, uint32_t* err, int parts = 1) {
+                                const float* v_scale, uint32_t* err, int parts = 1, int chain = 0) {
   const int cap = (topk + 3) & ~3;
   if constexpr (kFp8) {
     const int staged = AttnSmem<D, true, kOneKvHead ? 2 : 1, kBlk>::bytes(cap) + 1024;
     if (staged <= kMaxSmem && parts == 1) {
       auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, true, kBlk>;
+      if constexpr (kBlk)
+        if (chain & kLeads) kern = attn_fwd_kernel<D, kOneKvHead, kFp8, true, true, false, true>;
       if (const cudaError_t e = check_launch_regs(kern)) return e;
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, staged);
       return launch_pdl_cluster(kern, grid, 1, dim3(kAttnThreads), staged, st, qm, km, vm, om, cap, units, n_units,
                                 tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
-                                v_scale, 1, err);
+                                v_scale, 1, err, chain);
     }
   }
   const int plain = AttnSmem<D, false, kOneKvHead ? 2 : 1, kBlk>::bytes(kMaxTopk) + 1024;
   auto kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false, kBlk>;
-  if constexpr (kBlk)
-    if (parts > 1) kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false, true, true>;
+  if constexpr (kBlk) {
+    if (parts > 1)
+      kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false, true, true>;
+    else if (chain & kLeads)
+      kern = attn_fwd_kernel<D, kOneKvHead, kFp8, false, true, false, true>;
+  }
   if (const cudaError_t e = check_launch_regs(kern)) return e;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plain);
   return launch_pdl_cluster(kern, grid, parts, dim3(kAttnThreads), plain, st, qm, km, vm, om, cap, units, n_units,
                             tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
-                            v_scale, parts, err);
+                            v_scale, parts, err, chain);
 }
 
 // [total_q, heads, D] bf16 rows as 3-D boxes of 64 columns x 1 head x 128 rows, 128-byte swizzle
@@ -1267,13 +1278,15 @@ msa_status launch_attn_prefill(const msa_plan_s* p, const void* q, const void* k
     const auto launch = p->d == 128 ? launch_attn_variant<128, false, true, true>
                                     : launch_attn_variant<64, false, true, true>;
     const int whole = p->n_attn_units - p->attn_split;
-    auto run = [&](int ctas, const AttnUnit* first, int n, int parts) {
+    auto run = [&](int ctas, const AttnUnit* first, int n, int parts, int chain) {
       return launch(dim3(ctas), st, qms, km, vm, om, p->topk, first, n, p->tiles_d, idx, kv_indices, p->num_pages, o, lse,
-                    p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d, parts);
+                    p->hq, p->hp, kv_div, scale_log2, k_scale, v_scale, p->err_d, parts, chain);
     };
-    e = whole > 0 ? run(std::min(whole, p->num_sms), units, whole, 1) : cudaSuccess;
+    e = whole > 0 ? run(std::min(whole, p->num_sms), units, whole, 1, p->attn_split > 0 || p->n_row_parts > 0 ? kLeads : 0)
+                  : cudaSuccess;
     if (e == cudaSuccess && p->attn_split > 0)
-      e = run(p->attn_split * p->attn_parts, units + whole, p->attn_split, p->attn_parts);
+      e = run(p->attn_split * p->attn_parts, units + whole, p->attn_split, p->attn_parts,
+              (whole > 0 ? kFollows : 0) | (p->n_row_parts > 0 ? kLeads : 0));
   } else if (fp8)
     e = launch_attn_variant<128, false, true>(grid, st, qm, km, vm, om, p->topk, units, p->n_attn_units, p->tiles_d,
                                               idx, kv_indices, p->num_pages, o, lse, p->hq, p->hp, kv_div, scale_log2,

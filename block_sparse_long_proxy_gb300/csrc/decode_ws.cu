@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
                      const int2* __restrict__ part_list, const int32_t* __restrict__ idx, const int32_t* __restrict__ kv_indices, int64_t num_pages,
                      const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int32_t hq, int32_t hsel,
-                     int32_t kv_div, int32_t topk, int32_t cs, float scale_log2, uint32_t* err) {
-  pdl_wait();
+                     int32_t kv_div, int32_t topk, int32_t cs, float scale_log2, int32_t chain, uint32_t* err) {
+  if (!kFew || !(chain & kFollows)) pdl_wait();
   using L = WsSmem<kD, NT>;
   constexpr int kPartBytes = L::kPartBytes, kBufBytes = L::kBufBytes, kMD = kD / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -401,7 +401,10 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
       if (d4 == 0) cta_ml[h] = make_float2(r.m, r.l);
     }
   }
-  if (cs == 1) return;
+  auto done = [&] {
+    if (kFew && (chain & kFollows) && threadIdx.x == 0) pdl_wait();
+  };
+  if (cs == 1) return done();
   cluster_sync();  // the row's CTAs have written their states
   for (int e = rank * kWsThreads + threadIdx.x; e < H * (kD / 4); e += cs * kWsThreads) {
     const int h = e / (kD / 4);
@@ -410,6 +413,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
         [&](int w) { return ld_cluster_f4(smem_u32(cta_o + e), w); }));
   }
   cluster_sync();  // nobody leaves while its state may be read
+  done();
 }
 
 template <bool kBlk, int D, int NT, bool kFew = false>
@@ -423,7 +427,8 @@ cudaError_t launch_ws(const msa_plan_s* p, int n_tiles, const int2* part_list, i
   return launch_pdl_cluster(kern, dim3(n_tiles * p->hp * cs), cs, dim3(kWsThreads), smem, st, km, vm,
                             static_cast<const __nv_bfloat16*>(q), p->tiles_d, part_list, idx, kv_indices, p->num_pages, k_scale,
                             v_scale, static_cast<__nv_bfloat16*>(out), lse, p->hq, p->hp, p->hp / p->hkv, p->topk, cs,
-                            1.4426950408889634f / sqrtf(static_cast<float>(D)), p->err_d);
+                            1.4426950408889634f / sqrtf(static_cast<float>(D)), kFew && p->n_attn_units > 0 ? kFollows : 0,
+                            p->err_d);
 }
 
 // CTAs a row: one for an SM at most, with a unit for every warp; clusters of

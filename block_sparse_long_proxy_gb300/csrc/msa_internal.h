@@ -142,6 +142,13 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return launch_pdl_cluster(kernel, grid, 1, block, smem, st, static_cast<Args&&>(args)...);
 }
 
+// Launches of one call that need nothing of each other run without a gap: all
+// but the last let the next one start early (kLeads), and all but the first
+// (kFollows) wait for the one before at their end instead of their start.  The
+// first of them waits for the stream's work before it lets the next one start,
+// and whatever follows the last finds all of them complete.
+enum : int32_t { kLeads = 1, kFollows = 2 };
+
 msa_status set_error(msa_status s, const char* fmt, ...);
 msa_status cuda_check(cudaError_t e, const char* what);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -21,6 +21,10 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // launch attribute it returns at once.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next kernel of the stream, if it was launched so, start once every
+// CTA of this one has called it (its pdl_wait still waits for this kernel's end).
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ uint64_t global_timer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
