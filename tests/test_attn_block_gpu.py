@@ -368,6 +368,49 @@ def test_calls_overlap_on_two_streams(cuda_dev):
             assert all(torch.equal(a[0], x) and torch.equal(a[1], y) for x, y in o)
 
 
+@pytest.mark.parametrize("qo, hq", [([1] * 20 + [260], 64), ([700, 3, 80, 500], 12), ([2] * 12, 16)])
+def test_steps_back_to_back(cuda_dev, qo, hq):
+    """A call's launches overlap each other, never the calls around them: appends
+    over the same slots and attention in turn, without a pause and as a graph,
+    give what they give one at a time."""
+    hkv, n = 4 if hq == 12 else 8, 12
+    case = _case("steps", qo, [q + 900 for q in qo], hq, hkv, hkv, 9, page_perm_seed=3)
+    inp = synth.make_inputs(case, device=cuda_dev)
+    plan = make_plan(case, inp)
+    idx = torch.from_numpy(random_idx(case, np.random.default_rng(1))).to(cuda_dev)
+    gen = torch.Generator(device=cuda_dev).manual_seed(3)
+    new = torch.randn((n, 2, sum(qo), hkv, 128), generator=gen, device=cuda_dev).bfloat16()
+    cache = [inp[name] for name in ("k_pages", "v_pages")]
+    scales = dict(k_scale=inp["k_scale"], v_scale=inp["v_scale"])
+    outs = torch.zeros((n,) + tuple(inp["q"].shape), dtype=torch.bfloat16, device=cuda_dev)
+    lse = torch.zeros((n, sum(qo), hq), device=cuda_dev)
+    copies = torch.zeros_like(outs)
+
+    def step(i):
+        plan.kv_append(new[i, 0], new[i, 1], *cache, inp["kv_indices"], **scales)
+        plan.sparse_attn(inp["q"], *cache, inp["kv_indices"], idx, out=outs[i], lse=lse[i], **scales)
+        copies[i].copy_(outs[i])
+    for i in range(n):
+        step(i)
+        torch.cuda.synchronize()
+    # a page's scale only grows while rows go behind others: the second pass starts where it ended
+    for i in range(n):
+        step(i)
+        torch.cuda.synchronize()
+    alone = outs.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(n):
+            step(i)
+    for run in (lambda: [step(i) for i in range(n)], graph.replay, graph.replay):
+        for t in (outs, lse, copies):
+            t.zero_()
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(outs, alone[0]) and torch.equal(lse, alone[1]) and torch.equal(copies, outs)
+    plan.check_errors()
+
+
 @pytest.mark.parametrize("qo", [1, 60])
 def test_pages_beyond_4_gib(cuda_dev, qo):
     """The last pages of pools of more than 2^32 bytes: append and attend as on
