@@ -501,8 +501,11 @@ cudaError_t launch_kv(const msa_plan_s* p, const RopeTable& tab, KvAppendArgs a,
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   a.k_ctas = p->n_append_units * a.groups[0];
   auto kern = kv_append_kernel<D, KIND>;
-  const int smem = (p->decode ? 1 : 128) * D * 4;  // (cos, sin) of D / 2 pairs of a page's rows
-  if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  constexpr int kRowBytes = D * 4;  // (cos, sin) of D / 2 pairs of a row
+  const int smem = (p->decode ? 1 : 128) * kRowBytes;
+  // the limit is the function's, for every host thread: always the most of any plan
+  if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * kRowBytes))
+    return e;
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kKvThreads), smem, st, tab, a);
 }
 

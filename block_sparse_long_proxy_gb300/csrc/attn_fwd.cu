@@ -1212,7 +1212,8 @@ cudaError_t launch_attn_variant(dim3 grid, cudaStream_t st, const QueryMaps<kBlk
       if constexpr (kBlk)
         if (chain & kLeads) kern = attn_fwd_kernel<D, kOneKvHead, kFp8, true, true, false, true>;
       if (const cudaError_t e = check_launch_regs(kern)) return e;
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, staged);
+      // the limit is the function's, for every host thread: always the most of any topk
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
       return launch_pdl_cluster(kern, grid, 1, dim3(kAttnThreads), staged, st, qm, km, vm, om, cap, units, n_units,
                                 tiles, idx, kv_indices, num_pages, o, lse, hq, hsel, kv_div, topk, scale_log2, k_scale,
                                 v_scale, 1, err, chain);
