@@ -17,17 +17,16 @@
 
 namespace msa {
 
-static thread_local std::string g_last_error;
+// a fixed buffer: the message of a call that found no memory needs none
+static thread_local char g_last_error[512] = "";
 // Allocation failures still to inject into msa_plan (msa_test_fail_plan_allocs).
 static std::atomic<int32_t> g_fail_allocs{0};
 
 msa_status set_error(msa_status s, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return s;
 }
 
@@ -224,7 +223,7 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
 
 extern "C" {
 
-const char* msa_last_error(void) { return g_last_error.c_str(); }
+const char* msa_last_error(void) { return g_last_error; }
 const char* msa_version(void) { return "0.1.0"; }
 
 msa_status msa_plan(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batch, int32_t num_qo_heads,

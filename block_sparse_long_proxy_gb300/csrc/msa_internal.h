@@ -6,7 +6,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <string>
 #include <vector>
 
 #include "../../include/msa.h"

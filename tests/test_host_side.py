@@ -93,3 +93,27 @@ assert launches >= 60 and len(limits) >= 12, (launches, len(limits))
 apart = {hex(f): sorted(v) for f, v in limits.items() if len(v) > 1}
 assert not apart, apart
 """)
+
+
+# plans whose tables differ: prefill and its backward, decode, block scales with tiles of few rows apart
+BATCHES = """
+BATCHES = [([300, 77, 2000], [300, 1000, 2100], 16, 4, 128, 6, BF16), ([1] * 9, [700 + i for i in range(9)], 16, 4, 128, 6, E4M3),
+           ([1] * 30 + [700, 4], [900] * 30 + [1500, 70], 64, 4, 128, 9, BLOCK)]
+"""
+
+
+def test_out_of_host_memory_is_a_status(child):
+    """No allocation left from the nth on, whichever that is: msa_plan answers
+    MSA_ERR_NO_MEMORY and has a message, which needs no memory either."""
+    child(BATCHES + """
+for batch in BATCHES:
+    for n in range(100000):
+        fake.fake_fail(n, -1)
+        s, h = plan(*batch)
+        fake.fake_fail(-1, -1)
+        if s == 0:
+            break
+        assert s == 4 and not h and lib.msa_last_error() == b"msa_plan: out of host memory", (n, s, lib.msa_last_error())
+    assert n > 20
+    lib.msa_plan_destroy(h)
+""")
