@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <atomic>
 #include <exception>
+#include <memory>
 #include <mutex>
 
 #include "msa_internal.h"
@@ -269,7 +270,9 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
     return set_error(MSA_ERR_INVALID_ARG, "msa_plan: num_pages * num_kv_heads above 2^24");
   if (flags != 0) return set_error(MSA_ERR_INVALID_ARG, "msa_plan: flags must be 0");
 
-  auto* p = new msa_plan_s();
+  // whatever ends this early, an exception too, gives back what the plan has by then
+  std::unique_ptr<msa_plan_s, decltype(&msa_plan_destroy)> owner(new msa_plan_s(), msa_plan_destroy);
+  msa_plan_s* const p = owner.get();
   p->batch = batch;
   p->hq = num_qo_heads;
   p->hkv = num_kv_heads;
@@ -286,10 +289,8 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
   bool all_one = true;
   for (int s = 0; s < batch; ++s) {
     const int64_t ql = qo_lens[s], kl = kv_lens[s];
-    if (ql < 0 || kl < 1 || ql > kl) {
-      delete p;
+    if (ql < 0 || kl < 1 || ql > kl)
       return set_error(MSA_ERR_INVALID_ARG, "msa_plan: sequence %d needs 0 <= qo_len <= kv_len and kv_len >= 1", s);
-    }
     if (ql != 1) all_one = false;
     const int64_t nb = (kl + kPage - 1) / kPage;
     p->max_blocks = static_cast<int32_t>(std::max<int64_t>(p->max_blocks, nb));
@@ -308,10 +309,8 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
     }
     q0 += ql;
     page_base += nb;
-    if (q0 > (int64_t(1) << 31) - 1 || page_base > (int64_t(1) << 31) - 1) {
-      delete p;
+    if (q0 > (int64_t(1) << 31) - 1 || page_base > (int64_t(1) << 31) - 1)
       return set_error(MSA_ERR_INVALID_ARG, "msa_plan: batch too large for 32-bit row / page indexing");
-    }
   }
   p->total_q = q0;
   p->n_page_entries = static_cast<int32_t>(page_base);
@@ -321,16 +320,12 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
     const char* c = getenv("MSA_CHECKS");
     p->checks = c != nullptr && c[0] != '\0' && strcmp(c, "0") != 0;
   }
-  if (p->n_tiles == 0) {
-    delete p;
+  if (p->n_tiles == 0)
     return set_error(MSA_ERR_INVALID_ARG, "msa_plan: no query rows in the batch");
-  }
 
   if (cudaGetDevice(&p->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess) {
-    delete p;
+      cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess)
     return set_error(MSA_ERR_CUDA, "msa_plan: no CUDA device");
-  }
 
   std::vector<int32_t> aux;
   proxy_plan_tables(p, aux);
@@ -352,13 +347,10 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
   int32_t inject = g_fail_allocs.load();
   while (inject > 0 && !g_fail_allocs.compare_exchange_weak(inject, inject - 1)) {
   }
-  if (inject > 0) {  // an injected failure: the same path as a real one, without the call
-    delete p;
+  if (inject > 0)  // an injected failure: the same path as a real one, without the call
     return set_error(MSA_ERR_NO_MEMORY, "msa_plan: cudaMalloc of %zu bytes failed (injected)", total);
-  }
   if (cudaMalloc(&p->dev_block, total) != cudaSuccess) {
     cudaGetLastError();
-    delete p;
     return set_error(MSA_ERR_NO_MEMORY, "msa_plan: cudaMalloc of %zu bytes failed", total);
   }
   char* base = static_cast<char*>(p->dev_block);
@@ -383,12 +375,8 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
   if (s == MSA_OK && p->fused_topk_d)  // the fused top-k's row counters start at zero
     s = cuda_check(cudaMemsetAsync(p->fused_topk_d, 0, fused_topk_counter_bytes(p), st), "msa_plan: clear counters");
   if (s == MSA_OK) s = cuda_check(cudaStreamSynchronize(st), "msa_plan: upload sync");
-  if (s != MSA_OK) {
-    cudaFree(p->dev_block);
-    delete p;
-    return s;
-  }
-  *out = p;
+  if (s != MSA_OK) return s;
+  *out = owner.release();
   return MSA_OK;
 }
 

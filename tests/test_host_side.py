@@ -117,3 +117,29 @@ for batch in BATCHES:
     assert n > 20
     lib.msa_plan_destroy(h)
 """)
+
+
+def test_a_failed_plan_leaves_nothing_behind(child):
+    """Whichever allocation fails, of the host's or the device's, what came before
+    it is given back; and so is all of a plan that is destroyed."""
+    child(BATCHES + """
+left = lambda: (fake.fake_live_host(), fake.fake_live_device())
+for batch in BATCHES:
+    before = left()
+    for n in range(100000):
+        fake.fake_fail(n, -1)
+        s, h = plan(*batch)
+        fake.fake_fail(-1, -1)
+        if s == 0:
+            break
+        assert s == 4 and left() == before, (n, s, before, left())
+    assert left()[0] > before[0] and left()[1] == before[1] + 1
+    lib.msa_plan_destroy(h)
+    assert left() == before
+    fake.fake_fail(-1, 0)
+    s, h = plan(*batch)
+    fake.fake_fail(-1, -1)
+    assert s == 4 and left() == before
+    for bad in ((batch[0], [0] * len(batch[0])), ([0] * len(batch[0]), batch[1])):
+        assert plan(*bad, *batch[2:])[0] == 1 and left() == before
+""")
