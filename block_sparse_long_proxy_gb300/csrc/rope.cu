@@ -18,6 +18,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <cmath>
 #include <new>
 
 #include "ptx.cuh"
@@ -111,6 +112,54 @@ msa_status launch_rope(const RopeTable& tab, const void* x, int64_t xs, const in
                     "msa_rope_apply: launch");
 }
 
+// Double-double numbers hi + lo (Dekker 1971, Knuth's two-sum): the table holds
+// 64 bits of a turn, and a position of 2^31 leaves the phase an error of 2^31
+// times the table's.
+struct DD {
+  double hi, lo;
+};
+DD two_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+DD operator+(DD a, DD b) {
+  const DD s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+DD operator*(DD a, DD b) {
+  const double p = a.hi * b.hi;
+  return two_sum(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+DD operator-(DD a) { return {-a.hi, -a.lo}; }
+DD operator/(DD a, DD b) {
+  const double q = a.hi / b.hi;
+  const DD r = a + -(b * DD{q, 0.0});
+  return two_sum(q, r.hi / b.hi);
+}
+// 2^k e^r with |r| <= ln 2 / 2, e^r as the 2^9th power of a Taylor sum; 1 is kept
+// apart until the end, since the squarings would multiply its rounding
+DD dd_exp(DD x) {
+  const DD ln2{0x1.62e42fefa39efp-1, 0x1.abc9e3b39803fp-56};
+  const double k = std::nearbyint(x.hi / ln2.hi);
+  DD r = x + -(ln2 * DD{k, 0.0});
+  r = {std::ldexp(r.hi, -9), std::ldexp(r.lo, -9)};
+  DD e{0.0, 0.0};  // e^r - 1, |r| < 2^-10: the first term left out is below 2^-120
+  for (int n = 10; n >= 1; --n) e = (DD{1.0, 0.0} + e) * r / DD{static_cast<double>(n), 0.0};
+  for (int i = 0; i < 9; ++i) e = DD{2 * e.hi, 2 * e.lo} + e * e;
+  e = DD{1.0, 0.0} + e;
+  return {std::ldexp(e.hi, static_cast<int>(k)), std::ldexp(e.lo, static_cast<int>(k))};
+}
+// one Newton step on e^y = x
+DD dd_log(double x) {
+  const DD y{std::log(x), 0.0};
+  return y + (DD{x, 0.0} * dd_exp(-y) + DD{-1.0, 0.0});
+}
+// x in [0, 1/2) in units of 2^-64, to the nearest
+uint64_t fraction64(DD x) {
+  const double a = std::ldexp(x.hi, 64), whole = std::floor(a);
+  return static_cast<uint64_t>(whole) + static_cast<uint64_t>(std::llrint((a - whole) + std::ldexp(x.lo, 64)));
+}
+
 }  // namespace
 }  // namespace msa
 
@@ -140,7 +189,9 @@ msa_status msa_rope_create(int32_t rotary_dim, msa_rope_layout layout, double ba
   if (!r) return set_error(MSA_ERR_NO_MEMORY, "%s: out of host memory", fn);
   const double two_pi = 6.283185307179586476925;
   const int pairs = rotary_dim / 2;
-  if (scaling == MSA_ROPE_NTK) base *= pow(factor, static_cast<double>(rotary_dim) / (rotary_dim - 2));
+  DD log_base = dd_log(base);
+  if (scaling == MSA_ROPE_NTK)
+    log_base = log_base + dd_log(factor) * (DD{double(rotary_dim), 0.0} / DD{rotary_dim - 2.0, 0.0});
   // YaRN: pairs that turn more than beta_fast times over the original length
   // keep their frequency, those below beta_slow are interpolated, a linear
   // ramp over the pair index joins them
@@ -151,13 +202,16 @@ msa_status msa_rope_create(int32_t rotary_dim, msa_rope_layout layout, double ba
     width = std::max(std::min(ceil(dim(beta_slow)), rotary_dim - 1.0) - lo, 1e-3);
   }
   for (int i = 0; i < pairs; ++i) {
-    double turns = pow(base, -2.0 * i / rotary_dim) / two_pi;
-    if (scaling == MSA_ROPE_LINEAR) turns /= factor;
+    const DD one{1.0, 0.0}, inv_two_pi{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57}, f{factor, 0.0};
+    DD turns = dd_exp(log_base * (DD{-2.0 * i, 0.0} / DD{double(rotary_dim), 0.0})) * inv_two_pi;
+    if (scaling == MSA_ROPE_LINEAR) turns = turns / f;
     if (scaling == MSA_ROPE_YARN) {
-      const double ramp = std::clamp((i - lo) / width, 0.0, 1.0);
-      turns = turns * (1.0 - ramp) + turns / factor * ramp;
+      DD ramp = DD{i - lo, 0.0} / DD{width, 0.0};
+      if (ramp.hi <= 0.0) ramp = {0.0, 0.0};
+      if (ramp.hi >= 1.0) ramp = one;
+      turns = turns * (one + -ramp) + turns / f * ramp;
     }
-    r->table.turns[i] = static_cast<uint64_t>(ldexp(turns, 64));  // turns <= 1 / (2 pi)
+    r->table.turns[i] = fraction64(turns);  // turns <= 1 / (2 pi)
   }
   const double m = scaling == MSA_ROPE_YARN && factor > 1.0 ? 0.1 * log(factor) + 1.0 : 1.0;
   r->table.mscale = static_cast<float>(m);

@@ -15,10 +15,10 @@ constexpr int kMaxRopePairs = 128;
 
 // Passed by value: the kernels read it from the constant bank, so a handle
 // owns no device memory and serves any device.  turns[i] is the fraction of a
-// full turn that pair i advances per position, in units of 2^-64: position *
-// turns mod 2^64 is then the exact phase (the product's multiple of a turn
-// falls off the top), where an fp32 angle has lost its last bits long before
-// position 10^5.
+// full turn that pair i advances per position, in units of 2^-64, to the
+// nearest: position * turns mod 2^64 is then the phase (the product's multiple
+// of a turn falls off the top) to 2^-34 of a turn at any int32 position, where
+// an fp32 angle has lost its last bits long before position 10^5.
 struct RopeTable {
   uint64_t turns[kMaxRopePairs];
   float mscale;         // factor on the rotated values (1 except for YaRN), and what

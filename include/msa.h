@@ -428,8 +428,8 @@ msa_status msa_sparse_decode_noalloc(const void* q, const void* k_pages, const v
  *  out           receives the handle; release with msa_rope_destroy.
  * Host memory only: the handle serves every device and stream, and calls that
  * were given it keep no reference to it (they copy the table at the launch).
- * Angles are exact to fp32 at every int32 position: the phase is an integer
- * product modulo one turn.
+ * Angles are right to fp32 at every int32 position: the table has 64-bit
+ * fractions of a turn, and the phase is an integer product modulo one turn.
  */
 msa_status msa_rope_create(int32_t rotary_dim, msa_rope_layout layout, double base, msa_rope_scaling scaling,
                            double factor, int32_t original_len, double beta_fast, double beta_slow,
@@ -442,7 +442,9 @@ void msa_rope_destroy(msa_rope_t rope);
  * pair i of a head,  a' = m (a cos t - b sin t),  b' = m (b cos t + a sin t);
  * dims from rotary_dim on are copied.  With inverse != 0 the rotation is by
  * -t (and still times m): the transpose, which takes the gradient of the
- * rotated heads to that of the heads.  Computed in fp32, rounded once.
+ * rotated heads to that of the heads.  cos, sin (times m), the products and
+ * their sum are rounded in fp32 each, as elementwise arithmetic rounds them; a
+ * bf16 result once more.
  *
  *  x             bf16 or fp32 [n_rows, heads, head_dim]; rows x_row_stride
  *                elements apart, heads dense within a row (a slice of a fused
