@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* kv_empty = kv_full + kStages;
   uint64_t* s_full = kv_empty + kStages;  // [2]
   uint64_t* p_full = s_full + 2;          // [2]
-  uint64_t* o_done = p_full + 2;          // [2]: a unit's last P.V of head h, or that it has none
+  uint64_t* o_done = p_full + 2;          // [2]: a unit's last P.V of head h, or that it has none (once a unit, as o_free)
   uint64_t* o_free = o_done + 2;          // [2]
   uint64_t* list_full = o_free + 2;       // [kListSlots]
   uint64_t* list_empty = list_full + kListSlots;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (k > 0 && !(ok = mbar_wait_inl(o_free, (k - 1) & 1, err) && mbar_wait_inl(o_free + 1, (k - 1) & 1, err)))
             break;
           mbar_arrive(o_done);
-          if (two) mbar_arrive(o_done + 1);
+          mbar_arrive(o_done + 1);
           continue;
         }
         if (!(ok = mbar_wait_inl(kv_full + (kv_it & 1), (kv_it >> 1) & 1, err))) break;
@@ -520,6 +520,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!two && i + 1 == n - 1) mma_commit(q_empty);
           } else {
             mma_commit(o_done);
+            if (!two) mma_commit(o_done + 1);
           }
           if (!two) continue;
           // head 1
@@ -691,7 +692,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    int od0 = 0, od1 = 0;  // units with a head 0 / head 1 so far
     int ost_uses = 0;      // 64-column boxes staged so far
     bool ok = true;
     for (int k = 0, ui = first_unit(); ui < n_units; ++k, ui += kSplit ? n_units : gridDim.x) {
@@ -709,13 +709,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const float o_scale = kFp8 && !kBlk ? v_scale[st.g] : 1.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(stat_empty + h * 2 + b);
+        if (ok) ok = mbar_wait_inl(o_done + h, k & 1, err);
         if (!active) {
           __syncwarp();
           if (lane == 0) mbar_arrive(o_free + h);
           continue;
         }
         const bool has_o = n > 0;
-        if (ok) ok = mbar_wait_inl(o_done + h, (h == 0 ? od0++ : od1++) & 1, err);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         const uint32_t o_addr = tmem + lane_base + 256 + h * D;
