@@ -336,10 +336,8 @@ __global__ void __launch_bounds__(kDThreads, NT == 1 ? 2 : 1)
         for (int kc = 0; kc < kD / 16; ++kc) {
           if (hl < G) {
             const uint2 v = *reinterpret_cast<const uint2*>(qr + kc * 16 + 4 * t4);
-            const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-            const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-            qf[nt][kc][0] = pack_f16x2(f0.x, f0.y);
-            qf[nt][kc][1] = pack_f16x2(f1.x, f1.y);
+            qf[nt][kc][0] = bf16x2_to_f16x2(v.x);  // beyond f16 saturating, as the prefill kernel has it
+            qf[nt][kc][1] = bf16x2_to_f16x2(v.y);
           } else {
             qf[nt][kc][0] = qf[nt][kc][1] = 0u;
           }

@@ -295,7 +295,8 @@ msa_status msa_proxy_topk(msa_plan_t plan, const void* pq, const void* pk_pages,
  *  k_pages, v_pages  [num_pages, Hkv, 128, d], bf16 or e4m3 per the plan
  *                    (MSA_KV_FP8_E4M3: head_dim 128, at decode at most 16
  *                    query heads per proxy head; the e4m3 MMAs run in f16, with
- *                    q rounded to f16, exact for |q| in [2^-14, 65504]).
+ *                    q rounded to f16, exact for |q| in [2^-14, 65504] and
+ *                    saturating beyond).
  *  kv_indices        int32 page table.
  *  kv_block_indexes  int32 [num_tiles, Hp, topk], as msa_topk_select writes
  *                    them.  Any order of distinct valid blocks is accepted,
