@@ -244,6 +244,16 @@ class Rope:
         return out
 
 
+class _PlanHandle(ctypes.c_void_p):
+    """A plan of libmsa, destroyed with the last that refers to it: the Plan, or a
+    view of its device tables."""
+
+    def __del__(self):
+        if self.value:
+            _lib.msa_plan_destroy(self)
+            self.value = None
+
+
 class Plan:
     """A validated batch shape with its device tables (msa_plan)."""
 
@@ -259,7 +269,7 @@ class Plan:
         self.num_pages = int(num_pages)
         self.kv_dtype = kv_dtype
         code = {"bf16": KV_BF16, "e4m3": KV_FP8_E4M3, "e4m3_block": KV_FP8_E4M3_BLOCK}[kv_dtype]
-        h = ctypes.c_void_p()
+        h = _PlanHandle()
         _check(_lib.msa_plan(qa, ka, b, num_qo_heads, num_kv_heads, num_proxy_heads, head_dim, proxy_head_dim,
                              page_size, topk, self.num_pages, code, 0, _stream(stream), ctypes.byref(h)),
                "msa_plan")
@@ -268,10 +278,10 @@ class Plan:
         self.max_blocks = _lib.msa_plan_max_blocks(h)
         self.total_q = _lib.msa_plan_total_q(h)
         self.n_page_entries = sum((k + 127) // 128 for k in self.kv_lens)
-        # a non-owning int32 view of the plan's device num_valid_pages table
+        # an int32 view of the plan's device num_valid_pages table
         nvp_ptr = _lib.msa_plan_num_valid_pages(h)
         self._nvp_raw = nvp_ptr
-        self.num_valid_pages = _device_view_int32(nvp_ptr, self.n_tiles, torch.cuda.current_device())
+        self.num_valid_pages = _device_view_int32(nvp_ptr, self.n_tiles, torch.cuda.current_device(), h)
         self.num_valid_pages_host = None
         # what the calls around a step check of their tensors, made once
         kvt = torch.bfloat16 if kv_dtype == "bf16" else torch.float8_e4m3fn
@@ -294,12 +304,6 @@ class Plan:
                             (torch.float32, ppool + (self.dp,), "dpk_pages"), pos, self._cache_needs[0])
         self._attn_needs = self._cache_needs + ((torch.bfloat16, self._q_shape, "q"), (
             torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes"))
-
-    def __del__(self):
-        h = getattr(self, "_h", None)
-        if h is not None and h.value:
-            _lib.msa_plan_destroy(h)
-            self._h = None
 
     # -- the cache
     def kv_append(self, k, v, k_pages, v_pages, kv_indices, k_scale=None, v_scale=None, rope=None, positions=None,
@@ -449,12 +453,13 @@ class Plan:
         _check(_lib.msa_check_errors(self._h, _stream(stream)), "msa_check_errors")
 
 
-def _device_view_int32(ptr, n, device_index):
+def _device_view_int32(ptr, n, device_index, owner):
     """Wrap a device int32 array owned by libmsa as a torch tensor without
-    copying (the plan keeps it alive)."""
+    copying; the tensor and its views keep `owner`, whose memory it is."""
     class _Holder:
         pass
     h = _Holder()
+    h.owner = owner
     h.__cuda_array_interface__ = {"shape": (n,), "typestr": "<i4", "data": (ptr, False), "version": 3,
                                   "strides": None}
     with torch.cuda.device(device_index):
