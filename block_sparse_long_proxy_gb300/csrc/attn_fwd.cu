@@ -294,8 +294,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       if (!ok) break;
       // the unit's blocks: padding skipped, entries past the tile's valid
-      // blocks dropped and reported, pages checked against the pool
-      int first = 0, count = topk;  // of the valid blocks, this part's
+      // blocks dropped and reported, pages checked against the pool (kBlk: a
+      // block on a page outside is dropped; otherwise page 0 is read in its place)
+      int first = 0, count = topk, seen = 0;  // of the valid blocks, this part's
       if (kSplit) {
         int total = 0;
         for (int b = 0; b < topk; b += 32) {
@@ -311,28 +312,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int j = kk < topk ? sel[kk] : -1;
         const bool valid = j >= 0 && j < tl.nvp;
         if (j >= tl.nvp) atomicOr(err, kErrDeviceCheck);
+        bool take = valid;
         int row = 0;
         if (valid) {
           int64_t page = kv_indices[tl.page_base + j];
           if (page < 0 || page >= num_pages) {
             atomicOr(err, kErrDeviceCheck);
             page = 0;
+            if (kBlk) take = false;
           }
           // K/V head of the unit's proxy head, or the single head of a one-head pool
           row = static_cast<int>((kOneKvHead ? page : page * hkv + u.g / kv_div) * 128);
         }
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, valid);
-        if (valid) {
-          const int o = n + __popc(m & ((1u << lane) - 1u)) - first;
-          if (!kSplit || (o >= 0 && o < count)) {
-            ls_j[o] = j;
-            ls_row[o] = row;
-            if (kBlk && o < 64) put_scale(kv_it + o, row);
-          }
+        const uint32_t below = (1u << lane) - 1u;
+        if (kSplit) {
+          const uint32_t v = __ballot_sync(0xFFFFFFFFu, valid);
+          const int rank = seen + __popc(v & below);
+          take = take && rank >= first && rank < first + count;
+          seen += __popc(v);
+        }
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, take);
+        if (take) {
+          const int o = n + __popc(m & below);
+          ls_j[o] = j;
+          ls_row[o] = row;
+          if (kBlk && o < 64) put_scale(kv_it + o, row);
         }
         n += __popc(m);
       }
-      if (kSplit) n = count;
       const bool pair = kOneKvHead && u.nh == 2;
       if (pair) {
         // the second proxy head's own blocks (selection row g + 1); the

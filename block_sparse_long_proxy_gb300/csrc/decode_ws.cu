@@ -21,9 +21,9 @@
 // kBlk: one scale for each (page, KV head) (BlockScale in msa_internal.h).  A
 // unit lies in one page, so its scales are three numbers a warp broadcasts
 // with the unit; they cost one fused add and one multiply a unit and thread.
-// Units wholly behind the query position are not loaded, and V rows behind it
-// are zeroed in shared memory (their bytes were never written, and 0 * NaN
-// would reach the output).
+// Units wholly behind the query position, or on a page outside the pool, are
+// not loaded, and V rows behind the position are zeroed in shared memory (their
+// bytes were never written, and 0 * NaN would reach the output).
 //
 // Few rows (kBlk): a row's warps are the warps of a cluster of cs CTAs, whose
 // merged states cross over distributed shared memory, with neither partials
@@ -143,13 +143,14 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
         atomicOr(err, kErrDeviceCheck);
       } else if (j >= 0) {
         int64_t page = kv_indices[tl.page_base + j];
-        if (page < 0 || page >= num_pages) {
+        const bool in_pool = page >= 0 && page < num_pages;
+        if (!in_pool) {
           atomicOr(err, kErrDeviceCheck);
           page = 0;
         }
         ukey = j * 128 + (u % kParts) * kKeys;
         urow = static_cast<int>((page * hkv + kvh) * 128 + (u % kParts) * kKeys);
-        if (kBlk && ukey > last) ukey = -1;
+        if (kBlk && (ukey > last || !in_pool)) ukey = -1;
       }
     }
     // compact the valid units to the low lanes (padding slots load nothing)

@@ -40,8 +40,9 @@
  *    by sequence, ceil(kv_len/128) entries per sequence (logical block j of
  *    sequence s is page kv_indices[sum_{s'<s} ceil(kv_len_s'/128) + j]).
  *    Page ids must lie in [0, num_pages); a kernel that meets one outside
- *    skips that block and raises MSA_ERR_DEVICE_CHECK in the plan's error
- *    word (read with msa_check_errors).
+ *    raises MSA_ERR_DEVICE_CHECK in the plan's error word (read with
+ *    msa_check_errors) and skips that block (the appends, and attention over
+ *    MSA_KV_FP8_E4M3_BLOCK pages) or reads page 0 in its place (the rest).
  *  - Errors: host-side argument checks return MSA_ERR_INVALID_ARG or
  *    MSA_ERR_UNSUPPORTED before anything is enqueued; a failed launch
  *    returns MSA_ERR_CUDA.  msa_last_error() gives a message for the
@@ -540,7 +541,7 @@ msa_status msa_append_bwd(msa_plan_t plan, msa_rope_t k_rope, msa_rope_t pk_rope
  * msa_check_errors -- waits for `stream`, then reads and clears the plan's
  * device error word: MSA_OK, MSA_ERR_TIMEOUT (a bounded wait inside a kernel
  * gave up; that kernel's outputs are unspecified), MSA_ERR_DEVICE_CHECK (a
- * kernel skipped a block whose page id was out of range) or, for plans
+ * kernel met a page id or a block out of range) or, for plans
  * created under MSA_CHECKS, MSA_ERR_NONFINITE (an output held a NaN), in
  * that order when several are set.
  */
