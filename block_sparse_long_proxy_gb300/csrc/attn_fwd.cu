@@ -150,7 +150,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     float* __restrict__ lse, int32_t hq, int32_t hsel, int32_t kv_div, int32_t topk,
                     float scale_log2, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                     int32_t parts, uint32_t* err, int32_t chain) {
-  if (!kSplit || !(chain & kFollows)) pdl_wait();
+  if (kSplit && (chain & kFollows))
+    fence_gpu();
+  else
+    pdl_wait();
   // a variant of its own: the call alone costs the others 1 % (32K prefill 862 -> 870 us)
   if (kLead || (kSplit && (chain & kLeads))) pdl_trigger();
   // kBlk: a unit of a tile of few rows has 2^lg heads side by side in the 128

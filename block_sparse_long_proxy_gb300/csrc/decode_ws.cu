@@ -92,7 +92,10 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1)
                      const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int32_t hq, int32_t hsel,
                      int32_t kv_div, int32_t topk, int32_t cs, float scale_log2, int32_t chain, uint32_t* err) {
-  if (!kFew || !(chain & kFollows)) pdl_wait();
+  if (kFew && (chain & kFollows))
+    fence_gpu();
+  else
+    pdl_wait();
   using L = WsSmem<kD, NT>;
   constexpr int kPartBytes = L::kPartBytes, kBufBytes = L::kBufBytes, kMD = kD / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];

@@ -143,9 +143,17 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 
 // Launches of one call that need nothing of each other run without a gap: all
 // but the last let the next one start early (kLeads), and all but the first
-// (kFollows) wait for the one before at their end instead of their start.  The
-// first of them waits for the stream's work before it lets the next one start,
-// and whatever follows the last finds all of them complete.
+// (kFollows) wait for the one before at their end instead of their start.
+//
+// What a kernel that follows reads before that wait: the call's inputs, and the
+// plan's tables.  Every CTA of the first launch has waited (griddepcontrol.wait)
+// for the stream's earlier work, which is then complete with its writes visible
+// on the GPU, before it lets the next launch start; a launch starts when all
+// CTAs of the one before have let it.  So those writes come before the first
+// instruction of each that follows; fence_gpu there keeps its reads from lines
+// that an L1 holds from before (TMA reads from L2).  It writes rows that no other
+// launch of the call reads or writes, and ends, by one thread a CTA that waits,
+// after the one before: whatever follows the last finds all of them complete.
 enum : int32_t { kLeads = 1, kFollows = 2 };
 
 msa_status set_error(msa_status s, const char* fmt, ...);
