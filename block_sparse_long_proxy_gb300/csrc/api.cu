@@ -36,6 +36,14 @@ msa_status cuda_check(cudaError_t e, const char* what) {
   return set_error(MSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+msa_status check_device(const char* fn, const msa_plan_s* p) {
+  int dev = 0;
+  const msa_status s = cuda_check(cudaGetDevice(&dev), fn);
+  if (s == MSA_OK && dev != p->device)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: the plan belongs to device %d, device %d is current", fn, p->device, dev);
+  return s;
+}
+
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -399,6 +407,7 @@ msa_status msa_proxy_maxscore(msa_plan_t plan, const void* pq, const void* pk_pa
     return set_error(MSA_ERR_INVALID_ARG, "msa_proxy_maxscore: NULL argument");
   if (!aligned16(pq) || !aligned16(pk_pages))
     return set_error(MSA_ERR_INVALID_ARG, "msa_proxy_maxscore: pq and pk_pages must be 16-byte aligned");
+  if (const msa_status dev = check_device("msa_proxy_maxscore", plan); dev != MSA_OK) return dev;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const msa_status s = plan->decode ? launch_proxy_decode(plan, pq, pk_pages, kv_indices, max_score, st)
                                     : launch_proxy_prefill(plan, pq, pk_pages, kv_indices, max_score, st);
@@ -413,6 +422,7 @@ msa_status msa_proxy_maxscore_fp8(msa_plan_t plan, const void* pq, const void* p
     return set_error(MSA_ERR_INVALID_ARG, "msa_proxy_maxscore_fp8: pq and pk_pages must be 16-byte aligned");
   if (!plan->decode)
     return set_error(MSA_ERR_UNSUPPORTED, "msa_proxy_maxscore_fp8: FP8 proxy K is implemented for decode batches only");
+  if (const msa_status dev = check_device("msa_proxy_maxscore_fp8", plan); dev != MSA_OK) return dev;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return scan_proxy(plan, launch_proxy_decode_fp8(plan, pq, pk_pages, pk_scale, kv_indices, max_score, st), pq,
                     pk_pages, kv_indices, 1, max_score, st);
@@ -429,6 +439,7 @@ msa_status msa_proxy_maxscore_nvfp4(msa_plan_t plan, const void* pq, const void*
   if (!plan->decode)
     return set_error(MSA_ERR_UNSUPPORTED,
                      "msa_proxy_maxscore_nvfp4: the NVFP4 proxy K is implemented for decode batches only");
+  if (const msa_status dev = check_device("msa_proxy_maxscore_nvfp4", plan); dev != MSA_OK) return dev;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // e2m1 codes have no NaN: pq and max_score are scanned
   return scan_proxy(plan,
@@ -443,6 +454,7 @@ msa_status msa_proxy_topk(msa_plan_t plan, const void* pq, const void* pk_pages,
     return set_error(MSA_ERR_INVALID_ARG, "msa_proxy_topk: NULL argument");
   if (!aligned16(pq) || !aligned16(pk_pages))
     return set_error(MSA_ERR_INVALID_ARG, "msa_proxy_topk: pq and pk_pages must be 16-byte aligned");
+  if (const msa_status dev = check_device("msa_proxy_topk", plan); dev != MSA_OK) return dev;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return scan_proxy(plan, launch_proxy_topk(plan, pq, pk_pages, kv_indices, max_score, kv_block_indexes, st), pq,
                     pk_pages, kv_indices, 2, max_score, st);
@@ -471,6 +483,7 @@ msa_status msa_sparse_attn(msa_plan_t plan, const void* q, const void* k_pages, 
   const bool fp8 = plan->kv_dtype != MSA_KV_BF16;
   if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
     return set_error(MSA_ERR_INVALID_ARG, "msa_sparse_attn: k_scale/v_scale must be given exactly for FP8 K/V");
+  if (const msa_status dev = check_device("msa_sparse_attn", plan); dev != MSA_OK) return dev;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // rows of more than 16 heads over block-scaled pages go through the prefill
   // kernel, as bf16 decode does
@@ -509,6 +522,7 @@ msa_status msa_sparse_attn_bwd(msa_plan_t plan, const void* q, const void* k_pag
                      "msa_sparse_attn_bwd: inputs must be 16-byte aligned and gradients 32-byte aligned");
   if (plan->kv_dtype != MSA_KV_BF16)
     return set_error(MSA_ERR_UNSUPPORTED, "msa_sparse_attn_bwd: bf16 K/V only");
+  if (const msa_status dev = check_device("msa_sparse_attn_bwd", plan); dev != MSA_OK) return dev;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   msa_status s = launch_attn_bwd(plan, q, k_pages, v_pages, kv_indices, kv_block_indexes, out, lse, dout, pq,
                                  pk_pages, kl_weight, dq, dk_pages, dv_pages, dpq, dpk_pages, st);

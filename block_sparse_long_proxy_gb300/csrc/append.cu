@@ -466,12 +466,8 @@ const RopeTable& table_of(msa_rope_t r) {
 
 // What every call here checks of its plan and rope.
 msa_status check_append(const char* fn, msa_plan_t plan, msa_rope_t rope, int32_t d) {
-  int dev = 0;
-  const msa_status s = cuda_check(cudaGetDevice(&dev), fn);
+  const msa_status s = check_device(fn, plan);
   if (s != MSA_OK) return s;
-  if (dev != plan->device)
-    return set_error(MSA_ERR_INVALID_ARG, "%s: the plan belongs to device %d, device %d is current", fn,
-                     plan->device, dev);
   if (rope && rope->table.rot > d)
     return set_error(MSA_ERR_INVALID_ARG, "%s: rotary_dim %d above the head's %d", fn, rope->table.rot, d);
   return MSA_OK;

@@ -158,6 +158,8 @@ enum : int32_t { kLeads = 1, kFollows = 2 };
 
 msa_status set_error(msa_status s, const char* fmt, ...);
 msa_status cuda_check(cudaError_t e, const char* what);
+// the current device is the plan's, whose memory its tables and workspace are
+msa_status check_device(const char* fn, const msa_plan_s* p);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // n rows of `width` bytes at x and at y share no byte, or are the same rows
 bool rows_disjoint_or_same(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t n,

@@ -43,6 +43,8 @@
  *    raises MSA_ERR_DEVICE_CHECK in the plan's error word (read with
  *    msa_check_errors) and skips that block (the appends, and attention over
  *    MSA_KV_FP8_E4M3_BLOCK pages) or reads page 0 in its place (the rest).
+ *  - A plan belongs to the device that was current when it was made; its
+ *    calls are refused (MSA_ERR_INVALID_ARG) while another one is.
  *  - Errors: host-side argument checks return MSA_ERR_INVALID_ARG or
  *    MSA_ERR_UNSUPPORTED before anything is enqueued; a failed launch
  *    returns MSA_ERR_CUDA.  msa_last_error() gives a message for the

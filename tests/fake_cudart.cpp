@@ -17,6 +17,7 @@ struct Event {
   long bytes;
 };
 std::atomic<long> live_host{0}, live_device{0};
+int device = 0;
 std::atomic<long> host_left{-1}, device_left{-1};  // allocations until they fail; below 0: they do not
 
 // a vector of its own allocator, outside the counts
@@ -69,7 +70,8 @@ void operator delete(void* p, const std::nothrow_t&) noexcept { operator delete(
 
 extern "C" {
 
-void fake_fail(long host, long device) { host_left = host, device_left = device; }
+void fake_fail(long on_host, long on_device) { host_left = on_host, device_left = on_device; }
+void fake_set_device(int d) { device = d; }
 long fake_live_host() { return live_host; }
 long fake_live_device() { return live_device; }
 long fake_events(Event* out, long most) {
@@ -79,7 +81,7 @@ long fake_events(Event* out, long most) {
 }
 
 cudaError_t cudaGetDevice(int* d) {
-  *d = 0;
+  *d = device;
   return cudaSuccess;
 }
 cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) {

@@ -23,7 +23,13 @@ lib.msa_last_error.restype = C.c_char_p
 lib.msa_plan.argtypes = [P, P] + [I] * 8 + [L, I, C.c_uint32, P, P]
 lib.msa_plan_destroy.argtypes = [P]
 lib.msa_kv_append.argtypes = [P, P, P, P, L, P, L] + [P] * 6
+lib.msa_pk_append.argtypes = [P, P, P, P, L] + [P] * 8
+lib.msa_append_bwd.argtypes = [P] * 12
+lib.msa_proxy_maxscore.argtypes = [P] * 6
+lib.msa_proxy_maxscore_fp8.argtypes = lib.msa_proxy_topk.argtypes = [P] * 7
+lib.msa_proxy_maxscore_nvfp4.argtypes = [P] * 8
 lib.msa_sparse_attn.argtypes = [P] * 11
+lib.msa_sparse_attn_bwd.argtypes = [P] * 11 + [C.c_float] + [P] * 6
 
 def plan(qo, kv, hq, hkv, d, topk, kind, pages=64):
     n, h = len(qo), P()
@@ -142,4 +148,43 @@ for batch in BATCHES:
     assert s == 4 and left() == before
     for bad in ((batch[0], [0] * len(batch[0])), ([0] * len(batch[0]), batch[1])):
         assert plan(*bad, *batch[2:])[0] == 1 and left() == before
+""")
+
+
+def test_plans_belong_to_their_device(child):
+    """Every call of a plan answers MSA_ERR_INVALID_ARG, and launches nothing, while
+    another device is current; and works again when the plan's is."""
+    child("""
+at = [P((i + 1) << 20) for i in range(16)]
+def calls(qo, kind):
+    s, h = plan(qo, [300] * len(qo), 8, 8, 128, 4, kind)
+    assert s == 0
+    sc = at[8:10] if kind != BF16 else [None, None]
+    yield lambda: lib.msa_kv_append(h, None, None, at[0], 1024, at[1], 1024, at[2], at[3], at[4], *sc, None)
+    yield lambda: lib.msa_pk_append(h, None, None, at[0], 64, at[1], at[2], None, None, None, None, None, None)
+    yield lambda: lib.msa_proxy_maxscore(h, at[0], at[1], at[2], at[3], None)
+    yield lambda: lib.msa_sparse_attn(h, at[0], at[1], at[2], at[3], at[4], *sc, at[5], None, None)
+    if max(qo) == 1:
+        yield lambda: lib.msa_proxy_maxscore_fp8(h, at[0], at[1], at[2], at[3], at[4], None)
+        yield lambda: lib.msa_proxy_maxscore_nvfp4(h, at[0], at[1], at[2], at[3], at[4], at[5], None)
+    else:
+        yield lambda: lib.msa_proxy_topk(h, at[0], at[1], at[2], None, at[3], None)
+    if kind == BF16:
+        yield lambda: lib.msa_append_bwd(h, None, None, None, at[0], at[1], None, None, at[2], None, None, None)
+        yield lambda: lib.msa_sparse_attn_bwd(h, *at[:10], 1.0, *at[10:15], None)
+    lib.msa_plan_destroy(h)
+n = 0
+for qo in ([1] * 3, [200, 5]):
+    for kind in (BF16, E4M3, BLOCK):
+        for call in calls(qo, kind):
+            before = len(events())
+            fake.fake_set_device(1)
+            assert call() == 1 and b"belongs to device 0, device 1 is current" in lib.msa_last_error(), lib.msa_last_error()
+            assert len(events()) == before
+            fake.fake_set_device(0)
+            if kind != BF16 or n == 0:
+                assert call() == 0, lib.msa_last_error()
+                assert len(events()) > before
+            n += 1
+assert n == 37, n
 """)
