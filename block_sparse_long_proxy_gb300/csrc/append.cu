@@ -229,10 +229,12 @@ __device__ __forceinline__ void kv_append(const RopeTable& tab, const KvAppendAr
         if (!(old > 0.f && old <= pow2(kMaxExp))) {  // never written: the old slots keep their bytes
           if (threadIdx.x == 0) atomicOr(a.err, kErrDeviceCheck);
         } else {
-          // another writer's scale need not be a power of two: round it up to one
-          const uint32_t ou = __float_as_uint(old);
+          // another writer's scale need not be a power of two: round it up to one;
+          // below the least it counts as that, as the attention has it
+          const float was = fmaxf(old, pow2(kMinExp));
+          const uint32_t ou = __float_as_uint(was);
           e = max(e, static_cast<int>(ou >> 23) - 127 + ((ou & 0x7FFFFFu) != 0u ? 1 : 0));
-          const float f = old * pow2(-e);
+          const float f = was * pow2(-e);
           if (f != 1.f) {
             uint4* q = reinterpret_cast<uint4*>(pool);
             for (int i = threadIdx.x; i < slot0 * (D / 16); i += kKvThreads) {

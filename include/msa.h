@@ -488,7 +488,8 @@ msa_status msa_rope_apply(msa_rope_t rope, const void* x, int64_t x_row_stride, 
  *        raises the scale, the slots before the new rows are converted to it.
  *        A page whose first slot is written starts anew, whatever scale it
  *        had.  A partly filled page whose scale is not in (0, 2^40] raises
- *        MSA_ERR_DEVICE_CHECK and its old slots keep their bytes.
+ *        MSA_ERR_DEVICE_CHECK and its old slots keep their bytes; one below
+ *        2^-40 counts as 2^-40, as in msa_sparse_attn.
  *    e4m3 conversions are to nearest, ties to even, saturating at +-448.
  * Other slots of the pages keep their contents.  A page id outside the pool is
  * reported (MSA_ERR_DEVICE_CHECK) and its rows are dropped.  One launch; the
