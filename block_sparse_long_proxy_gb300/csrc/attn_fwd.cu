@@ -1060,7 +1060,9 @@ static int slots_of(int heads, int lg) { return (heads + (1 << lg) - 1) >> lg; }
 // their own.  A block step takes about 1.65 us for a head and 1.78 for two (0.35
 // more where no other unit reads the same blocks, which then come from HBM), a
 // unit 6 besides, the merge 3 and a second launch 6.  Clusters of 8 are not
-// placed as densely as the SMs would allow: 15 run at once.
+// placed as densely as the SMs would allow: 15 run at once.  The times are those
+// of head_dim 128 and stand for 64 as well, which has shorter steps; the
+// longest unit's blocks stand for every unit's.
 // Measured (us; heads a unit / parts):
 //   rows x heads, blocks     1/1    1/2    1/4    1/8    2/1    2/2    2/4
 //     128 x 32, 16          33.8   24.4  [17.9]  41.7   38.3   29.2   21.1
