@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* kv_empty = kv_full + kStages;
   uint64_t* s_full = kv_empty + kStages;  // [2]
   uint64_t* p_full = s_full + 2;          // [2]
-  uint64_t* o_done = p_full + 2;          // [2]: a unit's last P.V of head h, or that it has none (once a unit, as o_free)
-  uint64_t* o_free = o_done + 2;          // [2]
+  uint64_t* o_done = p_full + 2;          // [2]: a unit's last P.V of head h
+  uint64_t* o_free = o_done + 2;          // [2]: the epilogue has read a unit's O_h (units with blocks, either head)
   uint64_t* list_full = o_free + 2;       // [kListSlots]
   uint64_t* list_empty = list_full + kListSlots;
   uint64_t* drain = list_empty + kListSlots;
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + 256 + h * D, tmem + h * 128 + kk * 8, vd + ((kk * 2048) >> 4), id_pv, acc || (kk > 0));
       };
-      int kv_it = 0, ch0 = 0, ch1 = 0;
+      int kv_it = 0, ch0 = 0, ch1 = 0, used = 0;  // used: units with blocks so far
       bool ok = true;
       for (int k = 0, ui = first_unit(); ok && ui < n_units; ++k, ui += kSplit ? n_units : gridDim.x) {
         if (!(ok = mbar_wait_inl(list_full + k % kListSlots, (k / kListSlots) & 1, err))) break;
@@ -489,17 +489,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_arrive(list_empty + k % kListSlots);
         if (!(ok = mbar_wait_inl(kFp8 ? q_ready : q_full, k & 1, err))) break;
         tc_fence_after();
-        // O_h of every unit is released by the epilogue once per unit; the
-        // MMA thread waits for that release in every unit (also where it
-        // issues nothing into O_h) and only then lets the epilogue have the
-        // unit's O_h (o_done, empty or not): a parity wait that the epilogue
-        // could run two phases ahead of would wait for ever, or end early
+        // A unit without blocks takes no part in o_done and o_free: what the
+        // epilogue does for it waits for nothing of this thread's, so a release of
+        // its own could complete before the wait for the one before it, and a
+        // parity wait two phases behind waits for ever or ends early.  Every
+        // other unit's release follows its o_done, committed after that wait.
         if (n == 0) {
           mma_commit(q_empty);
-          if (k > 0 && !(ok = mbar_wait_inl(o_free, (k - 1) & 1, err) && mbar_wait_inl(o_free + 1, (k - 1) & 1, err)))
-            break;
-          mbar_arrive(o_done);
-          mbar_arrive(o_done + 1);
           continue;
         }
         if (!(ok = mbar_wait_inl(kv_full + (kv_it & 1), (kv_it >> 1) & 1, err))) break;
@@ -516,8 +512,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (!(ok = mbar_wait_inl(p_full, (ch0 + i) & 1, err))) break;
           // the first P.V of a unit overwrites O_h: the previous unit's
           // epilogue must have read it (the QKs above already overlap it)
-          if (i == 0 && k > 0 && !(ok = mbar_wait_inl(o_free, (k - 1) & 1, err))) break;
-          if (i == 0 && k > 0 && !two && !(ok = mbar_wait_inl(o_free + 1, (k - 1) & 1, err))) break;
+          if (i == 0 && used > 0 && !(ok = mbar_wait_inl(o_free, (used - 1) & 1, err))) break;
+          if (i == 0 && used > 0 && !two && !(ok = mbar_wait_inl(o_free + 1, (used - 1) & 1, err))) break;
           if (kFp8 && !(ok = mbar_wait_inl(v_full + s, (it >> 1) & 1, err))) break;
           tc_fence_after();
           pv(0, s, i > 0);
@@ -530,12 +526,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!two && i + 1 == n - 1) mma_commit(q_empty);
           } else {
             mma_commit(o_done);
-            if (!two) mma_commit(o_done + 1);
           }
           if (!two) continue;
           // head 1
           if (!(ok = mbar_wait_inl(p_full + 1, (ch1 + i) & 1, err))) break;
-          if (i == 0 && k > 0 && !(ok = mbar_wait_inl(o_free + 1, (k - 1) & 1, err))) break;
+          if (i == 0 && used > 0 && !(ok = mbar_wait_inl(o_free + 1, (used - 1) & 1, err))) break;
           tc_fence_after();
           pv(1, s, i > 0);
           mma_commit(kv_empty + s);
@@ -550,6 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ch0 += n;
         if (two) ch1 += n;
         kv_it += n;
+        ++used;
       }
       mma_commit(drain);
       mbar_wait_inl(drain, 0, err);
@@ -702,6 +698,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    int od0 = 0, od1 = 0;  // units with blocks of head 0 / head 1 so far
     int ost_uses = 0;      // 64-column boxes staged so far
     bool ok = true;
     for (int k = 0, ui = first_unit(); ui < n_units; ++k, ui += kSplit ? n_units : gridDim.x) {
@@ -719,13 +716,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const float o_scale = kFp8 && !kBlk ? v_scale[st.g] : 1.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(stat_empty + h * 2 + b);
-        if (ok) ok = mbar_wait_inl(o_done + h, k & 1, err);
         if (!active) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(o_free + h);
+          if (lane == 0 && n > 0) mbar_arrive(o_free + h);
           continue;
         }
         const bool has_o = n > 0;
+        if (has_o && ok) ok = mbar_wait_inl(o_done + h, (h == 0 ? od0++ : od1++) & 1, err);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         const uint32_t o_addr = tmem + lane_base + 256 + h * D;
@@ -749,7 +746,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (c == D / 32 - 1) {  // all of O_h is in registers: the next unit's P.V may overwrite it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_free + h);
+            if (lane == 0 && has_o) mbar_arrive(o_free + h);
           }
           if (kSplit) {  // a part's O as it is, for the merge
 #pragma unroll
