@@ -38,13 +38,13 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 
 # dram bytes of one attention-forward launch at the 32K prefill workload from
 # an ncu capture, valid only for the kernel source it was taken on.
-# Captured on S=16384 (15424 selected tile-blocks: 245.5 MB read + 107.8 MB
+# Captured on S=16384 (15424 selected tile-blocks: 244.7 MB read + 108.0 MB
 # written) and scaled by selected tile-blocks to the S=32768 launch (31808).
 NCU_TRAFFIC = {
     # (DRAM bytes read + written) of one launch of the small S=16384 capture and the
     # (tile, group, block) selections it processed; scaled to a launch by selections.
-    "attn_fwd.cu": {"src": "dfd07b8e3f3a76e5", "bytes": 246252032 + 107771136, "sel": 15424},
-    "attn_fwd.cu:fp8": {"src": "dfd07b8e3f3a76e5", "bytes": 180852736 + 100995584, "sel": 15424},
+    "attn_fwd.cu": {"src": "8733f451dbfc3a0a", "bytes": 244742144 + 107976960, "sel": 15424},
+    "attn_fwd.cu:fp8": {"src": "8733f451dbfc3a0a", "bytes": 180960000 + 101196544, "sel": 15424},
 }
 
 

@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t v, float f) {
 // memory and serve all heads of the CTA (with eight angles computed for every
 // 16 values the call took 67 us, half of it issuing instructions), and the
 // next head's rows are on their way while this one's amax is reduced.  32768 rows, 8 heads, d
-// 128 (201 MB): 41.7 us, 4.8 TB/s (2.4 us less with the shorter angle polynomials,
+// 128 (201 MB): 41.5 us, 4.8 TB/s (2.4 us less with the shorter angle polynomials,
 // whose last bits change a few codes).
 enum RopeKind { kPlain, kHalf, kInterleaved };
 
