@@ -406,6 +406,52 @@ __global__ void __launch_bounds__(kPkThreads)
   pools.block_scales[row * kChunks + c] = static_cast<uint8_t>(sc);
 }
 
+// Rows of a latent cache, [latent | key part], the key part rotated: chunk c of a
+// row is 16 values, of the latent copied as they are.  Rows share nothing, so
+// blockIdx.y takes a page's rows by kLatentRows.
+constexpr int kLatentRows = 16;
+
+__global__ void __launch_bounds__(kThreads)
+    latent_append_kernel(const __grid_constant__ RopeTable tab, const AppendUnit* __restrict__ units,
+                         const __nv_bfloat16* __restrict__ latent, int64_t latent_stride,
+                         const __nv_bfloat16* __restrict__ key, int64_t key_stride, const int32_t* __restrict__ positions,
+                         const int32_t* __restrict__ kv_indices, int64_t num_pages, int32_t latent_dim, int32_t rope_dim,
+                         __nv_bfloat16* __restrict__ pages, uint32_t* err) {
+  pdl_wait();
+  const AppendUnit u = units[blockIdx.x];
+  const int64_t page = kv_indices[u.entry];
+  const int slot0 = u.slot0_n & 0xFF, n = u.slot0_n >> 8;
+  if (page < 0 || page >= num_pages) {
+    if (threadIdx.x == 0) atomicOr(err, kErrDeviceCheck);
+    return;
+  }
+  const int copied = latent_dim / 16, chunks = copied + rope_dim / 16;
+  const int first = blockIdx.y * kLatentRows, rows = min(kLatentRows, n - first);
+  for (int e = threadIdx.x; e < rows * chunks; e += kThreads) {
+    const int i = first + e / chunks, c = e % chunks;
+    __nv_bfloat16* dst = pages + (page * 128 + slot0 + i) * (latent_dim + rope_dim);
+    if (c < copied) {
+      const uint4* src = reinterpret_cast<const uint4*>(latent + (u.row + i) * latent_stride + 16 * c);
+      const uint4 x = src[0], y = src[1];
+      uint4* to = reinterpret_cast<uint4*>(dst + 16 * c);
+      to[0] = x, to[1] = y;
+      continue;
+    }
+    const RopeChunk ch = rope_chunk(tab, c - copied);
+    const __nv_bfloat16* src = key + (u.row + i) * key_stride;
+    float x[16];
+    load8(src + ch.lo, x);
+    load8(src + ch.hi, x + 8);
+    if (ch.rotated) {
+      float cs[8], sn[8];
+      rope_angles(tab, c - copied, positions ? positions[u.row + i] : u.pos + i, false, cs, sn);
+      rope_rotate(tab.interleaved != 0, cs, sn, x);
+    }
+    store8(dst + latent_dim + ch.lo, x);
+    store8(dst + latent_dim + ch.hi, x + 8);
+  }
+}
+
 // Gradient pages to rows: dK (rotated back), dV and dpk (rotated back).
 // blockIdx.y: KV heads of K, then of V, then the proxy head.
 //
@@ -509,6 +555,14 @@ cudaError_t launch_kv(const msa_plan_s* p, const RopeTable& tab, KvAppendArgs a,
 
 }  // namespace
 
+msa_status check_latent_dims(const char* fn, int32_t latent_dim, int32_t rope_dim) {
+  if (latent_dim < 128 || latent_dim > 512 || latent_dim % 128 != 0)
+    return set_error(MSA_ERR_UNSUPPORTED, "%s: latent_dim must be 128, 256, 384 or 512", fn);
+  if (rope_dim < 16 || rope_dim > 64 || rope_dim % 16 != 0)
+    return set_error(MSA_ERR_UNSUPPORTED, "%s: rope_dim must be 16, 32, 48 or 64", fn);
+  return MSA_OK;
+}
+
 void append_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   p->append_units_off = static_cast<int64_t>(aux.size());
   int64_t row = 0, base = 0;
@@ -609,6 +663,32 @@ msa_status msa_pk_append(msa_plan_t plan, msa_rope_t rope, const int32_t* positi
   };
   s = cuda_check(plan->dp == 64 ? run(pk_append_kernel<64>) : run(pk_append_kernel<32>), "msa_pk_append: launch");
   if (s == MSA_OK) s = scan_strided(plan, pk, plan->total_q, plan->dp, pk_row_stride, st);
+  return s;
+}
+
+msa_status msa_latent_append(msa_plan_t plan, msa_rope_t rope, const int32_t* positions, const void* latent,
+                             int64_t latent_row_stride, const void* key, int64_t key_row_stride,
+                             const int32_t* kv_indices, int32_t latent_dim, int32_t rope_dim, void* latent_pages,
+                             msa_stream_t stream) {
+  const char* fn = "msa_latent_append";
+  if (!plan || !latent || !key || !kv_indices || !latent_pages)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: NULL argument", fn);
+  msa_status s = check_latent_dims(fn, latent_dim, rope_dim);
+  if (s == MSA_OK) s = check_append(fn, plan, rope, rope_dim);
+  if (s == MSA_OK) s = check_rows(fn, "latent", latent, latent_row_stride, latent_dim);
+  if (s == MSA_OK) s = check_rows(fn, "key", key, key_row_stride, rope_dim);
+  if (s != MSA_OK) return s;
+  if (!aligned16(latent_pages)) return set_error(MSA_ERR_INVALID_ARG, "%s: latent_pages must be 16-byte aligned", fn);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  s = cuda_check(launch_pdl(latent_append_kernel, dim3(plan->n_append_units, plan->decode ? 1 : 128 / kLatentRows),
+                            dim3(kThreads), 0, st, table_of(rope),
+                            reinterpret_cast<const AppendUnit*>(plan->aux_d + plan->append_units_off),
+                            static_cast<const __nv_bfloat16*>(latent), latent_row_stride,
+                            static_cast<const __nv_bfloat16*>(key), key_row_stride, positions, kv_indices,
+                            plan->num_pages, latent_dim, rope_dim, static_cast<__nv_bfloat16*>(latent_pages), plan->err_d),
+                 "msa_latent_append: launch");
+  if (s == MSA_OK) s = scan_strided(plan, latent, plan->total_q, latent_dim, latent_row_stride, st);
+  if (s == MSA_OK) s = scan_strided(plan, key, plan->total_q, rope_dim, key_row_stride, st);
   return s;
 }
 

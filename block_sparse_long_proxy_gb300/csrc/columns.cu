@@ -1,0 +1,852 @@
+// Attention of few query rows over the paged caches: trees of drafted tokens
+// over K/V pages (msa_tree_attn), and the absorbed form over a cache of one
+// shared latent vector a token (msa_latent_attn).
+//
+// For query row i of tile t and head h of proxy head p, over the keys of the
+// blocks kv_block_indexes[t, p, :] that i sees,
+//   s = q[i,h] . k[key] * scale,  out = sum softmax(s) v[key],  lse = ln sum e^s.
+// In the latent cache every head's key is [latent | rotated part] and its
+// value the latent: one array, read once for both products.
+//
+// The heads of p (all of them, in the latent cache) share keys and values, so a
+// tile of a few rows is already a matrix: its columns are the (row, head)
+// pairs, column c being head c % G of row c / G.  Products are transposed,
+//   S^T [128 keys x N] = K_block . Q^T         (M = 128 keys)
+//   O^T [dims x N]    += V_block^T . P^T       (M = 128 dims a product)
+// so that a block always fills the 128 M rows of tcgen05.mma, however few the
+// columns, and N = 16..128 follows the batch.  (With the rows as M, eight heads
+// of one row would fill 8 of 128.)  O^T of 64 columns and a 512-wide latent
+// takes 256 TMEM columns, where 64 x 512 with the rows as M takes all 512.
+//
+// Roles: warp 8 lists the blocks and issues TMA loads into a ring of 32 KB slots
+// (K or V of a block; 128 of the latent's dims); warp 9 issues the products; warps
+// 0-3 and 4-7 take half the columns each, a thread being a key: they mask, find
+// each column's maximum, and write P^T (bf16, or f16 for e4m3 caches: half a
+// step is 2^-9 or 2^-12 of a weight, the sums being of the unrounded ones) back to
+// shared memory.  The latent's P^T goes where the block's rotated part
+// was, which no product reads after S^T.  e4m3: warps 10-13 expand the codes
+// to f16 (exact) inside the slot.
+//
+// Softmax in the log2 domain; a column's reference moves only when its maximum
+// grows by more than 2^8, so O^T is rarely rescaled.  Sums stay with the thread
+// that has the key, in fp32, and are added over the keys once, at the end.
+//
+// The block scales of MSA_KV_FP8_E4M3_BLOCK are a BlockScale (msa_internal.h);
+// static scales are the same with one scale for all pages.
+//
+// Visibility: key offset e = key - pos0 (pos0: the tile's first position) is
+// seen by all rows below 0, by none from 128 on, and by row i in between iff bit
+// e of its 128-bit mask is set: the tree's, or bits 0..i (causal).  A key that
+// no column sees has its V row zeroed in shared memory: its bytes may be
+// anything, and 0 * NaN is NaN.
+//
+// Few tiles: the CTAs of a cluster take a part of the blocks each and merge O^T,
+// m and l over distributed shared memory; no workspace, so calls may overlap.
+#include "msa_internal.h"
+#include "ptx.cuh"
+
+#include <algorithm>
+
+namespace msa {
+namespace {
+
+enum Cache { kBf16, kE4m3, kLatent };
+
+constexpr int kSoftWarps = 8;
+constexpr int kSlotBytes = 32768;
+constexpr int kMaxParts = 8;
+
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
+  if constexpr (C == 8) tmem_ld8(taddr, r);
+  if constexpr (C == 16) tmem_ld16(taddr, r);
+  if constexpr (C == 32) tmem_ld32(taddr, r);
+}
+template <int C>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+  if constexpr (C == 8) tmem_st8(taddr, r);
+  if constexpr (C >= 16) tmem_st16(taddr, r);
+  if constexpr (C == 32) tmem_st16(taddr + 16, r + 16);
+}
+
+struct ColArgs {
+  const __nv_bfloat16* q;   // [total_q, hq, dq]
+  const TileInfo* tiles;
+  const int32_t* idx;
+  const int32_t* kv_indices;
+  const uint4* tree_mask;   // nullptr: causal
+  const float* k_scale;
+  const float* v_scale;
+  __nv_bfloat16* out;       // [total_q, hq, dv]
+  float* lse;
+  uint32_t* err;
+  int64_t num_pages;
+  int32_t hq, hp, hkv;
+  int32_t topk, parts, max_groups;
+  int32_t dq, dv;
+  int32_t kc;               // 64-column chunks of a key
+  int32_t mt;               // 128-row products of O^T
+  int32_t per_page;         // e4m3: a scale for each (page, KV head)
+  float scale_log2;
+};
+
+template <int KIND, int N>
+struct ColSmem {
+  static constexpr bool kLat = KIND == kLatent;
+  static constexpr int kQChunk = N * 128;
+  static constexpr int kPBytes = kLat ? 0 : (N > 64 ? 32768 : 16384);
+  static constexpr int kSlots = kLat ? (N == 64 ? 4 : 5) : 4;
+  static constexpr int kTails = kLat ? (N == 16 ? 2 : 1) : 0;  // slots of the rotated part, then P^T
+  static constexpr int kTailBytes = 16384;
+  static constexpr int kQOff = 0;
+  static constexpr int kPOff = kQOff + (kLat ? 9 : 2) * kQChunk;
+  static constexpr int kRingOff = kPOff + kPBytes;
+  static constexpr int kTailOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kBarOff = kTailOff + kTails * kTailBytes;
+  static constexpr int kMaskOff = kBarOff + 8 * 32;        // [N] 128-bit masks of the columns, then their union
+  static constexpr int kColOff = kMaskOff + 16 * (N + 1);  // (m, l) of the columns
+  static constexpr int kRedOff = kColOff + 8 * N;          // [2][2][4][N / 2] column maxima of the warps, by block parity
+  static constexpr int kShiftOff = kRedOff + 32 * N;       // [8 warps][N / 2], twice: shift, rescaling factor
+  static constexpr int kListOff = kShiftOff + 2 * 16 * N;
+  static __host__ __device__ constexpr int bytes(int topk) {
+    return kListOff + ((topk + 3) & ~3) * (KIND == kE4m3 ? 12 : 4);
+  }
+  static_assert(kQChunk % 1024 == 0 && kRingOff % 1024 == 0 && kTailOff % 1024 == 0, "swizzled tiles");
+  // after the last block, a part's O^T: [N][dims] floats where the ring was (512 dims at most for
+  // the latent cache, 128 for the others)
+  static_assert(N * (kLat ? 512 : 128) * 4 <= kSlots * kSlotBytes, "O^T of a part fits the ring");
+  // the weights of a merge, where Q was
+  static_assert(N * kMaxParts * 4 <= kPOff, "weights fit Q's place");
+};
+
+template <int KIND>
+constexpr int col_threads() {
+  return KIND == kE4m3 ? 448 : 320;
+}
+
+template <int KIND, int N>
+__global__ void __launch_bounds__(col_threads<KIND>(), 1)
+    columns_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const ColArgs a) {
+  using L = ColSmem<KIND, N>;
+  constexpr bool kLat = KIND == kLatent, kFp8 = KIND == kE4m3;
+  constexpr int kThreads = col_threads<KIND>();
+  constexpr int HN = N / 2;                     // columns of a warpgroup
+  constexpr int CH = HN < 32 ? HN : 32;         // of them, in registers at a time
+  constexpr int NCH = HN / CH;
+  constexpr int S = L::kSlots;
+  constexpr uint32_t kTmemCols = kLat ? 8 * N : 4 * N;  // S^T twice, O^T of up to 4 products or 1
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* full = bars;               // [S]: a slot's bytes (e4m3: codes) have landed
+  uint64_t* empty = full + S;          // [S]
+  uint64_t* ready = kFp8 ? empty + S : full;  // [S]: e4m3: expanded
+  uint64_t* tail_full = empty + 2 * S;        // [kTails]
+  uint64_t* tail_empty = tail_full + 2;
+  uint64_t* s_full = tail_empty + 2;   // [2]
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 1);
+  int32_t* n_slot = reinterpret_cast<int32_t*>(tmem_slot + 1);
+  uint32_t* cmask = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
+  float2* col_ml = reinterpret_cast<float2*>(smem + L::kColOff);
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);  // page | place of the block << 24
+  float2* scales = reinterpret_cast<float2*>(list + ((a.topk + 3) & ~3));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = blockIdx.x % a.parts, unit = blockIdx.x / a.parts;
+  const int group = unit % a.max_groups, p = unit / a.max_groups % a.hp, t = unit / a.max_groups / a.hp;
+  const int G = a.hq / a.hp;
+  pdl_wait();
+  const TileInfo tl = a.tiles[t];
+  const int c0 = group * N, cols = min(N, tl.rows * G - c0);
+  if (cols <= 0) return;  // a tile of fewer rows than the batch's most (the whole cluster)
+  const int kvh = p / (a.hp / a.hkv);
+
+  // ------------------------------------------------------------- prologue
+  if (warp == 8) {
+    if (lane == 0) {
+      prefetch_tmap(&k_map);
+      if (!kLat) prefetch_tmap(&v_map);
+      for (int s = 0; s < S; ++s) {
+        mbar_init(full + s, 1);
+        mbar_init(empty + s, 1);
+        if (kFp8) mbar_init(ready + s, 4);
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(tail_full + s, 1);
+        mbar_init(tail_empty + s, 1);
+        mbar_init(s_full + s, 1);
+      }
+      mbar_init(p_full, kSoftWarps);
+      mbar_init(pv_done, 1);
+      fence_mbar_init();
+    }
+    // this part's blocks: padding skipped, what lies behind the tile's last block or on a
+    // page outside the pool dropped and reported
+    const int32_t* sel = a.idx + (static_cast<int64_t>(t) * a.hp + p) * a.topk;
+    int first = 0, count = a.topk, seen = 0, n = 0;
+    if (a.parts > 1) {
+      int total = 0;
+      for (int b = 0; b < a.topk; b += 32) {
+        const int j = b + lane < a.topk ? sel[b + lane] : -1;
+        total += __popc(__ballot_sync(0xFFFFFFFFu, j >= 0 && j < tl.nvp));
+      }
+      first = total * part / a.parts;
+      count = total * (part + 1) / a.parts - first;
+    }
+    const int first_masked = tl.pos0 >> 7;
+    for (int b = 0; b < a.topk; b += 32) {
+      const int j = b + lane < a.topk ? sel[b + lane] : -1;
+      const bool valid = j >= 0 && j < tl.nvp;
+      const uint32_t v = __ballot_sync(0xFFFFFFFFu, valid), below = (1u << lane) - 1u;
+      const int rank = seen + __popc(v & below);
+      seen += __popc(v);
+      bool take = valid && rank >= first && rank < first + count, bad = j >= tl.nvp;
+      int64_t page = 0;
+      if (take) {
+        page = a.kv_indices[tl.page_base + j];
+        if (page < 0 || page >= a.num_pages) take = false, bad = true;
+      }
+      if (bad) atomicOr(a.err, kErrDeviceCheck);
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, take);
+      if (take) {
+        const int o = n + __popc(m & below);
+        list[o] = static_cast<uint32_t>(page) | static_cast<uint32_t>(max(j - first_masked + 1, 0)) << 24;
+        if (kFp8) {
+          const int64_t at = a.per_page ? page * a.hkv + kvh : kvh;
+          const BlockScale bs = block_scale_of(a.k_scale[at], a.v_scale[at]);
+          scales[o] = make_float2(bs.ks * a.scale_log2, bs.log2_vs);
+        }
+      }
+      n += __popc(m);
+    }
+    if (lane == 0) *n_slot = n;
+  } else if (warp == 9) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  // Q^T's columns, 64 dims a chunk, and what each sees
+  for (int e = threadIdx.x; e < N * a.kc * 8; e += kThreads) {
+    const int c = e / (a.kc * 8), u = e % (a.kc * 8);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (c < cols && u * 8 < a.dq) {
+      const int row = (c0 + c) / G, head = p * G + (c0 + c) % G;
+      v = *reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(tl.q_begin + row) * a.hq + head) * a.dq + u * 8);
+      if (kFp8) {
+        v.x = bf16x2_to_f16x2(v.x);
+        v.y = bf16x2_to_f16x2(v.y);
+        v.z = bf16x2_to_f16x2(v.z);
+        v.w = bf16x2_to_f16x2(v.w);
+      }
+    }
+    *reinterpret_cast<uint4*>(smem + L::kQOff + (u >> 3) * L::kQChunk + c * 128 + (((u & 7) ^ (c & 7)) << 4)) = v;
+  }
+  for (int e = threadIdx.x; e < N * 4; e += kThreads) {
+    const int c = e >> 2, w = e & 3, row = (c0 + c) / G;
+    // bits of word w below n
+    auto low = [&](int n) { return n >= 32 * (w + 1) ? 0xFFFFFFFFu : n <= 32 * w ? 0u : (1u << (n - 32 * w)) - 1u; };
+    uint32_t m = 0u;
+    if (c < cols)
+      m = a.tree_mask ? reinterpret_cast<const uint32_t*>(a.tree_mask + tl.q_begin + row)[w] & low(tl.rows) : low(row + 1);
+    cmask[e] = m;
+  }
+  fence_async_shared();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x < 4) {
+    uint32_t any = 0u;
+    for (int c = 0; c < N; ++c) any |= cmask[4 * c + threadIdx.x];
+    cmask[4 * N + threadIdx.x] = any;
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_slot;
+  const int n = *n_slot;
+  // key offset of lane 0 of block i's rows; places: 0 before the tile, 1 its first block, 2 the next
+  auto offset0 = [&](uint32_t entry) { return (static_cast<int>(entry >> 24) - 1) * 128 - (tl.pos0 & 127); };
+  auto seen_by_any = [&](int e) { return e < 0 || (e < 128 && (cmask[4 * N + (e >> 5)] >> (e & 31) & 1u)); };
+  // slot uses so far -> slot and phase
+  auto slot_of = [&](int u) { return u % S; };
+  auto phase_of = [&](int u) { return static_cast<uint32_t>(u / S & 1); };
+  const int per = kLat ? a.mt : 2;  // slot uses a block
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const int64_t page = list[i] & 0xFFFFFFu;
+        const int row = static_cast<int>((page * a.hkv + kvh) * 128);
+        for (int h = 0; h < per && ok; ++h) {
+          const int u = i * per + h, s = slot_of(u);
+          if (!(ok = mbar_wait(empty + s, phase_of(u) ^ 1, a.err))) break;
+          uint8_t* dst = smem + L::kRingOff + s * kSlotBytes;
+          if (kFp8) {
+            mbar_expect_tx(full + s, 128 * a.dv);
+            tma_load_2d(dst + 16384, h == 0 ? &k_map : &v_map, full + s, 0, row);
+          } else if (kLat) {
+            mbar_expect_tx(full + s, kSlotBytes);
+            for (int c = 0; c < 2; ++c) tma_load_2d(dst + c * 16384, &k_map, full + s, (2 * h + c) * 64, row);
+          } else {
+            mbar_expect_tx(full + s, a.kc * 16384);
+            for (int c = 0; c < a.kc; ++c)
+              tma_load_2d(dst + c * 16384, h == 0 ? &k_map : &v_map, full + s, c * 64, row);
+          }
+        }
+        if (kLat && ok) {
+          constexpr int T = L::kTails > 0 ? L::kTails : 1;
+          const int s = i % T;
+          if (!(ok = mbar_wait(tail_empty + s, (i / T & 1) ^ 1, a.err))) break;
+          mbar_expect_tx(tail_full + s, L::kTailBytes);
+          tma_load_2d(smem + L::kTailOff + s * L::kTailBytes, &k_map, tail_full + s, 128 * a.mt, row);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t id_qk = kFp8 ? idesc_f16_f32(128, N, false, false) : idesc_bf16_f32(128, N, false, false);
+      constexpr uint32_t id_pv = kFp8 ? idesc_f16_f32(128, N, true, true) : idesc_bf16_f32(128, N, true, true);
+      const uint64_t kd0 = smem_desc(smem_u32(smem + L::kRingOff), 16, 1024, kSwizzle128);
+      const uint64_t qd0 = smem_desc(smem_u32(smem + L::kQOff), 16, 1024, kSwizzle128);
+      // V^T: 64 dims a chunk, the second 64 one chunk on; at dims 64 both halves of M are the one chunk
+      const uint64_t vd0 = smem_desc(smem_u32(smem + L::kRingOff), a.dv == 64 ? 0 : 16384, 1024, kSwizzle128);
+      const uint64_t td0 = smem_desc(smem_u32(smem + L::kTailOff), 16, 1024, kSwizzle128);
+      const uint64_t pd0 = smem_desc(smem_u32(smem + (kLat ? L::kTailOff : L::kPOff)), 16384, 1024, kSwizzle128);
+      constexpr int T = L::kTails > 0 ? L::kTails : 1;
+      bool ok = true;
+      auto qk = [&](int i) {
+        const uint32_t d = tmem + (i & 1) * N;
+        uint32_t acc = 0;
+        for (int h = 0; h < (kLat ? a.mt : 1); ++h) {
+          const int u = i * per + h, s = slot_of(u);
+          if (!(ok = mbar_wait(ready + s, phase_of(u), a.err))) return;
+          tc_fence_after();
+          const uint64_t kd = kd0 + s * (kSlotBytes >> 4), qd = qd0 + h * 2 * (L::kQChunk >> 4);
+          for (int c = 0; c < (kLat ? 2 : a.kc); ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              mma_ss(d, kd + ((c * 16384 + kk * 32) >> 4), qd + ((c * L::kQChunk + kk * 32) >> 4), id_qk, acc);
+              acc = 1;
+            }
+          if (!kLat) mma_commit(empty + s);
+        }
+        if (kLat) {
+          const int s = i % T;
+          if (!(ok = mbar_wait(tail_full + s, i / T & 1, a.err))) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(d, td0 + ((s * L::kTailBytes + kk * 32) >> 4), qd0 + ((2 * a.mt * L::kQChunk + kk * 32) >> 4), id_qk, 1);
+        }
+        mma_commit(s_full + (i & 1));
+      };
+      if (n > 0) qk(0);
+      for (int i = 0; i < n && ok; ++i) {
+        // the latent's slots serve S^T of block i until its P.V: the next block's loads wait for that
+        if (!kLat && i + 1 < n) qk(i + 1);
+        if (!ok || !(ok = mbar_wait(p_full, i & 1, a.err))) break;
+        tc_fence_after();
+        const uint64_t pd = pd0 + (kLat ? (i % T) * (L::kTailBytes >> 4) : 0);
+        for (int h = 0; h < a.mt && ok; ++h) {
+          const int u = kLat ? i * per + h : i * per + 1, s = slot_of(u);
+          if (!kLat) {
+            if (!(ok = mbar_wait(ready + s, phase_of(u), a.err))) break;
+            tc_fence_after();
+          }
+          const uint64_t vd = vd0 + s * (kSlotBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss(tmem + (2 + h) * N, vd + ((kk * 2048) >> 4), pd + ((kk * 2048) >> 4), id_pv, i > 0 || kk > 0);
+          mma_commit(empty + s);
+        }
+        if (kLat) mma_commit(tail_empty + i % T);
+        mma_commit(pv_done);
+        if (kLat && ok && i + 1 < n) qk(i + 1);
+      }
+    }
+  } else if (warp < kSoftWarps) {
+    // ------------------------------------------------------------- softmax
+    // Every warp goes through all n blocks whatever its waits say (they are
+    // skipped after one that gave up), so the warpgroup's barriers stay whole.
+    const int wg = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    float* const red0 = reinterpret_cast<float*>(smem + L::kRedOff) + wg * 8 * HN;
+    float* shift = reinterpret_cast<float*>(smem + L::kShiftOff) + warp * 2 * HN;
+    float* alpha = shift + HN;
+    auto group_sync = [&] {
+      if (wg == 0)
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      else
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+    };
+    const uint32_t o_addr = tmem + lane_base + 2 * N + wg * HN;
+    float l[HN], m[NCH];  // sums of this thread's keys; references of columns 32 k + lane
+#pragma unroll
+    for (int c = 0; c < HN; ++c) l[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) m[k] = -INFINITY;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = mbar_wait(bar, parity, a.err);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    };
+    for (int i = 0; i < n; ++i) {
+      wait(s_full + (i & 1), i >> 1 & 1);
+      tc_fence_after();
+      const uint32_t entry = list[i];
+      const uint32_t s_addr = tmem + lane_base + (i & 1) * N + wg * HN;
+      float sl2 = a.scale_log2, log2_vs = 0.f, inv_vs = 1.f;
+      if (kFp8) {
+        const float2 sc = scales[i];
+        sl2 = sc.x, log2_vs = sc.y, inv_vs = ex2_approx(-sc.y);
+      }
+      const bool masked = entry >> 24 != 0;
+      const int e = offset0(entry) + r;
+      float* const red = red0 + (i & 1) * 4 * HN;  // a warp may be a block ahead of another's reads
+      uint32_t s[CH];
+      auto load = [&](int k) {
+        tmem_ld<CH>(s_addr + k * 32, s);
+        tmem_wait_ld();
+        if (masked && e >= 0) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            const bool see = e < 128 && (cmask[4 * (wg * HN + k * 32 + c) + (e >> 5 & 3)] >> (e & 31) & 1u);
+            if (!see) s[c] = __float_as_uint(-INFINITY);
+          }
+        }
+      };
+      // column maxima over the block's keys
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) {
+        load(k);
+        __syncwarp();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const float x = redux_max(__uint_as_float(s[c]));
+          if (lane == c) mx = x;
+        }
+        if (lane < CH) red[quarter * HN + k * 32 + lane] = mx;
+      }
+      group_sync();
+      bool moved = false;
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+        if (lane < CH) {
+          const int c = k * 32 + lane;
+          const float mx = fmaxf(fmaxf(red[c], red[HN + c]), fmaxf(red[2 * HN + c], red[3 * HN + c]));
+          const float t2 = kFp8 ? fmaf(mx, sl2, log2_vs) : mx * sl2;
+          const float m_new = t2 > m[k] + 8.f ? t2 : m[k];
+          const float m_use = m_new == -INFINITY ? 0.f : m_new;
+          alpha[c] = m_new == m[k] ? 1.f : ex2_approx(m[k] - m_use);
+          shift[c] = kFp8 ? log2_vs - m_use : -m_use;
+          moved = moved || m_new != m[k];
+          m[k] = m_new;
+        }
+      __syncwarp();
+      // P^T has one place, and the rescaling needs O^T whole
+      if (i > 0 && !kLat) wait(pv_done, (i - 1) & 1);
+      if (__any_sync(0xFFFFFFFFu, moved) && i > 0) {
+        if (kLat) wait(pv_done, (i - 1) & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < HN; ++c) l[c] *= alpha[c];
+        for (int h = 0; h < a.mt; ++h)
+#pragma unroll 1
+          for (int k = 0; k < NCH; ++k) {
+            uint32_t o[CH];
+            tmem_ld<CH>(o_addr + h * N + k * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < CH; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[k * 32 + c]);
+            tmem_st<CH>(o_addr + h * N + k * 32, o);
+          }
+        tmem_wait_st();
+      }
+      uint8_t* pt = smem + (kLat ? L::kTailOff + (i % (L::kTails > 0 ? L::kTails : 1)) * L::kTailBytes : L::kPOff);
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) {
+        if (NCH > 1) load(k);
+#pragma unroll
+        for (int c = 0; c < CH; c += 8) {
+          uint4 w;
+          uint32_t* pw = &w.x;
+#pragma unroll
+          for (int d = 0; d < 8; d += 2) {
+            const float2 sh = *reinterpret_cast<const float2*>(shift + k * 32 + c + d);
+            float x0, x1;
+            ffma2v(x0, x1, __uint_as_float(s[c + d]), __uint_as_float(s[c + d + 1]), sl2, sl2, sh.x, sh.y);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            if (kFp8)
+              ffma2v(l[k * 32 + c + d], l[k * 32 + c + d + 1], p0, p1, inv_vs, inv_vs, l[k * 32 + c + d], l[k * 32 + c + d + 1]);
+            else
+              fadd2(l[k * 32 + c + d], l[k * 32 + c + d + 1], p0, p1);
+            pw[d / 2] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+          const int col = wg * HN + k * 32 + c;
+          *reinterpret_cast<uint4*>(pt + (col >> 6) * 16384 + r * 128 + (((col >> 3 & 7) ^ (r & 7)) << 4)) = w;
+        }
+      }
+      if (!kFp8 && masked && wg == 0) {  // V rows that no column sees (e4m3: the converters)
+        if (!kLat) wait(full + slot_of(2 * i + 1), phase_of(2 * i + 1));
+        if (!seen_by_any(e))
+          for (int h = 0; h < (kLat ? a.mt : 1); ++h) {
+            uint8_t* v = smem + L::kRingOff + slot_of(kLat ? i * per + h : 2 * i + 1) * kSlotBytes + r * 128;
+            for (int c = 0; c < (kLat ? 2 : a.kc); ++c)
+#pragma unroll
+              for (int b = 0; b < 8; ++b) *reinterpret_cast<uint4*>(v + c * 16384 + b * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+      }
+      fence_async_shared();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+
+    // ------------------------------------------------------------ epilogue
+    if (n > 0) wait(pv_done, (n - 1) & 1);
+    tc_fence_after();
+    group_sync();  // red is free
+    float* const red = red0;
+    float total[NCH];
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      total[k] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float x = l[k * 32 + c];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+        if (lane == c) total[k] = x;
+      }
+      if (lane < CH) red[quarter * HN + k * 32 + lane] = total[k];
+    }
+    group_sync();
+#pragma unroll
+    for (int k = 0; k < NCH; ++k)
+      if (lane < CH) {
+        const int c = k * 32 + lane;
+        total[k] = (red[c] + red[HN + c]) + (red[2 * HN + c] + red[3 * HN + c]);
+        alpha[c] = total[k] > 0.f ? 1.f / total[k] : 0.f;
+        if (quarter == 0) {
+          col_ml[wg * HN + c] = make_float2(ok ? m[k] : -INFINITY, total[k]);
+          const int cg = c0 + wg * HN + c;
+          if (a.parts == 1 && a.lse != nullptr && wg * HN + c < cols)
+            a.lse[static_cast<int64_t>(tl.q_begin + cg / G) * a.hq + p * G + cg % G] =
+                total[k] > 0.f ? (m[k] + log2f(total[k])) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+    __syncwarp();
+    float* part_o = reinterpret_cast<float*>(smem + L::kRingOff);
+    for (int h = 0; h < a.mt; ++h)
+#pragma unroll 1
+      for (int k = 0; k < NCH; ++k) {
+        uint32_t o[CH];
+        if (n > 0) {
+          tmem_ld<CH>(o_addr + h * N + k * 32, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int c = 0; c < CH; ++c) o[c] = 0u;
+        }
+        if (h * 128 + r >= a.dv) continue;  // dims 64: the upper half repeats the lower
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int col = wg * HN + k * 32 + c, cg = c0 + col;
+          if (col >= cols) break;
+          if (a.parts > 1)
+            part_o[col * a.dv + h * 128 + r] = __uint_as_float(o[c]);
+          else
+            a.out[(static_cast<int64_t>(tl.q_begin + cg / G) * a.hq + p * G + cg % G) * a.dv + h * 128 + r] =
+                __float2bfloat16_rn(__uint_as_float(o[c]) * alpha[k * 32 + c]);
+        }
+      }
+  } else if (kFp8) {
+    // ---------------------------------------------------------- converters
+    // A thread has one key's codes in registers before it writes that key's f16
+    // row, the only one that overlaps them (dims 128; at dims 64 none does).
+    const int r = threadIdx.x - 32 * (kSoftWarps + 2), sw = r & 7;
+    bool ok = true;
+    for (int u = 0; u < 2 * n; ++u) {
+      const int s = slot_of(u);
+      uint8_t* buf = smem + L::kRingOff + s * kSlotBytes;
+      const uint32_t entry = list[u >> 1];
+      const bool zero = (u & 1) && entry >> 24 != 0 && !seen_by_any(offset0(entry) + r);
+      if (ok) ok = mbar_wait(full + s, phase_of(u), a.err);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      auto expand = [&](uint4 v, int unit) {  // sixteen codes -> f16 units 2 unit, 2 unit + 1
+        if (zero) v = make_uint4(0u, 0u, 0u, 0u);
+        uint8_t* dst = buf + (unit >> 2) * 16384 + r * 128;
+        const int u0 = (unit & 3) * 2;
+        *reinterpret_cast<uint4*>(dst + ((u0 ^ sw) << 4)) = make_uint4(
+            e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
+        *reinterpret_cast<uint4*>(dst + (((u0 + 1) ^ sw) << 4)) = make_uint4(
+            e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+      };
+      uint4 v[8];
+      if (a.dv == 128) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 128 + ((c ^ sw) << 4));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) expand(v[c], c);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) expand(v[c], c);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready + s);
+    }
+  }
+
+  // ------------------------------------------------------------------- end
+  tc_fence_before();
+  if (a.parts == 1) {
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
+  cluster_sync();  // every part's O^T, m and l are in its shared memory
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+  float* wts = reinterpret_cast<float*>(smem + L::kQOff);  // [column][part]
+  for (int c = threadIdx.x; c < cols; c += kThreads) {
+    float2 ml[kMaxParts];
+    float mm = -INFINITY, sum = 0.f;
+    const uint32_t at = smem_u32(col_ml + c);
+#pragma unroll
+    for (int w = 0; w < kMaxParts; ++w)
+      if (w < a.parts) ml[w] = ld_cluster_f2(at, w), mm = fmaxf(mm, ml[w].x);
+#pragma unroll
+    for (int w = 0; w < kMaxParts; ++w)
+      if (w < a.parts) {
+        ml[w].x = ml[w].x == -INFINITY ? 0.f : ex2_approx(ml[w].x - mm);
+        sum += ml[w].y * ml[w].x;
+      }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int w = 0; w < kMaxParts; ++w)
+      if (w < a.parts) wts[c * kMaxParts + w] = ml[w].x * inv;
+    const int cg = c0 + c;
+    if (part == 0 && a.lse != nullptr)
+      a.lse[static_cast<int64_t>(tl.q_begin + cg / G) * a.hq + p * G + cg % G] =
+          sum > 0.f ? (mm + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  }
+  __syncthreads();
+  const int dv4 = a.dv / 4;
+  for (int e = part * kThreads + threadIdx.x; e < cols * dv4; e += a.parts * kThreads) {
+    const int c = e / dv4, cg = c0 + c;
+    const uint32_t at = smem_u32(smem + L::kRingOff) + 16u * e;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kMaxParts; ++w)
+      if (w < a.parts) {
+        const float x = wts[c * kMaxParts + w];
+        const float4 v = ld_cluster_f4(at, w);
+        o.x += v.x * x, o.y += v.y * x, o.z += v.z * x, o.w += v.w * x;
+      }
+    *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(tl.q_begin + cg / G) * a.hq + p * G + cg % G) * a.dv +
+                              4 * (e % dv4)) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  }
+  cluster_sync();  // nobody leaves while its part may be read
+}
+
+template <int KIND, int N>
+cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  using L = ColSmem<KIND, N>;
+  const int G = p->hq / p->hp;
+  int64_t units = 0;
+  int groups = 1, blocks = 1;
+  for (const TileInfo& t : p->tiles) {
+    const int g = (t.rows * G + N - 1) / N;
+    units += int64_t(p->hp) * g;
+    groups = std::max(groups, g);
+    blocks = std::max(blocks, std::min(t.nvp, p->topk));
+  }
+  int parts = 1;
+  while (parts < kMaxParts && parts * 2 <= blocks && units * parts * 2 <= p->num_sms) parts *= 2;
+  a.parts = parts;
+  a.max_groups = groups;
+  const int64_t ctas = int64_t(p->n_tiles) * p->hp * groups * parts;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  auto kern = columns_kernel<KIND, N>;
+  // the limit is the function's, for every host thread: always the most of any topk
+  static_assert(L::bytes(1024) + 1024 <= 232448, "shared memory at the largest topk");
+  if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(1024) + 1024))
+    return e;
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), parts, dim3(col_threads<KIND>()),
+                            L::bytes(p->topk) + 1024, st, km, vm, a);
+}
+
+// Columns of the widest tile, for the choice of N.
+int most_columns(const msa_plan_s* p) {
+  int rows = 1;
+  for (const TileInfo& t : p->tiles) rows = std::max(rows, t.rows);
+  return rows * (p->hq / p->hp);
+}
+
+}  // namespace
+
+msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,
+                            const int32_t* kv_indices, const int32_t* idx, const int32_t* tree_mask, const float* k_scale,
+                            const float* v_scale, void* out, float* lse, cudaStream_t st) {
+  const bool fp8 = p->kv_dtype != MSA_KV_BF16;
+  CUtensorMap km, vm;
+  const uint64_t dims[2] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->num_pages) * p->hkv * 128};
+  const uint64_t str[1] = {static_cast<uint64_t>(p->d) * (fp8 ? 1 : 2)};
+  const uint32_t box[2] = {fp8 ? static_cast<uint32_t>(p->d) : 64u, 128};
+  const int swz = fp8 ? p->d : 128;
+  if (!encode_tensor_map(&km, 2, k_pages, dims, str, box, fp8 ? 0 : 1, swz) ||
+      !encode_tensor_map(&vm, 2, v_pages, dims, str, box, fp8 ? 0 : 1, swz))
+    return set_error(MSA_ERR_CUDA, "msa_tree_attn: tensor map encoding failed");
+  ColArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.tiles = p->tiles_d;
+  a.idx = idx;
+  a.kv_indices = kv_indices;
+  a.tree_mask = reinterpret_cast<const uint4*>(tree_mask);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.err = p->err_d;
+  a.num_pages = p->num_pages;
+  a.hq = p->hq, a.hp = p->hp, a.hkv = p->hkv;
+  a.topk = p->topk;
+  a.dq = a.dv = p->d;
+  a.kc = p->d / 64;
+  a.mt = 1;
+  a.per_page = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK;
+  a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(p->d));
+  const int c = most_columns(p);
+  const auto launch = fp8 ? (c <= 16 ? launch_columns<kE4m3, 16> : c <= 32 ? launch_columns<kE4m3, 32>
+                             : c <= 64 ? launch_columns<kE4m3, 64> : launch_columns<kE4m3, 128>)
+                          : (c <= 16 ? launch_columns<kBf16, 16> : c <= 32 ? launch_columns<kBf16, 32>
+                             : c <= 64 ? launch_columns<kBf16, 64> : launch_columns<kBf16, 128>);
+  return cuda_check(launch(p, a, km, vm, st), "msa_tree_attn: launch");
+}
+
+msa_status launch_latent_attn(const msa_plan_s* p, const void* q, const void* latent_pages, const int32_t* kv_indices,
+                              const int32_t* idx, const int32_t* tree_mask, int32_t latent_dim, int32_t rope_dim,
+                              float scale, void* out, float* lse, cudaStream_t st) {
+  CUtensorMap km;
+  const int width = latent_dim + rope_dim;
+  // boxes of 64 columns; the last one's columns past the row are zeros
+  const uint64_t dims[2] = {static_cast<uint64_t>(width), static_cast<uint64_t>(p->num_pages) * 128};
+  const uint64_t str[1] = {static_cast<uint64_t>(width) * 2};
+  const uint32_t box[2] = {64, 128};
+  if (!encode_tensor_map(&km, 2, latent_pages, dims, str, box, 1, 128))
+    return set_error(MSA_ERR_CUDA, "msa_latent_attn: tensor map encoding failed");
+  ColArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.tiles = p->tiles_d;
+  a.idx = idx;
+  a.kv_indices = kv_indices;
+  a.tree_mask = reinterpret_cast<const uint4*>(tree_mask);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.err = p->err_d;
+  a.num_pages = p->num_pages;
+  a.hq = p->hq, a.hp = p->hp, a.hkv = 1;
+  a.topk = p->topk;
+  a.dq = width;
+  a.dv = latent_dim;
+  a.kc = latent_dim / 64 + 1;
+  a.mt = latent_dim / 128;
+  a.scale_log2 = 1.4426950408889634f * scale;
+  const int c = most_columns(p);
+  const auto launch = c <= 16 ? launch_columns<kLatent, 16> : c <= 32 ? launch_columns<kLatent, 32>
+                                                                      : launch_columns<kLatent, 64>;
+  return cuda_check(launch(p, a, km, km, st), "msa_latent_attn: launch");
+}
+
+namespace {
+
+// The tiles of a tree are its sequence's drafts: one tile a sequence, whose
+// masks have 128 bits.
+msa_status check_tree(const char* fn, const msa_plan_s* p) {
+  for (int32_t n : p->qo_lens)
+    if (n > kTile) return set_error(MSA_ERR_UNSUPPORTED, "%s: a tree has at most %d drafts, a sequence has %d", fn, kTile, n);
+  return MSA_OK;
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+msa_status msa_tree_attn(msa_plan_t plan, const void* q, const void* k_pages, const void* v_pages,
+                         const int32_t* kv_indices, const int32_t* kv_block_indexes, const int32_t* tree_mask,
+                         const float* k_scale, const float* v_scale, void* out, float* lse, msa_stream_t stream) {
+  const char* fn = "msa_tree_attn";
+  if (!plan || !q || !k_pages || !v_pages || !kv_indices || !kv_block_indexes || !tree_mask || !out)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: NULL argument", fn);
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
+    return set_error(MSA_ERR_INVALID_ARG, "%s: q, k_pages, v_pages, out must be 16-byte aligned", fn);
+  if (!aligned4(tree_mask)) return set_error(MSA_ERR_INVALID_ARG, "%s: tree_mask must be 4-byte aligned", fn);
+  const bool fp8 = plan->kv_dtype != MSA_KV_BF16;
+  if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
+    return set_error(MSA_ERR_INVALID_ARG, "%s: k_scale/v_scale must be given exactly for FP8 K/V", fn);
+  msa_status s = check_tree(fn, plan);
+  if (s == MSA_OK) s = check_device(fn, plan);
+  if (s != MSA_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  s = launch_tree_attn(plan, q, k_pages, v_pages, kv_indices, kv_block_indexes, tree_mask, k_scale, v_scale, out, lse, st);
+  const int64_t rows = plan->total_q * plan->hq;
+  if (s == MSA_OK) s = scan_rows(plan, q, rows * plan->d, 2, st);
+  if (s == MSA_OK) s = scan_rows(plan, out, rows * plan->d, 2, st);
+  if (s == MSA_OK) s = scan_rows(plan, lse, rows, 4, st);
+  return s;
+}
+
+msa_status msa_latent_attn(msa_plan_t plan, const void* q, const void* latent_pages, const int32_t* kv_indices,
+                           const int32_t* kv_block_indexes, const int32_t* tree_mask, int32_t latent_dim,
+                           int32_t rope_dim, float scale, void* out, float* lse, msa_stream_t stream) {
+  const char* fn = "msa_latent_attn";
+  if (!plan || !q || !latent_pages || !kv_indices || !kv_block_indexes || !out)
+    return set_error(MSA_ERR_INVALID_ARG, "%s: NULL argument", fn);
+  if (const msa_status s = check_latent_dims(fn, latent_dim, rope_dim); s != MSA_OK) return s;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return set_error(MSA_ERR_INVALID_ARG, "%s: scale must be positive", fn);
+  if (!aligned16(q) || !aligned16(latent_pages) || !aligned16(out))
+    return set_error(MSA_ERR_INVALID_ARG, "%s: q, latent_pages, out must be 16-byte aligned", fn);
+  if (!aligned4(tree_mask)) return set_error(MSA_ERR_INVALID_ARG, "%s: tree_mask must be 4-byte aligned", fn);
+  msa_status s = tree_mask ? check_tree(fn, plan) : MSA_OK;
+  if (s == MSA_OK) s = check_device(fn, plan);
+  if (s != MSA_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  s = launch_latent_attn(plan, q, latent_pages, kv_indices, kv_block_indexes, tree_mask, latent_dim, rope_dim, scale, out,
+                         lse, st);
+  const int64_t rows = plan->total_q * plan->hq;
+  if (s == MSA_OK) s = scan_rows(plan, q, rows * (latent_dim + rope_dim), 2, st);
+  if (s == MSA_OK) s = scan_rows(plan, out, rows * latent_dim, 2, st);
+  if (s == MSA_OK) s = scan_rows(plan, lse, rows, 4, st);
+  return s;
+}
+
+}  // extern "C"

@@ -107,6 +107,7 @@ struct msa_plan_s {
   int32_t n_page_entries = 0;        // sum over sequences of ceil(kv_len / 128)
   int64_t append_units_off = 0;      // cache appends: one unit per page that gets rows
   int32_t n_append_units = 0;
+  int64_t entry_keys_off = 0;        // latent expansion: keys of each page-table entry's page
   void* bwd_d = nullptr;             // backward scratch (D, proxy LSE, inverse index)
 };
 
@@ -177,6 +178,7 @@ void proxy_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
 void attn_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
 void bwd_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
 void append_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
+void expand_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux);
 size_t bwd_scratch_bytes(const msa_plan_s* p);
 size_t fused_topk_scratch_bytes(const msa_plan_s* p);  // 0 when msa_proxy_topk is unsupported
 size_t fused_topk_counter_bytes(const msa_plan_s* p);  // leading part that starts at zero
@@ -246,6 +248,16 @@ msa_status launch_attn_bwd(const msa_plan_s* p, const void* q, const void* k_pag
                            const void* out, const float* lse, const void* dout, const void* pq,
                            const void* pk_pages, float kl_weight, float* dq, float* dk, float* dv,
                            float* dpq, float* dpk, cudaStream_t st);
+
+// the dims that a latent cache may have (append.cu)
+msa_status check_latent_dims(const char* fn, int32_t latent_dim, int32_t rope_dim);
+// attention of few rows, the (row, head) pairs as columns (columns.cu)
+msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,
+                            const int32_t* kv_indices, const int32_t* idx, const int32_t* tree_mask, const float* k_scale,
+                            const float* v_scale, void* out, float* lse, cudaStream_t st);
+msa_status launch_latent_attn(const msa_plan_s* p, const void* q, const void* latent_pages, const int32_t* kv_indices,
+                              const int32_t* idx, const int32_t* tree_mask, int32_t latent_dim, int32_t rope_dim,
+                              float scale, void* out, float* lse, cudaStream_t st);
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
 // dtype_bf16_or_u8: 0 uint8, 1 bf16, 2 fp32.

@@ -57,6 +57,10 @@ SIGNATURES = {
     "msa_kv_append": (_i32, [_p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p]),
     "msa_pk_append": (_i32, [_p, _p, _p, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _p]),
     "msa_append_bwd": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p]),
+    "msa_tree_attn": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p]),
+    "msa_latent_append": (_i32, [_p, _p, _p, _p, _i64, _p, _i64, _p, _i32, _i32, _p, _p]),
+    "msa_latent_attn": (_i32, [_p, _p, _p, _p, _p, _p, _i32, _i32, _f32, _p, _p, _p]),
+    "msa_latent_expand": (_i32, [_p, _p, _p, _p, _p, _i32, _i32, _p, _p, _p]),
     "msa_check_errors": (_i32, [_p, _p]),
     "msa_selftest_wait_timeout": (_i32, [_p]),
     "msa_test_fail_plan_allocs": (None, [_i32]),
@@ -302,6 +306,8 @@ class Plan:
         self._pk_shape = (self.total_q, 1, self.dp)
         self._grad_needs = ((torch.float32, pool, "dk_pages"), (torch.float32, pool, "dv_pages"),
                             (torch.float32, ppool + (self.dp,), "dpk_pages"), pos, self._cache_needs[0])
+        self._mask_need = (torch.int32, (self.total_q, 4), "tree_mask")
+        self._idx_need = (torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes")
         self._attn_needs = self._cache_needs + ((torch.bfloat16, self._q_shape, "q"), (
             torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes"))
 
@@ -347,6 +353,35 @@ class Plan:
                                    kv_indices.data_ptr(), _ptr(dk_pages), _ptr(dv_pages), _ptr(dpk_pages), _ptr(dk),
                                    _ptr(dv), _ptr(dpk), _stream(stream)), "msa_append_bwd")
         return dk, dv, dpk
+
+    def latent_append(self, latent, key, latent_pages, kv_indices, rope=None, positions=None, stream=None):
+        """The batch's new rows of a latent cache (msa_latent_append): latent
+        [total_q, 1, latent_dim] and key [total_q, 1, rope_dim] bf16, at strides,
+        into latent_pages [P, 1, 128, latent_dim + rope_dim]; key rotated by
+        `rope` at int32 positions [total_q], or at its key positions."""
+        n, width = latent.shape[-1], key.shape[-1]
+        latent_stride = _rows(latent, torch.bfloat16, (self.total_q, 1, n), "latent")
+        key_stride = _rows(key, torch.bfloat16, (self.total_q, 1, width), "key")
+        _need(latent_pages, torch.bfloat16, (self.num_pages, 1, 128, n + width), "latent_pages")
+        _need(kv_indices, *self._cache_needs[0])
+        if positions is not None:
+            _need(positions, torch.int32, (self.total_q,), "positions")
+        _check(_lib.msa_latent_append(self._h, rope and rope._h, _ptr(positions), latent.data_ptr(), latent_stride,
+                                      key.data_ptr(), key_stride, kv_indices.data_ptr(), n, width,
+                                      latent_pages.data_ptr(), _stream(stream)), "msa_latent_append")
+
+    def latent_expand(self, latent_pages, w_k, w_v, kv_indices, k_pages, v_pages, stream=None):
+        """K and V pages [P, Hkv, 128, d] out of a latent cache's (msa_latent_expand):
+        w_k [Hkv, d - rope_dim, latent_dim] and w_v [Hkv, d, latent_dim] bf16."""
+        n = w_v.shape[-1]
+        width = latent_pages.shape[-1] - n
+        _need(latent_pages, torch.bfloat16, (self.num_pages, 1, 128, n + width), "latent_pages")
+        _need(w_k, torch.bfloat16, (self.hkv, self.d - width, n), "w_k")
+        _need(w_v, torch.bfloat16, (self.hkv, self.d, n), "w_v")
+        _need_all((kv_indices, k_pages, v_pages), self._cache_needs)
+        _check(_lib.msa_latent_expand(self._h, latent_pages.data_ptr(), w_k.data_ptr(), w_v.data_ptr(),
+                                      kv_indices.data_ptr(), n, width, k_pages.data_ptr(), v_pages.data_ptr(),
+                                      _stream(stream)), "msa_latent_expand")
 
     # -- stage 1
     def proxy_maxscore(self, pq, pk_pages, kv_indices, out=None, stream=None):
@@ -424,6 +459,49 @@ class Plan:
         _check(_lib.msa_sparse_attn(self._h, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                     kv_indices.data_ptr(), kv_block_indexes.data_ptr(), _ptr(k_scale), _ptr(v_scale),
                                     out.data_ptr(), _ptr(lse), _stream(stream)), "msa_sparse_attn")
+        return out, lse
+
+    def _outputs(self, out, lse, shape, want_lse, dev):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, torch.bfloat16, shape, "out")
+        if lse is not None:
+            _need(lse, torch.float32, self._lse_shape, "lse")
+        elif want_lse:
+            lse = torch.empty(self._lse_shape, dtype=torch.float32, device=dev)
+        return out, lse
+
+    def tree_attn(self, q, k_pages, v_pages, kv_indices, kv_block_indexes, tree_mask, k_scale=None, v_scale=None,
+                  out=None, lse=None, want_lse=True, stream=None):
+        """Attention of drafted tokens over the cache (msa_tree_attn): row i sees
+        the keys before the drafts, and draft b of its sequence iff bit b % 32 of
+        tree_mask[i, b // 32] is set (int32 [total_q, 4])."""
+        _need_all((kv_indices, k_pages, v_pages, q, kv_block_indexes) if self.kv_dtype == "bf16" else
+                  (kv_indices, k_pages, v_pages, k_scale, v_scale, q, kv_block_indexes), self._attn_needs)
+        _need(tree_mask, *self._mask_need)
+        out, lse = self._outputs(out, lse, self._q_shape, want_lse, q.device)
+        _check(_lib.msa_tree_attn(self._h, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_indices.data_ptr(),
+                                  kv_block_indexes.data_ptr(), tree_mask.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                                  out.data_ptr(), _ptr(lse), _stream(stream)), "msa_tree_attn")
+        return out, lse
+
+    def latent_attn(self, q, latent_pages, kv_indices, kv_block_indexes, rope_dim, scale, tree_mask=None, out=None,
+                    lse=None, want_lse=True, stream=None):
+        """Absorbed attention over a latent cache (msa_latent_attn): q [total_q, Hq,
+        latent_dim + rope_dim] bf16, out [total_q, Hq, latent_dim]; causal, or by
+        tree_mask as tree_attn has it."""
+        width = q.shape[-1]
+        _need(q, torch.bfloat16, (self.total_q, self.hq, width), "q")
+        _need(latent_pages, torch.bfloat16, (self.num_pages, 1, 128, width), "latent_pages")
+        _need(kv_indices, *self._cache_needs[0])
+        _need(kv_block_indexes, *self._idx_need)
+        if tree_mask is not None:
+            _need(tree_mask, *self._mask_need)
+        out, lse = self._outputs(out, lse, (self.total_q, self.hq, width - rope_dim), want_lse, q.device)
+        _check(_lib.msa_latent_attn(self._h, q.data_ptr(), latent_pages.data_ptr(), kv_indices.data_ptr(),
+                                    kv_block_indexes.data_ptr(), _ptr(tree_mask), width - rope_dim, rope_dim,
+                                    float(scale), out.data_ptr(), _ptr(lse), _stream(stream)), "msa_latent_attn")
         return out, lse
 
     # -- training extension

@@ -41,8 +41,9 @@
  *    sequence s is page kv_indices[sum_{s'<s} ceil(kv_len_s'/128) + j]).
  *    Page ids must lie in [0, num_pages); a kernel that meets one outside
  *    raises MSA_ERR_DEVICE_CHECK in the plan's error word (read with
- *    msa_check_errors) and skips that block (the appends, and attention over
- *    MSA_KV_FP8_E4M3_BLOCK pages) or reads page 0 in its place (the rest).
+ *    msa_check_errors) and skips that block (the appends, attention over
+ *    MSA_KV_FP8_E4M3_BLOCK pages, tree attention, and the calls of a latent
+ *    cache) or reads page 0 in its place (the rest).
  *  - A plan belongs to the device that was current when it was made; its
  *    calls are refused (MSA_ERR_INVALID_ARG) while another one is.
  *  - Errors: host-side argument checks return MSA_ERR_INVALID_ARG or
@@ -539,6 +540,102 @@ msa_status msa_pk_append(msa_plan_t plan, msa_rope_t rope, const int32_t* positi
 msa_status msa_append_bwd(msa_plan_t plan, msa_rope_t k_rope, msa_rope_t pk_rope, const int32_t* positions,
                           const int32_t* kv_indices, const float* dk_pages, const float* dv_pages,
                           const float* dpk_pages, float* dk, float* dv, float* dpk, msa_stream_t stream);
+
+/*
+ * msa_tree_attn -- block-sparse attention for trees of drafted tokens
+ * (speculative decoding): a sequence's query rows are the drafts of one step,
+ * whose K and V msa_kv_append has written at key positions kv_len - qo_len ..
+ * kv_len (`positions` there takes each draft's place in the text, the tree's
+ * depth).  Row i sees every key before the drafts, and draft b of its sequence
+ * iff bit b % 32 of word b / 32 of tree_mask[i] is set: its ancestors and
+ * itself, but any mask serves.  Otherwise as msa_sparse_attn: the rows of a tile
+ * share kv_block_indexes[t, p, :] (msa_topk_select's, for instance).
+ *
+ *  q                 bf16 [total_q, Hq, d].
+ *  k_pages, v_pages, k_scale, v_scale   as msa_sparse_attn, of any kv_dtype at
+ *                    head_dim 64 or 128.  Scales, static ones too, are taken as
+ *                    lying in [2^-40, 2^40].
+ *  kv_block_indexes  int32 [num_tiles, Hp, topk]: distinct blocks in any order,
+ *                    -1 anywhere.
+ *  tree_mask         int32 [total_q, 4]; bits of drafts that the sequence does
+ *                    not have are ignored.
+ *  out               bf16 [total_q, Hq, d].
+ *  lse               fp32 [total_q, Hq] or NULL.
+ * A row that sees no key of its selection gets out = 0 and lse = -inf.  Keys
+ * that no row of a tile sees, those behind a sequence's last key among them,
+ * may hold any bytes; a key that some row sees must be finite.  FP8: q is
+ * rounded to f16 and saturates beyond 65504, as in msa_sparse_attn.  A page id
+ * outside the pool is reported and its block skipped.  At most 128 drafts a
+ * sequence (MSA_ERR_UNSUPPORTED otherwise).  One launch without workspace:
+ * calls of one plan may overlap.
+ */
+msa_status msa_tree_attn(msa_plan_t plan, const void* q, const void* k_pages, const void* v_pages,
+                         const int32_t* kv_indices, const int32_t* kv_block_indexes, const int32_t* tree_mask,
+                         const float* k_scale, const float* v_scale, void* out, float* lse, msa_stream_t stream);
+
+/*
+ * A latent cache keeps one row [latent | key part] a token, shared by all
+ * heads: head h's key is [w_k[h] . latent | key part], the key part carrying the
+ * rotary position, and its value w_v[h] . latent.  Pages, page table and block
+ * selections are those of K/V caches.  latent_dim is 128, 256, 384 or 512,
+ * rope_dim (the key part's width) 16, 32, 48 or 64.
+ *
+ * msa_latent_append -- writes a batch's new rows into the cache, as
+ * msa_kv_append does K, the key part rotated when a rope is given.
+ *
+ *  latent        bf16 [total_q, latent_dim], rows latent_row_stride elements
+ *                apart; key: bf16 [total_q, rope_dim], rows key_row_stride
+ *                apart; rows start on 16-byte boundaries.
+ *  latent_pages  bf16 [num_pages, 1, 128, latent_dim + rope_dim].
+ * rope, positions, kv_indices, errors: as msa_kv_append.
+ */
+msa_status msa_latent_append(msa_plan_t plan, msa_rope_t rope, const int32_t* positions, const void* latent,
+                             int64_t latent_row_stride, const void* key, int64_t key_row_stride,
+                             const int32_t* kv_indices, int32_t latent_dim, int32_t rope_dim, void* latent_pages,
+                             msa_stream_t stream);
+
+/*
+ * msa_latent_attn -- block-sparse attention over a latent cache in the absorbed
+ * form, for decode steps, draft trees and chunks: with q[i,h] = [w_k[h]^T .
+ * q_nope | rotated part], s = scale * q[i,h] . row[key] and out = P . latent, of
+ * which the caller's w_v[h] makes the head's output.  Which keys a row sees is
+ * causal, or msa_tree_attn's with a tree_mask.
+ *
+ *  q                 bf16 [total_q, Hq, latent_dim + rope_dim].
+ *  latent_pages      as msa_latent_append wrote them.
+ *  kv_block_indexes  int32 [num_tiles, Hp, topk]: proxy head p's blocks serve
+ *                    query heads [p*Hq/Hp, (p+1)*Hq/Hp).
+ *  tree_mask         int32 [total_q, 4], or NULL.
+ *  scale             > 0: the softmax scale of the heads before absorption.
+ *  out               bf16 [total_q, Hq, latent_dim].
+ *  lse               fp32 [total_q, Hq] or NULL.
+ * The plan's num_kv_heads, head_dim and kv_dtype are not read.  Rows without
+ * keys, unseen keys, bad pages and overlapping calls: as msa_tree_attn.
+ */
+msa_status msa_latent_attn(msa_plan_t plan, const void* q, const void* latent_pages, const int32_t* kv_indices,
+                           const int32_t* kv_block_indexes, const int32_t* tree_mask, int32_t latent_dim,
+                           int32_t rope_dim, float scale, void* out, float* lse, msa_stream_t stream);
+
+/*
+ * msa_latent_expand -- the expanded form, for prefills: K and V pages that
+ * msa_sparse_attn reads, out of the pages of a latent cache that the plan's
+ * sequences name:
+ *   k_pages[page, h, slot] = [w_k[h] . latent | key part],
+ *   v_pages[page, h, slot] = w_v[h] . latent,
+ * summed in fp32 and rounded once.  h runs over the plan's KV heads.
+ *
+ *  latent_pages      as msa_latent_append wrote them.
+ *  w_k               bf16 [Hkv, d - rope_dim, latent_dim], rope_dim < d;
+ *  w_v               bf16 [Hkv, d, latent_dim]; 16-byte aligned.
+ *  k_pages, v_pages  bf16 [num_pages, Hkv, 128, d], 32-byte aligned (output;
+ *                    slots behind a sequence's last key and pages that the
+ *                    plan's sequences do not name keep their contents).
+ * bf16 plans only.  A page id outside the pool is reported and its page
+ * left out.
+ */
+msa_status msa_latent_expand(msa_plan_t plan, const void* latent_pages, const void* w_k, const void* w_v,
+                             const int32_t* kv_indices, int32_t latent_dim, int32_t rope_dim, void* k_pages,
+                             void* v_pages, msa_stream_t stream);
 
 /*
  * msa_check_errors -- waits for `stream`, then reads and clears the plan's

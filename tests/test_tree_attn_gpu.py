@@ -1,0 +1,316 @@
+"""msa_tree_attn against its definition in 64 bits: trees of every shape over the
+three caches, what must not be read, clusters, captures, streams and bad pages."""
+import numpy as np
+import pytest
+import torch
+
+from tests.tree_cases import attend, chain_mask, check, selection, tree_mask
+
+pytestmark = pytest.mark.gpu
+
+
+def _msa():
+    from block_sparse_long_proxy_gb300 import msa
+    return msa
+
+
+class Case:
+    """A batch of trees: caches with NaN wherever no row looks."""
+
+    def __init__(self, dev, qo, kv, hq, hkv, hp, d, topk, kind, seed=0, grow=0.0, empty=0.1, irregular=True):
+        rng = np.random.default_rng(seed)
+        gen = torch.Generator(device=dev).manual_seed(seed)
+        self.qo, self.kv, self.hq, self.hkv, self.hp, self.d, self.topk, self.kind = qo, kv, hq, hkv, hp, d, topk, kind
+        nb = [(k + 127) // 128 for k in kv]
+        self.p = p = sum(nb) + 2
+        table = rng.permutation(p)[:sum(nb)].astype(np.int32)
+        self.table = torch.from_numpy(table).to(dev)
+        words, self.seen = tree_mask(qo, rng, empty)
+        self.mask = torch.from_numpy(words).to(dev)
+        self.idx_h = selection(qo, kv, hp, topk, rng, irregular)
+        self.idx = torch.from_numpy(self.idx_h).to(dev)
+        self.q = torch.randn((sum(qo), hq, d), generator=gen, device=dev).to(torch.bfloat16)
+        shape = (p, hkv, 128, d)
+        self.pages, self.scales, self.values = [], [], []
+        for which in range(2):
+            x = torch.randn(shape, generator=gen, device=dev)
+            if which == 0 and grow:  # later blocks' keys are larger: the running maximum keeps moving
+                at = np.concatenate([np.arange(n) for n in nb])
+                f = torch.ones(p, device=dev)
+                f[self.table.long()] = torch.from_numpy(1 + grow * at).float().to(dev)
+                x = x * f[:, None, None, None]
+            if kind == "bf16":
+                pages, scale = x.to(torch.bfloat16), None
+                value = pages.double()
+            else:
+                pages = (x * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+                if kind == "e4m3":
+                    scale = 0.012 * (1 + torch.rand(hkv, generator=gen, device=dev))
+                    value = pages.double() * scale.double()[None, :, None, None]
+                else:
+                    scale = torch.exp2(torch.randint(-8, -4, (p, hkv), generator=gen, device=dev).float())
+                    value = pages.double() * scale.double()[:, :, None, None]
+            # NaN in pages that no table names, behind each last key, and at drafts that no row sees
+            hole = torch.ones((p, 128), dtype=torch.bool, device=dev)
+            base, r0 = 0, 0
+            for q, k, n in zip(qo, kv, nb):
+                hidden = ~self.seen[r0:r0 + q, :q].any(0)
+                for j in range(n):
+                    key = np.arange(128) + 128 * j
+                    bad = key >= k
+                    draft = (key >= k - q) & (key < k)
+                    bad[draft] |= hidden[key[draft] - (k - q)]
+                    hole[int(table[base + j])] = torch.from_numpy(bad).to(dev)
+                base, r0 = base + n, r0 + q
+            h = hole[:, None, :].expand(p, hkv, 128)
+            if kind == "bf16":
+                pages[h] = float("nan")
+            else:
+                pages.view(torch.uint8)[h] = 0x7F
+            self.pages.append(pages)
+            self.scales.append(scale)
+            self.values.append(value)
+        self.vmax = float(self.values[1].abs().max())
+
+    def plan(self):
+        return _msa().Plan(self.qo, self.kv, self.hq, self.hkv, self.hp, self.d, 64, self.topk, self.p, kv_dtype=self.kind)
+
+    def run(self, plan, **kw):
+        return plan.tree_attn(self.q, *self.pages, self.table, kw.pop("idx", self.idx), kw.pop("mask", self.mask),
+                              k_scale=self.scales[0], v_scale=self.scales[1], **kw)
+
+    def ref(self, idx=None, seen="tree"):
+        m = self.hp // self.hkv
+        of = lambda x: lambda e, h: x[int(self.table[e]), h // m]  # noqa: E731
+        return attend(self.q, of(self.values[0]), of(self.values[1]), self.qo, self.kv,
+                      self.idx_h if idx is None else idx, self.d ** -0.5, self.seen if seen == "tree" else seen)
+
+    def check(self, out, lse, ref):
+        n = self.topk * 128
+        check(out, lse, ref, self.d, self.kind, n, 0.0 if self.kind == "bf16" else 2.0 ** -25 * n * self.vmax * 16)
+
+
+# 16 in `room` above: the largest weight belongs to a page whose value scale may be 8 times smaller than
+# the largest one's, and to a code of half of 448
+
+
+SHAPES = {  # qo, kv, hq, hkv, hp, topk
+    "one draft, nothing before": ([1], [1], 8, 8, 8, 1),
+    "one row each": ([1] * 5, [128, 129, 300, 1, 1000], 8, 2, 2, 5),
+    "from the page's edge": ([16, 16, 17, 3], [128 + 16, 127 + 16, 255 + 17, 130], 16, 2, 2, 3),
+    "across an edge, three heads": ([61, 2, 40], [700, 2, 1290], 12, 4, 4, 4),
+    "two selections a KV head": ([7, 30], [900, 333], 16, 2, 4, 6),
+    "nothing before": ([128, 128, 33, 1], [128, 200, 33, 2], 4, 4, 4, 2),
+    "widest trees, one head": ([128, 100], [128 * 5 + 1, 777], 2, 2, 2, 9),
+    "widest trees, 16 heads": ([128], [1500], 32, 2, 2, 12),
+    "a long selection over a cluster": ([9], [128 * 70 + 5], 8, 1, 1, 70),
+    "five heads": ([13] * 3, [600, 13, 140], 20, 4, 4, 3),
+    "sequences without rows": ([0, 5, 0, 2], [10, 300, 400, 129], 6, 2, 2, 2),
+}
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e4m3_block"])
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: s.replace(" ", "_"))
+def test_trees(cuda_dev, shape, d, kind):
+    qo, kv, hq, hkv, hp, topk = SHAPES[shape]
+    c = Case(cuda_dev, qo, kv, hq, hkv, hp, d, topk, kind, seed=len(shape))
+    plan = c.plan()
+    out, lse = c.run(plan)
+    plan.check_errors()
+    c.check(out, lse, c.ref())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e4m3_block"])
+@pytest.mark.parametrize("rows", [1, 3, 8, 40])
+def test_maxima_that_keep_moving(cuda_dev, rows, kind):
+    """Keys that grow from block to block: sums and outputs are rescaled at many."""
+    c = Case(cuda_dev, [rows] * 2, [3000, 2500], 8, 2, 2, 128, 24, kind, seed=rows, grow=0.4, irregular=False)
+    c.idx_h.sort(-1)
+    c.idx = torch.from_numpy(c.idx_h).to(cuda_dev)
+    plan = c.plan()
+    out, lse = c.run(plan)
+    plan.check_errors()
+    c.check(out, lse, c.ref())
+
+
+def test_chain_is_the_causal_attention(cuda_dev):
+    """A tree that is a chain has the rows of msa_sparse_attn."""
+    c = Case(cuda_dev, [30, 5], [900, 260], 16, 4, 4, 128, 4, "bf16", seed=3, empty=0.0)
+    c.pages = [torch.nan_to_num(p) for p in c.pages]
+    mask = torch.from_numpy(chain_mask(c.qo)).to(cuda_dev)
+    plan = c.plan()
+    out, lse = c.run(plan, mask=mask)
+    want, want_lse = plan.sparse_attn(c.q, *c.pages, c.table, c.idx)
+    plan.check_errors()
+    c.check(out, lse, c.ref(seen=None))
+    fin = torch.isfinite(want_lse)
+    assert torch.equal(torch.isfinite(lse), fin) and (lse - want_lse)[fin].abs().max() <= 1e-4
+    # both sides round weights and outputs to bf16
+    assert (out.float() - want.float()).abs().max() <= 2 * 2.0 ** -8 * 2 * c.vmax
+
+
+def test_outputs_given_streams_and_repeats(cuda_dev):
+    """Given outputs, no lse, another stream, two calls of a plan at once, and the same
+    bits every time."""
+    c = Case(cuda_dev, [16] * 4, [900, 3000, 131, 2000], 16, 2, 2, 128, 16, "e4m3_block", seed=9)
+    plan = c.plan()
+    out, lse = c.run(plan)
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    others = []
+    torch.cuda.synchronize()
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            others.append(c.run(plan))
+    c.run(plan, out=o2, lse=l2, stream=streams[0])
+    torch.cuda.synchronize()
+    plan.check_errors()
+    c.check(out, lse, c.ref())
+    for a, b in others + [(o2, l2)]:
+        assert torch.equal(a, out) and torch.equal(b, lse)
+    o3, none = c.run(plan, want_lse=False)
+    assert none is None and torch.equal(o3, out)
+
+
+def test_captured_and_replayed(cuda_dev):
+    """Two graphs of one plan, replayed at once, on inputs that change in place."""
+    c = Case(cuda_dev, [8] * 3, [700, 1500, 260], 16, 2, 2, 128, 8, "bf16", seed=4)
+    plan = c.plan()
+    c.run(plan)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c.run(plan))
+        graphs.append(g)
+    gen = torch.Generator(device=cuda_dev).manual_seed(77)
+    c.q.copy_(torch.randn(c.q.shape, generator=gen, device=cuda_dev))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for s, g in zip(streams, graphs):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    plan.check_errors()
+    ref = c.ref()
+    for out, lse in outs:
+        c.check(out, lse, ref)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e4m3_block"])
+def test_bad_pages_are_skipped_and_reported(cuda_dev, kind):
+    """Blocks on pages outside the pool, and blocks behind a tile's last, count as not
+    selected."""
+    c = Case(cuda_dev, [16, 4], [128 * 9 + 7, 650], 16, 2, 2, 128, 8, kind, seed=6, irregular=False)
+    rng = np.random.default_rng(8)
+    table = c.table.cpu().numpy().copy()
+    bad = rng.random(table.size) < 0.3
+    bad[0] = True
+    ids = np.where(bad, rng.choice([-1, -2 ** 31, c.p, 2 ** 31 - 1, 2 ** 24], table.size), table).astype(np.int32)
+    base = np.array([0, 10])
+    named = c.idx_h.copy()
+    named[(named >= 0) & bad[base[:, None, None] + np.maximum(named, 0)]] = -1
+    sel = c.idx_h.copy()
+    sel[1, 0, np.argmax(sel[1, 0] < 0)] = 6              # the sequence has blocks 0..5
+    plan = c.plan()
+    good = c.table
+    c.table = torch.from_numpy(ids).to(cuda_dev)
+    out, lse = c.run(plan, idx=torch.from_numpy(sel).to(cuda_dev))
+    with pytest.raises(_msa().MsaError) as e:
+        plan.check_errors()
+    assert e.value.status == 6
+    c.table = good
+    c.check(out, lse, c.ref(idx=named))
+
+
+def test_draft_step(cuda_dev):
+    """A step as a server takes it: drafts appended at their places in the text,
+    blocks scored and selected, the tree attended, and the accepted path appended
+    again; the cache is then that of the tokens taken one by one."""
+    msa = _msa()
+    gen = torch.Generator(device=cuda_dev).manual_seed(1)
+    ctx, d, hkv, hq, topk = [300, 1000], 128, 2, 16, 4
+    parent = [[-1, 0, 0, 1, 2, 2, 4], [-1, -1, 0, 1, 3]]
+    depth = [[0, 1, 1, 2, 2, 2, 3], [0, 0, 1, 1, 2]]
+    taken = [[0, 2, 4, 6], [1, 3]]
+    qo = [len(p) for p in parent]
+    nb = [(c + 128 + 127) // 128 for c in ctx]
+    p, rows = sum(nb), sum(qo)
+    rand = lambda *s: torch.randn(s, generator=gen, device=cuda_dev).to(torch.bfloat16)  # noqa: E731
+    tables = lambda kv: torch.cat([torch.arange(sum(nb[:s]), sum(nb[:s]) + (kv[s] + 127) // 128) for s in range(2)]).to(  # noqa: E731
+        torch.int32).to(cuda_dev)
+    k_pages, v_pages, pk_pages = rand(p, hkv, 128, d), rand(p, hkv, 128, d), rand(p, 1, 128, 64)
+    k, v, pk = rand(rows, hkv, d), rand(rows, hkv, d), rand(rows, 1, 64)
+    q, pq = rand(rows, hq, d), rand(rows, hkv, 64)
+    rope, prope = msa.Rope(d), msa.Rope(64)
+    seen = np.zeros((rows, 128), bool)
+    r0 = 0
+    for par in parent:
+        for i, a in enumerate(par):
+            if a >= 0:
+                seen[r0 + i] = seen[r0 + a]
+            seen[r0 + i, i] = True
+        r0 += len(par)
+    words = (seen.reshape(-1, 4, 32).astype(np.uint64) << np.arange(32, dtype=np.uint64)).sum(-1).astype(np.uint32).view(np.int32)
+    pos = torch.tensor([c + x for c, dd in zip(ctx, depth) for x in dd], dtype=torch.int32, device=cuda_dev)
+
+    kv = [c + n for c, n in zip(ctx, qo)]
+    plan = msa.Plan(qo, kv, hq, hkv, hkv, d, 64, topk, p)
+    table = tables(kv)
+    old_k, old_v = k_pages.clone(), v_pages.clone()
+    plan.kv_append(k, v, k_pages, v_pages, table, rope=rope, positions=pos)
+    plan.pk_append(pk, table, pk_pages=pk_pages, rope=prope, positions=pos)
+    qr, pqr = rope.apply(q, pos), prope.apply(pq, pos)
+    score = plan.proxy_maxscore(pqr, pk_pages, table)
+    idx = msa.topk_select(score, topk, plan.num_valid_pages)
+    out, lse = plan.tree_attn(qr, k_pages, v_pages, table, idx, torch.from_numpy(words).to(cuda_dev))
+    plan.check_errors()
+    of = lambda x: lambda e, h: x[int(table[e]), h].double()  # noqa: E731
+    ref = attend(qr, of(k_pages), of(v_pages), qo, kv, idx.cpu().numpy(), d ** -0.5, seen)
+    check(out, lse, ref, d, "bf16", topk * 128)
+
+    # a draft's row is that of its path alone, over the same blocks
+    kt, vt = old_k.clone(), old_v.clone()
+    n = [len(t) for t in taken]
+    at = torch.tensor([sum(qo[:s]) + i for s in range(2) for i in taken[s]], device=cuda_dev)
+    kv1 = [c + m for c, m in zip(ctx, n)]
+    step = msa.Plan(n, kv1, hq, hkv, hkv, d, 64, topk, p)
+    step.kv_append(k[at], v[at], kt, vt, tables(kv1), rope=rope)
+    same, _ = step.sparse_attn(qr[at], kt, vt, tables(kv1), idx)
+    o, _, a, _ = ref
+    assert ((same.double() - o[at]).abs() <= 2.0 ** -7 * a[at] + 2.0 ** -8 * o[at].abs()).all()
+    # the accepted rows behind the context, as their tokens one by one would have left them
+    accept = msa.Plan(n, kv1, hq, hkv, hkv, d, 64, topk, p)
+    accept.kv_append(k[at], v[at], k_pages, v_pages, tables(kv1), rope=rope)
+    for s in range(2):
+        for i in range(ctx[s], kv1[s]):
+            page, slot = sum(nb[:s]) + i // 128, i % 128
+            assert torch.equal(k_pages[page, :, slot], kt[page, :, slot]) and torch.equal(v_pages[page, :, slot], vt[page, :, slot])
+
+
+def test_refusals(cuda_dev):
+    msa = _msa()
+    c = Case(cuda_dev, [4], [200], 8, 2, 2, 128, 2, "bf16")
+    plan = c.plan()
+
+    def status(fn):
+        with pytest.raises(msa.MsaError) as e:
+            fn()
+        return e.value.status
+    long = Case(cuda_dev, [100], [200], 8, 2, 2, 128, 2, "bf16")
+    wide = msa.Plan([129], [200], 8, 2, 2, 128, 64, 2, long.p)
+    q = torch.zeros((129, 8, 128), device=cuda_dev).bfloat16()
+    mask = torch.zeros((129, 4), dtype=torch.int32, device=cuda_dev)
+    idx = torch.zeros((2, 2, 2), dtype=torch.int32, device=cuda_dev)
+    assert status(lambda: wide.tree_attn(q, *long.pages, long.table, idx, mask)) == 2
+    assert status(lambda: plan.tree_attn(c.q, *c.pages, c.table, c.idx, c.mask, k_scale=torch.ones(2, device=cuda_dev),
+                                         v_scale=torch.ones(2, device=cuda_dev))) == 1
+    with pytest.raises(TypeError):
+        plan.tree_attn(c.q, *c.pages, c.table, c.idx, c.mask.long())
+    for bad in (c.mask[:, :2].contiguous(), c.mask[:2].contiguous(), c.mask.repeat(1, 2)[:, :4]):
+        with pytest.raises(ValueError):
+            plan.tree_attn(c.q, *c.pages, c.table, c.idx, bad)
+    off = torch.zeros(c.q.numel() + 4, device=cuda_dev).bfloat16()[4:].view(c.q.shape)
+    assert status(lambda: plan.tree_attn(off, *c.pages, c.table, c.idx, c.mask)) == 1

@@ -1,0 +1,119 @@
+"""The host side of tree and latent attention over a CUDA runtime of host functions:
+what is refused, before anything is enqueued, and what a call launches."""
+from tests.test_host_side import child  # noqa: F401
+
+CALLS = """
+lib.msa_tree_attn.argtypes = [P] * 12
+lib.msa_latent_append.argtypes = [P] * 4 + [L, P, L, P, I, I, P, P]
+lib.msa_latent_attn.argtypes = [P] * 6 + [I, I, C.c_float, P, P, P]
+lib.msa_latent_expand.argtypes = [P] * 5 + [I, I, P, P, P]
+lib.msa_rope_create.argtypes = [I, I, C.c_double, I, C.c_double, I, C.c_double, C.c_double, P]
+at = [(i + 1) << 20 for i in range(16)]
+
+def tree(h, kind, **kw):
+    a = dict(q=at[0], k=at[1], v=at[2], table=at[3], idx=at[4], mask=at[5], ks=at[6] if kind != BF16 else None,
+             vs=at[7] if kind != BF16 else None, out=at[8], lse=at[9]) | kw
+    return lib.msa_tree_attn(h, *[P(x) if x else None for x in a.values()], None)
+def append(h, **kw):
+    a = dict(rope=None, pos=None, c=at[0], cs=256, key=at[1], ks=32, table=at[2], n=256, w=32, pages=at[3]) | kw
+    p = lambda x: P(x) if x else None
+    return lib.msa_latent_append(h, a["rope"], p(a["pos"]), p(a["c"]), a["cs"], p(a["key"]), a["ks"], p(a["table"]), a["n"],
+                                 a["w"], p(a["pages"]), None)
+def attn(h, **kw):
+    a = dict(q=at[0], pages=at[1], table=at[2], idx=at[3], mask=None, n=256, w=32, scale=0.1, out=at[4], lse=None) | kw
+    p = lambda x: P(x) if x else None
+    return lib.msa_latent_attn(h, p(a["q"]), p(a["pages"]), p(a["table"]), p(a["idx"]), p(a["mask"]), a["n"], a["w"], a["scale"],
+                               p(a["out"]), p(a["lse"]), None)
+def expand(h, **kw):
+    a = dict(pages=at[0], wk=at[1], wv=at[2], table=at[3], n=256, w=32, k=at[4], v=at[5]) | kw
+    p = lambda x: P(x) if x else None
+    return lib.msa_latent_expand(h, p(a["pages"]), p(a["wk"]), p(a["wv"]), p(a["table"]), a["n"], a["w"], p(a["k"]), p(a["v"]), None)
+def launches():
+    return sum(kind == 1 for _, kind, _ in events())
+def refused(status, call):
+    before = launches()
+    assert call() == status, (call(), lib.msa_last_error())
+    assert launches() == before
+"""
+
+
+def test_refusals(child):  # noqa: F811
+    child(CALLS + """
+for kind in (BF16, E4M3, BLOCK):
+    s, h = plan([5, 128], [300, 128], 8, 2, 128, 4, kind)
+    assert s == 0 and tree(h, kind) == 0 and launches() > 0
+    for name in ("q", "k", "v", "table", "idx", "mask", "out"):
+        refused(1, lambda: tree(h, kind, **{name: None}))
+    for name in ("q", "k", "v", "out"):
+        refused(1, lambda: tree(h, kind, **{name: at[0] + 8}))
+    refused(1, lambda: tree(h, kind, mask=at[5] + 2))
+    assert tree(h, kind, mask=at[5] + 4) == 0 and tree(h, kind, lse=None) == 0
+    for name in ("ks", "vs"):
+        refused(1, lambda: tree(h, kind, **{name: None if kind != BF16 else at[6]}))
+    refused(1, lambda: tree(None, kind))
+    lib.msa_plan_destroy(h)
+s, h = plan([129], [300], 8, 2, 128, 4, BF16)
+refused(2, lambda: tree(h, BF16))
+refused(2, lambda: attn(h, mask=at[5]))
+assert attn(h) == 0
+lib.msa_plan_destroy(h)
+
+s, h = plan([5, 1], [300, 1], 8, 2, 128, 4, BF16)
+rope = P()
+assert lib.msa_rope_create(48, 0, 1e4, 0, 1.0, 0, 0.0, 0.0, C.byref(rope)) == 0
+for call, need in ((append, ("c", "key", "table", "pages")), (attn, ("q", "pages", "table", "idx", "out")),
+                   (expand, ("pages", "wk", "wv", "table", "k", "v"))):
+    assert call(h) == 0
+    refused(1, lambda: call(None))
+    for name in need:
+        refused(1, lambda: call(h, **{name: None}))
+        if name not in ("table", "idx"):
+            refused(1, lambda: call(h, **{name: at[10] + 8}))
+    for n, w in ((0, 32), (64, 32), (320, 32), (640, 32), (-128, 32), (256, 0), (256, 8), (256, 80), (256, -16)):
+        refused(2, lambda: call(h, n=n, w=w, **(dict(cs=1024, ks=128) if call is append else {})))
+for kw in (dict(cs=248), dict(ks=24), dict(cs=260), dict(rope=rope), dict(ks=1 << 41)):
+    refused(1, lambda: append(h, **kw))
+assert append(h, cs=288, ks=288) == 0
+refused(1, lambda: expand(h, k=at[5]))
+refused(1, lambda: expand(h, v=at[5] + 16))
+for scale in (0.0, -1.0, float("nan"), float("inf")):
+    refused(1, lambda: attn(h, scale=scale))
+lib.msa_plan_destroy(h)
+s, h = plan([5], [300], 8, 2, 64, 4, BF16)
+refused(1, lambda: expand(h, w=64))
+lib.msa_plan_destroy(h)
+s, h = plan([5], [300], 8, 2, 128, 4, BLOCK)
+refused(2, lambda: expand(h))
+assert append(h) == 0 and attn(h) == 0
+""")
+
+
+def test_plans_belong_to_their_device(child):  # noqa: F811
+    child(CALLS + """
+s, h = plan([5, 1], [300, 1], 8, 2, 128, 4, BF16)
+for call in (lambda: tree(h, BF16), lambda: append(h), lambda: attn(h), lambda: expand(h)):
+    fake.fake_set_device(1)
+    refused(1, call)
+    assert b"belongs to device 0, device 1 is current" in lib.msa_last_error()
+    fake.fake_set_device(0)
+    assert call() == 0
+""")
+
+
+def test_one_limit_of_shared_memory_a_kernel(child):  # noqa: F811
+    """Plans of any topk ask for one limit, and launch within it."""
+    child(CALLS + """
+limit = {}
+for topk in (1, 16, 1024):
+    for qo in ([1], [3], [8, 1], [3, 60], [128]):
+        for kind in (BF16, E4M3, BLOCK):
+            s, h = plan(qo, [300] * len(qo), 16, 2, 128, topk, kind)
+            assert s == 0 and tree(h, kind) == 0 and attn(h) == 0
+            lib.msa_plan_destroy(h)
+for func, kind, size in events():
+    if kind == 0:
+        assert limit.setdefault(func, size) == size
+    else:
+        assert size <= limit[func] <= 232448
+assert len(limit) >= 11
+""")
