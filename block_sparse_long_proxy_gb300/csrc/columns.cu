@@ -24,7 +24,7 @@
 // each column's maximum, and write P^T (bf16, or f16 for e4m3 caches: half a
 // step is 2^-9 or 2^-12 of a weight, the sums being of the unrounded ones) back to
 // shared memory.  The latent's P^T goes where the block's rotated part
-// was, which no product reads after S^T.  e4m3: warps 10-13 expand the codes
+// was, which no product reads after S^T.  e4m3: four more warps expand the codes
 // to f16 (exact) inside the slot.
 //
 // Softmax in the log2 domain; a column's reference moves only when its maximum
@@ -52,14 +52,27 @@ namespace {
 
 enum Cache { kBf16, kE4m3, kLatent };
 
-constexpr int kSoftWarps = 8;
 constexpr int kSlotBytes = 32768;
-constexpr int kMaxParts = 8;
+constexpr int kMaxParts = 16;
+constexpr int kConvWarps = 4;  // e4m3 only
 
 __device__ __forceinline__ float redux_max(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
+}
+// Named barrier `id` over 128 threads that also returns the OR of p over them.
+__device__ __forceinline__ bool bar_sync_or(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "bar.red.or.pred b, %2, 128, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "r"(id)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -120,9 +133,10 @@ struct ColSmem {
   static constexpr int kBarOff = kTailOff + kTails * kTailBytes;
   static constexpr int kMaskOff = kBarOff + 8 * 32;        // [N] 128-bit masks of the columns, then their union
   static constexpr int kColOff = kMaskOff + 16 * (N + 1);  // (m, l) of the columns
-  static constexpr int kRedOff = kColOff + 8 * N;          // [2][2][4][N / 2] column maxima of the warps, by block parity
-  static constexpr int kShiftOff = kRedOff + 32 * N;       // [8 warps][N / 2], twice: shift, rescaling factor
-  static constexpr int kListOff = kShiftOff + 2 * 16 * N;
+  static constexpr int kRedOff = kColOff + 8 * N;          // [warpgroup][4][columns] column maxima, or sums, of the warps
+  static constexpr int kShiftOff = kRedOff + 16 * N;       // [warp][columns], twice: shift, rescaling factor
+  static constexpr int kRowOff = kShiftOff + 2 * 16 * N;
+  static constexpr int kListOff = kRowOff + 8 * N;
   static __host__ __device__ constexpr int bytes(int topk) {
     return kListOff + ((topk + 3) & ~3) * (KIND == kE4m3 ? 12 : 4);
   }
@@ -134,22 +148,53 @@ struct ColSmem {
   static_assert(N * kMaxParts * 4 <= kPOff, "weights fit Q's place");
 };
 
-template <int KIND>
+// Softmax warpgroups: 8 to 32 columns each.  Two of them left the passes over S^T
+// waiting for their own latencies.
+template <int N>
+constexpr int soft_warps() {
+  return N == 16 ? 8 : 16;
+}
+template <int KIND, int N>
 constexpr int col_threads() {
-  return KIND == kE4m3 ? 448 : 320;
+  return 32 * (soft_warps<N>() + 2 + (KIND == kE4m3 ? kConvWarps : 0));
+}
+
+// Sums of CH values a lane over the warp's lanes: lane c (mod CH) has the sum of
+// column c, in a fixed order.
+template <int CH>
+__device__ __forceinline__ float column_sums(float (&x)[CH], int lane) {
+#pragma unroll
+  for (int d = 16; d >= CH; d >>= 1)
+#pragma unroll
+    for (int j = 0; j < CH; ++j) x[j] += __shfl_xor_sync(0xFFFFFFFFu, x[j], d);
+#pragma unroll
+  for (int d = CH < 32 ? CH / 2 : 16; d > 0; d >>= 1)
+#pragma unroll
+    for (int j = 0; j < d; ++j) {
+      const bool up = lane & d;
+      const float send = up ? x[j] : x[j + d];
+      x[j] = (up ? x[j + d] : x[j]) + __shfl_xor_sync(0xFFFFFFFFu, send, d);
+    }
+  return x[0];
+}
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 template <int KIND, int N>
-__global__ void __launch_bounds__(col_threads<KIND>(), 1)
+__global__ void __launch_bounds__(col_threads<KIND, N>(), 1)
     columns_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const ColArgs a) {
   using L = ColSmem<KIND, N>;
   constexpr bool kLat = KIND == kLatent, kFp8 = KIND == kE4m3;
-  constexpr int kThreads = col_threads<KIND>();
-  constexpr int HN = N / 2;                     // columns of a warpgroup
-  constexpr int CH = HN < 32 ? HN : 32;         // of them, in registers at a time
+  constexpr int kThreads = col_threads<KIND, N>();
+  constexpr int kSoftWarps = soft_warps<N>(), kProducer = kSoftWarps, kIssuer = kSoftWarps + 1;
+  constexpr int HN = N / (kSoftWarps / 4);      // columns of a warpgroup
+  constexpr int CH = 8;                         // of them, in registers at a time
   constexpr int NCH = HN / CH;
-  constexpr int S = L::kSlots;
+  constexpr int S = L::kSlots, T = L::kTails > 0 ? L::kTails : 1;
   constexpr uint32_t kTmemCols = kLat ? 8 * N : 4 * N;  // S^T twice, O^T of up to 4 products or 1
+  constexpr float kUnset = 1e30f;  // minus the reference of a column that has none yet
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -165,6 +210,7 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
   int32_t* n_slot = reinterpret_cast<int32_t*>(tmem_slot + 1);
   uint32_t* cmask = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
   float2* col_ml = reinterpret_cast<float2*>(smem + L::kColOff);
+  int64_t* col_row = reinterpret_cast<int64_t*>(smem + L::kRowOff);  // (query row, head) of the columns, as a row of q and out
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);  // page | place of the block << 24
   float2* scales = reinterpret_cast<float2*>(list + ((a.topk + 3) & ~3));
 
@@ -172,21 +218,17 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
   const int part = blockIdx.x % a.parts, unit = blockIdx.x / a.parts;
   const int group = unit % a.max_groups, p = unit / a.max_groups % a.hp, t = unit / a.max_groups / a.hp;
   const int G = a.hq / a.hp;
-  pdl_wait();
-  const TileInfo tl = a.tiles[t];
-  const int c0 = group * N, cols = min(N, tl.rows * G - c0);
-  if (cols <= 0) return;  // a tile of fewer rows than the batch's most (the whole cluster)
   const int kvh = p / (a.hp / a.hkv);
 
   // ------------------------------------------------------------- prologue
-  if (warp == 8) {
+  if (warp == kProducer) {
     if (lane == 0) {
       prefetch_tmap(&k_map);
       if (!kLat) prefetch_tmap(&v_map);
       for (int s = 0; s < S; ++s) {
         mbar_init(full + s, 1);
         mbar_init(empty + s, 1);
-        if (kFp8) mbar_init(ready + s, 4);
+        if (kFp8) mbar_init(ready + s, kConvWarps);
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(tail_full + s, 1);
@@ -197,14 +239,65 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
       mbar_init(pv_done, 1);
       fence_mbar_init();
     }
+    if (lane < 4) cmask[4 * N + lane] = 0u;
+  } else if (warp == kIssuer) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  const TileInfo tl = a.tiles[t];
+  const int32_t* sel = a.idx + (static_cast<int64_t>(t) * a.hp + p) * a.topk;
+  const int j0 = warp == kProducer && lane < a.topk ? sel[lane] : -1;
+  const int c0 = group * N, cols = min(N, tl.rows * G - c0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (cols <= 0) {  // a tile of fewer rows than the batch's most (the whole cluster)
+    if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
+  const int per = kLat ? a.mt : 2;  // slot uses a block
+  // slot uses so far -> slot and phase
+  auto slot_of = [&](int u) { return u % S; };
+  auto phase_of = [&](int u) { return static_cast<uint32_t>(u / S & 1); };
+  // load h of block i: a slot, or (latent, h == per) the rotated part
+  auto produce = [&](int i, int h) {
+    const int row = static_cast<int>((static_cast<int64_t>(list[i] & 0xFFFFFFu) * a.hkv + kvh) * 128);
+    if (kLat && h == per) {
+      const int s = i % T;
+      if (!mbar_wait_inl(tail_empty + s, (i / T & 1) ^ 1, a.err)) return false;
+      mbar_expect_tx(tail_full + s, L::kTailBytes);
+      tma_load_2d(smem + L::kTailOff + s * L::kTailBytes, &k_map, tail_full + s, 128 * a.mt, row);
+      return true;
+    }
+    const int u = i * per + h, s = slot_of(u);
+    if (!mbar_wait_inl(empty + s, phase_of(u) ^ 1, a.err)) return false;
+    uint8_t* dst = smem + L::kRingOff + s * kSlotBytes;
+    if (kFp8) {
+      mbar_expect_tx(full + s, 128 * a.dv);
+      tma_load_2d(dst + 16384, h == 0 ? &k_map : &v_map, full + s, 0, row);
+    } else if (kLat) {
+      mbar_expect_tx(full + s, kSlotBytes);
+      for (int c = 0; c < 2; ++c) tma_load_2d(dst + c * 16384, &k_map, full + s, (2 * h + c) * 64, row);
+    } else {
+      mbar_expect_tx(full + s, a.kc * 16384);
+      for (int c = 0; c < a.kc; ++c)
+        tma_load_2d(dst + c * 16384, h == 0 ? &k_map : &v_map, full + s, c * 64, row);
+    }
+    return true;
+  };
+  const int first_blocks = kLat ? 1 : S / 2;  // loaded before the columns are there
+  int started = 0;
+  if (warp == kProducer) {
     // this part's blocks: padding skipped, what lies behind the tile's last block or on a
     // page outside the pool dropped and reported
-    const int32_t* sel = a.idx + (static_cast<int64_t>(t) * a.hp + p) * a.topk;
+    auto at = [&](int b) { return b == 0 ? j0 : b + lane < a.topk ? sel[b + lane] : -1; };
     int first = 0, count = a.topk, seen = 0, n = 0;
     if (a.parts > 1) {
       int total = 0;
       for (int b = 0; b < a.topk; b += 32) {
-        const int j = b + lane < a.topk ? sel[b + lane] : -1;
+        const int j = at(b);
         total += __popc(__ballot_sync(0xFFFFFFFFu, j >= 0 && j < tl.nvp));
       }
       first = total * part / a.parts;
@@ -212,7 +305,7 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
     }
     const int first_masked = tl.pos0 >> 7;
     for (int b = 0; b < a.topk; b += 32) {
-      const int j = b + lane < a.topk ? sel[b + lane] : -1;
+      const int j = at(b);
       const bool valid = j >= 0 && j < tl.nvp;
       const uint32_t v = __ballot_sync(0xFFFFFFFFu, valid), below = (1u << lane) - 1u;
       const int rank = seen + __popc(v & below);
@@ -225,100 +318,92 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
       }
       if (bad) atomicOr(a.err, kErrDeviceCheck);
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, take);
-      if (take) {
-        const int o = n + __popc(m & below);
-        list[o] = static_cast<uint32_t>(page) | static_cast<uint32_t>(max(j - first_masked + 1, 0)) << 24;
-        if (kFp8) {
-          const int64_t at = a.per_page ? page * a.hkv + kvh : kvh;
-          const BlockScale bs = block_scale_of(a.k_scale[at], a.v_scale[at]);
-          scales[o] = make_float2(bs.ks * a.scale_log2, bs.log2_vs);
-        }
-      }
+      const int o = n + __popc(m & below);
+      if (take) list[o] = static_cast<uint32_t>(page) | static_cast<uint32_t>(max(j - first_masked + 1, 0)) << 24;
       n += __popc(m);
+      __syncwarp();
+      if (b == 0) {
+        started = min(n, first_blocks);
+        if (lane == 0)
+          for (int i = 0; i < started; ++i)
+            for (int h = 0; h < per + kLat; ++h) produce(i, h);
+      }
+      if (kFp8 && take) {
+        const int64_t sat = a.per_page ? page * a.hkv + kvh : kvh;
+        const BlockScale bs = block_scale_of(a.k_scale[sat], a.v_scale[sat]);
+        scales[o] = make_float2(bs.ks * a.scale_log2, bs.log2_vs);
+      }
     }
     if (lane == 0) *n_slot = n;
-  } else if (warp == 9) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
-  // Q^T's columns, 64 dims a chunk, and what each sees
-  for (int e = threadIdx.x; e < N * a.kc * 8; e += kThreads) {
-    const int c = e / (a.kc * 8), u = e % (a.kc * 8);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (c < cols && u * 8 < a.dq) {
-      const int row = (c0 + c) / G, head = p * G + (c0 + c) % G;
-      v = *reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(tl.q_begin + row) * a.hq + head) * a.dq + u * 8);
-      if (kFp8) {
-        v.x = bf16x2_to_f16x2(v.x);
-        v.y = bf16x2_to_f16x2(v.y);
-        v.z = bf16x2_to_f16x2(v.z);
-        v.w = bf16x2_to_f16x2(v.w);
+  } else {
+    // Q^T's columns, 64 dims a chunk, a warp a column
+    const int w = warp < kProducer ? warp : warp - 1;
+    constexpr int kLoaders = kThreads / 32 - 1;
+    const uint32_t qs = smem_u32(smem + L::kQOff);
+    const int units = a.kc * 8;
+    if (kFp8) {
+      // two or four columns a warp at once, converted on the way
+      const int lg = a.kc == 2 ? 4 : 3;
+      constexpr int kMost = (N * 16 + kLoaders * 32 - 1) / (kLoaders * 32);
+      uint4 v[kMost];
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        const int e = (k * kLoaders + w) * 32 + lane, c = e >> lg, u = e & (units - 1);
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < cols)
+          v[k] = *reinterpret_cast<const uint4*>(
+              a.q + (static_cast<int64_t>(tl.q_begin + (c0 + c) / G) * a.hq + p * G + (c0 + c) % G) * a.dq + u * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        const int e = (k * kLoaders + w) * 32 + lane, c = e >> lg, u = e & (units - 1);
+        if (c < N)
+          *reinterpret_cast<uint4*>(smem + L::kQOff + (u >> 3) * L::kQChunk + c * 128 + (((u & 7) ^ (c & 7)) << 4)) =
+              make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z), bf16x2_to_f16x2(v[k].w));
+      }
+    } else {
+      for (int c = w; c < N; c += kLoaders) {
+        const __nv_bfloat16* src = a.q;
+        if (c < cols) src += (static_cast<int64_t>(tl.q_begin + (c0 + c) / G) * a.hq + p * G + (c0 + c) % G) * a.dq;
+        for (int u = lane; u < units; u += 32) {
+          const bool there = c < cols && u * 8 < a.dq;
+          copy16_async(qs + (u >> 3) * L::kQChunk + c * 128 + (((u & 7) ^ (c & 7)) << 4), there ? src + u * 8 : a.q, there);
+        }
       }
     }
-    *reinterpret_cast<uint4*>(smem + L::kQOff + (u >> 3) * L::kQChunk + c * 128 + (((u & 7) ^ (c & 7)) << 4)) = v;
-  }
-  for (int e = threadIdx.x; e < N * 4; e += kThreads) {
-    const int c = e >> 2, w = e & 3, row = (c0 + c) / G;
-    // bits of word w below n
-    auto low = [&](int n) { return n >= 32 * (w + 1) ? 0xFFFFFFFFu : n <= 32 * w ? 0u : (1u << (n - 32 * w)) - 1u; };
-    uint32_t m = 0u;
-    if (c < cols)
-      m = a.tree_mask ? reinterpret_cast<const uint32_t*>(a.tree_mask + tl.q_begin + row)[w] & low(tl.rows) : low(row + 1);
-    cmask[e] = m;
+    // what each column is, and sees
+    const int th = w * 32 + lane;
+    for (int c = th; c < N; c += kLoaders * 32)
+      col_row[c] = static_cast<int64_t>(tl.q_begin + (c0 + c) / G) * a.hq + p * G + (c0 + c) % G;
+    for (int e0 = w * 32; e0 < N * 4; e0 += kLoaders * 32) {
+      const int e = e0 + lane, c = e % N, wd = e / N, row = (c0 + c) / G;
+      // bits of word wd below n
+      auto low = [&](int n) { return n >= 32 * (wd + 1) ? 0xFFFFFFFFu : n <= 32 * wd ? 0u : (1u << (n - 32 * wd)) - 1u; };
+      uint32_t m = 0u;
+      if (c < cols)
+        m = a.tree_mask ? reinterpret_cast<const uint32_t*>(a.tree_mask + tl.q_begin + row)[wd] & low(tl.rows) : low(row + 1);
+      cmask[4 * c + wd] = m;
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) m |= __shfl_xor_sync(0xFFFFFFFFu, m, d);
+      if ((lane & 15) == 0 && m != 0u) atomicOr(cmask + 4 * N + wd, m);
+    }
+    if (!kFp8) asm volatile("cp.async.wait_all;" ::: "memory");
   }
   fence_async_shared();
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  if (threadIdx.x < 4) {
-    uint32_t any = 0u;
-    for (int c = 0; c < N; ++c) any |= cmask[4 * c + threadIdx.x];
-    cmask[4 * N + threadIdx.x] = any;
-  }
-  __syncthreads();
-  const uint32_t tmem = *tmem_slot;
   const int n = *n_slot;
   // key offset of lane 0 of block i's rows; places: 0 before the tile, 1 its first block, 2 the next
   auto offset0 = [&](uint32_t entry) { return (static_cast<int>(entry >> 24) - 1) * 128 - (tl.pos0 & 127); };
   auto seen_by_any = [&](int e) { return e < 0 || (e < 128 && (cmask[4 * N + (e >> 5)] >> (e & 31) & 1u)); };
-  // slot uses so far -> slot and phase
-  auto slot_of = [&](int u) { return u % S; };
-  auto phase_of = [&](int u) { return static_cast<uint32_t>(u / S & 1); };
-  const int per = kLat ? a.mt : 2;  // slot uses a block
 
-  if (warp == 8) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       bool ok = true;
-      for (int i = 0; i < n && ok; ++i) {
-        const int64_t page = list[i] & 0xFFFFFFu;
-        const int row = static_cast<int>((page * a.hkv + kvh) * 128);
-        for (int h = 0; h < per && ok; ++h) {
-          const int u = i * per + h, s = slot_of(u);
-          if (!(ok = mbar_wait(empty + s, phase_of(u) ^ 1, a.err))) break;
-          uint8_t* dst = smem + L::kRingOff + s * kSlotBytes;
-          if (kFp8) {
-            mbar_expect_tx(full + s, 128 * a.dv);
-            tma_load_2d(dst + 16384, h == 0 ? &k_map : &v_map, full + s, 0, row);
-          } else if (kLat) {
-            mbar_expect_tx(full + s, kSlotBytes);
-            for (int c = 0; c < 2; ++c) tma_load_2d(dst + c * 16384, &k_map, full + s, (2 * h + c) * 64, row);
-          } else {
-            mbar_expect_tx(full + s, a.kc * 16384);
-            for (int c = 0; c < a.kc; ++c)
-              tma_load_2d(dst + c * 16384, h == 0 ? &k_map : &v_map, full + s, c * 64, row);
-          }
-        }
-        if (kLat && ok) {
-          constexpr int T = L::kTails > 0 ? L::kTails : 1;
-          const int s = i % T;
-          if (!(ok = mbar_wait(tail_empty + s, (i / T & 1) ^ 1, a.err))) break;
-          mbar_expect_tx(tail_full + s, L::kTailBytes);
-          tma_load_2d(smem + L::kTailOff + s * L::kTailBytes, &k_map, tail_full + s, 128 * a.mt, row);
-        }
-      }
+      for (int i = started; i < n && ok; ++i)
+        for (int h = 0; h < per + kLat && ok; ++h) ok = produce(i, h);
     }
-  } else if (warp == 9) {
+  } else if (warp == kIssuer) {
     // ----------------------------------------------------------------- MMA
     if (lane == 0) {
       constexpr uint32_t id_qk = kFp8 ? idesc_f16_f32(128, N, false, false) : idesc_bf16_f32(128, N, false, false);
@@ -329,14 +414,13 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
       const uint64_t vd0 = smem_desc(smem_u32(smem + L::kRingOff), a.dv == 64 ? 0 : 16384, 1024, kSwizzle128);
       const uint64_t td0 = smem_desc(smem_u32(smem + L::kTailOff), 16, 1024, kSwizzle128);
       const uint64_t pd0 = smem_desc(smem_u32(smem + (kLat ? L::kTailOff : L::kPOff)), 16384, 1024, kSwizzle128);
-      constexpr int T = L::kTails > 0 ? L::kTails : 1;
       bool ok = true;
       auto qk = [&](int i) {
         const uint32_t d = tmem + (i & 1) * N;
         uint32_t acc = 0;
         for (int h = 0; h < (kLat ? a.mt : 1); ++h) {
           const int u = i * per + h, s = slot_of(u);
-          if (!(ok = mbar_wait(ready + s, phase_of(u), a.err))) return;
+          if (!(ok = mbar_wait_inl(ready + s, phase_of(u), a.err))) return;
           tc_fence_after();
           const uint64_t kd = kd0 + s * (kSlotBytes >> 4), qd = qd0 + h * 2 * (L::kQChunk >> 4);
           for (int c = 0; c < (kLat ? 2 : a.kc); ++c)
@@ -349,7 +433,7 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
         }
         if (kLat) {
           const int s = i % T;
-          if (!(ok = mbar_wait(tail_full + s, i / T & 1, a.err))) return;
+          if (!(ok = mbar_wait_inl(tail_full + s, i / T & 1, a.err))) return;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -361,13 +445,13 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
       for (int i = 0; i < n && ok; ++i) {
         // the latent's slots serve S^T of block i until its P.V: the next block's loads wait for that
         if (!kLat && i + 1 < n) qk(i + 1);
-        if (!ok || !(ok = mbar_wait(p_full, i & 1, a.err))) break;
+        if (!ok || !(ok = mbar_wait_inl(p_full, i & 1, a.err))) break;
         tc_fence_after();
         const uint64_t pd = pd0 + (kLat ? (i % T) * (L::kTailBytes >> 4) : 0);
         for (int h = 0; h < a.mt && ok; ++h) {
           const int u = kLat ? i * per + h : i * per + 1, s = slot_of(u);
           if (!kLat) {
-            if (!(ok = mbar_wait(ready + s, phase_of(u), a.err))) break;
+            if (!(ok = mbar_wait_inl(ready + s, phase_of(u), a.err))) break;
             tc_fence_after();
           }
           const uint64_t vd = vd0 + s * (kSlotBytes >> 4);
@@ -387,24 +471,23 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
     // skipped after one that gave up), so the warpgroup's barriers stay whole.
     const int wg = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    float* const red0 = reinterpret_cast<float*>(smem + L::kRedOff) + wg * 8 * HN;
-    float* shift = reinterpret_cast<float*>(smem + L::kShiftOff) + warp * 2 * HN;
+    float* const red = reinterpret_cast<float*>(smem + L::kRedOff) + wg * 4 * HN;
+    float* shift = reinterpret_cast<float*>(smem + L::kShiftOff) + warp * 2 * HN;  // minus the references
     float* alpha = shift + HN;
-    auto group_sync = [&] {
-      if (wg == 0)
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-      else
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-    };
+    auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
     const uint32_t o_addr = tmem + lane_base + 2 * N + wg * HN;
-    float l[HN], m[NCH];  // sums of this thread's keys; references of columns 32 k + lane
+    float l[NCH][CH], m[NCH];  // sums of this thread's keys; references of columns CH k + lane
 #pragma unroll
-    for (int c = 0; c < HN; ++c) l[c] = 0.f;
+    for (int k = 0; k < NCH; ++k) {
+      m[k] = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) m[k] = -INFINITY;
+      for (int c = 0; c < CH; ++c) l[k][c] = 0.f;
+      if (lane < CH) shift[k * CH + lane] = kUnset;
+    }
+    __syncwarp();
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = mbar_wait(bar, parity, a.err);
+      if (ok) ok = mbar_wait_inl(bar, parity, a.err);
       ok = __all_sync(0xFFFFFFFFu, ok);
     };
     for (int i = 0; i < n; ++i) {
@@ -419,99 +502,126 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
       }
       const bool masked = entry >> 24 != 0;
       const int e = offset0(entry) + r;
-      float* const red = red0 + (i & 1) * 4 * HN;  // a warp may be a block ahead of another's reads
       uint32_t s[CH];
       auto load = [&](int k) {
-        tmem_ld<CH>(s_addr + k * 32, s);
+        tmem_ld<CH>(s_addr + k * CH, s);
         tmem_wait_ld();
         if (masked && e >= 0) {
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
-            const bool see = e < 128 && (cmask[4 * (wg * HN + k * 32 + c) + (e >> 5 & 3)] >> (e & 31) & 1u);
+            const bool see = e < 128 && (cmask[4 * (wg * HN + k * CH + c) + (e >> 5 & 3)] >> (e & 31) & 1u);
             if (!see) s[c] = __float_as_uint(-INFINITY);
           }
         }
       };
-      // column maxima over the block's keys
+      // logits of columns c and c + 1 of chunk k less their references, log2
+      auto logits = [&](int k, int c, float2 sh, float& x0, float& x1) {
+        ffma2v(x0, x1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl2, sl2, sh.x, sh.y);
+      };
+      // with the block's log2 of the value scale, which every column's logits have
+      auto put_shift = [&] {
+#pragma unroll
+        for (int k = 0; k < NCH; ++k)
+          if (lane < CH) shift[k * CH + lane] = (m[k] == -INFINITY ? kUnset : -m[k]) + log2_vs;
+        __syncwarp();
+      };
+      if (kFp8) put_shift();
+      // does any column outgrow its reference?  (one without has kUnset, which any logit outgrows)
+      float far = -INFINITY;
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
         load(k);
-        __syncwarp();
-        float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const float x = redux_max(__uint_as_float(s[c]));
-          if (lane == c) mx = x;
+        for (int c = 0; c < CH; c += 4) {
+          const float4 sh = *reinterpret_cast<const float4*>(shift + k * CH + c);
+          float x0, x1, x2, x3;
+          logits(k, c, make_float2(sh.x, sh.y), x0, x1);
+          logits(k, c + 2, make_float2(sh.z, sh.w), x2, x3);
+          far = fmax3(fmax3(far, x0, x1), x2, x3);
         }
-        if (lane < CH) red[quarter * HN + k * 32 + lane] = mx;
       }
-      group_sync();
-      bool moved = false;
+      const bool grown = bar_sync_or(1 + wg, far > 8.f);
+      if (grown) {
 #pragma unroll
-      for (int k = 0; k < NCH; ++k)
-        if (lane < CH) {
-          const int c = k * 32 + lane;
-          const float mx = fmaxf(fmaxf(red[c], red[HN + c]), fmaxf(red[2 * HN + c], red[3 * HN + c]));
-          const float t2 = kFp8 ? fmaf(mx, sl2, log2_vs) : mx * sl2;
-          const float m_new = t2 > m[k] + 8.f ? t2 : m[k];
-          const float m_use = m_new == -INFINITY ? 0.f : m_new;
-          alpha[c] = m_new == m[k] ? 1.f : ex2_approx(m[k] - m_use);
-          shift[c] = kFp8 ? log2_vs - m_use : -m_use;
-          moved = moved || m_new != m[k];
-          m[k] = m_new;
-        }
-      __syncwarp();
-      // P^T has one place, and the rescaling needs O^T whole
-      if (i > 0 && !kLat) wait(pv_done, (i - 1) & 1);
-      if (__any_sync(0xFFFFFFFFu, moved) && i > 0) {
-        if (kLat) wait(pv_done, (i - 1) & 1);
-        tc_fence_after();
+        for (int k = 0; k < NCH; ++k) {
+          if (NCH > 1) load(k);
+          __syncwarp();
+          float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < HN; ++c) l[c] *= alpha[c];
-        for (int h = 0; h < a.mt; ++h)
-#pragma unroll 1
-          for (int k = 0; k < NCH; ++k) {
-            uint32_t o[CH];
-            tmem_ld<CH>(o_addr + h * N + k * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < CH; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[k * 32 + c]);
-            tmem_st<CH>(o_addr + h * N + k * 32, o);
+          for (int c = 0; c < CH; ++c) {
+            const float x = redux_max(__uint_as_float(s[c]));
+            if (lane == c) mx = x;
           }
-        tmem_wait_st();
+          if (lane < CH) red[quarter * HN + k * CH + lane] = mx;
+        }
+        group_sync();
+#pragma unroll
+        for (int k = 0; k < NCH; ++k)
+          if (lane < CH) {
+            const int c = k * CH + lane;
+            const float mx = fmaxf(fmaxf(red[c], red[HN + c]), fmaxf(red[2 * HN + c], red[3 * HN + c]));
+            const float t2 = kFp8 ? fmaf(mx, sl2, log2_vs) : mx * sl2;
+            const float m_new = t2 > m[k] + 8.f ? t2 : m[k];
+            alpha[c] = m_new == m[k] ? 1.f : ex2_approx(m[k] - m_new);
+            m[k] = m_new;
+          }
+        put_shift();
+        if (i > 0) {  // O^T whole, then rescaled
+          wait(pv_done, (i - 1) & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < NCH; ++k)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) l[k][c] *= alpha[k * CH + c];
+          for (int h = 0; h < a.mt; ++h)
+#pragma unroll 1
+            for (int k = 0; k < NCH; ++k) {
+              uint32_t o[CH];
+              tmem_ld<CH>(o_addr + h * N + k * CH, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < CH; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[k * CH + c]);
+              tmem_st<CH>(o_addr + h * N + k * CH, o);
+            }
+          tmem_wait_st();
+        }
       }
-      uint8_t* pt = smem + (kLat ? L::kTailOff + (i % (L::kTails > 0 ? L::kTails : 1)) * L::kTailBytes : L::kPOff);
+      if (i > 0 && !kLat) wait(pv_done, (i - 1) & 1);  // P^T has one place
+      uint8_t* pt = smem + (kLat ? L::kTailOff + (i % T) * L::kTailBytes : L::kPOff);
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
         if (NCH > 1) load(k);
 #pragma unroll
         for (int c = 0; c < CH; c += 8) {
-          uint4 w;
-          uint32_t* pw = &w.x;
+          uint32_t w[4];
 #pragma unroll
-          for (int d = 0; d < 8; d += 2) {
-            const float2 sh = *reinterpret_cast<const float2*>(shift + k * 32 + c + d);
-            float x0, x1;
-            ffma2v(x0, x1, __uint_as_float(s[c + d]), __uint_as_float(s[c + d + 1]), sl2, sl2, sh.x, sh.y);
-            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            if (kFp8)
-              ffma2v(l[k * 32 + c + d], l[k * 32 + c + d + 1], p0, p1, inv_vs, inv_vs, l[k * 32 + c + d], l[k * 32 + c + d + 1]);
-            else
-              fadd2(l[k * 32 + c + d], l[k * 32 + c + d + 1], p0, p1);
-            pw[d / 2] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          for (int d = 0; d < 8; d += 4) {
+            const float4 sh = *reinterpret_cast<const float4*>(shift + k * CH + c + d);
+#pragma unroll
+            for (int b = 0; b < 4; b += 2) {
+              const int x = c + d + b;
+              float x0, x1;
+              logits(k, x, b == 0 ? make_float2(sh.x, sh.y) : make_float2(sh.z, sh.w), x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              if (kFp8)
+                ffma2v(l[k][x], l[k][x + 1], p0, p1, inv_vs, inv_vs, l[k][x], l[k][x + 1]);
+              else
+                fadd2(l[k][x], l[k][x + 1], p0, p1);
+              w[(d + b) / 2] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            }
           }
-          const int col = wg * HN + k * 32 + c;
-          *reinterpret_cast<uint4*>(pt + (col >> 6) * 16384 + r * 128 + (((col >> 3 & 7) ^ (r & 7)) << 4)) = w;
+          const int col = wg * HN + k * CH + c;
+          *reinterpret_cast<uint4*>(pt + (col >> 6) * 16384 + r * 128 + (((col >> 3 & 7) ^ (r & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (!kFp8 && masked && wg == 0) {  // V rows that no column sees (e4m3: the converters)
+      if (!kFp8 && masked) {  // V rows that no column sees (e4m3: the converters), 64 dims a warpgroup in turn
         if (!kLat) wait(full + slot_of(2 * i + 1), phase_of(2 * i + 1));
         if (!seen_by_any(e))
-          for (int h = 0; h < (kLat ? a.mt : 1); ++h) {
-            uint8_t* v = smem + L::kRingOff + slot_of(kLat ? i * per + h : 2 * i + 1) * kSlotBytes + r * 128;
-            for (int c = 0; c < (kLat ? 2 : a.kc); ++c)
+          for (int c = wg; c < (kLat ? 2 * a.mt : a.kc); c += kSoftWarps / 4) {
+            uint8_t* v = smem + L::kRingOff + slot_of(kLat ? i * per + (c >> 1) : 2 * i + 1) * kSlotBytes + (c & 1) * 16384;
 #pragma unroll
-              for (int b = 0; b < 8; ++b) *reinterpret_cast<uint4*>(v + c * 16384 + b * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int b = 0; b < 8; ++b) *reinterpret_cast<uint4*>(v + r * 128 + ((b ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           }
       }
       fence_async_shared();
@@ -521,98 +631,101 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
     }
 
     // ------------------------------------------------------------ epilogue
-    if (n > 0) wait(pv_done, (n - 1) & 1);
-    tc_fence_after();
     group_sync();  // red is free
-    float* const red = red0;
     float total[NCH];
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      total[k] = 0.f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        float x = l[k * 32 + c];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-        if (lane == c) total[k] = x;
-      }
-      if (lane < CH) red[quarter * HN + k * 32 + lane] = total[k];
+      total[k] = column_sums<CH>(l[k], lane);
+      if (lane < CH) red[quarter * HN + k * CH + lane] = total[k];
     }
     group_sync();
 #pragma unroll
     for (int k = 0; k < NCH; ++k)
       if (lane < CH) {
-        const int c = k * 32 + lane;
+        const int c = k * CH + lane;
         total[k] = (red[c] + red[HN + c]) + (red[2 * HN + c] + red[3 * HN + c]);
         alpha[c] = total[k] > 0.f ? 1.f / total[k] : 0.f;
         if (quarter == 0) {
           col_ml[wg * HN + c] = make_float2(ok ? m[k] : -INFINITY, total[k]);
-          const int cg = c0 + wg * HN + c;
           if (a.parts == 1 && a.lse != nullptr && wg * HN + c < cols)
-            a.lse[static_cast<int64_t>(tl.q_begin + cg / G) * a.hq + p * G + cg % G] =
-                total[k] > 0.f ? (m[k] + log2f(total[k])) * 0.69314718055994531f : -INFINITY;
+            a.lse[col_row[wg * HN + c]] = total[k] > 0.f ? (m[k] + log2f(total[k])) * 0.69314718055994531f : -INFINITY;
         }
       }
     __syncwarp();
+    if (n > 0) wait(pv_done, (n - 1) & 1);
+    tc_fence_after();
     float* part_o = reinterpret_cast<float*>(smem + L::kRingOff);
     for (int h = 0; h < a.mt; ++h)
 #pragma unroll 1
       for (int k = 0; k < NCH; ++k) {
         uint32_t o[CH];
         if (n > 0) {
-          tmem_ld<CH>(o_addr + h * N + k * 32, o);
+          tmem_ld<CH>(o_addr + h * N + k * CH, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int c = 0; c < CH; ++c) o[c] = 0u;
         }
         if (h * 128 + r >= a.dv) continue;  // dims 64: the upper half repeats the lower
+        const int col0 = wg * HN + k * CH;
+        if (a.parts > 1) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int col = wg * HN + k * 32 + c, cg = c0 + col;
-          if (col >= cols) break;
-          if (a.parts > 1)
-            part_o[col * a.dv + h * 128 + r] = __uint_as_float(o[c]);
-          else
-            a.out[(static_cast<int64_t>(tl.q_begin + cg / G) * a.hq + p * G + cg % G) * a.dv + h * 128 + r] =
-                __float2bfloat16_rn(__uint_as_float(o[c]) * alpha[k * 32 + c]);
+          for (int c = 0; c < CH; ++c)
+            if (col0 + c < cols) part_o[(col0 + c) * a.dv + h * 128 + r] = __uint_as_float(o[c]);
+          continue;
+        }
+        // even lanes take two dims of column c, odd lanes of column c + 1
+        const bool odd = lane & 1;
+        __nv_bfloat16* to = a.out + h * 128 + (r & ~1);
+#pragma unroll
+        for (int c = 0; c < CH; c += 2) {
+          const float2 inv = *reinterpret_cast<const float2*>(alpha + k * CH + c);
+          const float v0 = __uint_as_float(o[c]) * inv.x, v1 = __uint_as_float(o[c + 1]) * inv.y;
+          const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+          if (col0 + c + odd < cols)
+            *reinterpret_cast<uint32_t*>(to + col_row[col0 + c + odd] * a.dv) = odd ? pack_bf16x2(other, v1) : pack_bf16x2(v0, other);
         }
       }
   } else if (kFp8) {
     // ---------------------------------------------------------- converters
     // A thread has one key's codes in registers before it writes that key's f16
     // row, the only one that overlaps them (dims 128; at dims 64 none does).
-    const int r = threadIdx.x - 32 * (kSoftWarps + 2), sw = r & 7;
+    const int r0 = threadIdx.x - 32 * (kSoftWarps + 2);
     bool ok = true;
     for (int u = 0; u < 2 * n; ++u) {
       const int s = slot_of(u);
       uint8_t* buf = smem + L::kRingOff + s * kSlotBytes;
       const uint32_t entry = list[u >> 1];
-      const bool zero = (u & 1) && entry >> 24 != 0 && !seen_by_any(offset0(entry) + r);
-      if (ok) ok = mbar_wait(full + s, phase_of(u), a.err);
+      const bool masked = (u & 1) && entry >> 24 != 0;
+      if (ok) ok = mbar_wait_inl(full + s, phase_of(u), a.err);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-      auto expand = [&](uint4 v, int unit) {  // sixteen codes -> f16 units 2 unit, 2 unit + 1
-        if (zero) v = make_uint4(0u, 0u, 0u, 0u);
-        uint8_t* dst = buf + (unit >> 2) * 16384 + r * 128;
-        const int u0 = (unit & 3) * 2;
-        *reinterpret_cast<uint4*>(dst + ((u0 ^ sw) << 4)) = make_uint4(
-            e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
-        *reinterpret_cast<uint4*>(dst + (((u0 + 1) ^ sw) << 4)) = make_uint4(
-            e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
-      };
-      uint4 v[8];
-      if (a.dv == 128) {
+#pragma unroll 1
+      for (int r = r0; r < 128; r += 32 * kConvWarps) {
+        const int sw = r & 7;
+        const bool zero = masked && !seen_by_any(offset0(entry) + r);
+        auto expand = [&](uint4 v, int unit) {  // sixteen codes -> f16 units 2 unit, 2 unit + 1
+          if (zero) v = make_uint4(0u, 0u, 0u, 0u);
+          uint8_t* dst = buf + (unit >> 2) * 16384 + r * 128;
+          const int u0 = (unit & 3) * 2;
+          *reinterpret_cast<uint4*>(dst + ((u0 ^ sw) << 4)) = make_uint4(
+              e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
+          *reinterpret_cast<uint4*>(dst + (((u0 + 1) ^ sw) << 4)) = make_uint4(
+              e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+        };
+        uint4 v[8];
+        if (a.dv == 128) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 128 + ((c ^ sw) << 4));
+          for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 128 + ((c ^ sw) << 4));
 #pragma unroll
-        for (int c = 0; c < 8; ++c) expand(v[c], c);
-      } else {
+          for (int c = 0; c < 8; ++c) expand(v[c], c);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+          for (int c = 0; c < 4; ++c)
+            v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) expand(v[c], c);
+          for (int c = 0; c < 4; ++c) expand(v[c], c);
+        }
       }
       fence_async_shared();
       __syncwarp();
@@ -625,12 +738,12 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
   if (a.parts == 1) {
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
     return;
   }
   cluster_sync();  // every part's O^T, m and l are in its shared memory
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
   float* wts = reinterpret_cast<float*>(smem + L::kQOff);  // [column][part]
   for (int c = threadIdx.x; c < cols; c += kThreads) {
     float2 ml[kMaxParts];
@@ -649,44 +762,85 @@ __global__ void __launch_bounds__(col_threads<KIND>(), 1)
 #pragma unroll
     for (int w = 0; w < kMaxParts; ++w)
       if (w < a.parts) wts[c * kMaxParts + w] = ml[w].x * inv;
-    const int cg = c0 + c;
     if (part == 0 && a.lse != nullptr)
-      a.lse[static_cast<int64_t>(tl.q_begin + cg / G) * a.hq + p * G + cg % G] =
-          sum > 0.f ? (mm + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      a.lse[col_row[c]] = sum > 0.f ? (mm + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
   __syncthreads();
   const int dv4 = a.dv / 4;
   for (int e = part * kThreads + threadIdx.x; e < cols * dv4; e += a.parts * kThreads) {
-    const int c = e / dv4, cg = c0 + c;
+    const int c = e / dv4;
     const uint32_t at = smem_u32(smem + L::kRingOff) + 16u * e;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kMaxParts; ++w)
-      if (w < a.parts) {
-        const float x = wts[c * kMaxParts + w];
-        const float4 v = ld_cluster_f4(at, w);
-        o.x += v.x * x, o.y += v.y * x, o.z += v.z * x, o.w += v.w * x;
-      }
-    *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(tl.q_begin + cg / G) * a.hq + p * G + cg % G) * a.dv +
-                              4 * (e % dv4)) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    for (int w0 = 0; w0 < kMaxParts; w0 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w)
+        if (w0 + w < a.parts) v[w] = ld_cluster_f4(at, w0 + w);
+#pragma unroll
+      for (int w = 0; w < 8; ++w)
+        if (w0 + w < a.parts) {
+          const float x = wts[c * kMaxParts + w0 + w];
+          o.x += v[w].x * x, o.y += v[w].y * x, o.z += v[w].z * x, o.w += v[w].w * x;
+        }
+    }
+    *reinterpret_cast<uint2*>(a.out + col_row[c] * a.dv + 4 * (e % dv4)) =
+        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   }
   cluster_sync();  // nobody leaves while its part may be read
 }
 
-template <int KIND, int N>
-cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
-  using L = ColSmem<KIND, N>;
+// Columns a CTA (N) and CTAs that share a unit's blocks (parts): the least estimated
+// time over the choices.  A CTA takes about start + blocks * step, both measured
+// (us, head_dim 128 or latent_dim 512, batches of one and of eight sequences):
+//              start, step        N = 16       32         64        128
+//   bf16                         7.7, 0.95  9.3, 0.97  11.2, 1.05  17.7, 1.1
+//   e4m3                         8.6, 1.05  10.3, 1.05  14, 1.05   18, 1.6
+//   latent                        11, 3.1    14, 3.1    18, 3.4
+// and no less than the blocks' bytes take from HBM at 6.3 TB/s.  The CTAs run in
+// rounds: 152, 76 clusters of 2, 36 of 4, 15 of 8, 7 of 16 at once (large clusters are
+// not placed as densely as the SMs would allow).  Examples (us, all choices tried):
+//   16 drafts, 64 / 8 heads, 16 blocks: 32 / 4 13.6, 64 / 4 15.6, 128 / 8 19.5, 16 / 1 23.1
+//   32 x 8 drafts, same: 64 / 1 61.9, 32 / 1 100, 16 / 1 160
+//   1 row, 64 heads, latent, 16 blocks: 16 / 16 13.3, 32 / 16 16.2, 64 / 8 23.2, 64 / 1 73
+//   32 rows, same: 64 / 4 35.8, 32 / 2 41.7, 64 / 2 49.3, 16 / 1 63
+struct ColShape {
+  int n, parts;
+};
+template <int KIND>
+ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
+  static constexpr double kStart[3][4] = {{7.7, 9.3, 11.2, 17.7}, {8.6, 10.3, 14, 18}, {11, 14, 18, 1e9}};
+  static constexpr double kStep[3][4] = {{0.95, 0.97, 1.05, 1.1}, {1.05, 1.05, 1.05, 1.6}, {3.1, 3.1, 3.4, 1e9}};
   const int G = p->hq / p->hp;
-  int64_t units = 0;
-  int groups = 1, blocks = 1;
-  for (const TileInfo& t : p->tiles) {
-    const int g = (t.rows * G + N - 1) / N;
-    units += int64_t(p->hp) * g;
-    groups = std::max(groups, g);
-    blocks = std::max(blocks, std::min(t.nvp, p->topk));
+  int blocks = 1;
+  for (const TileInfo& t : p->tiles) blocks = std::max(blocks, std::min(t.nvp, p->topk));
+  ColShape best{16, 1};
+  double least = 1e300;
+  for (int k = 0; k < (KIND == kLatent ? 3 : 4); ++k) {
+    const int n = 16 << k;
+    int64_t units = 0, sets = 0;
+    for (const TileInfo& t : p->tiles) units += int64_t(p->hp) * ((t.rows * G + n - 1) / n), sets += p->hp;
+    for (int parts = 1; parts <= kMaxParts && parts <= blocks; parts *= 2) {
+      static constexpr int kClusters[5] = {0, 76, 36, 15, 7};
+      const int lg = parts == 1 ? 0 : parts == 2 ? 1 : parts == 4 ? 2 : parts == 8 ? 3 : 4;
+      const int64_t room = std::max<int64_t>(1, lg == 0 ? p->num_sms : int64_t(kClusters[lg]) * p->num_sms / 152);
+      const int64_t rounds = (units + room - 1) / room;
+      const double at_once = static_cast<double>(std::min(units, room) * parts);
+      const double hbm = at_once * block_bytes * sets / units / 6.3e6;  // us a block step
+      const double us = rounds * (kStart[KIND][k] * (KIND == kLatent ? 0.4 + 0.6 * size : 1.0) +
+                                  (blocks + parts - 1) / parts * std::max(kStep[KIND][k] * size, hbm));
+      if (us < least) least = us, best = {n, parts};
+    }
   }
-  int parts = 1;
-  while (parts < kMaxParts && parts * 2 <= blocks && units * parts * 2 <= p->num_sms) parts *= 2;
+  return best;
+}
+
+template <int KIND, int N>
+cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, const CUtensorMap& vm, int parts,
+                           cudaStream_t st) {
+  using L = ColSmem<KIND, N>;
+  int groups = 1;
+  for (const TileInfo& t : p->tiles) groups = std::max(groups, (t.rows * (p->hq / p->hp) + N - 1) / N);
   a.parts = parts;
   a.max_groups = groups;
   const int64_t ctas = int64_t(p->n_tiles) * p->hp * groups * parts;
@@ -696,15 +850,20 @@ cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km
   static_assert(L::bytes(1024) + 1024 <= 232448, "shared memory at the largest topk");
   if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(1024) + 1024))
     return e;
-  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), parts, dim3(col_threads<KIND>()),
+  if (parts > 8)
+    if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), parts, dim3(col_threads<KIND, N>()),
                             L::bytes(p->topk) + 1024, st, km, vm, a);
 }
 
-// Columns of the widest tile, for the choice of N.
-int most_columns(const msa_plan_s* p) {
-  int rows = 1;
-  for (const TileInfo& t : p->tiles) rows = std::max(rows, t.rows);
-  return rows * (p->hq / p->hp);
+template <int KIND>
+cudaError_t launch_shape(ColShape c, const msa_plan_s* p, const ColArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
+                         cudaStream_t st) {
+  if constexpr (KIND != kLatent)
+    if (c.n == 128) return launch_columns<KIND, 128>(p, a, km, vm, c.parts, st);
+  return c.n == 16   ? launch_columns<KIND, 16>(p, a, km, vm, c.parts, st)
+         : c.n == 32 ? launch_columns<KIND, 32>(p, a, km, vm, c.parts, st)
+                     : launch_columns<KIND, 64>(p, a, km, vm, c.parts, st);
 }
 
 }  // namespace
@@ -740,12 +899,11 @@ msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pa
   a.mt = 1;
   a.per_page = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(p->d));
-  const int c = most_columns(p);
-  const auto launch = fp8 ? (c <= 16 ? launch_columns<kE4m3, 16> : c <= 32 ? launch_columns<kE4m3, 32>
-                             : c <= 64 ? launch_columns<kE4m3, 64> : launch_columns<kE4m3, 128>)
-                          : (c <= 16 ? launch_columns<kBf16, 16> : c <= 32 ? launch_columns<kBf16, 32>
-                             : c <= 64 ? launch_columns<kBf16, 64> : launch_columns<kBf16, 128>);
-  return cuda_check(launch(p, a, km, vm, st), "msa_tree_attn: launch");
+  const int64_t block_bytes = int64_t(256) * p->d * (fp8 ? 1 : 2);
+  const double size = p->d == 128 ? 1.0 : 0.7;
+  const cudaError_t e = fp8 ? launch_shape<kE4m3>(column_shape<kE4m3>(p, block_bytes, size), p, a, km, vm, st)
+                            : launch_shape<kBf16>(column_shape<kBf16>(p, block_bytes, size), p, a, km, vm, st);
+  return cuda_check(e, "msa_tree_attn: launch");
 }
 
 msa_status launch_latent_attn(const msa_plan_s* p, const void* q, const void* latent_pages, const int32_t* kv_indices,
@@ -776,10 +934,8 @@ msa_status launch_latent_attn(const msa_plan_s* p, const void* q, const void* la
   a.kc = latent_dim / 64 + 1;
   a.mt = latent_dim / 128;
   a.scale_log2 = 1.4426950408889634f * scale;
-  const int c = most_columns(p);
-  const auto launch = c <= 16 ? launch_columns<kLatent, 16> : c <= 32 ? launch_columns<kLatent, 32>
-                                                                      : launch_columns<kLatent, 64>;
-  return cuda_check(launch(p, a, km, km, st), "msa_latent_attn: launch");
+  const ColShape c = column_shape<kLatent>(p, int64_t(256) * width, width / 576.0);
+  return cuda_check(launch_shape<kLatent>(c, p, a, km, km, st), "msa_latent_attn: launch");
 }
 
 namespace {
