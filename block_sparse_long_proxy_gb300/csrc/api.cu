@@ -341,6 +341,7 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
   bwd_plan_tables(p, aux);
   append_plan_tables(p, aux);
   expand_plan_tables(p, aux);
+  column_plan_counts(p);
 
   // device block: tiles | nvp | error word | aux tables | decode partials |
   // backward scratch | fused top-k counters and candidates

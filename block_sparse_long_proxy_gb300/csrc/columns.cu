@@ -46,6 +46,7 @@
 #include "ptx.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 namespace msa {
 namespace {
@@ -811,15 +812,12 @@ template <int KIND>
 ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
   static constexpr double kStart[3][4] = {{7.7, 9.3, 11.2, 17.7}, {8.6, 10.3, 14, 18}, {11, 14, 18, 1e9}};
   static constexpr double kStep[3][4] = {{0.95, 0.97, 1.05, 1.1}, {1.05, 1.05, 1.05, 1.6}, {3.1, 3.1, 3.4, 1e9}};
-  const int G = p->hq / p->hp;
-  int blocks = 1;
-  for (const TileInfo& t : p->tiles) blocks = std::max(blocks, std::min(t.nvp, p->topk));
+  const int blocks = std::min(p->max_nvp, p->topk);
   ColShape best{16, 1};
   double least = 1e300;
   for (int k = 0; k < (KIND == kLatent ? 3 : 4); ++k) {
     const int n = 16 << k;
-    int64_t units = 0, sets = 0;
-    for (const TileInfo& t : p->tiles) units += int64_t(p->hp) * ((t.rows * G + n - 1) / n), sets += p->hp;
+    const int64_t units = p->col_units[k], sets = int64_t(p->n_tiles) * p->hp;
     for (int parts = 1; parts <= kMaxParts && parts <= blocks; parts *= 2) {
       static constexpr int kClusters[5] = {0, 76, 36, 15, 7};
       const int lg = parts == 1 ? 0 : parts == 2 ? 1 : parts == 4 ? 2 : parts == 8 ? 3 : 4;
@@ -839,8 +837,7 @@ template <int KIND, int N>
 cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, const CUtensorMap& vm, int parts,
                            cudaStream_t st) {
   using L = ColSmem<KIND, N>;
-  int groups = 1;
-  for (const TileInfo& t : p->tiles) groups = std::max(groups, (t.rows * (p->hq / p->hp) + N - 1) / N);
+  const int groups = (p->max_tile_rows * (p->hq / p->hp) + N - 1) / N;
   a.parts = parts;
   a.max_groups = groups;
   const int64_t ctas = int64_t(p->n_tiles) * p->hp * groups * parts;
@@ -848,10 +845,14 @@ cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km
   auto kern = columns_kernel<KIND, N>;
   // the limit is the function's, for every host thread: always the most of any topk
   static_assert(L::bytes(1024) + 1024 <= 232448, "shared memory at the largest topk");
-  if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(1024) + 1024))
-    return e;
-  if (parts > 8)
+  static std::atomic<uint64_t> devices{0};  // that have these limits (the call takes about a microsecond)
+  const uint64_t bit = p->device < 64 ? uint64_t(1) << p->device : 0;
+  if ((devices.load(std::memory_order_acquire) & bit) == 0) {
+    if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(1024) + 1024))
+      return e;
     if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+    devices.fetch_or(bit, std::memory_order_release);
+  }
   return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), parts, dim3(col_threads<KIND, N>()),
                             L::bytes(p->topk) + 1024, st, km, vm, a);
 }
@@ -867,6 +868,15 @@ cudaError_t launch_shape(ColShape c, const msa_plan_s* p, const ColArgs& a, cons
 }
 
 }  // namespace
+
+void column_plan_counts(msa_plan_s* p) {
+  const int G = p->hq / p->hp;
+  for (const TileInfo& t : p->tiles) {
+    p->max_tile_rows = std::max(p->max_tile_rows, t.rows);
+    p->max_nvp = std::max(p->max_nvp, t.nvp);
+    for (int k = 0; k < 4; ++k) p->col_units[k] += int64_t(p->hp) * ((int64_t(t.rows) * G + (16 << k) - 1) >> (4 + k));
+  }
+}
 
 msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,
                             const int32_t* kv_indices, const int32_t* idx, const int32_t* tree_mask, const float* k_scale,

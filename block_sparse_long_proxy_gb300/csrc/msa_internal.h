@@ -107,6 +107,8 @@ struct msa_plan_s {
   int32_t n_page_entries = 0;        // sum over sequences of ceil(kv_len / 128)
   int64_t append_units_off = 0;      // cache appends: one unit per page that gets rows
   int32_t n_append_units = 0;
+  int32_t max_tile_rows = 1, max_nvp = 1;  // of any tile
+  int64_t col_units[4] = {};         // attention of few rows: units of 16, 32, 64 and 128 columns
   int64_t entry_keys_off = 0;        // latent expansion: keys of each page-table entry's page
   void* bwd_d = nullptr;             // backward scratch (D, proxy LSE, inverse index)
 };
@@ -252,6 +254,7 @@ msa_status launch_attn_bwd(const msa_plan_s* p, const void* q, const void* k_pag
 // the dims that a latent cache may have (append.cu)
 msa_status check_latent_dims(const char* fn, int32_t latent_dim, int32_t rope_dim);
 // attention of few rows, the (row, head) pairs as columns (columns.cu)
+void column_plan_counts(msa_plan_s* p);
 msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pages, const void* v_pages,
                             const int32_t* kv_indices, const int32_t* idx, const int32_t* tree_mask, const float* k_scale,
                             const float* v_scale, void* out, float* lse, cudaStream_t st);

@@ -114,6 +114,6 @@ for func, kind, size in events():
     if kind == 0:
         assert limit.setdefault(func, size) == size
     else:
-        assert size <= limit[func] <= 232448
-assert len(limit) >= 11
+        assert size <= limit[func] <= 232448, (size, limit[func])
+assert len(limit) >= 6, len(limit)
 """)
