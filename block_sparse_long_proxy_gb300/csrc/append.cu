@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(kPkThreads)
   pools.block_scales[row * kChunks + c] = static_cast<uint8_t>(sc);
 }
 
-// Rows of a latent cache, [latent | key part], the key part rotated: chunk c of a
-// row is 16 values, of the latent copied as they are.  Rows share nothing, so
+// Rows of a latent cache, [latent | key part], the key part rotated: a thread has
+// 16 values of it, or copies 16 bytes of the latent.  Rows share nothing, so
 // blockIdx.y takes a page's rows by kLatentRows.
 constexpr int kLatentRows = 16;
 
@@ -425,30 +425,40 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0) atomicOr(err, kErrDeviceCheck);
     return;
   }
-  const int copied = latent_dim / 16, chunks = copied + rope_dim / 16;
   const int first = blockIdx.y * kLatentRows, rows = min(kLatentRows, n - first);
+  const int64_t width = latent_dim + rope_dim;
+  __nv_bfloat16* const out = pages + (page * 128 + slot0 + first) * width;
+  // the key parts: full warps of them, whose angles are most of what is computed
+  const int chunks = rope_dim / 16;
   for (int e = threadIdx.x; e < rows * chunks; e += kThreads) {
-    const int i = first + e / chunks, c = e % chunks;
-    __nv_bfloat16* dst = pages + (page * 128 + slot0 + i) * (latent_dim + rope_dim);
-    if (c < copied) {
-      const uint4* src = reinterpret_cast<const uint4*>(latent + (u.row + i) * latent_stride + 16 * c);
-      const uint4 x = src[0], y = src[1];
-      uint4* to = reinterpret_cast<uint4*>(dst + 16 * c);
-      to[0] = x, to[1] = y;
-      continue;
-    }
-    const RopeChunk ch = rope_chunk(tab, c - copied);
-    const __nv_bfloat16* src = key + (u.row + i) * key_stride;
+    const int i = e / chunks, c = e % chunks;
+    const RopeChunk ch = rope_chunk(tab, c);
+    const __nv_bfloat16* src = key + (u.row + first + i) * key_stride;
     float x[16];
     load8(src + ch.lo, x);
     load8(src + ch.hi, x + 8);
     if (ch.rotated) {
       float cs[8], sn[8];
-      rope_angles(tab, c - copied, positions ? positions[u.row + i] : u.pos + i, false, cs, sn);
+      rope_angles(tab, c, positions ? positions[u.row + first + i] : u.pos + first + i, false, cs, sn);
       rope_rotate(tab.interleaved != 0, cs, sn, x);
     }
-    store8(dst + latent_dim + ch.lo, x);
-    store8(dst + latent_dim + ch.hi, x + 8);
+    store8(out + i * width + latent_dim + ch.lo, x);
+    store8(out + i * width + latent_dim + ch.hi, x + 8);
+  }
+  // the latents, four 16-byte loads on their way at a time, the last warps first
+  const int per_row = latent_dim / 8, total = rows * per_row;
+  for (int e0 = kThreads - 1 - threadIdx.x; e0 < total; e0 += 4 * kThreads) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = e0 + k * kThreads;
+      if (e < total) v[k] = *reinterpret_cast<const uint4*>(latent + (u.row + first + e / per_row) * latent_stride + e % per_row * 8);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = e0 + k * kThreads;
+      if (e < total) *reinterpret_cast<uint4*>(out + e / per_row * width + e % per_row * 8) = v[k];
+    }
   }
 }
 

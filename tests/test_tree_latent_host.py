@@ -115,5 +115,5 @@ for func, kind, size in events():
         assert limit.setdefault(func, size) == size
     else:
         assert size <= limit[func] <= 232448, (size, limit[func])
-assert len(limit) >= 6, len(limit)
+assert len(limit) >= 3, len(limit)
 """)
