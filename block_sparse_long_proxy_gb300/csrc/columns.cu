@@ -55,7 +55,6 @@ enum Cache { kBf16, kE4m3, kLatent };
 
 constexpr int kSlotBytes = 32768;
 constexpr int kMaxParts = 16;
-constexpr int kConvWarps = 4;  // e4m3 only
 
 __device__ __forceinline__ float redux_max(float x) {
   float r;
@@ -98,6 +97,24 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
   if constexpr (C == 32) tmem_st16(taddr + 16, r + 16);
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// mma_ss and mma_commit by the lane that has `leader`
+__device__ __forceinline__ void mma_ss_if(bool leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(bool leader, uint64_t* bar) {
+  if (leader) mma_commit(bar);
+}
+
 struct ColArgs {
   const __nv_bfloat16* q;   // [total_q, hq, dq]
   const TileInfo* tiles;
@@ -119,12 +136,12 @@ struct ColArgs {
   float scale_log2;
 };
 
-template <int KIND, int N>
+template <int KIND, int N, bool TWO>
 struct ColSmem {
   static constexpr bool kLat = KIND == kLatent;
   static constexpr int kQChunk = N * 128;
   static constexpr int kPBytes = kLat ? 0 : (N > 64 ? 32768 : 16384);
-  static constexpr int kSlots = kLat ? (N == 64 ? 4 : 5) : 4;
+  static constexpr int kSlots = kLat ? (N == 64 ? 4 : 5) : TWO ? 2 : 4;
   static constexpr int kTails = kLat ? (N == 16 ? 2 : 1) : 0;  // slots of the rotated part, then P^T
   static constexpr int kTailBytes = 16384;
   static constexpr int kQOff = 0;
@@ -144,20 +161,24 @@ struct ColSmem {
   static_assert(kQChunk % 1024 == 0 && kRingOff % 1024 == 0 && kTailOff % 1024 == 0, "swizzled tiles");
   // after the last block, a part's O^T: [N][dims] floats where the ring was (512 dims at most for
   // the latent cache, 128 for the others)
-  static_assert(N * (kLat ? 512 : 128) * 4 <= kSlots * kSlotBytes, "O^T of a part fits the ring");
+  static_assert(TWO || N * (kLat ? 512 : 128) * 4 <= kSlots * kSlotBytes, "O^T of a part fits the ring");
   // the weights of a merge, where Q was
   static_assert(N * kMaxParts * 4 <= kPOff, "weights fit Q's place");
 };
 
-// Softmax warpgroups: 8 to 32 columns each.  Two of them left the passes over S^T
-// waiting for their own latencies.
-template <int N>
+// Softmax warpgroups: 8 to 32 columns each.  Alone on an SM, two of them leave the
+// passes over S^T waiting for their own latencies.
+template <int N, bool TWO>
 constexpr int soft_warps() {
-  return N == 16 ? 8 : 16;
+  return N == 16 || TWO ? 8 : 16;
 }
-template <int KIND, int N>
+template <int KIND, bool TWO>
+constexpr int conv_warps() {
+  return KIND == kE4m3 ? (TWO ? 2 : 4) : 0;
+}
+template <int KIND, int N, bool TWO>
 constexpr int col_threads() {
-  return 32 * (soft_warps<N>() + 2 + (KIND == kE4m3 ? kConvWarps : 0));
+  return 32 * (soft_warps<N, TWO>() + 2 + conv_warps<KIND, TWO>());
 }
 
 // Sums of CH values a lane over the warp's lanes: lane c (mod CH) has the sum of
@@ -183,13 +204,13 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-template <int KIND, int N>
-__global__ void __launch_bounds__(col_threads<KIND, N>(), 1)
+template <int KIND, int N, bool TWO>
+__global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
     columns_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const ColArgs a) {
-  using L = ColSmem<KIND, N>;
+  using L = ColSmem<KIND, N, TWO>;
   constexpr bool kLat = KIND == kLatent, kFp8 = KIND == kE4m3;
-  constexpr int kThreads = col_threads<KIND, N>();
-  constexpr int kSoftWarps = soft_warps<N>(), kProducer = kSoftWarps, kIssuer = kSoftWarps + 1;
+  constexpr int kThreads = col_threads<KIND, N, TWO>(), kConvWarps = conv_warps<KIND, TWO>();
+  constexpr int kSoftWarps = soft_warps<N, TWO>(), kProducer = kSoftWarps, kIssuer = kSoftWarps + 1;
   constexpr int HN = N / (kSoftWarps / 4);      // columns of a warpgroup
   constexpr int CH = 8;                         // of them, in registers at a time
   constexpr int NCH = HN / CH;
@@ -406,7 +427,15 @@ __global__ void __launch_bounds__(col_threads<KIND, N>(), 1)
     }
   } else if (warp == kIssuer) {
     // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
+    // The whole warp goes through the loop, one elected lane issuing: descriptors
+    // are then the warp's, not a lane's, and need no move to uniform registers.
+    {
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const int nn = __shfl_sync(0xFFFFFFFFu, n, 0);
+      const bool leader = elect_one();
+      auto waited = [&](uint64_t* bar, uint32_t parity) {
+        return static_cast<bool>(__all_sync(0xFFFFFFFFu, mbar_wait_inl(bar, parity, a.err)));
+      };
       constexpr uint32_t id_qk = kFp8 ? idesc_f16_f32(128, N, false, false) : idesc_bf16_f32(128, N, false, false);
       constexpr uint32_t id_pv = kFp8 ? idesc_f16_f32(128, N, true, true) : idesc_bf16_f32(128, N, true, true);
       const uint64_t kd0 = smem_desc(smem_u32(smem + L::kRingOff), 16, 1024, kSwizzle128);
@@ -417,53 +446,53 @@ __global__ void __launch_bounds__(col_threads<KIND, N>(), 1)
       const uint64_t pd0 = smem_desc(smem_u32(smem + (kLat ? L::kTailOff : L::kPOff)), 16384, 1024, kSwizzle128);
       bool ok = true;
       auto qk = [&](int i) {
-        const uint32_t d = tmem + (i & 1) * N;
+        const uint32_t d = tm + (i & 1) * N;
         uint32_t acc = 0;
         for (int h = 0; h < (kLat ? a.mt : 1); ++h) {
           const int u = i * per + h, s = slot_of(u);
-          if (!(ok = mbar_wait_inl(ready + s, phase_of(u), a.err))) return;
+          if (!(ok = waited(ready + s, phase_of(u)))) return;
           tc_fence_after();
           const uint64_t kd = kd0 + s * (kSlotBytes >> 4), qd = qd0 + h * 2 * (L::kQChunk >> 4);
           for (int c = 0; c < (kLat ? 2 : a.kc); ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              mma_ss(d, kd + ((c * 16384 + kk * 32) >> 4), qd + ((c * L::kQChunk + kk * 32) >> 4), id_qk, acc);
+              mma_ss_if(leader, d, kd + ((c * 16384 + kk * 32) >> 4), qd + ((c * L::kQChunk + kk * 32) >> 4), id_qk, acc);
               acc = 1;
             }
-          if (!kLat) mma_commit(empty + s);
+          if (!kLat) mma_commit_if(leader, empty + s);
         }
         if (kLat) {
           const int s = i % T;
-          if (!(ok = mbar_wait_inl(tail_full + s, i / T & 1, a.err))) return;
+          if (!(ok = waited(tail_full + s, i / T & 1))) return;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss(d, td0 + ((s * L::kTailBytes + kk * 32) >> 4), qd0 + ((2 * a.mt * L::kQChunk + kk * 32) >> 4), id_qk, 1);
+            mma_ss_if(leader, d, td0 + ((s * L::kTailBytes + kk * 32) >> 4), qd0 + ((2 * a.mt * L::kQChunk + kk * 32) >> 4), id_qk, 1);
         }
-        mma_commit(s_full + (i & 1));
+        mma_commit_if(leader, s_full + (i & 1));
       };
-      if (n > 0) qk(0);
-      for (int i = 0; i < n && ok; ++i) {
+      if (nn > 0) qk(0);
+      for (int i = 0; i < nn && ok; ++i) {
         // the latent's slots serve S^T of block i until its P.V: the next block's loads wait for that
-        if (!kLat && i + 1 < n) qk(i + 1);
-        if (!ok || !(ok = mbar_wait_inl(p_full, i & 1, a.err))) break;
+        if (!kLat && i + 1 < nn) qk(i + 1);
+        if (!ok || !(ok = waited(p_full, i & 1))) break;
         tc_fence_after();
         const uint64_t pd = pd0 + (kLat ? (i % T) * (L::kTailBytes >> 4) : 0);
         for (int h = 0; h < a.mt && ok; ++h) {
           const int u = kLat ? i * per + h : i * per + 1, s = slot_of(u);
           if (!kLat) {
-            if (!(ok = mbar_wait_inl(ready + s, phase_of(u), a.err))) break;
+            if (!(ok = waited(ready + s, phase_of(u)))) break;
             tc_fence_after();
           }
           const uint64_t vd = vd0 + s * (kSlotBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ss(tmem + (2 + h) * N, vd + ((kk * 2048) >> 4), pd + ((kk * 2048) >> 4), id_pv, i > 0 || kk > 0);
-          mma_commit(empty + s);
+            mma_ss_if(leader, tm + (2 + h) * N, vd + ((kk * 2048) >> 4), pd + ((kk * 2048) >> 4), id_pv, i > 0 || kk > 0);
+          mma_commit_if(leader, empty + s);
         }
-        if (kLat) mma_commit(tail_empty + i % T);
-        mma_commit(pv_done);
-        if (kLat && ok && i + 1 < n) qk(i + 1);
+        if (kLat) mma_commit_if(leader, tail_empty + i % T);
+        mma_commit_if(leader, pv_done);
+        if (kLat && ok && i + 1 < nn) qk(i + 1);
       }
     }
   } else if (warp < kSoftWarps) {
@@ -669,7 +698,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N>(), 1)
         }
         if (h * 128 + r >= a.dv) continue;  // dims 64: the upper half repeats the lower
         const int col0 = wg * HN + k * CH;
-        if (a.parts > 1) {
+        if (!TWO && a.parts > 1) {
 #pragma unroll
           for (int c = 0; c < CH; ++c)
             if (col0 + c < cols) part_o[(col0 + c) * a.dv + h * 128 + r] = __uint_as_float(o[c]);
@@ -736,7 +765,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N>(), 1)
 
   // ------------------------------------------------------------------- end
   tc_fence_before();
-  if (a.parts == 1) {
+  if (TWO || a.parts == 1) {
     __syncthreads();
     tc_fence_after();
     if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
@@ -807,13 +836,14 @@ __global__ void __launch_bounds__(col_threads<KIND, N>(), 1)
 //   32 rows, same: 64 / 4 35.8, 32 / 2 41.7, 64 / 2 49.3, 16 / 1 63
 struct ColShape {
   int n, parts;
+  bool two;
 };
 template <int KIND>
 ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
   static constexpr double kStart[3][4] = {{7.7, 9.3, 11.2, 17.7}, {8.6, 10.3, 14, 18}, {11, 14, 18, 1e9}};
   static constexpr double kStep[3][4] = {{0.95, 0.97, 1.05, 1.1}, {1.05, 1.05, 1.05, 1.6}, {3.1, 3.1, 3.4, 1e9}};
   const int blocks = std::min(p->max_nvp, p->topk);
-  ColShape best{16, 1};
+  ColShape best{16, 1, false};
   double least = 1e300;
   for (int k = 0; k < (KIND == kLatent ? 3 : 4); ++k) {
     const int n = 16 << k;
@@ -827,22 +857,22 @@ ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
       const double hbm = at_once * block_bytes * sets / units / 6.3e6;  // us a block step
       const double us = rounds * (kStart[KIND][k] * (KIND == kLatent ? 0.4 + 0.6 * size : 1.0) +
                                   (blocks + parts - 1) / parts * std::max(kStep[KIND][k] * size, hbm));
-      if (us < least) least = us, best = {n, parts};
+      if (us < least) least = us, best = {n, parts, false};
     }
   }
   return best;
 }
 
-template <int KIND, int N>
+template <int KIND, int N, bool TWO>
 cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, const CUtensorMap& vm, int parts,
                            cudaStream_t st) {
-  using L = ColSmem<KIND, N>;
+  using L = ColSmem<KIND, N, TWO>;
   const int groups = (p->max_tile_rows * (p->hq / p->hp) + N - 1) / N;
   a.parts = parts;
   a.max_groups = groups;
   const int64_t ctas = int64_t(p->n_tiles) * p->hp * groups * parts;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  auto kern = columns_kernel<KIND, N>;
+  auto kern = columns_kernel<KIND, N, TWO>;
   // the limit is the function's, for every host thread: always the most of any topk
   static_assert(L::bytes(1024) + 1024 <= 232448, "shared memory at the largest topk");
   static std::atomic<uint64_t> devices{0};  // that have these limits (the call takes about a microsecond)
@@ -853,18 +883,23 @@ cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km
     if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
     devices.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), parts, dim3(col_threads<KIND, N>()),
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), parts, dim3(col_threads<KIND, N, TWO>()),
                             L::bytes(p->topk) + 1024, st, km, vm, a);
 }
 
 template <int KIND>
 cudaError_t launch_shape(ColShape c, const msa_plan_s* p, const ColArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                          cudaStream_t st) {
-  if constexpr (KIND != kLatent)
-    if (c.n == 128) return launch_columns<KIND, 128>(p, a, km, vm, c.parts, st);
-  return c.n == 16   ? launch_columns<KIND, 16>(p, a, km, vm, c.parts, st)
-         : c.n == 32 ? launch_columns<KIND, 32>(p, a, km, vm, c.parts, st)
-                     : launch_columns<KIND, 64>(p, a, km, vm, c.parts, st);
+  if constexpr (KIND != kLatent) {
+    if (c.two)
+      return c.n == 16   ? launch_columns<KIND, 16, true>(p, a, km, vm, 1, st)
+             : c.n == 32 ? launch_columns<KIND, 32, true>(p, a, km, vm, 1, st)
+                         : launch_columns<KIND, 64, true>(p, a, km, vm, 1, st);
+    if (c.n == 128) return launch_columns<KIND, 128, false>(p, a, km, vm, c.parts, st);
+  }
+  return c.n == 16   ? launch_columns<KIND, 16, false>(p, a, km, vm, c.parts, st)
+         : c.n == 32 ? launch_columns<KIND, 32, false>(p, a, km, vm, c.parts, st)
+                     : launch_columns<KIND, 64, false>(p, a, km, vm, c.parts, st);
 }
 
 }  // namespace
