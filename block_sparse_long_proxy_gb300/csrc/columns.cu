@@ -97,11 +97,6 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
   if constexpr (C == 32) tmem_st16(taddr + 16, r + 16);
 }
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 // mma_ss and mma_commit by the lane that has `leader`
 __device__ __forceinline__ void mma_ss_if(bool leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -149,8 +144,9 @@ struct ColSmem {
   static constexpr int kRingOff = kPOff + kPBytes;
   static constexpr int kTailOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kBarOff = kTailOff + kTails * kTailBytes;
-  static constexpr int kMaskOff = kBarOff + 8 * 32;        // [N] 128-bit masks of the columns, then their union
-  static constexpr int kColOff = kMaskOff + 16 * (N + 1);  // (m, l) of the columns
+  static constexpr int kMaskWords = N > 32 ? N / 32 : 1;
+  static constexpr int kMaskOff = kBarOff + 8 * 32;        // [128 key offsets] the columns that see it
+  static constexpr int kColOff = kMaskOff + 512 * kMaskWords;  // (m, l) of the columns
   static constexpr int kRedOff = kColOff + 8 * N;          // [warpgroup][4][columns] column maxima, or sums, of the warps
   static constexpr int kShiftOff = kRedOff + 16 * N;       // [warp][columns], twice: shift, rescaling factor
   static constexpr int kRowOff = kShiftOff + 2 * 16 * N;
@@ -230,7 +226,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   uint64_t* pv_done = p_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 1);
   int32_t* n_slot = reinterpret_cast<int32_t*>(tmem_slot + 1);
-  uint32_t* cmask = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
+  uint32_t* seen_by = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
   float2* col_ml = reinterpret_cast<float2*>(smem + L::kColOff);
   int64_t* col_row = reinterpret_cast<int64_t*>(smem + L::kRowOff);  // (query row, head) of the columns, as a row of q and out
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);  // page | place of the block << 24
@@ -246,7 +242,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   if (warp == kProducer) {
     if (lane == 0) {
       prefetch_tmap(&k_map);
-      if (!kLat) prefetch_tmap(&v_map);
+      prefetch_tmap(&v_map);
       for (int s = 0; s < S; ++s) {
         mbar_init(full + s, 1);
         mbar_init(empty + s, 1);
@@ -261,7 +257,6 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       mbar_init(pv_done, 1);
       fence_mbar_init();
     }
-    if (lane < 4) cmask[4 * N + lane] = 0u;
   } else if (warp == kIssuer) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
@@ -283,29 +278,37 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   // slot uses so far -> slot and phase
   auto slot_of = [&](int u) { return u % S; };
   auto phase_of = [&](int u) { return static_cast<uint32_t>(u / S & 1); };
-  // load h of block i: a slot, or (latent, h == per) the rotated part
-  auto produce = [&](int i, int h) {
-    const int row = static_cast<int>((static_cast<int64_t>(list[i] & 0xFFFFFFu) * a.hkv + kvh) * 128);
+  // load h of block i: a slot, or (latent, h == per) the rotated part; by the whole
+  // producer warp, `leader` issuing
+  auto produce = [&](int i, int h, bool leader) {
+    const int row = __shfl_sync(
+        0xFFFFFFFFu, static_cast<int>((static_cast<int64_t>(list[i] & 0xFFFFFFu) * a.hkv + kvh) * 128), 0);
+    auto waited = [&](uint64_t* bar, uint32_t parity) {
+      return static_cast<bool>(__all_sync(0xFFFFFFFFu, mbar_wait_inl(bar, parity, a.err)));
+    };
     if (kLat && h == per) {
       const int s = i % T;
-      if (!mbar_wait_inl(tail_empty + s, (i / T & 1) ^ 1, a.err)) return false;
-      mbar_expect_tx(tail_full + s, L::kTailBytes);
-      tma_load_2d(smem + L::kTailOff + s * L::kTailBytes, &k_map, tail_full + s, 128 * a.mt, row);
+      if (i >= T && !waited(tail_empty + s, (i / T & 1) ^ 1)) return false;
+      if (leader) {
+        mbar_expect_tx(tail_full + s, L::kTailBytes);
+        tma_load_2d(smem + L::kTailOff + s * L::kTailBytes, &k_map, tail_full + s, 128 * a.mt, row);
+      }
       return true;
     }
     const int u = i * per + h, s = slot_of(u);
-    if (!mbar_wait_inl(empty + s, phase_of(u) ^ 1, a.err)) return false;
+    if (u >= S && !waited(empty + s, phase_of(u) ^ 1)) return false;
     uint8_t* dst = smem + L::kRingOff + s * kSlotBytes;
-    if (kFp8) {
-      mbar_expect_tx(full + s, 128 * a.dv);
-      tma_load_2d(dst + 16384, h == 0 ? &k_map : &v_map, full + s, 0, row);
-    } else if (kLat) {
-      mbar_expect_tx(full + s, kSlotBytes);
-      for (int c = 0; c < 2; ++c) tma_load_2d(dst + c * 16384, &k_map, full + s, (2 * h + c) * 64, row);
-    } else {
-      mbar_expect_tx(full + s, a.kc * 16384);
-      for (int c = 0; c < a.kc; ++c)
-        tma_load_2d(dst + c * 16384, h == 0 ? &k_map : &v_map, full + s, c * 64, row);
+    if (leader) {
+      if (kFp8) {
+        mbar_expect_tx(full + s, 128 * a.dv);
+        tma_load_2d(dst + 16384, h == 0 ? &k_map : &v_map, full + s, 0, row);
+      } else if (kLat) {
+        mbar_expect_tx(full + s, kSlotBytes);
+        tma_load_3d(dst, &v_map, full + s, 0, row, 2 * h);
+      } else {
+        mbar_expect_tx(full + s, a.kc * 16384);
+        tma_load_3d(dst, h == 0 ? &k_map : &v_map, full + s, 0, row, 0);
+      }
     }
     return true;
   };
@@ -346,9 +349,9 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       __syncwarp();
       if (b == 0) {
         started = min(n, first_blocks);
-        if (lane == 0)
-          for (int i = 0; i < started; ++i)
-            for (int h = 0; h < per + kLat; ++h) produce(i, h);
+        const bool leader = elect_one();
+        for (int i = 0; i < started; ++i)
+          for (int h = 0; h < per + kLat; ++h) produce(i, h, leader);
       }
       if (kFp8 && take) {
         const int64_t sat = a.per_page ? page * a.hkv + kvh : kvh;
@@ -404,10 +407,19 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       uint32_t m = 0u;
       if (c < cols)
         m = a.tree_mask ? reinterpret_cast<const uint32_t*>(a.tree_mask + tl.q_begin + row)[wd] & low(tl.rows) : low(row + 1);
-      cmask[4 * c + wd] = m;
+      // a row of bits a column -> a row a key offset; lane b keeps offset 32 wd + b
+      uint32_t mine = 0u;
 #pragma unroll
-      for (int d = 8; d > 0; d >>= 1) m |= __shfl_xor_sync(0xFFFFFFFFu, m, d);
-      if ((lane & 15) == 0 && m != 0u) atomicOr(cmask + 4 * N + wd, m);
+      for (int d = 0; d < 32; ++d) {
+        const uint32_t w = __ballot_sync(0xFFFFFFFFu, m >> d & 1u);
+        if (lane == d) mine = w;
+      }
+      if (N >= 32) {
+        seen_by[(32 * (e0 / N) + lane) * L::kMaskWords + e0 % N / 32] = mine;
+      } else {  // 16 columns of two words
+        seen_by[64 * (e0 / 32) + lane] = mine & 0xFFFFu;
+        seen_by[64 * (e0 / 32) + 32 + lane] = mine >> 16;
+      }
     }
     if (!kFp8) asm volatile("cp.async.wait_all;" ::: "memory");
   }
@@ -416,15 +428,19 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   const int n = *n_slot;
   // key offset of lane 0 of block i's rows; places: 0 before the tile, 1 its first block, 2 the next
   auto offset0 = [&](uint32_t entry) { return (static_cast<int>(entry >> 24) - 1) * 128 - (tl.pos0 & 127); };
-  auto seen_by_any = [&](int e) { return e < 0 || (e < 128 && (cmask[4 * N + (e >> 5)] >> (e & 31) & 1u)); };
+  auto seen_by_any = [&](int e) {
+    if (e < 0 || e >= 128) return e < 0;
+    uint32_t any = 0u;
+    for (int w = 0; w < L::kMaskWords; ++w) any |= seen_by[e * L::kMaskWords + w];
+    return any != 0u;
+  };
 
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      bool ok = true;
-      for (int i = started; i < n && ok; ++i)
-        for (int h = 0; h < per + kLat && ok; ++h) ok = produce(i, h);
-    }
+    const bool leader = elect_one();
+    bool ok = true;
+    for (int i = started; i < n && ok; ++i)
+      for (int h = 0; h < per + kLat && ok; ++h) ok = produce(i, h, leader);
   } else if (warp == kIssuer) {
     // ----------------------------------------------------------------- MMA
     // The whole warp goes through the loop, one elected lane issuing: descriptors
@@ -532,16 +548,17 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       }
       const bool masked = entry >> 24 != 0;
       const int e = offset0(entry) + r;
+      uint32_t vis = 0xFFFFFFFFu;  // this warpgroup's columns that see the key
+      if (masked && e >= 0)
+        vis = e < 128 ? seen_by[e * L::kMaskWords + wg * HN / 32] >> (wg * HN % 32) : 0u;
       uint32_t s[CH];
       auto load = [&](int k) {
         tmem_ld<CH>(s_addr + k * CH, s);
         tmem_wait_ld();
-        if (masked && e >= 0) {
+        if (masked) {
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            const bool see = e < 128 && (cmask[4 * (wg * HN + k * CH + c) + (e >> 5 & 3)] >> (e & 31) & 1u);
-            if (!see) s[c] = __float_as_uint(-INFINITY);
-          }
+          for (int c = 0; c < CH; ++c)
+            if (!(vis >> (k * CH + c) & 1u)) s[c] = __float_as_uint(-INFINITY);
         }
       };
       // logits of columns c and c + 1 of chunk k less their references, log2
@@ -699,9 +716,9 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
         if (h * 128 + r >= a.dv) continue;  // dims 64: the upper half repeats the lower
         const int col0 = wg * HN + k * CH;
         if (!TWO && a.parts > 1) {
+          float* to = part_o + col0 * a.dv + h * 128 + r;
 #pragma unroll
-          for (int c = 0; c < CH; ++c)
-            if (col0 + c < cols) part_o[(col0 + c) * a.dv + h * 128 + r] = __uint_as_float(o[c]);
+          for (int c = 0; c < CH; ++c, to += a.dv) *to = __uint_as_float(o[c]);
           continue;
         }
         // even lanes take two dims of column c, odd lanes of column c + 1
@@ -796,22 +813,27 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       a.lse[col_row[c]] = sum > 0.f ? (mm + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
   __syncthreads();
-  const int dv4 = a.dv / 4;
-  for (int e = part * kThreads + threadIdx.x; e < cols * dv4; e += a.parts * kThreads) {
+  // a share of the items each, four dims of one column, the parts' from this CTA's
+  // own on (all CTAs reading one part's at a time took 1.5 times as long)
+  const int dv4 = a.dv / 4, items = cols * dv4, last = items * (part + 1) / a.parts;
+  for (int e = items * part / a.parts + threadIdx.x; e < last; e += kThreads) {
     const int c = e / dv4;
     const uint32_t at = smem_u32(smem + L::kRingOff) + 16u * e;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w0 = 0; w0 < kMaxParts; w0 += 8) {
+    for (int k0 = 0; k0 < kMaxParts; k0 += 8) {
+      if (k0 >= a.parts) break;
       float4 v[8];
 #pragma unroll
-      for (int w = 0; w < 8; ++w)
-        if (w0 + w < a.parts) v[w] = ld_cluster_f4(at, w0 + w);
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < a.parts)
+          v[k] = k0 + k == 0 ? reinterpret_cast<const float4*>(smem + L::kRingOff)[e]
+                             : ld_cluster_f4(at, (part + k0 + k) & (a.parts - 1));
 #pragma unroll
-      for (int w = 0; w < 8; ++w)
-        if (w0 + w < a.parts) {
-          const float x = wts[c * kMaxParts + w0 + w];
-          o.x += v[w].x * x, o.y += v[w].y * x, o.z += v[w].z * x, o.w += v[w].w * x;
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < a.parts) {
+          const float x = wts[c * kMaxParts + ((part + k0 + k) & (a.parts - 1))];
+          o.x += v[k].x * x, o.y += v[k].y * x, o.z += v[k].z * x, o.w += v[k].w * x;
         }
     }
     *reinterpret_cast<uint2*>(a.out + col_row[c] * a.dv + 4 * (e % dv4)) =
@@ -918,12 +940,14 @@ msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pa
                             const float* v_scale, void* out, float* lse, cudaStream_t st) {
   const bool fp8 = p->kv_dtype != MSA_KV_BF16;
   CUtensorMap km, vm;
-  const uint64_t dims[2] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->num_pages) * p->hkv * 128};
-  const uint64_t str[1] = {static_cast<uint64_t>(p->d) * (fp8 ? 1 : 2)};
-  const uint32_t box[2] = {fp8 ? static_cast<uint32_t>(p->d) : 64u, 128};
-  const int swz = fp8 ? p->d : 128;
-  if (!encode_tensor_map(&km, 2, k_pages, dims, str, box, fp8 ? 0 : 1, swz) ||
-      !encode_tensor_map(&vm, 2, v_pages, dims, str, box, fp8 ? 0 : 1, swz))
+  // bf16: a block in one load, 64 columns (128-byte rows) after the other; e4m3: whole rows of codes
+  const uint64_t rows = static_cast<uint64_t>(p->num_pages) * p->hkv * 128, d = p->d;
+  const uint64_t dims[3] = {fp8 ? d : 64, rows, d / 64};
+  const uint64_t str[2] = {d * (fp8 ? 1 : 2), 128};
+  const uint32_t box[3] = {static_cast<uint32_t>(dims[0]), 128, static_cast<uint32_t>(d / 64)};
+  const int swz = fp8 ? p->d : 128, rank = fp8 ? 2 : 3;
+  if (!encode_tensor_map(&km, rank, k_pages, dims, str, box, fp8 ? 0 : 1, swz) ||
+      !encode_tensor_map(&vm, rank, v_pages, dims, str, box, fp8 ? 0 : 1, swz))
     return set_error(MSA_ERR_CUDA, "msa_tree_attn: tensor map encoding failed");
   ColArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -954,13 +978,16 @@ msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pa
 msa_status launch_latent_attn(const msa_plan_s* p, const void* q, const void* latent_pages, const int32_t* kv_indices,
                               const int32_t* idx, const int32_t* tree_mask, int32_t latent_dim, int32_t rope_dim,
                               float scale, void* out, float* lse, cudaStream_t st) {
-  CUtensorMap km;
+  CUtensorMap km, vm;
   const int width = latent_dim + rope_dim;
-  // boxes of 64 columns; the last one's columns past the row are zeros
-  const uint64_t dims[2] = {static_cast<uint64_t>(width), static_cast<uint64_t>(p->num_pages) * 128};
-  const uint64_t str[1] = {static_cast<uint64_t>(width) * 2};
-  const uint32_t box[2] = {64, 128};
-  if (!encode_tensor_map(&km, 2, latent_pages, dims, str, box, 1, 128))
+  // the rotated part: a box of 64 columns, those past the row zeros; the latent's
+  // 128 dims of a slot: two boxes of 64 columns in one load
+  const uint64_t rows = static_cast<uint64_t>(p->num_pages) * 128;
+  const uint64_t dims[2] = {static_cast<uint64_t>(width), rows}, dims3[3] = {64, rows, static_cast<uint64_t>(latent_dim / 64)};
+  const uint64_t str[2] = {static_cast<uint64_t>(width) * 2, 128};
+  const uint32_t box[2] = {64, 128}, box3[3] = {64, 128, 2};
+  if (!encode_tensor_map(&km, 2, latent_pages, dims, str, box, 1, 128) ||
+      !encode_tensor_map(&vm, 3, latent_pages, dims3, str, box3, 1, 128))
     return set_error(MSA_ERR_CUDA, "msa_latent_attn: tensor map encoding failed");
   ColArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -980,7 +1007,7 @@ msa_status launch_latent_attn(const msa_plan_s* p, const void* q, const void* la
   a.mt = latent_dim / 128;
   a.scale_log2 = 1.4426950408889634f * scale;
   const ColShape c = column_shape<kLatent>(p, int64_t(256) * width, width / 576.0);
-  return cuda_check(launch_shape<kLatent>(c, p, a, km, km, st), "msa_latent_attn: launch");
+  return cuda_check(launch_shape<kLatent>(c, p, a, km, vm, st), "msa_latent_attn: launch");
 }
 
 namespace {

@@ -68,12 +68,12 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uin
     }
   }
 }
-// D (256 rows, 128 a CTA) (+)= A (128 rows a CTA) * B^T (half of N rows a CTA)
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D (256 rows, 128 a CTA) (+)= A (128 rows a CTA) * B^T (half of N rows a CTA), by the lane that has `leader`
+__device__ __forceinline__ void mma_pair(bool leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
 // 16 lanes of tensor memory x 8 N columns: lane t has rows t / 4 and t / 4 + 8, and
@@ -246,33 +246,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
   } else if (warp == 9) {
-    if (lane == 0 && rank == 0) {  // issues for both CTAs
+    if (rank == 0) {  // issues for both CTAs: the whole warp goes through the loop, one elected lane issuing
       const uint32_t id = idesc_bf16_f32(256, n, false, false);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       const uint64_t ad = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128);
       const uint64_t bd0 = smem_desc(smem_u32(smem + kABytes), 16, 1024, kSwizzle128);
+      const bool leader = elect_one();
       bool ok = true;
+      auto all = [&](bool done) { return static_cast<bool>(__all_sync(0xFFFFFFFFu, done)); };
       Ring ring;
       int acc = 0;
       for (int k = 0, u = unit0; u < units && ok; ++k, u += step) {
         const int heads = heads_of(u);
         for (int i = 0; i < heads && ok; ++i, ++acc) {
           const int h = head_of(u, i);
-          const uint32_t d = tmem + (acc & 1) * 256;
-          if (!(ok = wait_cluster(d_empty + (acc & 1), (acc >> 1 & 1) ^ 1, a.err))) break;
+          const uint32_t d = tm + (acc & 1) * 256;
+          if (!(ok = all(wait_cluster(d_empty + (acc & 1), (acc >> 1 & 1) ^ 1, a.err)))) break;
           for (int j = 0, c = h % steps; j < steps; ++j, c = c + 1 == steps ? 0 : c + 1, ring.next(a.stages)) {
             const int s = ring.s;
-            if (i == 0 && !(ok = mbar_wait_inl(a_full + c, k & 1, a.err))) break;
-            if (!(ok = mbar_wait_inl(b_full + s, ring.phase, a.err))) break;
+            if (i == 0 && !(ok = all(mbar_wait_inl(a_full + c, k & 1, a.err)))) break;
+            if (!(ok = all(mbar_wait_inl(b_full + s, ring.phase, a.err)))) break;
             tc_fence_after();
             const uint64_t bd = bd0 + s * (stage_bytes >> 4), ac = ad + c * (32768 >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_pair(d, ac + ((kk / 4 * 16384 + kk % 4 * 32) >> 4), bd + ((kk / 4 * chunk_bytes + kk % 4 * 32) >> 4), id,
-                       j > 0 || kk > 0);
-            commit_pair(b_empty + s);
-            if (i == heads - 1) commit_pair(a_empty + c);
+              mma_pair(leader, d, ac + ((kk / 4 * 16384 + kk % 4 * 32) >> 4), bd + ((kk / 4 * chunk_bytes + kk % 4 * 32) >> 4),
+                       id, j > 0 || kk > 0);
+            if (leader) {
+              commit_pair(b_empty + s);
+              if (i == heads - 1) commit_pair(a_empty + c);
+            }
           }
-          if (ok) commit_pair(d_full + (acc & 1));
+          if (ok && leader) commit_pair(d_full + (acc & 1));
         }
       }
     }
