@@ -168,13 +168,10 @@ template <int N, bool TWO>
 constexpr int soft_warps() {
   return N == 16 || TWO ? 8 : 16;
 }
-template <int KIND, bool TWO>
-constexpr int conv_warps() {
-  return KIND == kE4m3 ? (TWO ? 2 : 4) : 0;
-}
+constexpr int kConvWarps = 4;  // e4m3 only
 template <int KIND, int N, bool TWO>
 constexpr int col_threads() {
-  return 32 * (soft_warps<N, TWO>() + 2 + conv_warps<KIND, TWO>());
+  return 32 * (soft_warps<N, TWO>() + 2 + (KIND == kE4m3 ? kConvWarps : 0));
 }
 
 // Sums of CH values a lane over the warp's lanes: lane c (mod CH) has the sum of
@@ -205,7 +202,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
     columns_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const ColArgs a) {
   using L = ColSmem<KIND, N, TWO>;
   constexpr bool kLat = KIND == kLatent, kFp8 = KIND == kE4m3;
-  constexpr int kThreads = col_threads<KIND, N, TWO>(), kConvWarps = conv_warps<KIND, TWO>();
+  constexpr int kThreads = col_threads<KIND, N, TWO>();
   constexpr int kSoftWarps = soft_warps<N, TWO>(), kProducer = kSoftWarps, kIssuer = kSoftWarps + 1;
   constexpr int HN = N / (kSoftWarps / 4);      // columns of a warpgroup
   constexpr int CH = 8;                         // of them, in registers at a time
@@ -842,45 +839,50 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   cluster_sync();  // nobody leaves while its part may be read
 }
 
-// Columns a CTA (N) and CTAs that share a unit's blocks (parts): the least estimated
-// time over the choices.  A CTA takes about start + blocks * step, both measured
-// (us, head_dim 128 or latent_dim 512, batches of one and of eight sequences):
+// Columns a CTA (N), CTAs that share a unit's blocks (parts), and whether two CTAs
+// share an SM: the least estimated time over the choices.  A CTA takes about
+// start + blocks * step, both measured (us, head_dim 128 or latent_dim 512):
 //              start, step        N = 16       32         64        128
-//   bf16                         7.7, 0.95  9.3, 0.97  11.2, 1.05  17.7, 1.1
-//   e4m3                         8.6, 1.05  10.3, 1.05  14, 1.05   18, 1.6
-//   latent                        11, 3.1    14, 3.1    18, 3.4
+//   bf16                         7.4, 0.5   9, 0.52    11.2, 0.7   15, 1.1
+//   e4m3                         8, 0.95    9.7, 1.05  10.8, 1.4   14, 1.75
+//   latent                       9, 2.0     11, 2.0    14.5, 2.45
 // and no less than the blocks' bytes take from HBM at 6.3 TB/s.  The CTAs run in
 // rounds: 152, 76 clusters of 2, 36 of 4, 15 of 8, 7 of 16 at once (large clusters are
-// not placed as densely as the SMs would allow).  Examples (us, all choices tried):
-//   16 drafts, 64 / 8 heads, 16 blocks: 32 / 4 13.6, 64 / 4 15.6, 128 / 8 19.5, 16 / 1 23.1
-//   32 x 8 drafts, same: 64 / 1 61.9, 32 / 1 100, 16 / 1 160
-//   1 row, 64 heads, latent, 16 blocks: 16 / 16 13.3, 32 / 16 16.2, 64 / 8 23.2, 64 / 1 73
-//   32 rows, same: 64 / 4 35.8, 32 / 2 41.7, 64 / 2 49.3, 16 / 1 63
+// not placed as densely as the SMs would allow).  Two on an SM hide each other's
+// start and end where there would be several rounds (bf16 up to 64 columns: 32 x 8
+// drafts 57.1 -> 52.4; e4m3, whose converters want the SM, 64.3 -> 67.7; the latent's
+// blocks fill the shared memory).  Examples (us, N / parts, all choices tried):
+//   16 drafts, 64 / 8 heads, 16 blocks: 32 / 4 11.1, 64 / 4 13.6, 128 / 8 16.8, 16 / 1 15.9
+//   32 x 8 drafts, same: 64 / 1 57.1, 32 / 1 79.3, 16 / 1 122
+//   1 row, 64 heads, latent, 16 blocks: 16 / 16 10.6, 32 / 16 12.5, 64 / 8 18.7, 64 / 1 53.9
+//   32 rows, same: 64 / 4 31.1, 32 / 2 32.4, 64 / 2 40.6, 16 / 1 45.5
 struct ColShape {
   int n, parts;
   bool two;
+  double us;
 };
 template <int KIND>
 ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
-  static constexpr double kStart[3][4] = {{7.7, 9.3, 11.2, 17.7}, {8.6, 10.3, 14, 18}, {11, 14, 18, 1e9}};
-  static constexpr double kStep[3][4] = {{0.95, 0.97, 1.05, 1.1}, {1.05, 1.05, 1.05, 1.6}, {3.1, 3.1, 3.4, 1e9}};
+  static constexpr double kStart[3][4] = {{7.4, 9, 11.2, 15}, {8, 9.7, 10.8, 14}, {9, 11, 14.5, 1e9}};
+  static constexpr double kStep[3][4] = {{0.5, 0.52, 0.7, 1.1}, {0.95, 1.05, 1.4, 1.75}, {2.0, 2.0, 2.45, 1e9}};
+  static constexpr int kClusters[5] = {152, 76, 36, 15, 7};
   const int blocks = std::min(p->max_nvp, p->topk);
-  ColShape best{16, 1, false};
-  double least = 1e300;
+  ColShape best{16, 1, false, 1e300};
   for (int k = 0; k < (KIND == kLatent ? 3 : 4); ++k) {
-    const int n = 16 << k;
     const int64_t units = p->col_units[k], sets = int64_t(p->n_tiles) * p->hp;
-    for (int parts = 1; parts <= kMaxParts && parts <= blocks; parts *= 2) {
-      static constexpr int kClusters[5] = {0, 76, 36, 15, 7};
-      const int lg = parts == 1 ? 0 : parts == 2 ? 1 : parts == 4 ? 2 : parts == 8 ? 3 : 4;
-      const int64_t room = std::max<int64_t>(1, lg == 0 ? p->num_sms : int64_t(kClusters[lg]) * p->num_sms / 152);
+    const double start = kStart[KIND][k] * (KIND == kLatent ? 0.4 + 0.6 * size : 1.0);
+    auto take = [&](int lg, bool two) {
+      const int parts = 1 << lg;
+      const int64_t room = std::max<int64_t>(1, int64_t(kClusters[lg]) * (two ? 2 : 1) * p->num_sms / 152);
       const int64_t rounds = (units + room - 1) / room;
       const double at_once = static_cast<double>(std::min(units, room) * parts);
       const double hbm = at_once * block_bytes * sets / units / 6.3e6;  // us a block step
-      const double us = rounds * (kStart[KIND][k] * (KIND == kLatent ? 0.4 + 0.6 * size : 1.0) +
-                                  (blocks + parts - 1) / parts * std::max(kStep[KIND][k] * size, hbm));
-      if (us < least) least = us, best = {n, parts, false};
-    }
+      const double step = kStep[KIND][k] * size * (two ? 1.9 : 1.0);
+      const double us = rounds * (start + (two ? 2 : 0) + (blocks + parts - 1) / parts * std::max(step, hbm));
+      if (us < best.us) best = {16 << k, parts, two, us};
+    };
+    for (int lg = 0; (1 << lg) <= kMaxParts && (1 << lg) <= blocks; ++lg) take(lg, false);
+    if (KIND == kBf16 && k < 3) take(0, true);
   }
   return best;
 }
@@ -912,13 +914,13 @@ cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km
 template <int KIND>
 cudaError_t launch_shape(ColShape c, const msa_plan_s* p, const ColArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                          cudaStream_t st) {
-  if constexpr (KIND != kLatent) {
+  if constexpr (KIND == kBf16)
     if (c.two)
       return c.n == 16   ? launch_columns<KIND, 16, true>(p, a, km, vm, 1, st)
              : c.n == 32 ? launch_columns<KIND, 32, true>(p, a, km, vm, 1, st)
                          : launch_columns<KIND, 64, true>(p, a, km, vm, 1, st);
+  if constexpr (KIND != kLatent)
     if (c.n == 128) return launch_columns<KIND, 128, false>(p, a, km, vm, c.parts, st);
-  }
   return c.n == 16   ? launch_columns<KIND, 16, false>(p, a, km, vm, c.parts, st)
          : c.n == 32 ? launch_columns<KIND, 32, false>(p, a, km, vm, c.parts, st)
                      : launch_columns<KIND, 64, false>(p, a, km, vm, c.parts, st);
@@ -969,7 +971,7 @@ msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pa
   a.per_page = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(p->d));
   const int64_t block_bytes = int64_t(256) * p->d * (fp8 ? 1 : 2);
-  const double size = p->d == 128 ? 1.0 : 0.7;
+  const double size = p->d == 128 ? 1.0 : 0.85;
   const cudaError_t e = fp8 ? launch_shape<kE4m3>(column_shape<kE4m3>(p, block_bytes, size), p, a, km, vm, st)
                             : launch_shape<kBf16>(column_shape<kBf16>(p, block_bytes, size), p, a, km, vm, st);
   return cuda_check(e, "msa_tree_attn: launch");
