@@ -97,13 +97,21 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
   if constexpr (C == 32) tmem_st16(taddr + 16, r + 16);
 }
 
-// mma_ss and mma_commit by the lane that has `leader`
+// mma_ss, mma_ts and mma_commit by the lane that has `leader`
 __device__ __forceinline__ void mma_ss_if(bool leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
 __device__ __forceinline__ void mma_commit_if(bool leader, uint64_t* bar) {
@@ -115,7 +123,7 @@ struct ColArgs {
   const TileInfo* tiles;
   const int32_t* idx;
   const int32_t* kv_indices;
-  const uint4* tree_mask;   // nullptr: causal
+  const uint32_t* tree_mask;  // [total_q, 4]; nullptr: causal
   const float* k_scale;
   const float* v_scale;
   __nv_bfloat16* out;       // [total_q, hq, dv]
@@ -130,6 +138,88 @@ struct ColArgs {
   int32_t per_page;         // e4m3: a scale for each (page, KV head)
   float scale_log2;
 };
+
+// the bits of word k of a 128-bit mask that lie below n
+__device__ __forceinline__ uint32_t low_bits(int k, int n) {
+  return n >= 32 * (k + 1) ? 0xFFFFFFFFu : n <= 32 * k ? 0u : (1u << (n - 32 * k)) - 1u;
+}
+
+// A part's blocks, by one warp: padding skipped, what lies behind the tile's last
+// block or on a page outside the pool dropped and reported.  list[]: page | place
+// << 24, the place 0 for a block before the tile's first position, 1 for that
+// position's, 2 for the next; scales[] as a BlockScale has them.  sel: the selection,
+// j0 its first 32.  first(n) is called when those are listed.
+template <bool FP8, class F>
+__device__ __forceinline__ int list_blocks(const ColArgs& a, const TileInfo& tl, const int32_t* sel, int j0, int kvh,
+                                           int part, int parts, uint32_t* list, float2* scales, F first32) {
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int b) { return b == 0 ? j0 : b + lane < a.topk ? sel[b + lane] : -1; };
+  int first = 0, count = a.topk, seen = 0, n = 0;
+  if (parts > 1) {
+    int total = 0;
+    for (int b = 0; b < a.topk; b += 32) {
+      const int j = at(b);
+      total += __popc(__ballot_sync(0xFFFFFFFFu, j >= 0 && j < tl.nvp));
+    }
+    first = total * part / parts;
+    count = total * (part + 1) / parts - first;
+  }
+  const int first_masked = tl.pos0 >> 7;
+  for (int b = 0; b < a.topk; b += 32) {
+    const int j = at(b);
+    const bool valid = j >= 0 && j < tl.nvp;
+    const uint32_t v = __ballot_sync(0xFFFFFFFFu, valid), below = (1u << lane) - 1u;
+    const int rank = seen + __popc(v & below);
+    seen += __popc(v);
+    bool take = valid && rank >= first && rank < first + count, bad = j >= tl.nvp;
+    int64_t page = 0;
+    if (take) {
+      page = a.kv_indices[tl.page_base + j];
+      if (page < 0 || page >= a.num_pages) take = false, bad = true;
+    }
+    if (bad) atomicOr(a.err, kErrDeviceCheck);
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, take);
+    const int o = n + __popc(m & below);
+    if (take) list[o] = static_cast<uint32_t>(page) | static_cast<uint32_t>(max(j - first_masked + 1, 0)) << 24;
+    n += __popc(m);
+    __syncwarp();
+    if (b == 0) first32(n);
+    if (FP8 && take) {
+      const int64_t sat = a.per_page ? page * a.hkv + kvh : kvh;
+      const BlockScale bs = block_scale_of(a.k_scale[sat], a.v_scale[sat]);
+      scales[o] = make_float2(bs.ks * a.scale_log2, bs.log2_vs);
+    }
+  }
+  return n;
+}
+
+// e4m3: one key's codes of a slot (upper half) to its f16 row, zeros for `zero`.  A
+// thread has the codes in registers before it writes that row, the only one that
+// overlaps them (dims 128; at dims 64 none does).
+__device__ __forceinline__ void expand_row(uint8_t* buf, int r, bool dims128, bool zero) {
+  const int sw = r & 7;
+  auto expand = [&](uint4 v, int unit) {  // sixteen codes -> f16 units 2 unit, 2 unit + 1
+    if (zero) v = make_uint4(0u, 0u, 0u, 0u);
+    uint8_t* dst = buf + (unit >> 2) * 16384 + r * 128;
+    const int u0 = (unit & 3) * 2;
+    *reinterpret_cast<uint4*>(dst + ((u0 ^ sw) << 4)) = make_uint4(
+        e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
+    *reinterpret_cast<uint4*>(dst + (((u0 + 1) ^ sw) << 4)) = make_uint4(
+        e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+  };
+  uint4 v[8];
+  if (dims128) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 128 + ((c ^ sw) << 4));
+#pragma unroll
+    for (int c = 0; c < 8; ++c) expand(v[c], c);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+#pragma unroll
+    for (int c = 0; c < 4; ++c) expand(v[c], c);
+  }
+}
 
 template <int KIND, int N, bool TWO>
 struct ColSmem {
@@ -312,50 +402,12 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   const int first_blocks = kLat ? 1 : S / 2;  // loaded before the columns are there
   int started = 0;
   if (warp == kProducer) {
-    // this part's blocks: padding skipped, what lies behind the tile's last block or on a
-    // page outside the pool dropped and reported
-    auto at = [&](int b) { return b == 0 ? j0 : b + lane < a.topk ? sel[b + lane] : -1; };
-    int first = 0, count = a.topk, seen = 0, n = 0;
-    if (a.parts > 1) {
-      int total = 0;
-      for (int b = 0; b < a.topk; b += 32) {
-        const int j = at(b);
-        total += __popc(__ballot_sync(0xFFFFFFFFu, j >= 0 && j < tl.nvp));
-      }
-      first = total * part / a.parts;
-      count = total * (part + 1) / a.parts - first;
-    }
-    const int first_masked = tl.pos0 >> 7;
-    for (int b = 0; b < a.topk; b += 32) {
-      const int j = at(b);
-      const bool valid = j >= 0 && j < tl.nvp;
-      const uint32_t v = __ballot_sync(0xFFFFFFFFu, valid), below = (1u << lane) - 1u;
-      const int rank = seen + __popc(v & below);
-      seen += __popc(v);
-      bool take = valid && rank >= first && rank < first + count, bad = j >= tl.nvp;
-      int64_t page = 0;
-      if (take) {
-        page = a.kv_indices[tl.page_base + j];
-        if (page < 0 || page >= a.num_pages) take = false, bad = true;
-      }
-      if (bad) atomicOr(a.err, kErrDeviceCheck);
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, take);
-      const int o = n + __popc(m & below);
-      if (take) list[o] = static_cast<uint32_t>(page) | static_cast<uint32_t>(max(j - first_masked + 1, 0)) << 24;
-      n += __popc(m);
-      __syncwarp();
-      if (b == 0) {
-        started = min(n, first_blocks);
-        const bool leader = elect_one();
-        for (int i = 0; i < started; ++i)
-          for (int h = 0; h < per + kLat; ++h) produce(i, h, leader);
-      }
-      if (kFp8 && take) {
-        const int64_t sat = a.per_page ? page * a.hkv + kvh : kvh;
-        const BlockScale bs = block_scale_of(a.k_scale[sat], a.v_scale[sat]);
-        scales[o] = make_float2(bs.ks * a.scale_log2, bs.log2_vs);
-      }
-    }
+    const int n = list_blocks<kFp8>(a, tl, sel, j0, kvh, part, a.parts, list, scales, [&](int n) {
+      started = min(n, first_blocks);
+      const bool leader = elect_one();
+      for (int i = 0; i < started; ++i)
+        for (int h = 0; h < per + kLat; ++h) produce(i, h, leader);
+    });
     if (lane == 0) *n_slot = n;
   } else {
     // Q^T's columns, 64 dims a chunk, a warp a column
@@ -399,11 +451,9 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       col_row[c] = static_cast<int64_t>(tl.q_begin + (c0 + c) / G) * a.hq + p * G + (c0 + c) % G;
     for (int e0 = w * 32; e0 < N * 4; e0 += kLoaders * 32) {
       const int e = e0 + lane, c = e % N, wd = e / N, row = (c0 + c) / G;
-      // bits of word wd below n
-      auto low = [&](int n) { return n >= 32 * (wd + 1) ? 0xFFFFFFFFu : n <= 32 * wd ? 0u : (1u << (n - 32 * wd)) - 1u; };
       uint32_t m = 0u;
       if (c < cols)
-        m = a.tree_mask ? reinterpret_cast<const uint32_t*>(a.tree_mask + tl.q_begin + row)[wd] & low(tl.rows) : low(row + 1);
+        m = a.tree_mask ? a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + row) + wd] & low_bits(wd, tl.rows) : low_bits(wd, row + 1);
       // a row of bits a column -> a row a key offset; lane b keeps offset 32 wd + b
       uint32_t mine = 0u;
 #pragma unroll
@@ -732,45 +782,16 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       }
   } else if (kFp8) {
     // ---------------------------------------------------------- converters
-    // A thread has one key's codes in registers before it writes that key's f16
-    // row, the only one that overlaps them (dims 128; at dims 64 none does).
-    const int r0 = threadIdx.x - 32 * (kSoftWarps + 2);
+    const int r = threadIdx.x - 32 * (kSoftWarps + 2);
     bool ok = true;
     for (int u = 0; u < 2 * n; ++u) {
       const int s = slot_of(u);
-      uint8_t* buf = smem + L::kRingOff + s * kSlotBytes;
       const uint32_t entry = list[u >> 1];
-      const bool masked = (u & 1) && entry >> 24 != 0;
+      const bool zero = (u & 1) && entry >> 24 != 0 && !seen_by_any(offset0(entry) + r);
       if (ok) ok = mbar_wait_inl(full + s, phase_of(u), a.err);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-#pragma unroll 1
-      for (int r = r0; r < 128; r += 32 * kConvWarps) {
-        const int sw = r & 7;
-        const bool zero = masked && !seen_by_any(offset0(entry) + r);
-        auto expand = [&](uint4 v, int unit) {  // sixteen codes -> f16 units 2 unit, 2 unit + 1
-          if (zero) v = make_uint4(0u, 0u, 0u, 0u);
-          uint8_t* dst = buf + (unit >> 2) * 16384 + r * 128;
-          const int u0 = (unit & 3) * 2;
-          *reinterpret_cast<uint4*>(dst + ((u0 ^ sw) << 4)) = make_uint4(
-              e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
-          *reinterpret_cast<uint4*>(dst + (((u0 + 1) ^ sw) << 4)) = make_uint4(
-              e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
-        };
-        uint4 v[8];
-        if (a.dv == 128) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 128 + ((c ^ sw) << 4));
-#pragma unroll
-          for (int c = 0; c < 8; ++c) expand(v[c], c);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            v[c] = *reinterpret_cast<const uint4*>(buf + 16384 + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
-#pragma unroll
-          for (int c = 0; c < 4; ++c) expand(v[c], c);
-        }
-      }
+      expand_row(smem + L::kRingOff + s * kSlotBytes, r, a.dv == 128, zero);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(ready + s);
@@ -839,6 +860,401 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   cluster_sync();  // nobody leaves while its part may be read
 }
 
+// Wide trees: the (row, head) pairs as the M rows of the products, 128 to a tile and
+// two tiles a CTA, as the prefill kernel has them,
+//   S [128 pairs x 128 keys] = Q . K^T,   O [128 pairs x dims] += P . V,
+// P in tensor memory where S was.  A thread has a whole row of S: its maximum and
+// sum need no other thread, where the columns' softmax takes a second pass and
+// a vote, and a block step serves 256 pairs in the time that it takes there for
+// 128.  Both tiles share every K and V block, and one tile's softmax overlaps the
+// other's products.
+constexpr int kRowSoftWarps = 8;
+
+template <bool FP8, int D>
+struct RowSmem {
+  static constexpr int kSlots = 4;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kRingOff = 2 * kTileBytes;
+  static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kAnyOff = kBarOff + 8 * 32;   // keys that some pair sees, by offset: 128 bits
+  static constexpr int kRowOff = kAnyOff + 16;       // the pairs as rows of q and out
+  static constexpr int kListOff = kRowOff + 8 * 256;
+  static __host__ __device__ constexpr int bytes(int topk) { return kListOff + ((topk + 3) & ~3) * (FP8 ? 12 : 4); }
+};
+template <bool FP8>
+constexpr int row_threads() {
+  return 32 * (kRowSoftWarps + 2 + (FP8 ? kConvWarps : 0));
+}
+
+template <bool FP8, int D>
+__global__ void __launch_bounds__(row_threads<FP8>(), 1)
+    rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const ColArgs a) {
+  using L = RowSmem<FP8, D>;
+  constexpr int kThreads = row_threads<FP8>(), S = L::kSlots, kProducer = kRowSoftWarps, kIssuer = kRowSoftWarps + 1;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // [S]
+  uint64_t* empty = full + S;               // [S]
+  uint64_t* ready = FP8 ? empty + S : full;  // [S]
+  uint64_t* s_full = empty + 2 * S;         // [2 tiles]
+  uint64_t* p_full = s_full + 2;            // [2]
+  uint64_t* o_done = p_full + 2;            // [2] the last P.V
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+  int32_t* n_slot = reinterpret_cast<int32_t*>(tmem_slot + 1);
+  uint32_t* any = reinterpret_cast<uint32_t*>(smem + L::kAnyOff);
+  int64_t* row_at = reinterpret_cast<int64_t*>(smem + L::kRowOff);
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);
+  float2* scales = reinterpret_cast<float2*>(list + ((a.topk + 3) & ~3));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = blockIdx.x % a.max_groups, p = blockIdx.x / a.max_groups % a.hp, t = blockIdx.x / a.max_groups / a.hp;
+  const int G = a.hq / a.hp, kvh = p / (a.hp / a.hkv);
+  if (warp == kProducer) {
+    if (lane == 0) {
+      prefetch_tmap(&k_map);
+      prefetch_tmap(&v_map);
+      for (int s = 0; s < S; ++s) {
+        mbar_init(full + s, 1);
+        mbar_init(empty + s, 1);
+        if (FP8) mbar_init(ready + s, kConvWarps);
+      }
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(s_full + h, 1);
+        mbar_init(p_full + h, 4);
+        mbar_init(o_done + h, 1);
+      }
+      fence_mbar_init();
+    }
+    if (lane < 4) any[lane] = 0u;
+  } else if (warp == kIssuer) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  const TileInfo tl = a.tiles[t];
+  const int32_t* sel = a.idx + (static_cast<int64_t>(t) * a.hp + p) * a.topk;
+  const int j0 = warp == kProducer && lane < a.topk ? sel[lane] : -1;
+  const int c0 = group * 256, pairs = min(256, tl.rows * G - c0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (pairs <= 0) {  // a tile of fewer rows than the batch's most
+    if (warp == kIssuer) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int tiles = pairs > 128 ? 2 : 1;
+  auto slot_of = [&](int u) { return u % S; };
+  auto phase_of = [&](int u) { return static_cast<uint32_t>(u / S & 1); };
+  auto produce = [&](int u, bool leader) {  // K (u even) or V of block u / 2
+    const int s = slot_of(u);
+    const int row = __shfl_sync(
+        0xFFFFFFFFu, static_cast<int>((static_cast<int64_t>(list[u >> 1] & 0xFFFFFFu) * a.hkv + kvh) * 128), 0);
+    if (u >= S && !__all_sync(0xFFFFFFFFu, mbar_wait_inl(empty + s, phase_of(u) ^ 1, a.err))) return false;
+    uint8_t* dst = smem + L::kRingOff + s * kSlotBytes;
+    const CUtensorMap* map = u & 1 ? &v_map : &k_map;
+    if (leader) {
+      mbar_expect_tx(full + s, 128 * D * (FP8 ? 1 : 2));
+      if (FP8)
+        tma_load_2d(dst + 16384, map, full + s, 0, row);
+      else
+        tma_load_3d(dst, map, full + s, 0, row, 0);
+    }
+    return true;
+  };
+  int started = 0;
+  if (warp == kProducer) {
+    const int n = list_blocks<FP8>(a, tl, sel, j0, kvh, 0, 1, list, scales, [&](int n) {
+      started = min(2 * n, S);
+      const bool leader = elect_one();
+      for (int u = 0; u < started; ++u) produce(u, leader);
+    });
+    if (lane == 0) *n_slot = n;
+  } else {
+    const int w = warp < kProducer ? warp : warp - 1;
+    constexpr int kLoaders = kThreads / 32 - 1, kUnits = D / 8;
+    for (int e = w * 32 + lane; e < 256; e += kLoaders * 32) {
+      const int row = (c0 + e) / G;
+      row_at[e] = static_cast<int64_t>(tl.q_begin + row) * a.hq + p * G + (c0 + e) % G;
+      if (e < pairs) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + row) + k] & low_bits(k, tl.rows);
+          if (x & ~any[k]) atomicOr(any + k, x);
+        }
+      }
+    }
+#pragma unroll 4
+    for (int e = w * 32 + lane; e < 256 * kUnits; e += kLoaders * 32) {
+      const int c = e / kUnits, u = e % kUnits;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (c < pairs)
+        v = *reinterpret_cast<const uint4*>(
+            a.q + (static_cast<int64_t>(tl.q_begin + (c0 + c) / G) * a.hq + p * G + (c0 + c) % G) * D + u * 8);
+      if (FP8)
+        v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+      *reinterpret_cast<uint4*>(smem + (c >> 7) * L::kTileBytes + (u >> 3) * 16384 + (c & 127) * 128 +
+                                (((u & 7) ^ (c & 7)) << 4)) = v;
+    }
+  }
+  fence_async_shared();
+  __syncthreads();
+  const int n = *n_slot;
+  auto offset0 = [&](uint32_t entry) { return (static_cast<int>(entry >> 24) - 1) * 128 - (tl.pos0 & 127); };
+  auto seen_by_any = [&](int e) { return e < 0 || (e < 128 && (any[e >> 5] >> (e & 31) & 1u)); };
+
+  if (warp == kProducer) {
+    const bool leader = elect_one();
+    for (int u = started; u < 2 * n; ++u)
+      if (!produce(u, leader)) break;
+  } else if (warp == kIssuer) {
+    // ----------------------------------------------------------------- MMA
+    // QK0 QK1 | PV0 QK0' PV1 QK1' | ...: one tile's softmax overlaps the other's products
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const int nn = __shfl_sync(0xFFFFFFFFu, n, 0);
+    const bool leader = elect_one();
+    auto waited = [&](uint64_t* bar, uint32_t parity) {
+      return static_cast<bool>(__all_sync(0xFFFFFFFFu, mbar_wait_inl(bar, parity, a.err)));
+    };
+    constexpr uint32_t id_qk = FP8 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t id_pv = FP8 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
+    const uint64_t qd0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128);
+    const uint64_t kd0 = smem_desc(smem_u32(smem + L::kRingOff), 16, 1024, kSwizzle128);
+    const uint64_t vd0 = smem_desc(smem_u32(smem + L::kRingOff), 16384, 1024, kSwizzle128);
+    auto qk = [&](int h, int s) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+        mma_ss_if(leader, tm + h * 128, qd0 + h * (L::kTileBytes >> 4) + off, kd0 + s * (kSlotBytes >> 4) + off, id_qk, kk > 0);
+      }
+      mma_commit_if(leader, s_full + h);
+    };
+    bool ok = nn == 0 || waited(ready, 0);
+    tc_fence_after();
+    if (ok && nn > 0) {
+      qk(0, 0);
+      if (tiles == 2) qk(1, 0);
+      mma_commit_if(leader, empty);
+    }
+    for (int i = 0; i < nn && ok; ++i) {
+      const int uv = 2 * i + 1, sv = slot_of(uv), sk = slot_of(uv + 1);
+      if (!(ok = waited(ready + sv, phase_of(uv)))) break;
+      for (int h = 0; h < tiles && ok; ++h) {
+        if (!(ok = waited(p_full + h, i & 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_if(leader, tm + 256 + h * D, tm + h * 128 + kk * 8, vd0 + sv * (kSlotBytes >> 4) + ((kk * 2048) >> 4), id_pv,
+                    i > 0 || kk > 0);
+        if (h == tiles - 1) mma_commit_if(leader, empty + sv);
+        if (i + 1 < nn) {
+          if (h == 0) {
+            if (!(ok = waited(ready + sk, phase_of(uv + 1)))) break;
+            tc_fence_after();
+          }
+          qk(h, sk);
+          if (h == tiles - 1) mma_commit_if(leader, empty + sk);
+        } else {
+          mma_commit_if(leader, o_done + h);
+        }
+      }
+    }
+  } else if (warp < kRowSoftWarps) {
+    // ------------------------------------------------------------- softmax
+    const int h = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + h * 128, o_addr = tmem + lane_base + 256 + h * D;
+    const bool there = h * 128 + r < pairs;
+    uint32_t mask[4] = {0u, 0u, 0u, 0u};
+    if (there) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mask[k] = a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + (c0 + h * 128 + r) / G) + k] & low_bits(k, tl.rows);
+    }
+    // bits e .. e + 31 of: ones below 0, the mask, zeros from 128 on
+    auto seen = [&](int e) {
+      const int k = e >> 5;
+      auto word = [&](int i) { return i < 0 ? 0xFFFFFFFFu : i == 0 ? mask[0] : i == 1 ? mask[1] : i == 2 ? mask[2] : i == 3 ? mask[3] : 0u; };
+      return __funnelshift_r(word(k), word(k + 1), e & 31);
+    };
+    float m = -INFINITY, l = 0.f;
+    bool ok = h < tiles;
+    const int blocks = ok ? n : 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = mbar_wait_inl(bar, parity, a.err);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    };
+    for (int i = 0; i < blocks; ++i) {
+      const uint32_t entry = list[i];
+      float sl2 = a.scale_log2, log2_vs = 0.f, inv_vs = 1.f;
+      if (FP8) {
+        const float2 sc = scales[i];
+        sl2 = sc.x, log2_vs = sc.y, inv_vs = ex2_approx(-sc.y);
+      }
+      const bool masked = entry >> 24 != 0;
+      const int e0 = offset0(entry);
+      wait(s_full + h, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[32];
+      auto load = [&](int c) {
+        tmem_ld32(s_addr + 32 * c, s);
+        tmem_wait_ld();
+        if (masked) {
+          const uint32_t v = seen(e0 + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!(v >> k & 1u)) s[k] = __float_as_uint(-INFINITY);
+        }
+      };
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        load(c);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          mx0 = fmax3(mx0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+          mx1 = fmax3(mx1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+        }
+      }
+      const float mx = fmaxf(mx0, mx1), mx2 = FP8 ? fmaf(mx, sl2, log2_vs) : mx * sl2;
+      const float m_new = mx2 > m + 8.f ? mx2 : m;
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = m_new == m ? 1.f : ex2_approx(m - m_use);
+      const float shift = log2_vs - m_use;
+      float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        load(c);
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]), sl2, shift);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          if (k & 1)
+            fadd2(sum2, sum3, p0, p1);
+          else
+            fadd2(sum0, sum1, p0, p1);
+          w[k] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+        }
+        tmem_st16(s_addr + 16 * c, w);  // over chunks of S that are read
+      }
+      const float sum = (sum0 + sum1) + (sum2 + sum3);
+      l = l * alpha + (FP8 ? sum * inv_vs : sum);
+      // P.V of the block before is complete: this block's S was issued after it
+      if (i > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tmem_st16(o_addr + 32 * c, o);
+          tmem_st16(o_addr + 32 * c + 16, o + 16);
+        }
+      }
+      m = m_new;
+      if (!FP8 && masked && h == 0) {  // V rows that no pair sees (e4m3: the converters)
+        wait(full + slot_of(2 * i + 1), phase_of(2 * i + 1));
+        if (!seen_by_any(e0 + r)) {
+          uint8_t* v = smem + L::kRingOff + slot_of(2 * i + 1) * kSlotBytes + r * 128;
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+              *reinterpret_cast<uint4*>(v + c * 16384 + ((b ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_async_shared();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + h);
+    }
+
+    // ------------------------------------------------------------ epilogue
+    if (h < tiles) {
+      if (n > 0) wait(o_done + h, 0);
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (there && ok && a.lse != nullptr)
+        a.lse[row_at[h * 128 + r]] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      const int quad = lane >> 2, j = lane & 3;
+#pragma unroll
+      for (int half16 = 0; half16 < 2; ++half16) {
+        float iv[2];
+        __nv_bfloat16* dst[2];
+        bool mine[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int rr = half16 * 16 + 8 * q + quad, pair = h * 128 + quarter * 32 + rr;
+          iv[q] = __shfl_sync(0xFFFFFFFFu, inv, rr);
+          mine[q] = pair < pairs && ok;
+          dst[q] = a.out + row_at[pair] * D + 8 * j;
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[16], w[4];
+          if (n > 0) {
+            tmem_ld_16x256<4>(o_addr + c + (static_cast<uint32_t>(half16 * 16) << 16), v);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = 0u;
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              w[g] = pack_bf16x2(__uint_as_float(v[4 * g + 2 * q]) * iv[q], __uint_as_float(v[4 * g + 2 * q + 1]) * iv[q]);
+            transpose4(w, j);
+            if (mine[q]) *reinterpret_cast<uint4*>(dst[q] + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  } else if (FP8) {
+    // ---------------------------------------------------------- converters
+    const int r = threadIdx.x - 32 * (kRowSoftWarps + 2);
+    bool ok = true;
+    for (int u = 0; u < 2 * n; ++u) {
+      const int s = slot_of(u);
+      const uint32_t entry = list[u >> 1];
+      const bool zero = (u & 1) && entry >> 24 != 0 && !seen_by_any(offset0(entry) + r);
+      if (ok) ok = mbar_wait_inl(full + s, phase_of(u), a.err);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      expand_row(smem + L::kRingOff + s * kSlotBytes, r, D == 128, zero);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready + s);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, 512);
+}
+
+template <bool FP8, int D>
+cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  using L = RowSmem<FP8, D>;
+  a.max_groups = (p->max_tile_rows * (p->hq / p->hp) + 255) / 256;
+  const int64_t ctas = int64_t(p->n_tiles) * p->hp * a.max_groups;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  auto kern = rows_kernel<FP8, D>;
+  static_assert(L::bytes(1024) + 1024 <= 232448, "shared memory at the largest topk");
+  static std::atomic<uint64_t> devices{0};
+  const uint64_t bit = p->device < 64 ? uint64_t(1) << p->device : 0;
+  if ((devices.load(std::memory_order_acquire) & bit) == 0) {
+    if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(1024) + 1024))
+      return e;
+    devices.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(row_threads<FP8>()), L::bytes(p->topk) + 1024, st, km, vm, a);
+}
+
 // Columns a CTA (N), CTAs that share a unit's blocks (parts), and whether two CTAs
 // share an SM: the least estimated time over the choices.  A CTA takes about
 // start + blocks * step, both measured (us, head_dim 128 or latent_dim 512):
@@ -887,6 +1303,14 @@ ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
   return best;
 }
 
+// The same estimate for the pairs as rows: 256 a CTA, no parts.
+double rows_us(const msa_plan_s* p, bool fp8, int64_t block_bytes, double size) {
+  const int64_t units = p->col_units[4], rounds = (units + p->num_sms - 1) / p->num_sms;
+  const double at_once = static_cast<double>(std::min<int64_t>(units, p->num_sms));
+  const double hbm = at_once * block_bytes * p->n_tiles * p->hp / units / 6.3e6;
+  return rounds * (12 + std::min(p->max_nvp, p->topk) * std::max((fp8 ? 1.8 : 1.7) * size, hbm));
+}
+
 template <int KIND, int N, bool TWO>
 cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, const CUtensorMap& vm, int parts,
                            cudaStream_t st) {
@@ -933,7 +1357,7 @@ void column_plan_counts(msa_plan_s* p) {
   for (const TileInfo& t : p->tiles) {
     p->max_tile_rows = std::max(p->max_tile_rows, t.rows);
     p->max_nvp = std::max(p->max_nvp, t.nvp);
-    for (int k = 0; k < 4; ++k) p->col_units[k] += int64_t(p->hp) * ((int64_t(t.rows) * G + (16 << k) - 1) >> (4 + k));
+    for (int k = 0; k < 5; ++k) p->col_units[k] += int64_t(p->hp) * ((int64_t(t.rows) * G + (16 << k) - 1) >> (4 + k));
   }
 }
 
@@ -956,7 +1380,7 @@ msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pa
   a.tiles = p->tiles_d;
   a.idx = idx;
   a.kv_indices = kv_indices;
-  a.tree_mask = reinterpret_cast<const uint4*>(tree_mask);
+  a.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.out = static_cast<__nv_bfloat16*>(out);
@@ -972,8 +1396,12 @@ msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pa
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(p->d));
   const int64_t block_bytes = int64_t(256) * p->d * (fp8 ? 1 : 2);
   const double size = p->d == 128 ? 1.0 : 0.85;
-  const cudaError_t e = fp8 ? launch_shape<kE4m3>(column_shape<kE4m3>(p, block_bytes, size), p, a, km, vm, st)
-                            : launch_shape<kBf16>(column_shape<kBf16>(p, block_bytes, size), p, a, km, vm, st);
+  const ColShape shape = fp8 ? column_shape<kE4m3>(p, block_bytes, size) : column_shape<kBf16>(p, block_bytes, size);
+  const cudaError_t e = rows_us(p, fp8, block_bytes, size) < shape.us
+                            ? (fp8 ? (p->d == 128 ? launch_rows<true, 128>(p, a, km, vm, st) : launch_rows<true, 64>(p, a, km, vm, st))
+                                   : (p->d == 128 ? launch_rows<false, 128>(p, a, km, vm, st) : launch_rows<false, 64>(p, a, km, vm, st)))
+                        : fp8 ? launch_shape<kE4m3>(shape, p, a, km, vm, st)
+                              : launch_shape<kBf16>(shape, p, a, km, vm, st);
   return cuda_check(e, "msa_tree_attn: launch");
 }
 
@@ -996,7 +1424,7 @@ msa_status launch_latent_attn(const msa_plan_s* p, const void* q, const void* la
   a.tiles = p->tiles_d;
   a.idx = idx;
   a.kv_indices = kv_indices;
-  a.tree_mask = reinterpret_cast<const uint4*>(tree_mask);
+  a.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.err = p->err_d;

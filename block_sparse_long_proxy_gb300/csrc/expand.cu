@@ -76,37 +76,6 @@ __device__ __forceinline__ void mma_pair(bool leader, uint32_t d, uint64_t a, ui
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
-// 16 lanes of tensor memory x 8 N columns: lane t has rows t / 4 and t / 4 + 8, and
-// of each eight columns 2 (t % 4) and the next.
-template <int N>
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t* r) {
-  if constexpr (N == 4)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-  else
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-// Lane j of four gets w[j] of all four, in their order.
-__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int j) {
-#pragma unroll
-  for (int d = 1; d < 4; d <<= 1)
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if ((k & d) == 0) {
-        const bool up = j & d;
-        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[k] : w[k | d], d);
-        if (up)
-          w[k] = got;
-        else
-          w[k | d] = got;
-      }
-}
 // A load into this CTA's shared memory that counts on CTA 0's barrier, at the same
 // place as `bar`: its thread, which issues for both, waits for the bytes of both.
 // (A thread of CTA 1 that passed on what its own barrier said took 1100 clocks a

@@ -108,7 +108,7 @@ struct msa_plan_s {
   int64_t append_units_off = 0;      // cache appends: one unit per page that gets rows
   int32_t n_append_units = 0;
   int32_t max_tile_rows = 1, max_nvp = 1;  // of any tile
-  int64_t col_units[4] = {};         // attention of few rows: units of 16, 32, 64 and 128 columns
+  int64_t col_units[5] = {};         // attention of few rows: units of 16, 32, 64, 128 and 256 (row, head) pairs
   int64_t entry_keys_off = 0;        // latent expansion: keys of each page-table entry's page
   void* bwd_d = nullptr;             // backward scratch (D, proxy LSE, inverse index)
 };

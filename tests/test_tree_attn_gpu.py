@@ -121,6 +121,50 @@ def test_trees(cuda_dev, shape, d, kind):
     c.check(out, lse, c.ref())
 
 
+WIDE = {  # batches whose (row, head) pairs fill the rows of the products (test_tree_latent_host.py)
+    "ragged": ([64, 100, 37, 128, 5, 128, 90, 128, 128, 65, 128, 33, 128, 128, 128, 128],
+               [700, 100, 300, 1000, 900, 128, 219, 1281, 640, 65, 777, 1290, 128 * 9 + 3, 500, 256, 131], 32, 4, 4, 5),
+    "odd heads, two selections": ([128] * 14, [300 + 97 * i for i in range(14)], 48, 4, 8, 7),
+}
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e4m3_block"])
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("shape", WIDE, ids=lambda s: s.replace(" ", "_"))
+def test_wide_trees(cuda_dev, shape, d, kind):
+    qo, kv, hq, hkv, hp, topk = WIDE[shape]
+    for grow in (0.0, 0.4):
+        c = Case(cuda_dev, qo, kv, hq, hkv, hp, d, topk, kind, seed=len(shape), grow=grow)
+        if grow:
+            c.idx_h.sort(-1)
+            c.idx = torch.from_numpy(c.idx_h).to(cuda_dev)
+        plan = c.plan()
+        out, lse = c.run(plan)
+        plan.check_errors()
+        c.check(out, lse, c.ref())
+
+
+def test_wide_trees_bad_pages(cuda_dev):
+    """As test_bad_pages_are_skipped_and_reported, over batches of wide trees."""
+    qo, kv, hq, hkv, hp, topk = WIDE["ragged"]
+    c = Case(cuda_dev, qo, kv, hq, hkv, hp, 128, topk, "bf16", seed=2, irregular=False)
+    table = c.table.cpu().numpy().copy()
+    bad = np.random.default_rng(5).random(table.size) < 0.2
+    ids = np.where(bad, -3, table).astype(np.int32)
+    named, base = c.idx_h.copy(), np.concatenate([[0], np.cumsum([(k + 127) // 128 for k in kv])])
+    for t in range(len(qo)):
+        sel = named[t]
+        sel[(sel >= 0) & bad[base[t] + np.maximum(sel, 0)]] = -1
+    plan, good = c.plan(), c.table
+    c.table = torch.from_numpy(ids).to(cuda_dev)
+    out, lse = c.run(plan)
+    with pytest.raises(_msa().MsaError) as e:
+        plan.check_errors()
+    assert e.value.status == 6
+    c.table = good
+    c.check(out, lse, c.ref(idx=named))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "e4m3_block"])
 @pytest.mark.parametrize("rows", [1, 3, 8, 40])
 def test_maxima_that_keep_moving(cuda_dev, rows, kind):

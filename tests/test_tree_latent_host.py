@@ -117,3 +117,24 @@ for func, kind, size in events():
         assert size <= limit[func] <= 232448, (size, limit[func])
 assert len(limit) >= 3, len(limit)
 """)
+
+
+def test_wide_trees_take_the_rows(child):  # noqa: F811
+    """The batches of wide trees that the GPU tests run go through another kernel than
+    narrow ones, and the largest among them too."""
+    import json
+    from tests.test_tree_attn_gpu import SHAPES, WIDE
+    child(CALLS + "import json\nSHAPES, WIDE = (json.loads(x) for x in %r)" % ([json.dumps(list(x.values())) for x in (SHAPES, WIDE)],) + """
+def kernel(qo, kv, hq, hkv, hp, topk, d, kind):
+    n, h = len(qo), P()
+    assert lib.msa_plan((I * n)(*qo), (I * n)(*kv), n, hq, hkv, hp, d, 64, 128, topk, 4096, kind, 0, None, C.byref(h)) == 0
+    before = len(events())
+    assert tree(h, kind) == 0
+    lib.msa_plan_destroy(h)
+    return [f for f, k, _ in events()[before:] if k == 1]
+for d in (64, 128):
+    for kind in (BF16, E4M3, BLOCK):
+        narrow = {f for s in SHAPES for f in kernel(*s, d, kind)}
+        wide = {f for s in WIDE for f in kernel(*s, d, kind)}
+        assert len(wide) == 1 and not wide & narrow, (d, kind, wide, narrow)
+""")
