@@ -436,9 +436,11 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
               make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z), bf16x2_to_f16x2(v[k].w));
       }
     } else {
-      for (int c = w; c < N; c += kLoaders) {
-        const __nv_bfloat16* src = a.q;
-        if (c < cols) src += (static_cast<int64_t>(tl.q_begin + (c0 + c) / G) * a.hq + p * G + (c0 + c) % G) * a.dq;
+      const int cl = c0 + w + lane * kLoaders;  // a lane finds one column's row (a division by G)
+      const int64_t at_l = static_cast<int64_t>(tl.q_begin + cl / G) * a.hq + p * G + cl % G;
+      for (int c = w, k = 0; c < N; c += kLoaders, ++k) {
+        const int64_t row = __shfl_sync(0xFFFFFFFFu, at_l, k);
+        const __nv_bfloat16* src = c < cols ? a.q + row * a.dq : a.q;
         for (int u = lane; u < units; u += 32) {
           const bool there = c < cols && u * 8 < a.dq;
           copy16_async(qs + (u >> 3) * L::kQChunk + c * 128 + (((u & 7) ^ (c & 7)) << 4), there ? src + u * 8 : a.q, there);
@@ -984,17 +986,30 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
         }
       }
     }
-#pragma unroll 4
-    for (int e = w * 32 + lane; e < 256 * kUnits; e += kLoaders * 32) {
-      const int c = e / kUnits, u = e % kUnits;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (c < pairs)
-        v = *reinterpret_cast<const uint4*>(
-            a.q + (static_cast<int64_t>(tl.q_begin + (c0 + c) / G) * a.hq + p * G + (c0 + c) % G) * D + u * 8);
-      if (FP8)
-        v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
-      *reinterpret_cast<uint4*>(smem + (c >> 7) * L::kTileBytes + (u >> 3) * 16384 + (c & 127) * 128 +
-                                (((u & 7) ^ (c & 7)) << 4)) = v;
+    if (w < 8) {  // Q, 32 pairs a warp: a lane finds one pair's row (a division by G), all load it
+      const int c1 = c0 + 32 * w + lane;
+      const int64_t row = static_cast<int64_t>(tl.q_begin + c1 / G) * a.hq + p * G + c1 % G;
+      constexpr int kAtOnce = 32 / kUnits, kIters = 32 / kAtOnce;  // pairs a pass, passes
+      const int u = lane % kUnits;
+      uint8_t* dst = smem + (w >> 2) * L::kTileBytes + (u >> 3) * 16384;
+      uint4 v[8];
+#pragma unroll
+      for (int k0 = 0; k0 < kIters; k0 += 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int j = (k0 + k) * kAtOnce + lane / kUnits;
+          const int64_t from = __shfl_sync(0xFFFFFFFFu, row, j);
+          v[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (32 * w + j < pairs) v[k] = *reinterpret_cast<const uint4*>(a.q + from * D + u * 8);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int c = 32 * (w & 3) + (k0 + k) * kAtOnce + lane / kUnits;
+          if (FP8)
+            v[k] = make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z), bf16x2_to_f16x2(v[k].w));
+          *reinterpret_cast<uint4*>(dst + c * 128 + (((u & 7) ^ (c & 7)) << 4)) = v[k];
+        }
+      }
     }
   }
   fence_async_shared();
