@@ -367,9 +367,19 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   auto phase_of = [&](int u) { return static_cast<uint32_t>(u / S & 1); };
   // load h of block i: a slot, or (latent, h == per) the rotated part; by the whole
   // producer warp, `leader` issuing
+  auto row_of = [&](int i) {
+    return __shfl_sync(0xFFFFFFFFu, static_cast<int>((static_cast<int64_t>(list[i] & 0xFFFFFFu) * a.hkv + kvh) * 128), 0);
+  };
+  // the latent's next block on its way to L2: its slots are free only once this block's P.V is done
+  auto prefetch = [&](int i, bool leader) {
+    const int row = row_of(i);
+    if (leader) {
+      for (int h = 0; h < a.mt; ++h) tma_prefetch_3d(&v_map, 0, row, 2 * h);
+      tma_prefetch_2d(&k_map, 128 * a.mt, row);
+    }
+  };
   auto produce = [&](int i, int h, bool leader) {
-    const int row = __shfl_sync(
-        0xFFFFFFFFu, static_cast<int>((static_cast<int64_t>(list[i] & 0xFFFFFFu) * a.hkv + kvh) * 128), 0);
+    const int row = row_of(i);
     auto waited = [&](uint64_t* bar, uint32_t parity) {
       return static_cast<bool>(__all_sync(0xFFFFFFFFu, mbar_wait_inl(bar, parity, a.err)));
     };
@@ -407,6 +417,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       const bool leader = elect_one();
       for (int i = 0; i < started; ++i)
         for (int h = 0; h < per + kLat; ++h) produce(i, h, leader);
+      if (kLat && n > started) prefetch(started, leader);
     });
     if (lane == 0) *n_slot = n;
   } else {
@@ -488,8 +499,10 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
     // ------------------------------------------------------------ producer
     const bool leader = elect_one();
     bool ok = true;
-    for (int i = started; i < n && ok; ++i)
+    for (int i = started; i < n && ok; ++i) {
+      if (kLat && i + 1 < n) prefetch(i + 1, leader);
       for (int h = 0; h < per + kLat && ok; ++h) ok = produce(i, h, leader);
+    }
   } else if (warp == kIssuer) {
     // ----------------------------------------------------------------- MMA
     // The whole warp goes through the loop, one elected lane issuing: descriptors
