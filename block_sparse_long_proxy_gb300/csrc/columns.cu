@@ -61,16 +61,16 @@ __device__ __forceinline__ float redux_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
-// Named barrier `id` over 128 threads that also returns the OR of p over them.
-__device__ __forceinline__ bool bar_sync_or(int id, bool p) {
+// Named barrier `id` over n threads that also returns the OR of p over them.
+__device__ __forceinline__ bool bar_sync_or(int id, bool p, int n) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred a, b;\n\t"
       "setp.ne.u32 a, %1, 0;\n\t"
-      "bar.red.or.pred b, %2, 128, a;\n\t"
+      "bar.red.or.pred b, %2, %3, a;\n\t"
       "selp.u32 %0, 1, 0, b;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(p)), "r"(id)
+      : "r"(static_cast<uint32_t>(p)), "r"(id), "r"(n)
       : "memory");
   return r != 0;
 }
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
           far = fmax3(fmax3(far, x0, x1), x2, x3);
         }
       }
-      const bool grown = bar_sync_or(1 + wg, far > 8.f);
+      const bool grown = bar_sync_or(1 + wg, far > 8.f, 128);
       if (grown) {
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
@@ -878,12 +878,13 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
 // Wide trees: the (row, head) pairs as the M rows of the products, 128 to a tile and
 // two tiles a CTA, as the prefill kernel has them,
 //   S [128 pairs x 128 keys] = Q . K^T,   O [128 pairs x dims] += P . V,
-// P in tensor memory where S was.  A thread has a whole row of S: its maximum and
-// sum need no other thread, where the columns' softmax takes a second pass and
-// a vote, and a block step serves 256 pairs in the time that it takes there for
-// 128.  Both tiles share every K and V block, and one tile's softmax overlaps the
-// other's products.
-constexpr int kRowSoftWarps = 8;
+// P in tensor memory where S was.  A thread has half a row of S, 64 keys, and its
+// half of the sum until the end; the row's reference moves, as a column's does, only
+// when some logit outgrows it by 2^8, which the tile's eight warps vote on, and
+// only then do the halves exchange their maxima.  A block step serves 256 pairs.
+// Both tiles share every K and V block, and one tile's softmax overlaps the other's
+// products.
+constexpr int kRowSoftWarps = 16;
 
 template <bool FP8, int D>
 struct RowSmem {
@@ -893,7 +894,8 @@ struct RowSmem {
   static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kAnyOff = kBarOff + 8 * 32;   // keys that some pair sees, by offset: 128 bits
   static constexpr int kRowOff = kAnyOff + 16;       // the pairs as rows of q and out
-  static constexpr int kListOff = kRowOff + 8 * 256;
+  static constexpr int kHalfOff = kRowOff + 8 * 256; // [tile][half][128] the halves' maxima, then sums
+  static constexpr int kListOff = kHalfOff + 4 * 512;
   static __host__ __device__ constexpr int bytes(int topk) { return kListOff + ((topk + 3) & ~3) * (FP8 ? 12 : 4); }
 };
 template <bool FP8>
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
       }
       for (int h = 0; h < 2; ++h) {
         mbar_init(s_full + h, 1);
-        mbar_init(p_full + h, 4);
+        mbar_init(p_full + h, 8);
         mbar_init(o_done + h, 1);
       }
       fence_mbar_init();
@@ -988,40 +990,41 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
   } else {
     const int w = warp < kProducer ? warp : warp - 1;
     constexpr int kLoaders = kThreads / 32 - 1, kUnits = D / 8;
+    if (w < 16) {  // Q, 16 pairs a warp: a lane finds one pair's row (a division by G), all load it
+      const int c1 = c0 + 16 * w + (lane & 15);
+      const int64_t row = static_cast<int64_t>(tl.q_begin + c1 / G) * a.hq + p * G + c1 % G;
+      constexpr int kAtOnce = 32 / kUnits, kIters = 16 / kAtOnce;  // pairs a pass, passes
+      const int u = lane % kUnits;
+      uint8_t* dst = smem + (w >> 3) * L::kTileBytes + (u >> 3) * 16384;
+      uint4 v[kIters];
+#pragma unroll
+      for (int k = 0; k < kIters; ++k) {
+        const int j = k * kAtOnce + lane / kUnits;
+        const int64_t from = __shfl_sync(0xFFFFFFFFu, row, j);
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (16 * w + j < pairs) v[k] = *reinterpret_cast<const uint4*>(a.q + from * D + u * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < kIters; ++k) {
+        const int c = 16 * (w & 7) + k * kAtOnce + lane / kUnits;
+        if (FP8)
+          v[k] = make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z), bf16x2_to_f16x2(v[k].w));
+        *reinterpret_cast<uint4*>(dst + c * 128 + (((u & 7) ^ (c & 7)) << 4)) = v[k];
+      }
+    }
     for (int e = w * 32 + lane; e < 256; e += kLoaders * 32) {
       const int row = (c0 + e) / G;
       row_at[e] = static_cast<int64_t>(tl.q_begin + row) * a.hq + p * G + (c0 + e) % G;
+      uint32_t x[4] = {0u, 0u, 0u, 0u};
       if (e < pairs) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t x = a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + row) + k] & low_bits(k, tl.rows);
-          if (x & ~any[k]) atomicOr(any + k, x);
-        }
+        for (int k = 0; k < 4; ++k)
+          x[k] = a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + row) + k] & low_bits(k, tl.rows);
       }
-    }
-    if (w < 8) {  // Q, 32 pairs a warp: a lane finds one pair's row (a division by G), all load it
-      const int c1 = c0 + 32 * w + lane;
-      const int64_t row = static_cast<int64_t>(tl.q_begin + c1 / G) * a.hq + p * G + c1 % G;
-      constexpr int kAtOnce = 32 / kUnits, kIters = 32 / kAtOnce;  // pairs a pass, passes
-      const int u = lane % kUnits;
-      uint8_t* dst = smem + (w >> 2) * L::kTileBytes + (u >> 3) * 16384;
-      uint4 v[8];
 #pragma unroll
-      for (int k0 = 0; k0 < kIters; k0 += 8) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = (k0 + k) * kAtOnce + lane / kUnits;
-          const int64_t from = __shfl_sync(0xFFFFFFFFu, row, j);
-          v[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (32 * w + j < pairs) v[k] = *reinterpret_cast<const uint4*>(a.q + from * D + u * 8);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int c = 32 * (w & 3) + (k0 + k) * kAtOnce + lane / kUnits;
-          if (FP8)
-            v[k] = make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z), bf16x2_to_f16x2(v[k].w));
-          *reinterpret_cast<uint4*>(dst + c * 128 + (((u & 7) ^ (c & 7)) << 4)) = v[k];
-        }
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t all = __reduce_or_sync(0xFFFFFFFFu, x[k]);
+        if (lane == 0 && all != 0u) atomicOr(any + k, all);
       }
     }
   }
@@ -1072,7 +1075,7 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts_if(leader, tm + 256 + h * D, tm + h * 128 + kk * 8, vd0 + sv * (kSlotBytes >> 4) + ((kk * 2048) >> 4), id_pv,
+          mma_ts_if(leader, tm + 256 + h * D, tm + h * 128 + kk / 4 * 64 + kk % 4 * 8, vd0 + sv * (kSlotBytes >> 4) + ((kk * 2048) >> 4), id_pv,
                     i > 0 || kk > 0);
         if (h == tiles - 1) mma_commit_if(leader, empty + sv);
         if (i + 1 < nn) {
@@ -1089,10 +1092,15 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
     }
   } else if (warp < kRowSoftWarps) {
     // ------------------------------------------------------------- softmax
-    const int h = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    // tile, half of the keys, pair; every warp of a tile goes through all n blocks
+    // whatever its waits say, so that the votes stay whole
+    const int h = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + h * 128, o_addr = tmem + lane_base + 256 + h * D;
+    const uint32_t s_addr = tmem + lane_base + h * 128 + half * 64;
+    const uint32_t o_addr = tmem + lane_base + 256 + h * D + half * (D / 2);
     const bool there = h * 128 + r < pairs;
+    float* const halves = reinterpret_cast<float*>(smem + L::kHalfOff) + h * 256;
+    auto tile_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + h) : "memory"); };
     uint32_t mask[4] = {0u, 0u, 0u, 0u};
     if (there) {
 #pragma unroll
@@ -1106,8 +1114,8 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
       return __funnelshift_r(word(k), word(k + 1), e & 31);
     };
     float m = -INFINITY, l = 0.f;
-    bool ok = h < tiles;
-    const int blocks = ok ? n : 0;
+    bool ok = true;
+    const int blocks = h < tiles ? n : 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok) ok = mbar_wait_inl(bar, parity, a.err);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1121,77 +1129,72 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
       }
       const bool masked = entry >> 24 != 0;
       const int e0 = offset0(entry);
+      uint32_t vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (masked) vis[0] = seen(e0 + half * 64), vis[1] = seen(e0 + half * 64 + 32);
       wait(s_full + h, i & 1);
-      if (!ok) break;
       tc_fence_after();
-      uint32_t s[32];
+      uint32_t s[16];
       auto load = [&](int c) {
-        tmem_ld32(s_addr + 32 * c, s);
+        tmem_ld16(s_addr + 16 * c, s);
         tmem_wait_ld();
         if (masked) {
-          const uint32_t v = seen(e0 + 32 * c);
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (!(v >> k & 1u)) s[k] = __float_as_uint(-INFINITY);
+          for (int k = 0; k < 16; ++k)
+            if (!(vis[c >> 1] >> (16 * (c & 1) + k) & 1u)) s[k] = __float_as_uint(-INFINITY);
         }
       };
-      float mx0 = -INFINITY, mx1 = -INFINITY;
+      float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         load(c);
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          mx0 = fmax3(mx0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-          mx1 = fmax3(mx1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+        for (int k = 0; k < 16; k += 2) mx = fmax3(mx, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+      }
+      const float mx2 = FP8 ? fmaf(mx, sl2, log2_vs) : mx * sl2;
+      if (bar_sync_or(1 + h, mx2 > m + 8.f, 256)) {  // m is -inf at first
+        halves[half * 128 + r] = mx2;
+        tile_sync();
+        const float both = fmaxf(mx2, halves[(half ^ 1) * 128 + r]);
+        const float m_new = both > m + 8.f ? both : m;
+        const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
+        l *= alpha;
+        m = m_new;
+        // P.V of the block before is complete: this block's S was issued after it
+        if (i > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {  // this half's dims
+            uint32_t o[16];
+            tmem_ld16(o_addr + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st16(o_addr + 16 * c, o);
+          }
         }
       }
-      const float mx = fmaxf(mx0, mx1), mx2 = FP8 ? fmaf(mx, sl2, log2_vs) : mx * sl2;
-      const float m_new = mx2 > m + 8.f ? mx2 : m;
-      const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = m_new == m ? 1.f : ex2_approx(m - m_use);
-      const float shift = log2_vs - m_use;
-      float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+      const float shift = log2_vs - (m == -INFINITY ? 0.f : m);
+      float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         load(c);
-        uint32_t w[16];
+        uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 8; ++k) {
           float x0, x1;
           ffma2(x0, x1, __uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]), sl2, shift);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          if (k & 1)
-            fadd2(sum2, sum3, p0, p1);
-          else
-            fadd2(sum0, sum1, p0, p1);
+          fadd2(sum0, sum1, p0, p1);
           w[k] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
         }
-        tmem_st16(s_addr + 16 * c, w);  // over chunks of S that are read
+        tmem_st8(s_addr + 8 * c, w);  // over keys of this half that are read
       }
-      const float sum = (sum0 + sum1) + (sum2 + sum3);
-      l = l * alpha + (FP8 ? sum * inv_vs : sum);
-      // P.V of the block before is complete: this block's S was issued after it
-      if (i > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + 32 * c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st16(o_addr + 32 * c, o);
-          tmem_st16(o_addr + 32 * c + 16, o + 16);
-        }
-      }
-      m = m_new;
-      if (!FP8 && masked && h == 0) {  // V rows that no pair sees (e4m3: the converters)
+      l += FP8 ? (sum0 + sum1) * inv_vs : sum0 + sum1;
+      if (!FP8 && masked && h == 0) {  // V rows that no pair sees (e4m3: the converters), 64 dims a half
         wait(full + slot_of(2 * i + 1), phase_of(2 * i + 1));
-        if (!seen_by_any(e0 + r)) {
-          uint8_t* v = smem + L::kRingOff + slot_of(2 * i + 1) * kSlotBytes + r * 128;
-          for (int c = 0; c < D / 64; ++c)
+        if (!seen_by_any(e0 + r) && half < D / 64) {
+          uint8_t* v = smem + L::kRingOff + slot_of(2 * i + 1) * kSlotBytes + half * 16384 + r * 128;
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
-              *reinterpret_cast<uint4*>(v + c * 16384 + ((b ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          for (int b = 0; b < 8; ++b) *reinterpret_cast<uint4*>(v + ((b ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async_shared();
       }
@@ -1203,10 +1206,14 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
 
     // ------------------------------------------------------------ epilogue
     if (h < tiles) {
+      tile_sync();  // halves is free
+      halves[half * 128 + r] = l;
+      tile_sync();
+      l = halves[r] + halves[128 + r];
       if (n > 0) wait(o_done + h, 0);
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      if (there && ok && a.lse != nullptr)
+      if (there && ok && half == 0 && a.lse != nullptr)
         a.lse[row_at[h * 128 + r]] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       const int quad = lane >> 2, j = lane & 3;
 #pragma unroll
@@ -1219,10 +1226,10 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
           const int rr = half16 * 16 + 8 * q + quad, pair = h * 128 + quarter * 32 + rr;
           iv[q] = __shfl_sync(0xFFFFFFFFu, inv, rr);
           mine[q] = pair < pairs && ok;
-          dst[q] = a.out + row_at[pair] * D + 8 * j;
+          dst[q] = a.out + row_at[pair] * D + half * (D / 2) + 8 * j;
         }
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D / 2; c += 32) {
           uint32_t v[16], w[4];
           if (n > 0) {
             tmem_ld_16x256<4>(o_addr + c + (static_cast<uint32_t>(half16 * 16) << 16), v);
@@ -1331,12 +1338,15 @@ ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
   return best;
 }
 
-// The same estimate for the pairs as rows: 256 a CTA, no parts.
-double rows_us(const msa_plan_s* p, bool fp8, int64_t block_bytes, double size) {
+// The same estimate for the pairs as rows: 256 a CTA, no parts.  Measured (us; 19
+// sequences of 32 drafts, 64 / 8 heads, 152 CTAs; 2, 4, 8, 16 and 32 blocks): bf16 11.1,
+// 16.5, 24.5, 37.9, 65.0; e4m3 11.5, 15.4, 23.0, 37.6, 64.2; head_dim 64 9.0, 12.1, 18.3,
+// 30.0, 52.3.  32 x 64 drafts, 16 blocks: 140; as columns, 128 a CTA, 293.
+double rows_us(const msa_plan_s* p, int64_t block_bytes, double size) {
   const int64_t units = p->col_units[4], rounds = (units + p->num_sms - 1) / p->num_sms;
   const double at_once = static_cast<double>(std::min<int64_t>(units, p->num_sms));
   const double hbm = at_once * block_bytes * p->n_tiles * p->hp / units / 6.3e6;
-  return rounds * (12 + std::min(p->max_nvp, p->topk) * std::max((fp8 ? 1.8 : 1.7) * size, hbm));
+  return rounds * (11 + std::min(p->max_nvp, p->topk) * std::max(1.68 * size, hbm));
 }
 
 template <int KIND, int N, bool TWO>
@@ -1425,7 +1435,7 @@ msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pa
   const int64_t block_bytes = int64_t(256) * p->d * (fp8 ? 1 : 2);
   const double size = p->d == 128 ? 1.0 : 0.85;
   const ColShape shape = fp8 ? column_shape<kE4m3>(p, block_bytes, size) : column_shape<kBf16>(p, block_bytes, size);
-  const cudaError_t e = rows_us(p, fp8, block_bytes, size) < shape.us
+  const cudaError_t e = rows_us(p, block_bytes, size) < shape.us
                             ? (fp8 ? (p->d == 128 ? launch_rows<true, 128>(p, a, km, vm, st) : launch_rows<true, 64>(p, a, km, vm, st))
                                    : (p->d == 128 ? launch_rows<false, 128>(p, a, km, vm, st) : launch_rows<false, 64>(p, a, km, vm, st)))
                         : fp8 ? launch_shape<kE4m3>(shape, p, a, km, vm, st)
