@@ -1328,7 +1328,7 @@ ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
       const int64_t rounds = (units + room - 1) / room;
       const double at_once = static_cast<double>(std::min(units, room) * parts);
       const double hbm = at_once * block_bytes * sets / units / 6.3e6;  // us a block step
-      const double step = kStep[KIND][k] * size * (two ? 1.9 : 1.0);
+      const double step = kStep[KIND][k] * size * (two ? 2.7 : 1.0);
       const double us = rounds * (start + (two ? 2 : 0) + (blocks + parts - 1) / parts * std::max(step, hbm));
       if (us < best.us) best = {16 << k, parts, two, us};
     };
@@ -1341,12 +1341,17 @@ ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
 // The same estimate for the pairs as rows: 256 a CTA, no parts.  Measured (us; 19
 // sequences of 32 drafts, 64 / 8 heads, 152 CTAs; 2, 4, 8, 16 and 32 blocks): bf16 11.1,
 // 16.5, 24.5, 37.9, 65.0; e4m3 11.5, 15.4, 23.0, 37.6, 64.2; head_dim 64 9.0, 12.1, 18.3,
-// 30.0, 52.3.  32 x 64 drafts, 16 blocks: 140; as columns, 128 a CTA, 293.
+// 30.0, 52.3; 128 pairs or fewer (16 x 16 drafts, 4 and 16 blocks) 12.2, 31.5, e4m3 12.6,
+// 31.9.  As rows, and as columns at their best (bf16; e4m3), 16 blocks:
+//    8 x 16 drafts   29.9, 24.2   30.7, 28.6      16 x 16   31.5, 36.4   31.9, 43.3
+//    4 x 64          33.7, 33.3   35.2, 41.2      32 x 16   60.8, 70.0   62.2, 84.7
+//    8 x 64          35.6, 65.8   36.1, 82.4      32 x 64   140, -       140, 293
 double rows_us(const msa_plan_s* p, int64_t block_bytes, double size) {
   const int64_t units = p->col_units[4], rounds = (units + p->num_sms - 1) / p->num_sms;
   const double at_once = static_cast<double>(std::min<int64_t>(units, p->num_sms));
   const double hbm = at_once * block_bytes * p->n_tiles * p->hp / units / 6.3e6;
-  return rounds * (11 + std::min(p->max_nvp, p->topk) * std::max(1.68 * size, hbm));
+  const bool two = p->max_tile_rows * (p->hq / p->hp) > 128;  // tiles a CTA
+  return rounds * ((two ? 11 : 6.5) + std::min(p->max_nvp, p->topk) * std::max((two ? 1.68 : 1.61) * size, hbm));
 }
 
 template <int KIND, int N, bool TWO>

@@ -120,8 +120,8 @@ assert len(limit) >= 3, len(limit)
 
 
 def test_wide_trees_take_the_rows(child):  # noqa: F811
-    """The batches of wide trees that the GPU tests run go through another kernel than
-    narrow ones, and the largest among them too."""
+    """The batches of wide trees that the GPU tests run all go through one kernel, and
+    narrow ones through others."""
     import json
     from tests.test_tree_attn_gpu import SHAPES, WIDE
     child(CALLS + "import json\nSHAPES, WIDE = (json.loads(x) for x in %r)" % ([json.dumps(list(x.values())) for x in (SHAPES, WIDE)],) + """
@@ -136,5 +136,5 @@ for d in (64, 128):
     for kind in (BF16, E4M3, BLOCK):
         narrow = {f for s in SHAPES for f in kernel(*s, d, kind)}
         wide = {f for s in WIDE for f in kernel(*s, d, kind)}
-        assert len(wide) == 1 and not wide & narrow, (d, kind, wide, narrow)
+        assert len(wide) == 1 and len(narrow - wide) > 1, (d, kind, wide, narrow)
 """)
