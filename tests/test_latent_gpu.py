@@ -341,3 +341,77 @@ def test_refusals(cuda_dev):
     e4 = [torch.zeros((c.p, 2, 128, 128), device=cuda_dev).to(torch.float8_e4m3fn) for _ in range(2)]
     with pytest.raises((ValueError, TypeError, msa.MsaError)):
         block.latent_expand(c.pages, z(2, 96, 256), z(2, 128, 256), c.table, *e4)
+
+
+def test_pools_beyond_4_gib(cuda_dev):
+    """Append, attention and expansion on pages behind the 2^32nd byte, bit for bit as
+    on small pools; other pages stay as they were."""
+    msa = _msa()
+    latent, rope, heads, d = 512, 64, 8, 128
+    kv, n = [300, 129], 5
+    far = 2 ** 32 // (128 * (latent + rope) * 2) + 7      # of the latents; K and V are larger
+    got = []
+    for pages in (n, far):
+        gen = torch.Generator(device=cuda_dev).manual_seed(6)
+        rand = lambda *s: torch.randn(s, generator=gen, device=cuda_dev).to(torch.bfloat16)  # noqa: E731
+        pool = torch.zeros((pages, 1, 128, latent + rope), device=cuda_dev, dtype=torch.bfloat16)
+        table = torch.tensor([4, 1, 0, 3, 2], dtype=torch.int32, device=cuda_dev) + (pages - n)
+        plan = msa.Plan(kv, kv, heads, heads, heads, d, 64, 2, pages)
+        plan.latent_append(rand(sum(kv), 1, latent), rand(sum(kv), 1, rope), pool, table, rope=msa.Rope(rope))
+        one = msa.Plan([1, 1], kv, 16, 1, 1, d, 64, 3, pages)
+        idx = torch.tensor([[[0, 1, 2]], [[0, 1, -1]]], dtype=torch.int32, device=cuda_dev)
+        out, lse = one.latent_attn(rand(2, 16, latent + rope), pool, table, idx, rope, 0.05)
+        k, v = (torch.zeros((pages, heads, 128, d), device=cuda_dev, dtype=torch.bfloat16) for _ in range(2))
+        plan.latent_expand(pool, rand(heads, d - rope, latent), rand(heads, d, latent), table, k, v)
+        plan.check_errors()
+        one.check_errors()
+        assert pages == n or not any(x[:n].any().item() for x in (pool, k, v))
+        got.append((pool[-n:].clone(), out, lse, k[-n:].clone(), v[-n:].clone()))
+        del pool, k, v
+    assert all(a.any() and torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_nan_is_reported_under_checks(cuda_dev, monkeypatch):
+    monkeypatch.setenv("MSA_CHECKS", "1")
+    msa = _msa()
+    c = Case(cuda_dev, [4], [200], 8, 1, 256, 32, 2, True, seed=2)
+    plan = c.plan()
+    c.run(plan)
+    plan.check_errors()
+    rows = torch.zeros((4, 1, 288), device=cuda_dev).bfloat16()
+    for at in (10, 270):                                  # the latent; the key part
+        rows.zero_()
+        rows[3, 0, at] = float("nan")
+        plan.latent_append(rows[..., :256], rows[..., 256:], c.pages, c.table)
+        with pytest.raises(msa.MsaError) as e:
+            plan.check_errors()
+        assert e.value.status == 7
+    rows.zero_()
+    plan.latent_append(rows[..., :256], rows[..., 256:], c.pages, c.table)
+    plan.check_errors()
+    c.q[1, 2, 3] = float("nan")
+    c.run(plan)
+    with pytest.raises(msa.MsaError) as e:
+        plan.check_errors()
+    assert e.value.status == 7
+
+
+def test_a_page_of_two_sequences(cuda_dev):
+    """A shared prefix: expansion writes a page named twice with the same bits, call after
+    call, and both sequences attend over it."""
+    msa = _msa()
+    gen = torch.Generator(device=cuda_dev).manual_seed(4)
+    rand = lambda *s: torch.randn(s, generator=gen, device=cuda_dev).to(torch.bfloat16)  # noqa: E731
+    kv, p, heads = [256 + 40, 256 + 7, 300], 8, 5
+    table = torch.tensor([2, 5, 0, 2, 5, 1, 5, 2, 7], dtype=torch.int32, device=cuda_dev)
+    c, w_k, w_v = rand(p, 1, 128, 576), rand(heads, 64, 512), rand(heads, 128, 512)
+    plan = msa.Plan([1] * 3, kv, heads, heads, heads, 128, 64, 3, p)
+    got = []
+    for _ in range(3):
+        k, v = torch.zeros((p, heads, 128, 128), device=cuda_dev).bfloat16(), torch.zeros((p, heads, 128, 128), device=cuda_dev).bfloat16()
+        plan.latent_expand(c, w_k, w_v, table, k, v)
+        got.append((k, v))
+    plan.check_errors()
+    assert all(torch.equal(a, b) for g in got[1:] for a, b in zip(got[0], g))
+    single = torch.einsum("ptc,hnc->phtn", c[[2, 5], 0, :, :512].double(), w_v.double())
+    assert (got[0][1][[2, 5]].double() - single).abs().max() <= 2.0 ** -8 * single.abs().max() + 1e-3

@@ -358,3 +358,93 @@ def test_refusals(cuda_dev):
             plan.tree_attn(c.q, *c.pages, c.table, c.idx, bad)
     off = torch.zeros(c.q.numel() + 4, device=cuda_dev).bfloat16()[4:].view(c.q.shape)
     assert status(lambda: plan.tree_attn(off, *c.pages, c.table, c.idx, c.mask)) == 1
+
+
+@pytest.mark.parametrize("kind, d, rows", [("bf16", 128, 5), ("e4m3", 128, 5), ("e4m3_block", 64, 5), ("bf16", 128, 100),
+                                           ("e4m3_block", 128, 100)])
+def test_pools_beyond_4_gib(cuda_dev, kind, d, rows):
+    """Pages behind the 2^32nd byte, bit for bit as out of a small pool."""
+    msa = _msa()
+    hkv, hq, size = 8, 64, 2 if kind == "bf16" else 1
+    far = 2 ** 32 // (hkv * 128 * d * size) + 5
+    batch = 2 if rows == 5 else 16                        # columns; rows
+    kv = [rows + 400 + i for i in range(batch)]
+    gen = torch.Generator(device=cuda_dev).manual_seed(3)
+    nb = sum((k + 127) // 128 for k in kv)
+    small = [torch.randint(0, 120, (nb, hkv, 128, d * size), generator=gen, device=cuda_dev, dtype=torch.uint8) for _ in "kv"]
+    if kind == "bf16":
+        small = [torch.randn((nb, hkv, 128, d), generator=gen, device=cuda_dev).to(torch.bfloat16) for _ in "kv"]
+    q = torch.randn((rows * batch, hq, d), generator=gen, device=cuda_dev).to(torch.bfloat16)
+    words, _ = tree_mask([rows] * batch, np.random.default_rng(1))
+    idx = torch.from_numpy(selection([rows] * batch, kv, hkv, 3, np.random.default_rng(2))).to(cuda_dev)
+    got = []
+    for pages in (nb, far):
+        pools = []
+        for x in small:
+            pool = torch.zeros((pages, *x.shape[1:]), dtype=x.dtype, device=cuda_dev)
+            pool[-nb:] = x
+            pools.append(pool if kind == "bf16" else pool.view(torch.float8_e4m3fn))
+        scale = None if kind == "bf16" else torch.full((hkv,) if kind == "e4m3" else (pages, hkv), 0.01, device=cuda_dev)
+        plan = msa.Plan([rows] * batch, kv, hq, hkv, hkv, d, 64, 3, pages, kv_dtype=kind)
+        table = torch.arange(pages - nb, pages, dtype=torch.int32, device=cuda_dev)
+        got.append(plan.tree_attn(q, *pools, table, idx, torch.from_numpy(words).to(cuda_dev), k_scale=scale, v_scale=scale))
+        plan.check_errors()
+        del pools, pool
+    assert got[0][0].any() and all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_nan_is_reported_under_checks(cuda_dev, monkeypatch):
+    """MSA_CHECKS: a NaN among the queries is reported; one where no row looks is not."""
+    monkeypatch.setenv("MSA_CHECKS", "1")
+    c = Case(cuda_dev, [8, 3], [300, 40], 16, 2, 2, 128, 3, "bf16", seed=1)
+    plan = c.plan()
+    c.run(plan)
+    plan.check_errors()
+    c.q[2, 1, 5] = float("nan")
+    c.run(plan)
+    with pytest.raises(_msa().MsaError) as e:
+        plan.check_errors()
+    assert e.value.status == 7
+
+
+def test_mask_of_any_alignment(cuda_dev):
+    """tree_mask needs 4-byte alignment only, for rows as for columns."""
+    for qo, kv, hq, hkv, hp, topk in (SHAPES["across an edge, three heads"], WIDE["ragged"]):
+        c = Case(cuda_dev, qo, kv, hq, hkv, hp, 128, topk, "bf16", seed=8)
+        plan = c.plan()
+        want = c.run(plan)
+        buf = torch.zeros(c.mask.numel() + 1, dtype=torch.int32, device=cuda_dev)
+        off = buf[1:].view(c.mask.shape)
+        off.copy_(c.mask)
+        got = c.run(plan, mask=off)
+        plan.check_errors()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_host_threads(cuda_dev):
+    """Calls of two plans from two host threads at once, first calls among them."""
+    import threading
+    cases = [Case(cuda_dev, [7, 30], [900, 333], 16, 2, 4, 128, 6, "bf16", seed=4),
+             Case(cuda_dev, *[[x for x in v] if isinstance(v, list) else v for v in WIDE["ragged"][:5]], 128, 5, "e4m3_block", seed=5)]
+    out, errors = [None, None], []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(cuda_dev)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                plan = cases[i].plan()
+                for _ in range(20):
+                    out[i] = cases[i].run(plan)
+                torch.cuda.current_stream().synchronize()
+                plan.check_errors()
+        except Exception as e:                           # noqa: BLE001
+            errors.append(e)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for c, (o, l) in zip(cases, out):
+        c.check(o, l, c.ref())
