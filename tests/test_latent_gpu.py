@@ -1,5 +1,7 @@
 """The latent cache against its definitions in 64 bits: append, absorbed attention,
 expansion, and the two forms of the attention against each other."""
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +10,13 @@ from oracle import msa_oracle as O
 from tests.tree_cases import attend, check, selection, tree_mask
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _collected():
+    """Plans that a test's tracebacks hold go with it."""
+    yield
+    gc.collect()
 
 
 def _msa():

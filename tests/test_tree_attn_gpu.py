@@ -1,5 +1,7 @@
 """msa_tree_attn against its definition in 64 bits: trees of every shape over the
 three caches, what must not be read, clusters, captures, streams and bad pages."""
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +9,13 @@ import torch
 from tests.tree_cases import attend, chain_mask, check, selection, tree_mask
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _collected():
+    """Plans that a test's tracebacks hold go with it."""
+    yield
+    gc.collect()
 
 
 def _msa():
