@@ -420,8 +420,11 @@ __global__ void __launch_bounds__(kThreads)
                          const __nv_bfloat16* __restrict__ key, int64_t key_stride, const int32_t* __restrict__ positions,
                          const int32_t* __restrict__ kv_indices, int64_t num_pages, int32_t latent_dim, int32_t rope_dim,
                          __nv_bfloat16* __restrict__ pages, uint32_t* err) {
+  // the plan's, which no kernel writes; at any multiple of 4 bytes
+  const int32_t* unit = reinterpret_cast<const int32_t*>(units + blockIdx.x);
+  const AppendUnit u{__ldcg(unit), __ldcg(unit + 1), __ldcg(unit + 2), __ldcg(unit + 3)};
   pdl_wait();
-  const AppendUnit u = units[blockIdx.x];
+  pdl_trigger();
   const int64_t page = kv_indices[u.entry];
   const int slot0 = u.slot0_n & 0xFF, n = u.slot0_n >> 8;
   if (page < 0 || page >= num_pages) {

@@ -18,12 +18,12 @@
 // of one row would fill 8 of 128.)  O^T of 64 columns and a 512-wide latent
 // takes 256 TMEM columns, where 64 x 512 with the rows as M takes all 512.
 //
-// Roles: warp 8 lists the blocks and issues TMA loads into a ring of 32 KB slots
-// (K or V of a block; 128 of the latent's dims); warp 9 issues the products; warps
-// 0-3 and 4-7 take half the columns each, a thread being a key: they mask, find
-// each column's maximum, and write P^T (bf16, or f16 for e4m3 caches: half a
-// step is 2^-9 or 2^-12 of a weight, the sums being of the unrounded ones) back to
-// shared memory.  The latent's P^T goes where the block's rotated part
+// Roles: one warp lists the blocks and issues TMA loads into a ring of 32 KB slots
+// (K or V of a block; 128 of the latent's dims); one issues the products; 8 or 16
+// softmax warps, each four of them a share of the columns and a thread a key,
+// mask, find each column's maximum, and write P^T (bf16, or f16 for e4m3 caches:
+// half a step is 2^-9 or 2^-12 of a weight, the sums being of the unrounded ones)
+// back to shared memory.  The latent's P^T goes where the block's rotated part
 // was, which no product reads after S^T.  e4m3: four more warps expand the codes
 // to f16 (exact) inside the slot.
 //
@@ -42,6 +42,19 @@
 //
 // Few tiles: the CTAs of a cluster take a part of the blocks each and merge O^T,
 // m and l over distributed shared memory; no workspace, so calls may overlap.
+//
+// Measured out of HBM, 16 blocks a row:
+//   32 trees of 8 rows, 64/8 heads, bf16 (277 MB): 51 us, 5.4 TB/s.  Bound by HBM.
+//   32 trees of 64 rows, 64/8 heads, e4m3 (138 GFLOP of products): 140 us (rows_kernel
+//     below; as columns 402), 0.98 PFLOP/s.  Bound by shared memory: the products
+//     read 192 KB of it a block and 256 pairs, the conversions 96 KB.
+//   latent, a chunk of 512 rows x 16 heads, 512 + 64 (73 GFLOP): 109 us, 0.67 PFLOP/s.
+//     Bound by shared memory: 575 KB a block and 64 columns, at 128 B/clk 4500 of
+//     the 5500 clocks that a block takes.
+//   latent decode, 32 sequences x 16 heads (75 MB): 30 us, 25 from the L2: a CTA has
+//     4 blocks, and the merge of 4 parts moves 98 KB a CTA.
+//   one tree of 16 rows: 13 us, one tile's chain of launch, tables, loads, products
+//     and merge.
 #include "msa_internal.h"
 #include "ptx.cuh"
 
@@ -138,6 +151,13 @@ struct ColArgs {
   int32_t per_page;         // e4m3: a scale for each (page, KV head)
   float scale_log2;
 };
+
+// A tile of the plan, before pdl_wait: no kernel writes the plan's tables, and L2 has
+// what msa_plan uploaded.
+__device__ __forceinline__ TileInfo plan_tile(const TileInfo* at) {
+  const int4 x = __ldcg(reinterpret_cast<const int4*>(at)), y = __ldcg(reinterpret_cast<const int4*>(at) + 1);
+  return TileInfo{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+}
 
 // the bits of word k of a 128-bit mask that lie below n
 __device__ __forceinline__ uint32_t low_bits(int k, int n) {
@@ -348,8 +368,9 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  const TileInfo tl = plan_tile(a.tiles + t);
   pdl_wait();
-  const TileInfo tl = a.tiles[t];
+  pdl_trigger();
   const int32_t* sel = a.idx + (static_cast<int64_t>(t) * a.hp + p) * a.topk;
   const int j0 = warp == kProducer && lane < a.topk ? sel[lane] : -1;
   const int c0 = group * N, cols = min(N, tl.rows * G - c0);
@@ -947,8 +968,9 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  const TileInfo tl = plan_tile(a.tiles + t);
   pdl_wait();
-  const TileInfo tl = a.tiles[t];
+  pdl_trigger();
   const int32_t* sel = a.idx + (static_cast<int64_t>(t) * a.hp + p) * a.topk;
   const int j0 = warp == kProducer && lane < a.topk ? sel[lane] : -1;
   const int c0 = group * 256, pairs = min(256, tl.rows * G - c0);

@@ -14,7 +14,7 @@
 // other.
 //
 // 32768 rows, 32 heads, 64 + 64 dims, latent 512 (581 MB, 206 GFLOP of products):
-// 158 us, 3.7 TB/s and 1.3 PFLOP/s.  The products are 0.6 of it; the rest is the
+// 153 us, 3.8 TB/s and 1.35 PFLOP/s.  The products are 0.6 of it; the rest is the
 // issuing thread's waits between them and the stores, which at latent 128 take
 // 116 us alone.  One CTA a page: 241 us.
 #include <algorithm>
@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  pdl_trigger();
   const int steps = a.chunks / 2;
   const int units = a.pairs * a.groups, unit0 = blockIdx.x / 2, step = gridDim.x / 2;
   auto head0 = [&](int u) { return u % a.groups * a.per_unit; };

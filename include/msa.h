@@ -55,7 +55,8 @@
  *    but "0") adds, after each of its calls, scans of that call's
  *    floating-point inputs (the query-side arrays q, pq, dout, and the pages
  *    of k/v/pk that kv_indices names; bf16 or e4m3, not the NVFP4 codes, nor
- *    MSA_KV_FP8_E4M3_BLOCK pages, whose unwritten slots may hold any bytes;
+ *    MSA_KV_FP8_E4M3_BLOCK pages, whose unwritten slots may hold any bytes,
+ *    nor the pages of msa_tree_attn and of a latent cache, likewise;
  *    the new rows of the appends) and
  *    outputs (max_score, out, lse, dq, dpq, the rows of msa_append_bwd; not
  *    the pages of dk/dv/dpk and of the caches, of which those not referenced
