@@ -86,6 +86,9 @@ def _check(status, where):
 
 
 _current_device = torch._C._cuda_getDevice
+# (shape, strides, dtype) on the current device, without the dispatcher: two outputs by
+# torch.empty take 3.5 us more of a call that takes 10
+_new = torch._C._dynamo.guards._empty_strided_cuda
 
 # The checks and conversions below run several times a call, and a decode step's
 # kernels are as short as they are: what passes is decided in one expression.
@@ -461,15 +464,16 @@ class Plan:
                                     out.data_ptr(), _ptr(lse), _stream(stream)), "msa_sparse_attn")
         return out, lse
 
-    def _outputs(self, out, lse, shape, want_lse, dev):
+    def _outputs(self, out, lse, shape, want_lse):
+        # (after the inputs' checks: they are on the current device, as what _new makes is)
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            out = _new(shape, (shape[1] * shape[2], shape[2], 1), torch.bfloat16)
         else:
             _need(out, torch.bfloat16, shape, "out")
         if lse is not None:
             _need(lse, torch.float32, self._lse_shape, "lse")
         elif want_lse:
-            lse = torch.empty(self._lse_shape, dtype=torch.float32, device=dev)
+            lse = _new(self._lse_shape, (self.hq, 1), torch.float32)
         return out, lse
 
     def tree_attn(self, q, k_pages, v_pages, kv_indices, kv_block_indexes, tree_mask, k_scale=None, v_scale=None,
@@ -480,7 +484,7 @@ class Plan:
         _need_all((kv_indices, k_pages, v_pages, q, kv_block_indexes) if self.kv_dtype == "bf16" else
                   (kv_indices, k_pages, v_pages, k_scale, v_scale, q, kv_block_indexes), self._attn_needs)
         _need(tree_mask, *self._mask_need)
-        out, lse = self._outputs(out, lse, self._q_shape, want_lse, q.device)
+        out, lse = self._outputs(out, lse, self._q_shape, want_lse)
         _check(_lib.msa_tree_attn(self._h, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_indices.data_ptr(),
                                   kv_block_indexes.data_ptr(), tree_mask.data_ptr(), _ptr(k_scale), _ptr(v_scale),
                                   out.data_ptr(), _ptr(lse), _stream(stream)), "msa_tree_attn")
@@ -498,7 +502,7 @@ class Plan:
         _need(kv_block_indexes, *self._idx_need)
         if tree_mask is not None:
             _need(tree_mask, *self._mask_need)
-        out, lse = self._outputs(out, lse, (self.total_q, self.hq, width - rope_dim), want_lse, q.device)
+        out, lse = self._outputs(out, lse, (self.total_q, self.hq, width - rope_dim), want_lse)
         _check(_lib.msa_latent_attn(self._h, q.data_ptr(), latent_pages.data_ptr(), kv_indices.data_ptr(),
                                     kv_block_indexes.data_ptr(), _ptr(tree_mask), width - rope_dim, rope_dim,
                                     float(scale), out.data_ptr(), _ptr(lse), _stream(stream)), "msa_latent_attn")
