@@ -845,53 +845,64 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   cluster_sync();  // every part's O^T, m and l are in its shared memory
   tc_fence_after();
   if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
+  // A share of the items each, four dims of one column.  Of more than four parts a
+  // thread reads four and its neighbours the others, from this CTA's own on (all CTAs
+  // reading one part's at a time took 1.5 times as long).  The first items are on
+  // their way while the weights are made.
   float* wts = reinterpret_cast<float*>(smem + L::kQOff);  // [column][part]
-  for (int c = threadIdx.x; c < cols; c += kThreads) {
-    float2 ml[kMaxParts];
-    float mm = -INFINITY, sum = 0.f;
-    const uint32_t at = smem_u32(col_ml + c);
+  const int lg_parts = 31 - __clz(a.parts), lg_by = max(lg_parts - 3, 0), mine = a.parts >> lg_by;
+  const int dv4 = a.dv / 4, items = cols * dv4;
+  const int first = items * part / a.parts, last = items * (part + 1) / a.parts;
+  const uint32_t ring = smem_u32(smem + L::kRingOff);
+  const int by = threadIdx.x & ((1 << lg_by) - 1);
+  float4 v[8];
+  auto from = [&](int k) { return (part + by * mine + k) & (a.parts - 1); };
+  auto fetch = [&](int e) {
 #pragma unroll
-    for (int w = 0; w < kMaxParts; ++w)
-      if (w < a.parts) ml[w] = ld_cluster_f2(at, w), mm = fmaxf(mm, ml[w].x);
-#pragma unroll
-    for (int w = 0; w < kMaxParts; ++w)
-      if (w < a.parts) {
-        ml[w].x = ml[w].x == -INFINITY ? 0.f : ex2_approx(ml[w].x - mm);
-        sum += ml[w].y * ml[w].x;
-      }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int w = 0; w < kMaxParts; ++w)
-      if (w < a.parts) wts[c * kMaxParts + w] = ml[w].x * inv;
-    if (part == 0 && a.lse != nullptr)
-      a.lse[col_row[c]] = sum > 0.f ? (mm + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    for (int k = 0; k < 8; ++k)
+      if (k < mine) v[k] = ld_cluster_f4(ring + 16u * e, from(k));
+  };
+  float2 ml = make_float2(-INFINITY, 0.f);  // of the first columns: a thread one part's
+  const int c_first = threadIdx.x >> lg_parts, w = threadIdx.x & (a.parts - 1);
+  if (c_first < cols) ml = ld_cluster_f2(smem_u32(col_ml + c_first), w);
+  int e = first + (threadIdx.x >> lg_by);
+  if (e < last) fetch(e);
+  for (int c = c_first; c - c_first < cols; c += kThreads >> lg_parts) {  // (all lanes of a warp alike)
+    if (c != c_first) ml = c < cols ? ld_cluster_f2(smem_u32(col_ml + c), w) : make_float2(-INFINITY, 0.f);
+    float mm = ml.x;
+    for (int d = 1; d < a.parts; d *= 2) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
+    const float scale = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+    float sum = ml.y * scale;
+    for (int d = 1; d < a.parts; d *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (c < cols) {
+      wts[c * kMaxParts + w] = sum > 0.f ? scale / sum : 0.f;
+      if (part == 0 && w == 0 && a.lse != nullptr)
+        a.lse[col_row[c]] = sum > 0.f ? (mm + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    }
   }
   __syncthreads();
-  // a share of the items each, four dims of one column, the parts' from this CTA's
-  // own on (all CTAs reading one part's at a time took 1.5 times as long)
-  const int dv4 = a.dv / 4, items = cols * dv4, last = items * (part + 1) / a.parts;
-  for (int e = items * part / a.parts + threadIdx.x; e < last; e += kThreads) {
+  // whole warps go round, as the parts' sums are added over neighbours
+  for (int e0 = first + ((threadIdx.x & ~31) >> lg_by); e0 < last; e0 += kThreads >> lg_by) {
     const int c = e / dv4;
-    const uint32_t at = smem_u32(smem + L::kRingOff) + 16u * e;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k0 = 0; k0 < kMaxParts; k0 += 8) {
-      if (k0 >= a.parts) break;
-      float4 v[8];
+    if (e < last) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k0 + k < a.parts)
-          v[k] = k0 + k == 0 ? reinterpret_cast<const float4*>(smem + L::kRingOff)[e]
-                             : ld_cluster_f4(at, (part + k0 + k) & (a.parts - 1));
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < a.parts) {
-          const float x = wts[c * kMaxParts + ((part + k0 + k) & (a.parts - 1))];
+        if (k < mine) {
+          const float x = wts[c * kMaxParts + from(k)];
           o.x += v[k].x * x, o.y += v[k].y * x, o.z += v[k].z * x, o.w += v[k].w * x;
         }
     }
-    *reinterpret_cast<uint2*>(a.out + col_row[c] * a.dv + 4 * (e % dv4)) =
-        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    const int at = e;
+    e += kThreads >> lg_by;
+    if (e < last) fetch(e);
+    for (int d = 1; d < 1 << lg_by; d *= 2) {
+      o.x += __shfl_xor_sync(0xFFFFFFFFu, o.x, d), o.y += __shfl_xor_sync(0xFFFFFFFFu, o.y, d);
+      o.z += __shfl_xor_sync(0xFFFFFFFFu, o.z, d), o.w += __shfl_xor_sync(0xFFFFFFFFu, o.w, d);
+    }
+    if (by == 0 && at < last)
+      *reinterpret_cast<uint2*>(a.out + col_row[c] * a.dv + 4 * (at % dv4)) =
+          make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   }
   cluster_sync();  // nobody leaves while its part may be read
 }
@@ -1040,7 +1051,7 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
       uint32_t x[4] = {0u, 0u, 0u, 0u};
       if (e < pairs) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           x[k] = a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + row) + k] & low_bits(k, tl.rows);
       }
 #pragma unroll
@@ -1126,7 +1137,7 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
     uint32_t mask[4] = {0u, 0u, 0u, 0u};
     if (there) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 8; ++k)
         mask[k] = a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + (c0 + h * 128 + r) / G) + k] & low_bits(k, tl.rows);
     }
     // bits e .. e + 31 of: ones below 0, the mask, zeros from 128 on
