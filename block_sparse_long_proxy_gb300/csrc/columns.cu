@@ -203,10 +203,14 @@ __device__ __forceinline__ int list_blocks(const ColArgs& a, const TileInfo& tl,
     if (take) list[o] = static_cast<uint32_t>(page) | static_cast<uint32_t>(max(j - first_masked + 1, 0)) << 24;
     n += __popc(m);
     __syncwarp();
-    if (b == 0) first32(n);
+    float ks = 0.f, vs = 0.f;  // on their way while the first loads are issued
     if (FP8 && take) {
       const int64_t sat = a.per_page ? page * a.hkv + kvh : kvh;
-      const BlockScale bs = block_scale_of(a.k_scale[sat], a.v_scale[sat]);
+      ks = a.k_scale[sat], vs = a.v_scale[sat];
+    }
+    if (b == 0) first32(n);
+    if (FP8 && take) {
+      const BlockScale bs = block_scale_of(ks, vs);
       scales[o] = make_float2(bs.ks * a.scale_log2, bs.log2_vs);
     }
   }
@@ -273,15 +277,22 @@ struct ColSmem {
 };
 
 // Softmax warpgroups: 8 to 32 columns each.  Alone on an SM, two of them leave the
-// passes over S^T waiting for their own latencies.
-template <int N, bool TWO>
+// passes over S^T waiting for their own latencies; e4m3 of 32 columns rather has the
+// registers for four more converter warps.
+template <int KIND, int N, bool TWO>
 constexpr int soft_warps() {
-  return N == 16 || TWO ? 8 : 16;
+  return N == 16 || TWO || (KIND == kE4m3 && N == 32) ? 8 : 16;
 }
-constexpr int kConvWarps = 4;  // e4m3 only
+// Converter warps, e4m3 only: four a slot; of eight, four have the K slots and four
+// the V slots.
+constexpr int kConvWarps = 4;
+template <int KIND, int N>
+constexpr int conv_warps() {
+  return KIND != kE4m3 ? 0 : N <= 32 ? 8 : 4;
+}
 template <int KIND, int N, bool TWO>
 constexpr int col_threads() {
-  return 32 * (soft_warps<N, TWO>() + 2 + (KIND == kE4m3 ? kConvWarps : 0));
+  return 32 * (soft_warps<KIND, N, TWO>() + 2 + conv_warps<KIND, N>());
 }
 
 // Sums of CH values a lane over the warp's lanes: lane c (mod CH) has the sum of
@@ -313,7 +324,8 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   using L = ColSmem<KIND, N, TWO>;
   constexpr bool kLat = KIND == kLatent, kFp8 = KIND == kE4m3;
   constexpr int kThreads = col_threads<KIND, N, TWO>();
-  constexpr int kSoftWarps = soft_warps<N, TWO>(), kProducer = kSoftWarps, kIssuer = kSoftWarps + 1;
+  constexpr int kSoftWarps = soft_warps<KIND, N, TWO>(), kProducer = kSoftWarps, kIssuer = kSoftWarps + 1;
+  constexpr int kConv = conv_warps<KIND, N>();
   constexpr int HN = N / (kSoftWarps / 4);      // columns of a warpgroup
   constexpr int CH = 8;                         // of them, in registers at a time
   constexpr int NCH = HN / CH;
@@ -430,10 +442,26 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
     }
     return true;
   };
+  // e4m3: slot use u's codes to f16, a thread a key, by four warps
+  auto convert = [&](int u, bool zero) {
+    const int s = slot_of(u);
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait_inl(full + s, phase_of(u), a.err))) return false;
+    expand_row(smem + L::kRingOff + s * kSlotBytes, (threadIdx.x - 32 * (kIssuer + 1)) & 127, a.dv == 128, zero);
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ready + s);
+    return true;
+  };
+  bool conv_ok = true, converted = false;
   const int first_blocks = kLat ? 1 : S / 2;  // loaded before the columns are there
   int started = 0;
   if (warp == kProducer) {
     const int n = list_blocks<kFp8>(a, tl, sel, j0, kvh, part, a.parts, list, scales, [&](int n) {
+      if (kFp8) {
+        if (lane == 0) n_slot[1] = n;  // for the converters: is the first block among them?
+        __syncwarp();
+        asm volatile("bar.arrive 7, %0;" ::"n"(32 + 32 * kConv) : "memory");
+      }
       started = min(n, first_blocks);
       const bool leader = elect_one();
       for (int i = 0; i < started; ++i)
@@ -441,10 +469,14 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       if (kLat && n > started) prefetch(started, leader);
     });
     if (lane == 0) *n_slot = n;
+  } else if (kFp8 && warp > kIssuer) {
+    // the first block's K, as soon as it has landed
+    asm volatile("bar.sync 7, %0;" ::"n"(32 + 32 * kConv) : "memory");
+    if (warp <= kIssuer + 4 && (converted = n_slot[1] > 0)) conv_ok = convert(0, false);
   } else {
     // Q^T's columns, 64 dims a chunk, a warp a column
     const int w = warp < kProducer ? warp : warp - 1;
-    constexpr int kLoaders = kThreads / 32 - 1;
+    constexpr int kLoaders = kSoftWarps + 1;
     const uint32_t qs = smem_u32(smem + L::kQOff);
     const int units = a.kc * 8;
     if (kFp8) {
@@ -818,19 +850,12 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       }
   } else if (kFp8) {
     // ---------------------------------------------------------- converters
-    const int r = threadIdx.x - 32 * (kSoftWarps + 2);
-    bool ok = true;
-    for (int u = 0; u < 2 * n; ++u) {
-      const int s = slot_of(u);
+    const int r = (threadIdx.x - 32 * (kIssuer + 1)) & 127;
+    const bool second = warp > kIssuer + 4;
+    constexpr int kStride = kConv == 4 ? 1 : 2;
+    for (int u = second ? 1 : converted ? kStride : 0; u < 2 * n && conv_ok; u += kStride) {
       const uint32_t entry = list[u >> 1];
-      const bool zero = (u & 1) && entry >> 24 != 0 && !seen_by_any(offset0(entry) + r);
-      if (ok) ok = mbar_wait_inl(full + s, phase_of(u), a.err);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      expand_row(smem + L::kRingOff + s * kSlotBytes, r, a.dv == 128, zero);
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ready + s);
+      conv_ok = convert(u, (u & 1) && entry >> 24 != 0 && !seen_by_any(offset0(entry) + r));
     }
   }
 
