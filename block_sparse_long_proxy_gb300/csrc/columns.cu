@@ -1372,8 +1372,8 @@ struct ColShape {
 };
 template <int KIND>
 ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
-  static constexpr double kStart[3][4] = {{7.4, 9, 11.2, 15}, {8, 9.7, 10.8, 14}, {9, 11, 14.5, 1e9}};
-  static constexpr double kStep[3][4] = {{0.5, 0.52, 0.7, 1.1}, {0.95, 1.05, 1.4, 1.75}, {2.0, 2.0, 2.45, 1e9}};
+  static constexpr double kStart[3][4] = {{7.4, 9, 11.2, 15}, {7.3, 8, 10, 13.5}, {9, 11, 14.5, 1e9}};
+  static constexpr double kStep[3][4] = {{0.5, 0.52, 0.7, 1.1}, {0.8, 0.88, 1.4, 1.75}, {2.0, 2.0, 2.45, 1e9}};
   static constexpr int kClusters[5] = {152, 76, 36, 15, 7};
   const int blocks = std::min(p->max_nvp, p->topk);
   ColShape best{16, 1, false, 1e300};
