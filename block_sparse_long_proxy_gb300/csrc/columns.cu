@@ -149,6 +149,7 @@ struct ColArgs {
   int32_t kc;               // 64-column chunks of a key
   int32_t mt;               // 128-row products of O^T
   int32_t per_page;         // e4m3: a scale for each (page, KV head)
+  int32_t q_tma;            // bf16: Q^T by q_map
   float scale_log2;
 };
 
@@ -320,7 +321,8 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool
 
 template <int KIND, int N, bool TWO>
 __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
-    columns_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const ColArgs a) {
+    columns_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                   const __grid_constant__ CUtensorMap q_map, const ColArgs a) {
   using L = ColSmem<KIND, N, TWO>;
   constexpr bool kLat = KIND == kLatent, kFp8 = KIND == kE4m3;
   constexpr int kThreads = col_threads<KIND, N, TWO>();
@@ -343,7 +345,8 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   uint64_t* s_full = tail_empty + 2;   // [2]
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 1);
+  uint64_t* q_full = pv_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
   int32_t* n_slot = reinterpret_cast<int32_t*>(tmem_slot + 1);
   uint32_t* seen_by = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
   float2* col_ml = reinterpret_cast<float2*>(smem + L::kColOff);
@@ -374,6 +377,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       }
       mbar_init(p_full, kSoftWarps);
       mbar_init(pv_done, 1);
+      mbar_init(q_full, 1);
       fence_mbar_init();
     }
   } else if (warp == kIssuer) {
@@ -499,6 +503,15 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
           *reinterpret_cast<uint4*>(smem + L::kQOff + (u >> 3) * L::kQChunk + c * 128 + (((u & 7) ^ (c & 7)) << 4)) =
               make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z), bf16x2_to_f16x2(v[k].w));
       }
+    } else if (a.q_tma) {
+      // what a box has beside the tile's columns (other rows' values) stays in its columns
+      if (warp == kIssuer && elect_one()) {
+        prefetch_tmap(&q_map);
+        mbar_expect_tx(q_full, a.kc * L::kQChunk);
+        for (int c = 0; c < a.kc; ++c)
+          tma_load_3d(smem + L::kQOff + c * L::kQChunk, &q_map, q_full, 64 * c, p * G + c0 % G, tl.q_begin + c0 / G);
+      }
+      __syncwarp();
     } else {
       const int cl = c0 + w + lane * kLoaders;  // a lane finds one column's row (a division by G)
       const int64_t at_l = static_cast<int64_t>(tl.q_begin + cl / G) * a.hq + p * G + cl % G;
@@ -602,7 +615,8 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
         }
         mma_commit_if(leader, s_full + (i & 1));
       };
-      if (nn > 0) qk(0);
+      if (!kFp8 && a.q_tma) ok = waited(q_full, 0);
+      if (nn > 0 && ok) qk(0);
       for (int i = 0; i < nn && ok; ++i) {
         // the latent's slots serve S^T of block i until its P.V: the next block's loads wait for that
         if (!kLat && i + 1 < nn) qk(i + 1);
@@ -1422,6 +1436,17 @@ cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km
   const int64_t ctas = int64_t(p->n_tiles) * p->hp * groups * parts;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   auto kern = columns_kernel<KIND, N, TWO>;
+  // Q^T in boxes where the columns of a CTA are whole rows, or lie in one: by 16-byte copies
+  // a CTA waits for them behind its first K and V (32 x 8 drafts 51.4 against 50.2 us)
+  CUtensorMap qm = km;
+  const int G = p->hq / p->hp;
+  if (KIND != kE4m3 && (N % G == 0 || G % N == 0)) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(a.dq), static_cast<uint64_t>(p->hq), static_cast<uint64_t>(p->total_q)};
+    const uint64_t str[2] = {2u * dims[0], 2u * dims[0] * dims[1]};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(std::min(G, N)), static_cast<uint32_t>(G < N ? N / G : 1)};
+    if (!encode_tensor_map(&qm, 3, a.q, dims, str, box, 1, 128)) return cudaErrorInvalidValue;
+    a.q_tma = 1;
+  }
   // the limit is the function's, for every host thread: always the most of any topk
   static_assert(L::bytes(1024) + 1024 <= 232448, "shared memory at the largest topk");
   static std::atomic<uint64_t> devices{0};  // that have these limits (the call takes about a microsecond)
@@ -1433,7 +1458,7 @@ cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km
     devices.fetch_or(bit, std::memory_order_release);
   }
   return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), parts, dim3(col_threads<KIND, N, TWO>()),
-                            L::bytes(p->topk) + 1024, st, km, vm, a);
+                            L::bytes(p->topk) + 1024, st, km, vm, qm, a);
 }
 
 template <int KIND>

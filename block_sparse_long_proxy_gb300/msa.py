@@ -309,10 +309,11 @@ class Plan:
         self._pk_shape = (self.total_q, 1, self.dp)
         self._grad_needs = ((torch.float32, pool, "dk_pages"), (torch.float32, pool, "dv_pages"),
                             (torch.float32, ppool + (self.dp,), "dpk_pages"), pos, self._cache_needs[0])
-        self._mask_need = (torch.int32, (self.total_q, 4), "tree_mask")
-        self._idx_need = (torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes")
         self._attn_needs = self._cache_needs + ((torch.bfloat16, self._q_shape, "q"), (
             torch.int32, (self.n_tiles, self.hp, self.topk), "kv_block_indexes"))
+        self._tree_needs = self._attn_needs + ((torch.int32, (self.total_q, 4), "tree_mask"),)
+        self._table_needs = (self._cache_needs[0],) + self._tree_needs[-2:]
+        self._latent_needs = {}  # by the rows' width
 
     # -- the cache
     def kv_append(self, k, v, k_pages, v_pages, kv_indices, k_scale=None, v_scale=None, rope=None, positions=None,
@@ -481,9 +482,8 @@ class Plan:
         """Attention of drafted tokens over the cache (msa_tree_attn): row i sees
         the keys before the drafts, and draft b of its sequence iff bit b % 32 of
         tree_mask[i, b // 32] is set (int32 [total_q, 4])."""
-        _need_all((kv_indices, k_pages, v_pages, q, kv_block_indexes) if self.kv_dtype == "bf16" else
-                  (kv_indices, k_pages, v_pages, k_scale, v_scale, q, kv_block_indexes), self._attn_needs)
-        _need(tree_mask, *self._mask_need)
+        _need_all((kv_indices, k_pages, v_pages, q, kv_block_indexes, tree_mask) if self.kv_dtype == "bf16" else
+                  (kv_indices, k_pages, v_pages, k_scale, v_scale, q, kv_block_indexes, tree_mask), self._tree_needs)
         out, lse = self._outputs(out, lse, self._q_shape, want_lse)
         _check(_lib.msa_tree_attn(self._h, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_indices.data_ptr(),
                                   kv_block_indexes.data_ptr(), tree_mask.data_ptr(), _ptr(k_scale), _ptr(v_scale),
@@ -496,12 +496,12 @@ class Plan:
         latent_dim + rope_dim] bf16, out [total_q, Hq, latent_dim]; causal, or by
         tree_mask as tree_attn has it."""
         width = q.shape[-1]
-        _need(q, torch.bfloat16, (self.total_q, self.hq, width), "q")
-        _need(latent_pages, torch.bfloat16, (self.num_pages, 1, 128, width), "latent_pages")
-        _need(kv_indices, *self._cache_needs[0])
-        _need(kv_block_indexes, *self._idx_need)
-        if tree_mask is not None:
-            _need(tree_mask, *self._mask_need)
+        needs = self._latent_needs.get(width)
+        if needs is None:
+            needs = self._latent_needs[width] = (
+                (torch.bfloat16, (self.total_q, self.hq, width), "q"),
+                (torch.bfloat16, (self.num_pages, 1, 128, width), "latent_pages")) + self._table_needs
+        _need_all((q, latent_pages, kv_indices, kv_block_indexes, tree_mask), needs, optional=True)
         out, lse = self._outputs(out, lse, (self.total_q, self.hq, width - rope_dim), want_lse)
         _check(_lib.msa_latent_attn(self._h, q.data_ptr(), latent_pages.data_ptr(), kv_indices.data_ptr(),
                                     kv_block_indexes.data_ptr(), _ptr(tree_mask), width - rope_dim, rope_dim,
