@@ -889,16 +889,16 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   // reading one part's at a time took 1.5 times as long).  The first items are on
   // their way while the weights are made.
   float* wts = reinterpret_cast<float*>(smem + L::kQOff);  // [column][part]
-  const int lg_parts = 31 - __clz(a.parts), lg_by = max(lg_parts - 3, 0), mine = a.parts >> lg_by;
+  const int lg_parts = 31 - __clz(a.parts), lg_by = max(lg_parts - 2, 0), mine = a.parts >> lg_by;
   const int dv4 = a.dv / 4, items = cols * dv4;
   const int first = items * part / a.parts, last = items * (part + 1) / a.parts;
   const uint32_t ring = smem_u32(smem + L::kRingOff);
   const int by = threadIdx.x & ((1 << lg_by) - 1);
-  float4 v[8];
+  float4 v[4];
   auto from = [&](int k) { return (part + by * mine + k) & (a.parts - 1); };
   auto fetch = [&](int e) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 4; ++k)
       if (k < mine) v[k] = ld_cluster_f4(ring + 16u * e, from(k));
   };
   float2 ml = make_float2(-INFINITY, 0.f);  // of the first columns: a thread one part's
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (e < last) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < 4; ++k)
         if (k < mine) {
           const float x = wts[c * kMaxParts + from(k)];
           o.x += v[k].x * x, o.y += v[k].y * x, o.z += v[k].z * x, o.w += v[k].w * x;
@@ -1090,7 +1090,7 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
       uint32_t x[4] = {0u, 0u, 0u, 0u};
       if (e < pairs) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 4; ++k)
           x[k] = a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + row) + k] & low_bits(k, tl.rows);
       }
 #pragma unroll
@@ -1176,7 +1176,7 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
     uint32_t mask[4] = {0u, 0u, 0u, 0u};
     if (there) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < 4; ++k)
         mask[k] = a.tree_mask[4 * static_cast<int64_t>(tl.q_begin + (c0 + h * 128 + r) / G) + k] & low_bits(k, tl.rows);
     }
     // bits e .. e + 31 of: ones below 0, the mask, zeros from 128 on
