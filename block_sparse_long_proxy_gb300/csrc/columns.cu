@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   constexpr int HN = N / (kSoftWarps / 4);      // columns of a warpgroup
   constexpr int CH = 8;                         // of them, in registers at a time
   constexpr int NCH = HN / CH;
+  constexpr bool kAhead = HN <= 16;
   constexpr int S = L::kSlots, T = L::kTails > 0 ? L::kTails : 1;
   constexpr uint32_t kTmemCols = kLat ? 8 * N : 4 * N;  // S^T twice, O^T of up to 4 products or 1
   constexpr float kUnset = 1e30f;  // minus the reference of a column that has none yet
@@ -702,25 +703,60 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
         __syncwarp();
       };
       if (kFp8) put_shift();
-      // does any column outgrow its reference?  (one without has kUnset, which any logit outgrows)
+      // P^T of chunk k by the present references, the sums that go with it, and the largest logit
+      uint32_t w[kAhead ? NCH : 1][4];
       float far = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < NCH; ++k) {
-        load(k);
+      auto weigh = [&](int k, uint32_t (&w)[4], float (&l)[CH]) {
 #pragma unroll
         for (int c = 0; c < CH; c += 4) {
           const float4 sh = *reinterpret_cast<const float4*>(shift + k * CH + c);
-          float x0, x1, x2, x3;
-          logits(k, c, make_float2(sh.x, sh.y), x0, x1);
-          logits(k, c + 2, make_float2(sh.z, sh.w), x2, x3);
-          far = fmax3(fmax3(far, x0, x1), x2, x3);
+#pragma unroll
+          for (int b = 0; b < 4; b += 2) {
+            float x0, x1;
+            logits(k, c + b, b == 0 ? make_float2(sh.x, sh.y) : make_float2(sh.z, sh.w), x0, x1);
+            far = fmax3(far, x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            if (kFp8)
+              ffma2v(l[c + b], l[c + b + 1], p0, p1, inv_vs, inv_vs, l[c + b], l[c + b + 1]);
+            else
+              fadd2(l[c + b], l[c + b + 1], p0, p1);
+            w[(c + b) / 2] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
         }
+      };
+      // does any column outgrow its reference?  (one without has kUnset, which any logit outgrows.)  With
+      // few columns a warpgroup, P^T is there when the vote is; when it is lost, it is made again.
+      float l_ahead[kAhead ? NCH : 1][CH];
+      bool grown = i == 0;
+      if (i > 0) {
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int k = 0; k < NCH; ++k) {
+            load(k);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) l_ahead[k][c] = l[k][c];
+            weigh(k, w[k], l_ahead[k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < NCH; ++k) {
+            load(k);
+#pragma unroll
+            for (int c = 0; c < CH; c += 4) {
+              const float4 sh = *reinterpret_cast<const float4*>(shift + k * CH + c);
+              float x0, x1, x2, x3;
+              logits(k, c, make_float2(sh.x, sh.y), x0, x1);
+              logits(k, c + 2, make_float2(sh.z, sh.w), x2, x3);
+              far = fmax3(fmax3(far, x0, x1), x2, x3);
+            }
+          }
+        }
+        grown = bar_sync_or(1 + wg, far > 8.f, 128);
       }
-      const bool grown = bar_sync_or(1 + wg, far > 8.f, 128);
       if (grown) {
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
-          if (NCH > 1) load(k);
+          load(k);
           __syncwarp();
           float mx = -INFINITY;
 #pragma unroll
@@ -766,30 +802,17 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       uint8_t* pt = smem + (kLat ? L::kTailOff + (i % T) * L::kTailBytes : L::kPOff);
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
-        if (NCH > 1) load(k);
+        auto& wk = w[kAhead ? k : 0];
+        if (!kAhead || grown) {
+          if (NCH > 1) load(k);
+          weigh(k, wk, l[k]);
+        } else {
 #pragma unroll
-        for (int c = 0; c < CH; c += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int d = 0; d < 8; d += 4) {
-            const float4 sh = *reinterpret_cast<const float4*>(shift + k * CH + c + d);
-#pragma unroll
-            for (int b = 0; b < 4; b += 2) {
-              const int x = c + d + b;
-              float x0, x1;
-              logits(k, x, b == 0 ? make_float2(sh.x, sh.y) : make_float2(sh.z, sh.w), x0, x1);
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              if (kFp8)
-                ffma2v(l[k][x], l[k][x + 1], p0, p1, inv_vs, inv_vs, l[k][x], l[k][x + 1]);
-              else
-                fadd2(l[k][x], l[k][x + 1], p0, p1);
-              w[(d + b) / 2] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-            }
-          }
-          const int col = wg * HN + k * CH + c;
-          *reinterpret_cast<uint4*>(pt + (col >> 6) * 16384 + r * 128 + (((col >> 3 & 7) ^ (r & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          for (int c = 0; c < CH; ++c) l[k][c] = l_ahead[kAhead ? k : 0][c];
         }
+        const int col = wg * HN + k * CH;
+        *reinterpret_cast<uint4*>(pt + (col >> 6) * 16384 + r * 128 + (((col >> 3 & 7) ^ (r & 7)) << 4)) =
+            make_uint4(wk[0], wk[1], wk[2], wk[3]);
       }
       if (!kFp8 && masked) {  // V rows that no column sees (e4m3: the converters), 64 dims a warpgroup in turn
         if (!kLat) wait(full + slot_of(2 * i + 1), phase_of(2 * i + 1));
