@@ -14,7 +14,7 @@
 // other.
 //
 // 32768 rows, 32 heads, 64 + 64 dims, latent 512 (581 MB, 206 GFLOP of products):
-// 153 us, 3.8 TB/s and 1.35 PFLOP/s.  The products are 0.6 of it; the rest is the
+// 139 us, 4.2 TB/s and 1.5 PFLOP/s (155 in passes without a pause).  The products are 0.7 of it; the rest is the
 // issuing thread's waits between them and the stores, which at latent 128 take
 // 116 us alone.  One CTA a page: 241 us.
 #include <algorithm>
@@ -39,11 +39,13 @@ __device__ __forceinline__ uint32_t cta_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Arrive on CTA 0's barrier at the same place as `bar`.
+// Arrive on CTA 0's barrier at the same place as `bar`: what is handed over is tensor
+// memory that was read, and tcgen05.wait::ld came before.  (A release would also
+// wait for the warp's stores to K and V: 152 us where this takes 139.)
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 // mbar_wait_inl for a barrier on which the other CTA arrives (the clock is read
