@@ -18,6 +18,7 @@
 // issuing thread's waits between them and the stores, which at latent 128 take
 // 116 us alone.  One CTA a page: 241 us.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "msa_internal.h"
@@ -398,7 +399,15 @@ msa_status launch_expand(const msa_plan_s* p, const void* latent_pages, const vo
                     : rope_dim == 48 ? (wide ? expand_kernel<128, 48> : expand_kernel<64, 48>)
                                      : expand_kernel<128, 64>;
   const int smem = kSmem + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the devices that have each kernel's limit (the call takes about a microsecond)
+  static std::atomic<uint64_t> devices[8];
+  std::atomic<uint64_t>& have = devices[rope_dim / 16 * 2 - 1 - wide];
+  const uint64_t bit = p->device < 64 ? uint64_t(1) << p->device : 0;
+  cudaError_t e = cudaSuccess;
+  if ((have.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) have.fetch_or(bit, std::memory_order_release);
+  }
   if (e == cudaSuccess)
     e = launch_pdl_cluster(kern, dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, p->num_sms / 2))), 2,
                            dim3(kThreads), smem, st, cm, km, v0, v1, a);

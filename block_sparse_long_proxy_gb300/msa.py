@@ -379,10 +379,9 @@ class Plan:
         w_k [Hkv, d - rope_dim, latent_dim] and w_v [Hkv, d, latent_dim] bf16."""
         n = w_v.shape[-1]
         width = latent_pages.shape[-1] - n
-        _need(latent_pages, torch.bfloat16, (self.num_pages, 1, 128, n + width), "latent_pages")
-        _need(w_k, torch.bfloat16, (self.hkv, self.d - width, n), "w_k")
-        _need(w_v, torch.bfloat16, (self.hkv, self.d, n), "w_v")
-        _need_all((kv_indices, k_pages, v_pages), self._cache_needs)
+        _need_all((kv_indices, k_pages, v_pages, latent_pages, w_k, w_v), self._cache_needs[:3] + (
+            (torch.bfloat16, (self.num_pages, 1, 128, n + width), "latent_pages"),
+            (torch.bfloat16, (self.hkv, self.d - width, n), "w_k"), (torch.bfloat16, (self.hkv, self.d, n), "w_v")))
         _check(_lib.msa_latent_expand(self._h, latent_pages.data_ptr(), w_k.data_ptr(), w_v.data_ptr(),
                                       kv_indices.data_ptr(), n, width, k_pages.data_ptr(), v_pages.data_ptr(),
                                       _stream(stream)), "msa_latent_expand")
