@@ -424,3 +424,49 @@ def test_a_page_of_two_sequences(cuda_dev):
     assert all(torch.equal(a, b) for g in got[1:] for a, b in zip(got[0], g))
     single = torch.einsum("ptc,hnc->phtn", c[[2, 5], 0, :, :512].double(), w_v.double())
     assert (got[0][1][[2, 5]].double() - single).abs().max() <= 2.0 ** -8 * single.abs().max() + 1e-3
+
+
+@pytest.mark.parametrize("hq", [3, 32, 50])
+def test_first_places_empty(cuda_dev, hq):
+    """Selections whose blocks all stand behind 32 empty places."""
+    c = Case(cuda_dev, [1, 2], [128 * 11, 300], hq, 1, 256, 32, 70, False, seed=17, irregular=False)
+    sel = np.full_like(c.idx_h, -1)
+    sel[:, :, 37:49] = c.idx_h[:, :, :12]
+    c.idx_h, c.idx = sel, torch.from_numpy(sel).to(cuda_dev)
+    plan = c.plan()
+    out, lse = c.run(plan)
+    plan.check_errors()
+    c.check(out, lse, c.ref())
+
+
+def test_calls_that_feed_each_other(cuda_dev):
+    """Append, attention and expansion in a chain without a pause, each one's output the next
+    one's input: the bits of the chain that waits after every call."""
+    m = _msa()
+    rng, kv, latent, rope, d = np.random.default_rng(31), [700, 130, 2000], 256, 32, 64
+    gen = torch.Generator(device=cuda_dev).manual_seed(31)
+    table, p = _table(kv, 2, rng, cuda_dev)
+    plan = m.Plan([1] * 3, kv, 8, 8, 8, d, 32, 4, p)
+    idx = torch.from_numpy(selection([1] * 3, kv, 8, 4, rng)).to(cuda_dev)
+    draw = lambda *shape: torch.randn(shape, generator=gen, device=cuda_dev).to(torch.bfloat16)  # noqa: E731
+    pages0, q, key = draw(p, 1, 128, latent + rope), draw(3, 8, latent + rope), draw(3, 1, rope)
+    w_k, w_v = draw(8, d - rope, latent), draw(8, d, latent)
+    first = draw(3, 8, latent)
+    turn = m.Rope(rope)
+    ends = []
+    for pause in (True, False):
+        wait = torch.cuda.synchronize if pause else lambda: None
+        pages, k, v = pages0.clone(), torch.zeros((p, 8, 128, d), dtype=torch.bfloat16, device=cuda_dev), None
+        v, out = torch.zeros_like(k), first.clone()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            plan.latent_append(out[:, :1], key, pages, table, rope=turn)
+            wait()
+            out, _ = plan.latent_attn(q, pages, table, idx, rope, 0.06)
+            wait()
+            plan.latent_expand(pages, w_k, w_v, table, k, v)
+            wait()
+        plan.check_errors()
+        ends.append((out, pages, k, v))
+    for x, y in zip(*ends):
+        assert torch.equal(x, y)

@@ -457,3 +457,39 @@ def test_two_host_threads(cuda_dev):
     assert not errors, errors
     for c, (o, l) in zip(cases, out):
         c.check(o, l, c.ref())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e4m3_block"])
+@pytest.mark.parametrize("rows", [1, 5, 14, 100])
+def test_first_places_empty(cuda_dev, rows, kind):
+    """Selections whose blocks all stand behind 32 empty places."""
+    c = Case(cuda_dev, [rows] * 2, [rows + 128 * 11, rows + 300], 8, 1, 1, 128, 70, kind, seed=17, irregular=False)
+    sel = np.full_like(c.idx_h, -1)
+    sel[:, :, 37:49] = c.idx_h[:, :, :12]
+    assert (sel[:, :, :37] == -1).all() and (sel[1] >= 0).sum() >= 3
+    plan = c.plan()
+    out, lse = c.run(plan, idx=torch.from_numpy(sel).to(cuda_dev))
+    plan.check_errors()
+    c.check(out, lse, c.ref(idx=sel))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3_block"])
+@pytest.mark.parametrize("rows", [2, 40])
+def test_calls_that_feed_each_other(cuda_dev, rows, kind):
+    """A chain of calls without a pause, each one's output the next one's queries: the bits of
+    the chain that waits after every call."""
+    c = Case(cuda_dev, [rows] * 3, [900, 3000, 650], 16, 2, 2, 128, 6, kind, seed=21)
+    plan = c.plan()
+    ends = []
+    for pause in (True, False):
+        a, b = c.q.clone(), torch.zeros_like(c.q)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            plan.tree_attn(a, *c.pages, c.table, c.idx, c.mask, k_scale=c.scales[0], v_scale=c.scales[1], out=b,
+                           want_lse=False)
+            a, b = b, a
+            if pause:
+                torch.cuda.synchronize()
+        plan.check_errors()
+        ends.append(a.clone())
+    assert torch.equal(*ends)
