@@ -44,16 +44,16 @@
 // m and l over distributed shared memory; no workspace, so calls may overlap.
 //
 // Measured out of HBM, 16 blocks a row:
-//   32 trees of 8 rows, 64/8 heads, bf16 (277 MB): 51 us, 5.4 TB/s.  Bound by HBM.
+//   32 trees of 8 rows, 64/8 heads, bf16 (277 MB): 50 us, 5.5 TB/s.  Bound by HBM.
 //   32 trees of 64 rows, 64/8 heads, e4m3 (138 GFLOP of products): 140 us (rows_kernel
-//     below; as columns 402), 0.98 PFLOP/s.  Bound by shared memory: the products
-//     read 192 KB of it a block and 256 pairs, the conversions 96 KB.
-//   latent, a chunk of 512 rows x 16 heads, 512 + 64 (73 GFLOP): 109 us, 0.67 PFLOP/s.
+//     below; as columns 293), 0.98 PFLOP/s.  Bound by a tile's chain from S to the next
+//     S, which issue slots stretch (half of them are used; the products take 40 %).
+//   latent, a chunk of 512 rows x 32 heads, 512 + 64 (73 GFLOP): 106 us, 0.69 PFLOP/s.
 //     Bound by shared memory: 575 KB a block and 64 columns, at 128 B/clk 4500 of
-//     the 5500 clocks that a block takes.
-//   latent decode, 32 sequences x 16 heads (75 MB): 30 us, 25 from the L2: a CTA has
+//     the 5400 clocks that a block takes.
+//   latent decode, 32 sequences x 64 heads (80 MB): 28 us, 24 from the L2: a CTA has
 //     4 blocks, and the merge of 4 parts moves 98 KB a CTA.
-//   one tree of 16 rows: 13 us, one tile's chain of launch, tables, loads, products
+//   one tree of 16 rows: 12 us, one tile's chain of launch, tables, loads, products
 //     and merge.
 #include "msa_internal.h"
 #include "ptx.cuh"
@@ -1390,18 +1390,19 @@ cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, c
 // start + blocks * step, both measured (us, head_dim 128 or latent_dim 512):
 //              start, step        N = 16       32         64        128
 //   bf16                         7.4, 0.5   9, 0.52    11.2, 0.7   15, 1.1
-//   e4m3                         8, 0.95    9.7, 1.05  10.8, 1.4   14, 1.75
+//   e4m3                         7.3, 0.8   8, 0.88    10, 1.4     13.5, 1.75
 //   latent                       9, 2.0     11, 2.0    14.5, 2.45
 // and no less than the blocks' bytes take from HBM at 6.3 TB/s.  The CTAs run in
 // rounds: 152, 76 clusters of 2, 36 of 4, 15 of 8, 7 of 16 at once (large clusters are
 // not placed as densely as the SMs would allow).  Two on an SM hide each other's
 // start and end where there would be several rounds (bf16 up to 64 columns: 32 x 8
-// drafts 57.1 -> 52.4; e4m3, whose converters want the SM, 64.3 -> 67.7; the latent's
+// drafts 54.2 -> 50.1; e4m3, whose converters want the SM, 64.3 -> 67.7; the latent's
 // blocks fill the shared memory).  Examples (us, N / parts, all choices tried):
-//   16 drafts, 64 / 8 heads, 16 blocks: 32 / 4 11.1, 64 / 4 13.6, 128 / 8 16.8, 16 / 1 15.9
-//   32 x 8 drafts, same: 64 / 1 57.1, 32 / 1 79.3, 16 / 1 122
-//   1 row, 64 heads, latent, 16 blocks: 16 / 16 10.6, 32 / 16 12.5, 64 / 8 18.7, 64 / 1 53.9
-//   32 rows, same: 64 / 4 31.1, 32 / 2 32.4, 64 / 2 40.6, 16 / 1 45.5
+//   16 drafts, 64 / 8 heads, bf16, 16 blocks: 32 / 4 10.3, 64 / 4 11.5, 16 / 2 11.7, 128 / 8 14.2
+//   the same, e4m3: 32 / 4 12.0, 64 / 4 14.1, 16 / 2 14.8, 128 / 8 16.2
+//   32 x 8 drafts, bf16: 64 / 1 54.2, 128 / 1 65.0, 32 / 1 79.3, 16 / 1 122
+//   1 row, 64 heads, latent, 16 blocks: 16 / 16 9.8, 32 / 16 11.8, 16 / 4 15.3, 64 / 8 16.1
+//   32 rows, same: 64 / 4 28.2, 32 / 2 29.9, 64 / 2 36.3, 16 / 1 41.4
 struct ColShape {
   int n, parts;
   bool two;
