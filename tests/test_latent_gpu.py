@@ -470,3 +470,31 @@ def test_calls_that_feed_each_other(cuda_dev):
         ends.append((out, pages, k, v))
     for x, y in zip(*ends):
         assert torch.equal(x, y)
+
+
+def test_other_tensors_after_accepted_ones(cuda_dev):
+    """What was accepted of one call's tensors says nothing of others: each check again, in any order,
+    and rows at another stride."""
+    c = Case(cuda_dev, [2, 3], [300, 140], 4, 1, 256, 32, 3, True)
+    plan = c.plan()
+    want = c.run(plan)
+    good = dict(q=c.q, latent_pages=c.pages, kv_indices=c.table, kv_block_indexes=c.idx, tree_mask=c.mask)
+    for name, bad, error in [("q", c.q[:, :, :128], ValueError), ("q", c.q.float(), TypeError), ("q", c.q.cpu(), ValueError),
+                             ("latent_pages", c.pages[:-1], ValueError), ("kv_indices", c.table.long(), TypeError),
+                             ("kv_block_indexes", c.idx.transpose(0, 2), ValueError), ("tree_mask", c.mask[:1], ValueError),
+                             ("q", c.q.transpose(0, 1).contiguous().transpose(0, 1), ValueError)]:
+        with pytest.raises(error):
+            plan.latent_attn(rope_dim=32, scale=c.scale, **dict(good, **{name: bad}))
+        got = plan.latent_attn(rope_dim=32, scale=c.scale, **good)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ValueError):
+        plan.latent_attn(rope_dim=300, scale=c.scale, **good)
+    gen = torch.Generator(device=cuda_dev).manual_seed(3)
+    new = torch.randn((5, 1, 3, 288), generator=gen, device=cuda_dev).to(torch.bfloat16)
+    ends = []
+    for dense in (True, False, True, False):
+        pages, row = c.pages.clone(), new[:, :, 1].contiguous() if dense else new[:, :, 1]
+        plan.latent_append(row[..., :256], row[..., 256:], pages, c.table)
+        ends.append(pages.view(torch.int16))
+    assert all(torch.equal(ends[0], x) for x in ends[1:]) and not torch.equal(ends[0], c.pages.view(torch.int16))
+    plan.check_errors()
