@@ -1403,18 +1403,15 @@ cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, c
 //   32 x 8 drafts, bf16: 64 / 1 54.2, 128 / 1 65.0, 32 / 1 79.3, 16 / 1 122
 //   1 row, 64 heads, latent, 16 blocks: 16 / 16 9.8, 32 / 16 11.8, 16 / 4 15.3, 64 / 8 16.1
 //   32 rows, same: 64 / 4 28.2, 32 / 2 29.9, 64 / 2 36.3, 16 / 1 41.4
-struct ColShape {
-  int n, parts;
-  bool two;
-  double us;
-};
+using Columns = msa_plan_s::Columns;
 template <int KIND>
-ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
+Columns column_shape(const msa_plan_s* p, int64_t block_bytes, double size, double& least) {
   static constexpr double kStart[3][4] = {{7.4, 9, 11.2, 15}, {7.3, 8, 10, 13.5}, {9, 11, 14.5, 1e9}};
   static constexpr double kStep[3][4] = {{0.5, 0.52, 0.7, 1.1}, {0.8, 0.88, 1.4, 1.75}, {2.0, 2.0, 2.45, 1e9}};
   static constexpr int kClusters[5] = {152, 76, 36, 15, 7};
   const int blocks = std::min(p->max_nvp, p->topk);
-  ColShape best{16, 1, false, 1e300};
+  Columns best{16, 1, false, false};
+  least = 1e300;
   for (int k = 0; k < (KIND == kLatent ? 3 : 4); ++k) {
     const int64_t units = p->col_units[k], sets = int64_t(p->n_tiles) * p->hp;
     const double start = kStart[KIND][k] * (KIND == kLatent ? 0.4 + 0.6 * size : 1.0);
@@ -1426,7 +1423,7 @@ ColShape column_shape(const msa_plan_s* p, int64_t block_bytes, double size) {
       const double hbm = at_once * block_bytes * sets / units / 6.3e6;  // us a block step
       const double step = kStep[KIND][k] * size * (two ? 2.7 : 1.0);
       const double us = rounds * (start + (two ? 2 : 0) + (blocks + parts - 1) / parts * std::max(step, hbm));
-      if (us < best.us) best = {16 << k, parts, two, us};
+      if (us < least) best = {16 << k, parts, two, false}, least = us;
     };
     for (int lg = 0; (1 << lg) <= kMaxParts && (1 << lg) <= blocks; ++lg) take(lg, false);
     if (KIND == kBf16 && k < 3) take(0, true);
@@ -1486,7 +1483,7 @@ cudaError_t launch_columns(const msa_plan_s* p, ColArgs a, const CUtensorMap& km
 }
 
 template <int KIND>
-cudaError_t launch_shape(ColShape c, const msa_plan_s* p, const ColArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
+cudaError_t launch_shape(Columns c, const msa_plan_s* p, const ColArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                          cudaStream_t st) {
   if constexpr (KIND == kBf16)
     if (c.two)
@@ -1508,6 +1505,16 @@ void column_plan_counts(msa_plan_s* p) {
     p->max_tile_rows = std::max(p->max_tile_rows, t.rows);
     p->max_nvp = std::max(p->max_nvp, t.nvp);
     for (int k = 0; k < 5; ++k) p->col_units[k] += int64_t(p->hp) * ((int64_t(t.rows) * G + (16 << k) - 1) >> (4 + k));
+  }
+  const bool fp8 = p->kv_dtype != MSA_KV_BF16;
+  const int64_t bytes = int64_t(256) * p->d * (fp8 ? 1 : 2);
+  const double size = p->d == 128 ? 1.0 : 0.85;
+  double us;
+  p->tree_shape = fp8 ? column_shape<kE4m3>(p, bytes, size, us) : column_shape<kBf16>(p, bytes, size, us);
+  p->tree_shape.rows = rows_us(p, bytes, size) < us;
+  for (int k = 0; k < 4; ++k) {  // (with the widest rotated part: blocks of 128 dims are a quarter smaller at most, of 512 8 %)
+    const int width = 128 * (k + 1) + 64;
+    p->latent_shape[k] = column_shape<kLatent>(p, int64_t(256) * width, width / 576.0, us);
   }
 }
 
@@ -1544,14 +1551,11 @@ msa_status launch_tree_attn(const msa_plan_s* p, const void* q, const void* k_pa
   a.mt = 1;
   a.per_page = p->kv_dtype == MSA_KV_FP8_E4M3_BLOCK;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(p->d));
-  const int64_t block_bytes = int64_t(256) * p->d * (fp8 ? 1 : 2);
-  const double size = p->d == 128 ? 1.0 : 0.85;
-  const ColShape shape = fp8 ? column_shape<kE4m3>(p, block_bytes, size) : column_shape<kBf16>(p, block_bytes, size);
-  const cudaError_t e = rows_us(p, block_bytes, size) < shape.us
-                            ? (fp8 ? (p->d == 128 ? launch_rows<true, 128>(p, a, km, vm, st) : launch_rows<true, 64>(p, a, km, vm, st))
-                                   : (p->d == 128 ? launch_rows<false, 128>(p, a, km, vm, st) : launch_rows<false, 64>(p, a, km, vm, st)))
-                        : fp8 ? launch_shape<kE4m3>(shape, p, a, km, vm, st)
-                              : launch_shape<kBf16>(shape, p, a, km, vm, st);
+  const Columns& shape = p->tree_shape;
+  const cudaError_t e = shape.rows ? (fp8 ? (p->d == 128 ? launch_rows<true, 128>(p, a, km, vm, st) : launch_rows<true, 64>(p, a, km, vm, st))
+                                          : (p->d == 128 ? launch_rows<false, 128>(p, a, km, vm, st) : launch_rows<false, 64>(p, a, km, vm, st)))
+                        : fp8      ? launch_shape<kE4m3>(shape, p, a, km, vm, st)
+                                   : launch_shape<kBf16>(shape, p, a, km, vm, st);
   return cuda_check(e, "msa_tree_attn: launch");
 }
 
@@ -1586,8 +1590,7 @@ msa_status launch_latent_attn(const msa_plan_s* p, const void* q, const void* la
   a.kc = latent_dim / 64 + 1;
   a.mt = latent_dim / 128;
   a.scale_log2 = 1.4426950408889634f * scale;
-  const ColShape c = column_shape<kLatent>(p, int64_t(256) * width, width / 576.0);
-  return cuda_check(launch_shape<kLatent>(c, p, a, km, vm, st), "msa_latent_attn: launch");
+  return cuda_check(launch_shape<kLatent>(p->latent_shape[latent_dim / 128 - 1], p, a, km, vm, st), "msa_latent_attn: launch");
 }
 
 namespace {

@@ -109,6 +109,11 @@ struct msa_plan_s {
   int32_t n_append_units = 0;
   int32_t max_tile_rows = 1, max_nvp = 1;  // of any tile
   int64_t col_units[5] = {};         // attention of few rows: units of 16, 32, 64, 128 and 256 (row, head) pairs
+  struct Columns {                   // columns a CTA, CTAs a unit, two CTAs an SM; or the pairs as rows
+    int32_t n, parts;
+    bool two, rows;
+  };
+  Columns tree_shape = {}, latent_shape[4] = {};  // msa_tree_attn; msa_latent_attn at 128, 256, 384 and 512 dims
   int64_t entry_keys_off = 0;        // latent expansion: keys of each page-table entry's page
   void* bwd_d = nullptr;             // backward scratch (D, proxy LSE, inverse index)
 };
