@@ -1391,7 +1391,8 @@ cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, c
 //              start, step        N = 16       32         64        128
 //   bf16                         7.4, 0.5   9, 0.52    11.2, 0.7   15, 1.1
 //   e4m3                         7.3, 0.8   8, 0.88    10, 1.4     13.5, 1.75
-//   latent                       9, 2.0     11, 2.0    14.5, 2.45
+//   latent                       8.8, 1.95  9.9, 2.08  12.3, 2.41
+// (latents of 128, 256 and 384 dims: 0.70, 0.80 and 0.90 of the start, 0.51, 0.68 and 0.84 of the step),
 // and no less than the blocks' bytes take from HBM at 6.3 TB/s.  The CTAs run in
 // rounds: 152, 76 clusters of 2, 36 of 4, 15 of 8, 7 of 16 at once (large clusters are
 // not placed as densely as the SMs would allow).  Two on an SM hide each other's
@@ -1406,22 +1407,22 @@ cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, c
 using Columns = msa_plan_s::Columns;
 template <int KIND>
 Columns column_shape(const msa_plan_s* p, int64_t block_bytes, double size, double& least) {
-  static constexpr double kStart[3][4] = {{7.4, 9, 11.2, 15}, {7.3, 8, 10, 13.5}, {9, 11, 14.5, 1e9}};
-  static constexpr double kStep[3][4] = {{0.5, 0.52, 0.7, 1.1}, {0.8, 0.88, 1.4, 1.75}, {2.0, 2.0, 2.45, 1e9}};
+  static constexpr double kStart[3][4] = {{7.4, 9, 11.2, 15}, {7.3, 8, 10, 13.5}, {8.8, 9.9, 12.3, 1e9}};
+  static constexpr double kStep[3][4] = {{0.5, 0.52, 0.7, 1.1}, {0.8, 0.88, 1.4, 1.75}, {1.95, 2.08, 2.41, 1e9}};
   static constexpr int kClusters[5] = {152, 76, 36, 15, 7};
   const int blocks = std::min(p->max_nvp, p->topk);
   Columns best{16, 1, false, false};
   least = 1e300;
   for (int k = 0; k < (KIND == kLatent ? 3 : 4); ++k) {
     const int64_t units = p->col_units[k], sets = int64_t(p->n_tiles) * p->hp;
-    const double start = kStart[KIND][k] * (KIND == kLatent ? 0.4 + 0.6 * size : 1.0);
+    const double start = kStart[KIND][k] * (KIND == kLatent ? 0.55 + 0.45 * size : 1.0);
     auto take = [&](int lg, bool two) {
       const int parts = 1 << lg;
       const int64_t room = std::max<int64_t>(1, int64_t(kClusters[lg]) * (two ? 2 : 1) * p->num_sms / 152);
       const int64_t rounds = (units + room - 1) / room;
       const double at_once = static_cast<double>(std::min(units, room) * parts);
       const double hbm = at_once * block_bytes * sets / units / 6.3e6;  // us a block step
-      const double step = kStep[KIND][k] * size * (two ? 2.7 : 1.0);
+      const double step = kStep[KIND][k] * (KIND == kLatent ? 0.27 + 0.73 * size : size) * (two ? 2.7 : 1.0);
       const double us = rounds * (start + (two ? 2 : 0) + (blocks + parts - 1) / parts * std::max(step, hbm));
       if (us < least) best = {16 << k, parts, two, false}, least = us;
     };
