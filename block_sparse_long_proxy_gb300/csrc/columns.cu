@@ -1389,11 +1389,12 @@ cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, c
 // share an SM: the least estimated time over the choices.  A CTA takes about
 // start + blocks * step, both measured (us, head_dim 128 or latent_dim 512):
 //              start, step        N = 16       32         64        128
-//   bf16                         7.4, 0.5   9, 0.52    11.2, 0.7   15, 1.1
-//   e4m3                         7.3, 0.8   8, 0.88    10, 1.4     13.5, 1.75
+//   bf16                         5.6, 0.6   6, 0.68    6.3, 1.05   8.6, 1.72
+//   e4m3                         5.2, 0.93  6.4, 1.0   6, 1.65     10.3, 1.87
 //   latent                       8.8, 1.95  9.9, 2.08  12.3, 2.41
 // (latents of 128, 256 and 384 dims: 0.70, 0.80 and 0.90 of the start, 0.51, 0.68 and 0.84 of the step),
-// and no less than the blocks' bytes take from HBM at 6.3 TB/s.  The CTAs run in
+// (1.2 more where bf16 or e4m3 parts merge), and no less than the blocks' bytes take from HBM at 6.3
+// TB/s, 3 us of it within the start.  The CTAs run in
 // rounds: 152, 76 clusters of 2, 36 of 4, 15 of 8, 7 of 16 at once (large clusters are
 // not placed as densely as the SMs would allow).  Two on an SM hide each other's
 // start and end where there would be several rounds (bf16 up to 64 columns: 32 x 8
@@ -1405,10 +1406,11 @@ cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, c
 //   1 row, 64 heads, latent, 16 blocks: 16 / 16 9.8, 32 / 16 11.8, 16 / 4 15.3, 64 / 8 16.1
 //   32 rows, same: 64 / 4 28.2, 32 / 2 29.9, 64 / 2 36.3, 16 / 1 41.4
 using Columns = msa_plan_s::Columns;
+constexpr double kAhead = 3;  // us of a start in which blocks stream already
 template <int KIND>
 Columns column_shape(const msa_plan_s* p, int64_t block_bytes, double size, double& least) {
-  static constexpr double kStart[3][4] = {{7.4, 9, 11.2, 15}, {7.3, 8, 10, 13.5}, {8.8, 9.9, 12.3, 1e9}};
-  static constexpr double kStep[3][4] = {{0.5, 0.52, 0.7, 1.1}, {0.8, 0.88, 1.4, 1.75}, {1.95, 2.08, 2.41, 1e9}};
+  static constexpr double kStart[3][4] = {{5.6, 6, 6.3, 8.6}, {5.2, 6.4, 6, 10.3}, {8.8, 9.9, 12.3, 1e9}};
+  static constexpr double kStep[3][4] = {{0.6, 0.68, 1.05, 1.72}, {0.93, 1.0, 1.65, 1.87}, {1.95, 2.08, 2.41, 1e9}};
   static constexpr int kClusters[5] = {152, 76, 36, 15, 7};
   const int blocks = std::min(p->max_nvp, p->topk);
   Columns best{16, 1, false, false};
@@ -1422,8 +1424,9 @@ Columns column_shape(const msa_plan_s* p, int64_t block_bytes, double size, doub
       const int64_t rounds = (units + room - 1) / room;
       const double at_once = static_cast<double>(std::min(units, room) * parts);
       const double hbm = at_once * block_bytes * sets / units / 6.3e6;  // us a block step
-      const double step = kStep[KIND][k] * (KIND == kLatent ? 0.27 + 0.73 * size : size) * (two ? 2.7 : 1.0);
-      const double us = rounds * (start + (two ? 2 : 0) + (blocks + parts - 1) / parts * std::max(step, hbm));
+      const double step = kStep[KIND][k] * (KIND == kLatent ? 0.27 + 0.73 * size : size) * (two ? 2.0 : 1.0);
+      const int most = (blocks + parts - 1) / parts;
+      const double us = rounds * (start + (two ? 2 : 0) + (parts > 1 && KIND != kLatent ? 1.2 : 0) + std::max(most * step, most * hbm - kAhead));
       if (us < least) best = {16 << k, parts, two, false}, least = us;
     };
     for (int lg = 0; (1 << lg) <= kMaxParts && (1 << lg) <= blocks; ++lg) take(lg, false);
@@ -1432,20 +1435,19 @@ Columns column_shape(const msa_plan_s* p, int64_t block_bytes, double size, doub
   return best;
 }
 
-// The same estimate for the pairs as rows: 256 a CTA, no parts.  Measured (us; 19
-// sequences of 32 drafts, 64 / 8 heads, 152 CTAs; 2, 4, 8, 16 and 32 blocks): bf16 11.1,
-// 16.5, 24.5, 37.9, 65.0; e4m3 11.5, 15.4, 23.0, 37.6, 64.2; head_dim 64 9.0, 12.1, 18.3,
-// 30.0, 52.3; 128 pairs or fewer (16 x 16 drafts, 4 and 16 blocks) 12.2, 31.5, e4m3 12.6,
-// 31.9.  As rows, and as columns at their best (bf16; e4m3), 16 blocks:
-//    8 x 16 drafts   29.9, 24.2   30.7, 28.6      16 x 16   31.5, 36.4   31.9, 43.3
-//    4 x 64          33.7, 33.3   35.2, 41.2      32 x 16   60.8, 70.0   62.2, 84.7
+// The same estimate for the pairs as rows: 256 a CTA, no parts.  Measured (us; 64 / 8
+// heads, 4, 6 and 16 blocks): 128 pairs or fewer a CTA bf16 11.8, 13.7, 29.2, e4m3 12.1,
+// 14.6, 29.8, head_dim 64 10.2, 12.0, 24.1; 256 pairs, 152 CTAs, 16 blocks 35, head_dim 64 30.
+// As rows, and as columns at their best (bf16; e4m3), 16 blocks:
+//    8 x 16 drafts   29.2, 23.1   29.8, 28.1      32 x 8    60.9, 49.5   60.8, 63.3
 //    8 x 64          35.6, 65.8   36.1, 82.4      32 x 64   140, -       140, 293
 double rows_us(const msa_plan_s* p, int64_t block_bytes, double size) {
   const int64_t units = p->col_units[4], rounds = (units + p->num_sms - 1) / p->num_sms;
   const double at_once = static_cast<double>(std::min<int64_t>(units, p->num_sms));
   const double hbm = at_once * block_bytes * p->n_tiles * p->hp / units / 6.3e6;
   const bool two = p->max_tile_rows * (p->hq / p->hp) > 128;  // tiles a CTA
-  return rounds * ((two ? 11 : 6.5) + std::min(p->max_nvp, p->topk) * std::max((two ? 1.68 : 1.61) * size, hbm));
+  const int blocks = std::min(p->max_nvp, p->topk);
+  return rounds * ((two ? 8 : 6.1) + std::max(blocks * (two ? 1.7 : 1.47) * size, blocks * hbm - kAhead));
 }
 
 template <int KIND, int N, bool TWO>
@@ -1509,7 +1511,7 @@ void column_plan_counts(msa_plan_s* p) {
   }
   const bool fp8 = p->kv_dtype != MSA_KV_BF16;
   const int64_t bytes = int64_t(256) * p->d * (fp8 ? 1 : 2);
-  const double size = p->d == 128 ? 1.0 : 0.85;
+  const double size = p->d == 128 ? 1.0 : 0.87;
   double us;
   p->tree_shape = fp8 ? column_shape<kE4m3>(p, bytes, size, us) : column_shape<kBf16>(p, bytes, size, us);
   p->tree_shape.rows = rows_us(p, bytes, size) < us;
