@@ -51,7 +51,7 @@
 //   latent, a chunk of 512 rows x 32 heads, 512 + 64 (73 GFLOP): 106 us, 0.69 PFLOP/s.
 //     Bound by shared memory: 575 KB a block and 64 columns, at 128 B/clk 4500 of
 //     the 5400 clocks that a block takes.
-//   latent decode, 32 sequences x 64 heads (80 MB): 28 us, 24 from the L2: a CTA has
+//   latent decode, 32 sequences x 64 heads (80 MB): 27 us, 24 from the L2: a CTA has
 //     4 blocks, and the merge of 4 parts moves 98 KB a CTA.
 //   one tree of 16 rows: 12 us, one tile's chain of launch, tables, loads, products
 //     and merge.
@@ -1408,7 +1408,7 @@ cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, c
 //   the same, e4m3: 32 / 4 12.0, 64 / 4 14.1, 16 / 2 14.8, 128 / 8 16.2
 //   32 x 8 drafts, bf16: 64 / 1 54.2, 128 / 1 65.0, 32 / 1 79.3, 16 / 1 122
 //   1 row, 64 heads, latent, 16 blocks: 16 / 16 9.8, 32 / 16 11.8, 16 / 4 15.3, 64 / 8 16.1
-//   32 rows, same: 64 / 4 28.2, 32 / 2 29.9, 64 / 2 36.3, 16 / 1 41.4
+//   32 rows, same: 64 / 4 27.2, 32 / 2 29.9, 64 / 2 36.3, 16 / 1 41.4
 using Columns = msa_plan_s::Columns;
 constexpr double kAhead = 3;  // us of a start in which blocks stream already
 template <int KIND>
