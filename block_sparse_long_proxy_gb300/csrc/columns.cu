@@ -45,9 +45,9 @@
 //
 // Measured out of HBM, 16 blocks a row:
 //   32 trees of 8 rows, 64/8 heads, bf16 (277 MB): 50 us, 5.5 TB/s.  Bound by HBM.
-//   32 trees of 64 rows, 64/8 heads, e4m3 (138 GFLOP of products): 140 us (rows_kernel
-//     below; as columns 293), 0.98 PFLOP/s.  Bound by a tile's chain from S to the next
-//     S, which issue slots stretch (half of them are used; the products take 40 %).
+//   32 trees of 64 rows, 64/8 heads, e4m3 (138 GFLOP of products): 137 us (rows_kernel
+//     below; as columns 293), 1.0 PFLOP/s.  Bound by a tile's chain from S to the next S,
+//     1.6 us of which the exponentials of both tiles are 1.07.
 //   latent, a chunk of 512 rows x 32 heads, 512 + 64 (73 GFLOP): 106 us, 0.69 PFLOP/s.
 //     Bound by shared memory: 575 KB a block and 64 columns, at 128 B/clk 4500 of
 //     the 5400 clocks that a block takes.
@@ -1244,10 +1244,17 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
       };
       float mx = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        load(c);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t x[32];
+        tmem_ld32(s_addr + 32 * c, x);
+        tmem_wait_ld();
+        if (masked) {
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) mx = fmax3(mx, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+          for (int k = 0; k < 32; ++k)
+            if (!(vis[c] >> k & 1u)) x[k] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) mx = fmax3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
       }
       const float mx2 = FP8 ? fmaf(mx, sl2, log2_vs) : mx * sl2;
       if (bar_sync_or(1 + h, mx2 > m + 8.f, 256)) {  // m is -inf at first
