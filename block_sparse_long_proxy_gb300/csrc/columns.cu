@@ -387,13 +387,15 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   }
   const TileInfo tl = plan_tile(a.tiles + t);
   pdl_wait();
-  pdl_trigger();
   const int32_t* sel = a.idx + (static_cast<int64_t>(t) * a.hp + p) * a.topk;
   const int j0 = warp == kProducer && lane < a.topk ? sel[lane] : -1;
   const int c0 = group * N, cols = min(N, tl.rows * G - c0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Not before this CTA has its tensor memory: where it has to wait for that of another
+  // stream's CTA, one of the next launch could take it first, and then waits for this one.
+  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   if (cols <= 0) {  // a tile of fewer rows than the batch's most (the whole cluster)
     if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
@@ -1047,13 +1049,13 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
   }
   const TileInfo tl = plan_tile(a.tiles + t);
   pdl_wait();
-  pdl_trigger();
   const int32_t* sel = a.idx + (static_cast<int64_t>(t) * a.hp + p) * a.topk;
   const int j0 = warp == kProducer && lane < a.topk ? sel[lane] : -1;
   const int c0 = group * 256, pairs = min(256, tl.rows * G - c0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();  // (as in columns_kernel)
   const uint32_t tmem = *tmem_slot;
   if (pairs <= 0) {  // a tile of fewer rows than the batch's most
     if (warp == kIssuer) tmem_dealloc(tmem, 512);

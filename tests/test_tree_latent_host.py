@@ -138,3 +138,19 @@ for d in (64, 128):
         wide = {f for s in WIDE for f in kernel(*s, d, kind)}
         assert len(wide) == 1 and len(narrow - wide) > 1, (d, kind, wide, narrow)
 """)
+
+
+def test_the_next_launch_starts_behind_the_tensor_memory():
+    """A CTA that lets the next launch start has its tensor memory: one of that launch could
+    otherwise take what it still waits for, and then wait for it to end."""
+    import os
+    import re
+    from tests.test_host_side import ROOT
+    for name, kernels in (("columns.cu", 2), ("expand.cu", 1)):
+        with open(os.path.join(ROOT, "block_sparse_long_proxy_gb300", "csrc", name)) as f:
+            bodies = re.split(r"__global__", f.read())[1:]
+        assert len(bodies) == kernels
+        for body in bodies:
+            alloc = re.search(r"tmem_alloc\(|tcgen05\.alloc", body).start()
+            there = body.index("__syncthreads();", alloc)
+            assert body.count("pdl_trigger();") == 1 and body.index("pdl_trigger();") > there
