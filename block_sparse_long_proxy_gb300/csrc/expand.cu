@@ -3,8 +3,8 @@
 //   K[h] = [w_k[h] . latent | rotated part],  V[h] = w_v[h] . latent.
 //
 // A matrix product of two pages' 256 rows with the head's rows of w_k and w_v
-// together (N = nope + d <= 240), on tcgen05 by pairs of SMs (cta_group::2), fp32
-// in tensor memory, rounded once to bf16.  A unit is (two page-table entries, a few
+// together (nope + d <= 240, N the next multiple of 32), on tcgen05 by pairs of SMs
+// (cta_group::2), fp32 in tensor memory, rounded once to bf16.  A unit is (two page-table entries, a few
 // heads): each CTA of a pair keeps its page's latents in shared memory (128 KB
 // at 512) while the heads' weights stream past, 64 dims a stage, of which each CTA
 // loads one half of the N rows for both: an SM reads 98 KB of weights a head
@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 352;        // 8 epilogue warps, B producer, MMA, A producer
 constexpr int kABytes = 8 * 16384;
 constexpr int kMaxStages = 8;
-constexpr int kRing = 92160;         // half the weights, 128 dims a stage: 3 stages at the widest (120 rows)
+constexpr int kRing = 98304;         // half the weights, 128 dims a stage: 3 stages at the widest (128 rows)
 constexpr int kBarOff = kABytes + kRing;
 constexpr int kSmem = kBarOff + 512;
 
@@ -101,6 +101,11 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// N of a head's products: its rows of w_k and w_v together, to the next multiple of
+// 32, which pairs of SMs with 256 rows take.  CTA 0 has the first half of N, CTA 1 the
+// other rows; what is behind them in its shared memory goes to columns that nobody reads.
+constexpr int product_cols(int nope, int d) { return (nope + d + 31) / 32 * 32; }
+
 struct ExpandArgs {
   const __nv_bfloat16* latent;
   const int32_t* kv_indices;
@@ -120,7 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap c_map, const __grid_constant__ CUtensorMap wk_map,
                   const __grid_constant__ CUtensorMap wv0_map, const __grid_constant__ CUtensorMap wv1_map,
                   const ExpandArgs a) {
-  constexpr int kNope = D - ROPE, n = kNope + D, half = n / 2, chunk_bytes = half * 128, stage_bytes = 2 * chunk_bytes;
+  constexpr int kNope = D - ROPE, n = product_cols(kNope, D), half = n / 2, chunk_bytes = half * 128, stage_bytes = 2 * chunk_bytes;
+  static_assert(n % 32 == 0 && n <= 256, "N of a product by a pair of SMs; 256 columns an accumulator");
+  static_assert(half > kNope && half % 8 == 0 && kNope % 8 == 0 && half <= kNope + D, "boxes of whole swizzled groups of rows");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the same place in both CTAs of the pair: their windows start alike
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = ring.s;
             if (!(ok = wait_cluster(b_empty + s, ring.phase ^ 1, a.err))) break;
             uint8_t* dst = smem + kABytes + s * stage_bytes;
-            if (rank == 0) mbar_expect_tx(b_full + s, 2 * stage_bytes);
+            if (rank == 0) mbar_expect_tx(b_full + s, 2 * (kNope + D) * 128);
             for (int e = 0; e < 2; ++e, dst += chunk_bytes) {
               const int x = (2 * c + e) * 64;
               if (rank == 0) {  // w_k's rows and the first of w_v's
@@ -364,7 +371,7 @@ msa_status launch_expand(const msa_plan_s* p, const void* latent_pages, const vo
                          const int32_t* kv_indices, int32_t latent_dim, int32_t rope_dim, void* k_pages, void* v_pages,
                          cudaStream_t st) {
   const int width = latent_dim + rope_dim, nope = p->d - rope_dim;
-  const int half = (nope + p->d) / 2;
+  const int half = product_cols(nope, p->d) / 2;
   CUtensorMap cm, km, v0, v1;
   auto rows = [](CUtensorMap* m, const void* base, int64_t n, int wide, int box_rows) {
     const uint64_t dims[2] = {static_cast<uint64_t>(wide), static_cast<uint64_t>(n)};
@@ -374,7 +381,7 @@ msa_status launch_expand(const msa_plan_s* p, const void* latent_pages, const vo
   };
   if (!rows(&cm, latent_pages, p->num_pages * 128, width, 128) || !rows(&km, w_k, int64_t(p->hkv) * nope, latent_dim, nope) ||
       !rows(&v0, w_v, int64_t(p->hkv) * p->d, latent_dim, half - nope) ||
-      !rows(&v1, w_v, int64_t(p->hkv) * p->d, latent_dim, half))
+      !rows(&v1, w_v, int64_t(p->hkv) * p->d, latent_dim, nope + p->d - half))
     return set_error(MSA_ERR_CUDA, "msa_latent_expand: tensor map encoding failed");
   ExpandArgs a{};
   a.latent = static_cast<const __nv_bfloat16*>(latent_pages);

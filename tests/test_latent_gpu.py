@@ -253,6 +253,14 @@ def test_expand(cuda_dev, kv, heads, latent, rope, d):
         assert torch.equal(got[~there[:, None].expand(-1, heads, -1)], o[~there[:, None].expand(-1, heads, -1)])
 
 
+@pytest.mark.parametrize("latent", [128, 384])
+@pytest.mark.parametrize("rope, d", [(16, 64), (32, 64), (48, 64), (16, 128), (32, 128), (48, 128), (64, 128)])
+def test_expand_of_every_width(cuda_dev, rope, d, latent):
+    """Each split of a head's dims, whose products have 80 to 240 columns: several heads, so
+    that both accumulators and all stages are used more than once."""
+    test_expand(cuda_dev, [300, 5, 128], 7, latent, rope, d)
+
+
 def test_expand_bad_pages(cuda_dev):
     msa = _msa()
     plan = msa.Plan([1], [300], 2, 2, 2, 64, 64, 1, 3)
