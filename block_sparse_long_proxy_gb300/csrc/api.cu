@@ -272,8 +272,9 @@ static msa_status make_plan(const int32_t* qo_lens, const int32_t* kv_lens, int3
     return set_error(MSA_ERR_INVALID_ARG, "msa_plan: num_pages out of range");
   if (kv_dtype != MSA_KV_BF16 && kv_dtype != MSA_KV_FP8_E4M3 && kv_dtype != MSA_KV_FP8_E4M3_BLOCK)
     return set_error(MSA_ERR_INVALID_ARG, "msa_plan: unknown kv_dtype");
-  // the kernels address K/V rows (page, head, slot) by 32-bit tensor-map coordinates;
-  // of the caches only this one fits in memory beyond them (head_dim 64)
+  // the kernels address K/V rows (page, head, slot) by 32-bit tensor-map coordinates; of the
+  // caches that msa_sparse_attn takes only this one fits in memory beyond them (head_dim
+  // 64).  msa_tree_attn, which takes static e4m3 at head_dim 64 too, checks for itself.
   if (kv_dtype == MSA_KV_FP8_E4M3_BLOCK && num_pages * num_kv_heads > (int64_t(1) << 24))
     return set_error(MSA_ERR_INVALID_ARG, "msa_plan: num_pages * num_kv_heads above 2^24");
   if (flags != 0) return set_error(MSA_ERR_INVALID_ARG, "msa_plan: flags must be 0");

@@ -1640,6 +1640,10 @@ msa_status msa_tree_attn(msa_plan_t plan, const void* q, const void* k_pages, co
   const bool fp8 = plan->kv_dtype != MSA_KV_BF16;
   if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
     return set_error(MSA_ERR_INVALID_ARG, "%s: k_scale/v_scale must be given exactly for FP8 K/V", fn);
+  // K/V rows are 32-bit coordinates of the loads, which read zeros beyond them.  (A latent
+  // cache has one head, and a plan at most 2^24 pages.)
+  if (plan->num_pages * plan->hkv > (int64_t(1) << 24))
+    return set_error(MSA_ERR_INVALID_ARG, "%s: num_pages * num_kv_heads above 2^24", fn);
   msa_status s = check_tree(fn, plan);
   if (s == MSA_OK) s = check_device(fn, plan);
   if (s != MSA_OK) return s;

@@ -568,7 +568,8 @@ msa_status msa_append_bwd(msa_plan_t plan, msa_rope_t k_rope, msa_rope_t pk_rope
  * rounded to f16 and saturates beyond 65504, as in msa_sparse_attn.  A page id
  * outside the pool is reported and its block skipped.  At most 128 drafts a
  * sequence (MSA_ERR_UNSUPPORTED otherwise).  One launch without workspace:
- * calls of one plan may overlap.
+ * calls of one plan may overlap.  num_pages * num_kv_heads at most 2^24, of any
+ * kv_dtype (MSA_ERR_INVALID_ARG otherwise).
  */
 msa_status msa_tree_attn(msa_plan_t plan, const void* q, const void* k_pages, const void* v_pages,
                          const int32_t* kv_indices, const int32_t* kv_block_indexes, const int32_t* tree_mask,

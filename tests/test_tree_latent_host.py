@@ -88,6 +88,24 @@ assert append(h) == 0 and attn(h) == 0
 """)
 
 
+def test_pools_beyond_32_bit_rows(child):  # noqa: F811
+    """K/V rows (page, head, slot) are 32-bit coordinates of the tree's loads: a pool of more is
+    refused, whatever its type.  A latent cache has one head."""
+    child(CALLS + """
+for kind in (BF16, E4M3):
+    for heads, pages, status in ((8, 1 << 21, 0), (8, (1 << 21) + 1, 1), (1, 1 << 24, 0), (3, 5592405, 0), (3, 5592406, 1)):
+        s, h = plan([5], [300], 24, heads, 64, 4, kind, pages)
+        assert s == 0
+        if status:
+            refused(status, lambda: tree(h, kind))
+            assert b"2^24" in lib.msa_last_error()
+        else:
+            assert tree(h, kind) == 0
+        assert attn(h) == 0 and append(h) == 0 and (kind != BF16 or expand(h) == 0)
+        lib.msa_plan_destroy(h)
+""")
+
+
 def test_plans_belong_to_their_device(child):  # noqa: F811
     child(CALLS + """
 s, h = plan([5, 1], [300, 1], 8, 2, 128, 4, BF16)
