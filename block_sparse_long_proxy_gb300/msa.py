@@ -369,16 +369,17 @@ class Plan:
         tensors = (latent, key, latent_pages, kv_indices)
         if positions is not None:
             tensors += (positions,)
-        strides = self._passed("latent_append", tensors)
-        if strides is None:
+        known = strides = self._passed("latent_append", tensors)
+        if known is None:
             strides = (_rows(latent, torch.bfloat16, (self.total_q, 1, n), "latent"),
                        _rows(key, torch.bfloat16, (self.total_q, 1, width), "key"))
             _need_all(tensors[2:], ((torch.bfloat16, (self.num_pages, 1, 128, n + width), "latent_pages"),
                                     self._cache_needs[0], (torch.int32, (self.total_q,), "positions")))
-            self._passes("latent_append", tensors, strides)
         _check(_lib.msa_latent_append(self._h, rope and rope._h, _ptr(positions), latent.data_ptr(), strides[0],
                                       key.data_ptr(), strides[1], kv_indices.data_ptr(), n, width,
                                       latent_pages.data_ptr(), _stream(stream)), "msa_latent_append")
+        if known is None:
+            self._passes("latent_append", tensors, strides)
 
     def latent_expand(self, latent_pages, w_k, w_v, kv_indices, k_pages, v_pages, stream=None):
         """K and V pages [P, Hkv, 128, d] out of a latent cache's (msa_latent_expand):
@@ -386,14 +387,16 @@ class Plan:
         n = w_v.shape[-1]
         width = latent_pages.shape[-1] - n
         tensors = (kv_indices, k_pages, v_pages, latent_pages, w_k, w_v)
-        if not self._passed("latent_expand", tensors):
+        known = self._passed("latent_expand", tensors)
+        if not known:
             _need_all(tensors, self._cache_needs[:3] + (
                 (torch.bfloat16, (self.num_pages, 1, 128, n + width), "latent_pages"),
                 (torch.bfloat16, (self.hkv, self.d - width, n), "w_k"), (torch.bfloat16, (self.hkv, self.d, n), "w_v")))
-            self._passes("latent_expand", tensors)
         _check(_lib.msa_latent_expand(self._h, latent_pages.data_ptr(), w_k.data_ptr(), w_v.data_ptr(),
                                       kv_indices.data_ptr(), n, width, k_pages.data_ptr(), v_pages.data_ptr(),
                                       _stream(stream)), "msa_latent_expand")
+        if not known:
+            self._passes("latent_expand", tensors)
 
     # -- stage 1
     def proxy_maxscore(self, pq, pk_pages, kv_indices, out=None, stream=None):
@@ -475,7 +478,8 @@ class Plan:
 
     # A step's calls come with tensors like the last step's: what the checks found holds for all of one
     # type, dtype, device, sizes and strides, and comparing those takes a quarter of the checks' time
-    # (a call of eight tensors 11.1 -> 8.7 us).
+    # (a call of eight tensors 11.1 -> 8.7 us).  Noted once the library has accepted the call: the tensors
+    # are then on the plan's device, which it has found to be the current one.
     def _passed(self, call, tensors):
         known = self._alike.get((call, len(tensors)))
         return known[1] if known is not None and known[0].check(*tensors) else None
@@ -484,7 +488,7 @@ class Plan:
         self._alike[call, len(tensors)] = _Alike(*tensors, dynamic_dims_sizes=None, dynamic_dims_strides=None), found
 
     def _outputs(self, out, lse, shape, want_lse):
-        # (after the inputs' checks: they are on the current device, as what _new makes is)
+        # (what _new makes is on the current device, which the library then compares with the plan's)
         if out is None:
             out = _new(shape, (shape[1] * shape[2], shape[2], 1), torch.bfloat16)
         else:
@@ -502,13 +506,15 @@ class Plan:
         tree_mask[i, b // 32] is set (int32 [total_q, 4])."""
         tensors = ((kv_indices, k_pages, v_pages, q, kv_block_indexes, tree_mask) if self.kv_dtype == "bf16" else
                    (kv_indices, k_pages, v_pages, k_scale, v_scale, q, kv_block_indexes, tree_mask))
-        if not self._passed("tree_attn", tensors):
+        known = self._passed("tree_attn", tensors)
+        if not known:
             _need_all(tensors, self._tree_needs)
-            self._passes("tree_attn", tensors)
         out, lse = self._outputs(out, lse, self._q_shape, want_lse)
         _check(_lib.msa_tree_attn(self._h, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_indices.data_ptr(),
                                   kv_block_indexes.data_ptr(), tree_mask.data_ptr(), _ptr(k_scale), _ptr(v_scale),
                                   out.data_ptr(), _ptr(lse), _stream(stream)), "msa_tree_attn")
+        if not known:
+            self._passes("tree_attn", tensors)
         return out, lse
 
     def latent_attn(self, q, latent_pages, kv_indices, kv_block_indexes, rope_dim, scale, tree_mask=None, out=None,
@@ -522,14 +528,16 @@ class Plan:
         tensors = (q, latent_pages, kv_indices, kv_block_indexes)
         if tree_mask is not None:
             tensors += (tree_mask,)
-        if not self._passed("latent_attn", tensors):
+        known = self._passed("latent_attn", tensors)
+        if not known:
             _need_all(tensors, ((torch.bfloat16, (self.total_q, self.hq, width), "q"),
                                 (torch.bfloat16, (self.num_pages, 1, 128, width), "latent_pages")) + self._table_needs)
-            self._passes("latent_attn", tensors)
         out, lse = self._outputs(out, lse, (self.total_q, self.hq, width - rope_dim), want_lse)
         _check(_lib.msa_latent_attn(self._h, q.data_ptr(), latent_pages.data_ptr(), kv_indices.data_ptr(),
                                     kv_block_indexes.data_ptr(), _ptr(tree_mask), width - rope_dim, rope_dim,
                                     float(scale), out.data_ptr(), _ptr(lse), _stream(stream)), "msa_latent_attn")
+        if not known:
+            self._passes("latent_attn", tensors)
         return out, lse
 
     # -- training extension

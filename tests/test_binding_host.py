@@ -1,0 +1,76 @@
+"""The binding's checks of tensors over a library that only answers: host tensors stand
+for the device's, device -1 being the current one."""
+import pytest
+import torch
+
+
+class Library:
+    """Answers every call with `status` and counts the calls of operators."""
+
+    def __init__(self):
+        self.status, self.calls = 0, 0
+
+    def __getattr__(self, name):
+        fixed = {"msa_plan": 0, "msa_plan_num_tiles": 2, "msa_plan_max_blocks": 3, "msa_plan_total_q": 5,
+                 "msa_plan_num_valid_pages": 0, "msa_last_error": b"refused"}
+        if name in fixed:
+            return lambda *a: fixed[name]
+
+        def call(*a):
+            self.calls += 1
+            return self.status
+        return call
+
+
+@pytest.fixture
+def host(monkeypatch):
+    from block_sparse_long_proxy_gb300 import msa
+    lib = Library()
+    monkeypatch.setattr(msa, "_lib", lib)
+    monkeypatch.setattr(msa, "_current_device", lambda: -1)
+    monkeypatch.setattr(msa, "_stream", lambda stream=None: None)
+    monkeypatch.setattr(msa, "_device_view_int32", lambda *a: None)
+    monkeypatch.setattr(msa, "_new", lambda shape, strides, dtype: torch.empty(shape, dtype=dtype))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return msa, lib
+
+
+def calls(msa, kind="bf16"):
+    """A plan, and each checked call by name: a function of its tensors, and the tensors."""
+    plan = msa.Plan([2, 3], [300, 140], 8, 2, 2, 64, 64, 3, 7, kv_dtype=kind)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i4 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    kv = (lambda: bf(7, 2, 128, 64)) if kind == "bf16" else (lambda: bf(7, 2, 128, 64).to(torch.float8_e4m3fn))  # noqa: E731
+    scale = () if kind == "bf16" else (torch.ones(2), torch.ones(2))
+    tree = (bf(5, 8, 64), kv(), kv(), i4(5), i4(2, 2, 3), i4(5, 4)) + scale
+    attn = (bf(5, 8, 160), bf(7, 1, 128, 160), i4(5), i4(2, 2, 3), i4(5, 4))
+    append = (bf(5, 1, 128), bf(5, 1, 32), bf(7, 1, 128, 160), i4(5))
+    expand = (bf(7, 1, 128, 160), bf(2, 32, 128), bf(2, 64, 128), i4(5), bf(7, 2, 128, 64), bf(7, 2, 128, 64))
+    table = {"tree_attn": (plan.tree_attn, tree)}
+    if kind == "bf16":
+        table |= {"latent_attn": (lambda *t: plan.latent_attn(*t[:4], 32, 0.1, tree_mask=t[4]), attn),
+                  "latent_append": (plan.latent_append, append), "latent_expand": (plan.latent_expand, expand)}
+    return plan, table
+
+
+@pytest.mark.parametrize("name", ["tree_attn", "latent_attn", "latent_append", "latent_expand"])
+def test_refused_calls_leave_no_record(host, monkeypatch, name):
+    """Tensors of a call that the library refused (the plan is another device's, for one) are
+    checked again: what a record says of their device holds for accepted calls only."""
+    msa, lib = host
+    plan, table = calls(msa)
+    fn, tensors = table[name]
+    lib.status = 1
+    for _ in range(2):
+        with pytest.raises(msa.MsaError):
+            fn(*tensors)
+    assert not plan._alike
+    lib.status, before = 0, lib.calls
+    monkeypatch.setattr(msa, "_current_device", lambda: 0)  # the plan's; the tensors are elsewhere
+    with pytest.raises(ValueError):
+        fn(*tensors)
+    assert lib.calls == before
+    monkeypatch.setattr(msa, "_current_device", lambda: -1)
+    for _ in range(3):
+        fn(*tensors)
+    assert lib.calls == before + 3
