@@ -74,3 +74,31 @@ def test_refused_calls_leave_no_record(host, monkeypatch, name):
     for _ in range(3):
         fn(*tensors)
     assert lib.calls == before + 3
+
+
+@pytest.mark.parametrize("name, kind, pair", [("tree_attn", "e4m3", (6, 7)), ("tree_attn", "bf16", (1, 2)),
+                                              ("latent_append", "bf16", (0, 1))])
+def test_one_tensor_twice(host, monkeypatch, name, kind, pair):
+    """A comparison of a call that has one tensor in two places never passes: none is made for it,
+    call after call, nor taken from another call's place."""
+    msa, lib = host
+    made, real = [], msa._Alike
+
+    def alike(*tensors, **kw):
+        made.append(len(tensors))
+        return real(*tensors, **kw)
+    monkeypatch.setattr(msa, "_Alike", alike)
+    plan, table = calls(msa, kind)
+    fn, tensors = table[name]
+    if name == "latent_append":                           # as wide as each other
+        tensors = (tensors[0][..., :32].contiguous(), tensors[1], torch.zeros((7, 1, 128, 64), dtype=torch.bfloat16), tensors[3])
+    args = (lambda t: fn(*t[:6], k_scale=t[6], v_scale=t[7])) if kind == "e4m3" else (lambda t: fn(*t))  # noqa: E731
+    twice = list(tensors)
+    twice[pair[1]] = twice[pair[0]]
+    for _ in range(3):
+        args(twice)
+    assert made == [] and lib.calls == 3
+    for _ in range(3):
+        args(tensors)
+        args(twice)
+    assert len(made) == 1 and lib.calls == 9
