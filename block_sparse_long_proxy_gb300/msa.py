@@ -86,11 +86,14 @@ def _check(status, where):
 
 
 _current_device = torch._C._cuda_getDevice
+# Two private parts of torch that save host time; one without them does without.
+_guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
 # (shape, strides, dtype) on the current device, without the dispatcher: two outputs by
 # torch.empty take 3.5 us more of a call that takes 10
-_new = torch._C._dynamo.guards._empty_strided_cuda
+_new = getattr(_guards, "_empty_strided_cuda", None) or (
+    lambda shape, strides, dtype: torch.empty(shape, dtype=dtype, device="cuda"))
 # type, dtype, device, sizes and strides of several tensors against those it was made of
-_Alike = torch._C._dynamo.guards.TensorGuards
+_Alike = getattr(_guards, "TensorGuards", None)
 
 # The checks and conversions below run several times a call, and a decode step's
 # kernels are as short as they are: what passes is decided in one expression.
@@ -485,9 +488,15 @@ class Plan:
         return known[1] if known is not None and known[0].check(*tensors) else None
 
     def _passes(self, call, tensors, found=True):
-        if len({*map(id, tensors)}) < len(tensors):  # one tensor twice, which no comparison lets pass
+        global _Alike
+        if _Alike is None or len({*map(id, tensors)}) < len(tensors):  # (one tensor twice: no comparison lets that pass)
             return
-        self._alike[call, len(tensors)] = _Alike(*tensors, dynamic_dims_sizes=None, dynamic_dims_strides=None), found
+        try:
+            alike = _Alike(*tensors, dynamic_dims_sizes=None, dynamic_dims_strides=None)
+        except TypeError:  # a torch that makes it in another way
+            _Alike = None
+            return
+        self._alike[call, len(tensors)] = alike, found
 
     def _outputs(self, out, lse, shape, want_lse):
         # (what _new makes is on the current device, which the library then compares with the plan's)

@@ -1,5 +1,9 @@
 """The binding's checks of tensors over a library that only answers: host tensors stand
 for the device's, device -1 being the current one."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -22,16 +26,22 @@ class Library:
         return call
 
 
-@pytest.fixture
-def host(monkeypatch):
+def stand_in(put):
+    """The binding over a Library, by put(object, name, value)."""
     from block_sparse_long_proxy_gb300 import msa
     lib = Library()
-    monkeypatch.setattr(msa, "_lib", lib)
-    monkeypatch.setattr(msa, "_current_device", lambda: -1)
-    monkeypatch.setattr(msa, "_stream", lambda stream=None: None)
-    monkeypatch.setattr(msa, "_device_view_int32", lambda *a: None)
+    put(msa, "_lib", lib)
+    put(msa, "_current_device", lambda: -1)
+    put(msa, "_stream", lambda stream=None: None)
+    put(msa, "_device_view_int32", lambda *a: None)
+    put(torch.cuda, "current_device", lambda: 0)
+    return msa, lib
+
+
+@pytest.fixture
+def host(monkeypatch):
+    msa, lib = stand_in(monkeypatch.setattr)
     monkeypatch.setattr(msa, "_new", lambda shape, strides, dtype: torch.empty(shape, dtype=dtype))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     return msa, lib
 
 
@@ -102,3 +112,37 @@ def test_one_tensor_twice(host, monkeypatch, name, kind, pair):
         args(tensors)
         args(twice)
     assert len(made) == 1 and lib.calls == 9
+
+
+MISSING = """
+import torch
+from torch._C._dynamo import guards
+%s
+import tests.test_binding_host as t
+msa, lib = t.stand_in(setattr)
+empty, devices = torch.empty, []
+def on_host(shape, dtype, device):
+    devices.append(device)
+    return empty(shape, dtype=dtype)
+torch.empty = on_host
+plan, table = t.calls(msa)
+for name, (fn, tensors) in table.items():
+    got = [fn(*tensors) for _ in range(3)]
+    if name in ("tree_attn", "latent_attn"):
+        for out, lse in got:
+            wide = 64 if name == "tree_attn" else 128
+            assert out.shape == (5, 8, wide) and out.dtype is torch.bfloat16 and out.is_contiguous()
+            assert lse.shape == (5, 8) and lse.dtype is torch.float32 and lse.is_contiguous()
+assert lib.calls == 12 and not plan._alike and devices == ["cuda"] * 12, (plan._alike, devices)
+"""
+
+
+@pytest.mark.parametrize("change", ["del guards._empty_strided_cuda, guards.TensorGuards", "del torch._C._dynamo",
+                                    "del guards._empty_strided_cuda\nguards.TensorGuards = lambda *a: None"],
+                         ids=["without either name", "without the module", "another constructor"])
+def test_torch_without_private_parts(change):
+    """What the binding takes of torch beyond its public names saves time only: without it every
+    call makes all checks and its outputs by torch.empty."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", MISSING % change], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
