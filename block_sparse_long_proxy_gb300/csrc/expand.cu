@@ -109,7 +109,7 @@ constexpr int product_cols(int nope, int d) { return (nope + d + 31) / 32 * 32; 
 struct ExpandArgs {
   const __nv_bfloat16* latent;
   const int32_t* kv_indices;
-  const int32_t* keys;    // keys of each entry's page, 1..128
+  const uint8_t* keys;    // keys of each entry's page, 1..128
   __nv_bfloat16* k_pages;
   __nv_bfloat16* v_pages;
   uint32_t* err;
@@ -386,7 +386,7 @@ msa_status launch_expand(const msa_plan_s* p, const void* latent_pages, const vo
   ExpandArgs a{};
   a.latent = static_cast<const __nv_bfloat16*>(latent_pages);
   a.kv_indices = kv_indices;
-  a.keys = p->aux_d + p->entry_keys_off;
+  a.keys = reinterpret_cast<const uint8_t*>(p->aux_d + p->entry_keys_off);
   a.k_pages = static_cast<__nv_bfloat16*>(k_pages);
   a.v_pages = static_cast<__nv_bfloat16*>(v_pages);
   a.err = p->err_d;
@@ -424,12 +424,20 @@ msa_status launch_expand(const msa_plan_s* p, const void* latent_pages, const vo
 
 }  // namespace
 
-// Keys of each page-table entry's page: 128, and what is left in a sequence's last (bf16 plans).
+// Keys of each page-table entry's page, a byte each: 128, and what is left in a sequence's
+// last.  Every plan of bf16 has them, those of decode steps over long contexts too, so they
+// are few bytes (32 sequences of 131072 keys: a plan takes 340 us with int32s, 302 with bytes,
+// 284 without).
 void expand_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   if (p->kv_dtype != MSA_KV_BF16) return;
   p->entry_keys_off = static_cast<int64_t>(aux.size());
-  for (int32_t k : p->kv_lens)
-    for (int32_t left = k; left > 0; left -= std::min(left, kPage)) aux.push_back(std::min(left, kPage));
+  static_assert(kPage == 128);
+  aux.resize(aux.size() + (p->n_page_entries + 3) / 4, static_cast<int32_t>(0x80808080u));
+  uint8_t* end = reinterpret_cast<uint8_t*>(aux.data() + p->entry_keys_off);
+  for (int32_t k : p->kv_lens) {
+    end += (int64_t(k) + kPage - 1) / kPage;
+    if (k % kPage != 0) end[-1] = static_cast<uint8_t>(k % kPage);
+  }
 }
 
 }  // namespace msa

@@ -114,7 +114,7 @@ struct msa_plan_s {
     bool two, rows;
   };
   Columns tree_shape = {}, latent_shape[4] = {};  // msa_tree_attn; msa_latent_attn at 128, 256, 384 and 512 dims
-  int64_t entry_keys_off = 0;        // latent expansion: keys of each page-table entry's page
+  int64_t entry_keys_off = 0;        // latent expansion: keys of each page-table entry's page, a byte each
   void* bwd_d = nullptr;             // backward scratch (D, proxy LSE, inverse index)
 };
 
