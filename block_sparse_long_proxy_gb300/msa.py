@@ -514,7 +514,10 @@ class Plan:
                   out=None, lse=None, want_lse=True, stream=None):
         """Attention of drafted tokens over the cache (msa_tree_attn): row i sees
         the keys before the drafts, and draft b of its sequence iff bit b % 32 of
-        tree_mask[i, b // 32] is set (int32 [total_q, 4])."""
+        tree_mask[i, b // 32] is set (int32 [total_q, 4]), of the selected blocks.
+        Drafts that cross a page's edge lie in two blocks, of which topk_select
+        takes the first by its score: set max_score[t, :, (kv_len - qo_len) // 128]
+        to inf before it, so that no draft loses its ancestors."""
         tensors = ((kv_indices, k_pages, v_pages, q, kv_block_indexes, tree_mask) if self.kv_dtype == "bf16" else
                    (kv_indices, k_pages, v_pages, k_scale, v_scale, q, kv_block_indexes, tree_mask))
         known = self._passed("tree_attn", tensors)
@@ -532,7 +535,7 @@ class Plan:
                     lse=None, want_lse=True, stream=None):
         """Absorbed attention over a latent cache (msa_latent_attn): q [total_q, Hq,
         latent_dim + rope_dim] bf16, out [total_q, Hq, latent_dim]; causal, or by
-        tree_mask as tree_attn has it."""
+        tree_mask as tree_attn has it (with the same word on page edges)."""
         width = q.shape[-1]
         if not 0 <= rope_dim < width:
             raise ValueError("rope_dim: %s, rows have %s" % (rope_dim, width))

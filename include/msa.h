@@ -550,7 +550,13 @@ msa_status msa_append_bwd(msa_plan_t plan, msa_rope_t k_rope, msa_rope_t pk_rope
  * depth).  Row i sees every key before the drafts, and draft b of its sequence
  * iff bit b % 32 of word b / 32 of tree_mask[i] is set: its ancestors and
  * itself, but any mask serves.  Otherwise as msa_sparse_attn: the rows of a tile
- * share kv_block_indexes[t, p, :] (msa_topk_select's, for instance).
+ * share kv_block_indexes[t, p, :] (msa_topk_select's, for instance), and a row sees
+ * keys of those blocks only, drafts among them.  Where the drafts cross a page's
+ * edge ((kv_len - qo_len) % 128 + qo_len > 128) the first of them, the root too, lie
+ * in the block before the last, which msa_topk_select takes by its score alone: it
+ * may leave those drafts unseen by the others and by themselves.  With
+ * max_score[t, :, (kv_len - qo_len) / 128] set to +inf before it (topk >= 2) every row
+ * has its ancestors and itself, wherever the edges fall.
  *
  *  q                 bf16 [total_q, Hq, d].
  *  k_pages, v_pages, k_scale, v_scale   as msa_sparse_attn, of any kv_dtype at
@@ -607,7 +613,8 @@ msa_status msa_latent_append(msa_plan_t plan, msa_rope_t rope, const int32_t* po
  *  latent_pages      as msa_latent_append wrote them.
  *  kv_block_indexes  int32 [num_tiles, Hp, topk]: proxy head p's blocks serve
  *                    query heads [p*Hq/Hp, (p+1)*Hq/Hp).
- *  tree_mask         int32 [total_q, 4], or NULL.
+ *  tree_mask         int32 [total_q, 4], or NULL.  Which blocks to select for drafts
+ *                    that cross a page's edge: as msa_tree_attn.
  *  scale             > 0: the softmax scale of the heads before absorption.
  *  out               bf16 [total_q, Hq, latent_dim].
  *  lse               fp32 [total_q, Hq] or NULL.

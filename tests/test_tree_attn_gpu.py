@@ -343,6 +343,63 @@ def test_draft_step(cuda_dev):
             assert torch.equal(k_pages[page, :, slot], kt[page, :, slot]) and torch.equal(v_pages[page, :, slot], vt[page, :, slot])
 
 
+@pytest.mark.parametrize("form", ["tree", "latent"])
+def test_drafts_across_a_page_edge(cuda_dev, form):
+    """Drafts in two blocks, the first of which scores least of all: selected as it is, they
+    lose the drafts there, and those their own keys; with its score set to inf, as the header
+    says, every row sees its ancestors and itself, and each of them counts."""
+    msa = _msa()
+    gen = torch.Generator(device=cuda_dev).manual_seed(12)
+    d, hkv, hq, topk, latent, turned = 64, 1, 8, 3, 128, 32
+    parent = [-1, 0, 0, 1, 2, 4, 5, 3]
+    qo, kv = [8, 8, 8], [128 * 6 + 3, 128 * 6, 128 * 6 + 8]     # five drafts before an edge; up to one; from one on
+    n = sum(qo)
+    seen = np.zeros((8, 128), bool)
+    for i, a in enumerate(parent):
+        if a >= 0:
+            seen[i] = seen[a]
+        seen[i, i] = True
+    seen = np.concatenate([seen] * 3)
+    words = torch.from_numpy((seen.reshape(-1, 4, 32).astype(np.uint64) << np.arange(32, dtype=np.uint64)).sum(-1).astype(
+        np.uint32).view(np.int32)).to(cuda_dev)
+    rand = lambda *s: torch.randn(s, generator=gen, device=cuda_dev).to(torch.bfloat16)  # noqa: E731
+    nb = [(k + 127) // 128 for k in kv]
+    table = torch.randperm(sum(nb), generator=gen, device=cuda_dev).to(torch.int32)
+    plan = msa.Plan(qo, kv, hq, hkv, hkv, d, 64, topk, sum(nb))
+    pos0 = [k - q for q, k in zip(qo, kv)]
+    first = [p // 128 for p in pos0]
+    score = torch.rand((3, 1, plan.max_blocks), generator=gen, device=cuda_dev)
+    score[torch.arange(3), 0, first] = -1.0
+    if form == "tree":
+        q, k, v = rand(n, hq, d), rand(sum(nb), hkv, 128, d), rand(sum(nb), hkv, 128, d)
+        scale, width, wide = d ** -0.5, d, d
+        run = lambda idx: plan.tree_attn(q, k, v, table, idx, words)  # noqa: E731
+        k_of, v_of = (lambda x: lambda e, h: x[int(table[e]), h].double())(k), (lambda x: lambda e, h: x[int(table[e]), h].double())(v)
+    else:
+        q, pages = rand(n, hq, latent + turned), rand(sum(nb), 1, 128, latent + turned)
+        scale, width, wide = 0.125, latent + 64, latent
+        run = lambda idx: plan.latent_attn(q, pages, table, idx, turned, scale, tree_mask=words)  # noqa: E731
+        k_of = lambda e, h: pages[int(table[e]), 0].double()  # noqa: E731
+        v_of = lambda e, h: k_of(e, h)[:, :latent]  # noqa: E731
+    for keep in (False, True):
+        if keep:
+            score[torch.arange(3), 0, first] = float("inf")
+        idx = msa.topk_select(score, topk, plan.num_valid_pages)
+        got = idx.cpu().numpy()
+        for t in range(3):
+            assert nb[t] - 1 in got[t, 0] and (first[t] in got[t, 0]) == (keep or first[t] == nb[t] - 1)
+        out, lse = run(idx)
+        plan.check_errors()
+        ref = attend(q, k_of, v_of, qo, kv, got, scale, seen)
+        check(out, lse, ref, width, "bf16" if form == "tree" else "latent", topk * 128)
+        # each draft's own key takes part: its value, times the weight, is what leaving it out would move
+        alone = seen.copy()
+        alone[np.arange(n), np.tile(np.arange(8), 3)] = False
+        moved = (attend(q, k_of, v_of, qo, kv, got, scale, alone)[0] - ref[0]).abs().amax((1, 2)).cpu().numpy()
+        lost = np.concatenate([[p + i < 128 * (b - 1) for i in range(8)] for p, b in zip(pos0, nb)])
+        assert lost.sum() == 5 and ((moved == 0) == (lost & (not keep))).all()
+
+
 def test_refusals(cuda_dev):
     msa = _msa()
     c = Case(cuda_dev, [4], [200], 8, 2, 2, 128, 2, "bf16")
