@@ -17,8 +17,9 @@ std::vector<Shape, Raw<Shape>> shapes;
 extern "C" {
 
 long fake_uploaded() { return uploaded; }
-// CTAs and cluster size of the last launch
+// the last launch: CTAs, kernel, cluster size
 int fake_last_ctas() { return shapes.back().ctas; }
+const void* fake_last_func() { return events.back().func; }
 int fake_last_cluster() { return shapes.back().cluster; }
 
 cudaError_t cudaMemcpyAsync(void* d, const void* s, size_t n, cudaMemcpyKind kind, cudaStream_t st) {
