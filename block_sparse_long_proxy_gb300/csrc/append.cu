@@ -410,8 +410,9 @@ __global__ void __launch_bounds__(kPkThreads)
 // 16 values of it, or copies 16 bytes of the latent.  Rows share nothing, so
 // blockIdx.y takes a page's rows by kLatentRows.
 //
-// Bound by HBM: 32768 rows of 512 + 64 (75.6 MB) take 15.8 us, 4.8 TB/s (16 rows a CTA
-// and four loads 19.1, 64 rows 16.4); 13.9 out of L2.
+// 32768 rows of 512 + 64 (75.6 MB) take 15.5 us, 4.9 TB/s (16 rows a CTA and four loads
+// 19.1, 64 rows 16.4).  Not bound by HBM alone, as 13.9 out of L2 shows: 1024 short CTAs
+// go through a chain of plan entry, page id, loads and stores each.
 constexpr int kLatentRows = 32;
 
 __global__ void __launch_bounds__(kThreads)

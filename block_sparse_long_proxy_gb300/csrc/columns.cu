@@ -21,9 +21,9 @@
 // Roles: one warp lists the blocks and issues TMA loads into a ring of 32 KB slots
 // (K or V of a block; 128 of the latent's dims); one issues the products; 8 or 16
 // softmax warps, each four of them a share of the columns and a thread a key,
-// mask, find each column's maximum, and write P^T (bf16, or f16 for e4m3 caches:
-// half a step is 2^-9 or 2^-12 of a weight, the sums being of the unrounded ones)
-// back to shared memory.  The latent's P^T goes where the block's rotated part
+// mask, find each column's maximum, and write P^T (bf16, or f16 for e4m3 caches: a
+// weight is off by 2^-8 or 2^-11 of itself at most, the sums being of the unrounded
+// ones) back to shared memory.  The latent's P^T goes where the block's rotated part
 // was, which no product reads after S^T.  e4m3: four more warps expand the codes
 // to f16 (exact) inside the slot.
 //
@@ -1419,7 +1419,7 @@ cudaError_t launch_rows(const msa_plan_s* p, ColArgs a, const CUtensorMap& km, c
 //   1 row, 64 heads, latent, 16 blocks: 16 / 16 9.8, 32 / 16 11.8, 16 / 4 15.3, 64 / 8 16.1
 //   32 rows, same: 64 / 4 27.2, 32 / 2 29.9, 64 / 2 36.3, 16 / 1 41.4
 using Columns = msa_plan_s::Columns;
-constexpr double kAhead = 3;  // us of a start in which blocks stream already
+constexpr double kStreamed = 3;  // us of a start in which blocks stream already
 template <int KIND>
 Columns column_shape(const msa_plan_s* p, int64_t block_bytes, double size, double& least) {
   static constexpr double kStart[3][4] = {{5.6, 6, 6.3, 8.6}, {5.2, 6.4, 6, 10.3}, {8.8, 9.9, 12.3, 1e9}};
@@ -1439,7 +1439,7 @@ Columns column_shape(const msa_plan_s* p, int64_t block_bytes, double size, doub
       const double hbm = at_once * block_bytes * sets / units / 6.3e6;  // us a block step
       const double step = kStep[KIND][k] * (KIND == kLatent ? 0.27 + 0.73 * size : size) * (two ? 2.0 : 1.0);
       const int most = (blocks + parts - 1) / parts;
-      const double us = rounds * (start + (two ? 2 : 0) + (parts > 1 && KIND != kLatent ? 1.2 : 0) + std::max(most * step, most * hbm - kAhead));
+      const double us = rounds * (start + (two ? 2 : 0) + (parts > 1 && KIND != kLatent ? 1.2 : 0) + std::max(most * step, most * hbm - kStreamed));
       if (us < least) best = {16 << k, parts, two, false}, least = us;
     };
     for (int lg = 0; (1 << lg) <= kMaxParts && (1 << lg) <= blocks; ++lg) take(lg, false);
@@ -1460,7 +1460,7 @@ double rows_us(const msa_plan_s* p, int64_t block_bytes, double size) {
   const double hbm = at_once * block_bytes * p->n_tiles * p->hp / units / 6.3e6;
   const bool two = p->max_tile_rows * (p->hq / p->hp) > 128;  // tiles a CTA
   const int blocks = std::min(p->max_nvp, p->topk);
-  return rounds * ((two ? 8 : 6.1) + std::max(blocks * (two ? 1.7 : 1.47) * size, blocks * hbm - kAhead));
+  return rounds * ((two ? 8 : 6.1) + std::max(blocks * (two ? 1.7 : 1.47) * size, blocks * hbm - kStreamed));
 }
 
 template <int KIND, int N, bool TWO>

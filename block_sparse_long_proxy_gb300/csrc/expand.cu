@@ -42,8 +42,12 @@ __device__ __forceinline__ uint32_t cta_rank() {
   return r;
 }
 // Arrive on CTA 0's barrier at the same place as `bar`: what is handed over is tensor
-// memory that was read, and tcgen05.wait::ld came before.  (A release would also
-// wait for the warp's stores to K and V: 152 us where this takes 139.)
+// memory that was read.  The next product may overwrite it by the rules of tensor
+// memory, which need no release: tcgen05.wait::ld has ended the reads,
+// tcgen05.fence::before_thread_sync orders them before the arrive, and
+// tcgen05.fence::after_thread_sync the issuing thread's products behind its wait; a
+// relaxed arrive and the wait that sees it are the order between the two threads.  (A
+// release would also wait for the warp's stores to K and V: 152 us where this took 139.)
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
