@@ -51,7 +51,7 @@
 //   latent, a chunk of 512 rows x 32 heads, 512 + 64 (73 GFLOP): 106 us, 0.69 PFLOP/s.
 //     Bound by shared memory: 575 KB a block and 64 columns, at 128 B/clk 4500 of
 //     the 5400 clocks that a block takes.
-//   latent decode, 32 sequences x 64 heads (80 MB): 27 us, 24 from the L2: a CTA has
+//   latent decode, 32 sequences x 64 heads (80 MB): 28 us, 24 from the L2: a CTA has
 //     4 blocks, and the merge of 4 parts moves 98 KB a CTA.
 //   one tree of 16 rows: 12 us, one tile's chain of launch, tables, loads, products
 //     and merge.

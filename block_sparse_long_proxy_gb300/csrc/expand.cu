@@ -14,8 +14,8 @@
 // other.
 //
 // 32768 rows, 32 heads, 64 + 64 dims, latent 512 (581 MB, 206 GFLOP of products):
-// 134 us, 4.3 TB/s and 1.54 PFLOP/s (155 in passes without a pause, at the power
-// limit).  The products are 0.8 of it; the rest is the
+// 137 us (133 to 143 by the GPU), 4.2 TB/s and 1.5 PFLOP/s (154 in passes without a
+// pause, at the power limit).  The products are 0.8 of it; the rest is the
 // issuing thread's waits between them and the stores, which at latent 128 take
 // 116 us alone.  One CTA a page: 241 us.
 #include <algorithm>
