@@ -436,7 +436,7 @@ void expand_plan_tables(msa_plan_s* p, std::vector<int32_t>& aux) {
   if (p->kv_dtype != MSA_KV_BF16) return;
   p->entry_keys_off = static_cast<int64_t>(aux.size());
   static_assert(kPage == 128);
-  aux.resize(aux.size() + (p->n_page_entries + 3) / 4, static_cast<int32_t>(0x80808080u));
+  aux.resize(aux.size() + (size_t(p->n_page_entries) + 3) / 4, static_cast<int32_t>(0x80808080u));
   uint8_t* end = reinterpret_cast<uint8_t*>(aux.data() + p->entry_keys_off);
   for (int32_t k : p->kv_lens) {
     end += (int64_t(k) + kPage - 1) / kPage;

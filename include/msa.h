@@ -555,8 +555,9 @@ msa_status msa_append_bwd(msa_plan_t plan, msa_rope_t k_rope, msa_rope_t pk_rope
  * edge ((kv_len - qo_len) % 128 + qo_len > 128) the first of them, the root too, lie
  * in the block before the last, which msa_topk_select takes by its score alone: it
  * may leave those drafts unseen by the others and by themselves.  With
- * max_score[t, :, (kv_len - qo_len) / 128] set to +inf before it (topk >= 2) every row
- * has its ancestors and itself, wherever the edges fall.
+ * max_score[t, :, (kv_len - qo_len) / 128] set to +inf before it (topk >= 2; where no
+ * edge is crossed that is the last block, which counts without its score) every row
+ * has its ancestors and itself.  msa_proxy_topk selects alike, but leaves no place for it.
  *
  *  q                 bf16 [total_q, Hq, d].
  *  k_pages, v_pages, k_scale, v_scale   as msa_sparse_attn, of any kv_dtype at
