@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 1;
   uint64_t* q_full = pv_done + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
+  uint64_t* drain = q_full + 1;        // every product issued is complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int32_t* n_slot = reinterpret_cast<int32_t*>(tmem_slot + 1);
   uint32_t* seen_by = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
   float2* col_ml = reinterpret_cast<float2*>(smem + L::kColOff);
@@ -379,6 +380,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       mbar_init(p_full, kSoftWarps);
       mbar_init(pv_done, 1);
       mbar_init(q_full, 1);
+      mbar_init(drain, 1);
       fence_mbar_init();
     }
   } else if (warp == kIssuer) {
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       tma_prefetch_2d(&k_map, 128 * a.mt, row);
     }
   };
+  int uses = 0, tails = 0;  // loads issued, to slots and of rotated parts
   auto produce = [&](int i, int h, bool leader) {
     const int row = row_of(i);
     auto waited = [&](uint64_t* bar, uint32_t parity) {
@@ -430,6 +433,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
         mbar_expect_tx(tail_full + s, L::kTailBytes);
         tma_load_2d(smem + L::kTailOff + s * L::kTailBytes, &k_map, tail_full + s, 128 * a.mt, row);
       }
+      tails = i + 1;
       return true;
     }
     const int u = i * per + h, s = slot_of(u);
@@ -447,6 +451,7 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
         tma_load_3d(dst, h == 0 ? &k_map : &v_map, full + s, 0, row, 0);
       }
     }
+    uses = u + 1;
     return true;
   };
   // e4m3: slot use u's codes to f16, a thread a key, by four warps
@@ -576,6 +581,10 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
       if (kLat && i + 1 < n) prefetch(i + 1, leader);
       for (int h = 0; h < per + kLat && ok; ++h) ok = produce(i, h, leader);
     }
+    // Nothing is under way to this CTA's shared memory when it leaves, although a role that
+    // gave up a wait leaves loads unused.
+    for (int u = max(uses - S, 0); u < uses; ++u) mbar_wait_inl(full + slot_of(u), phase_of(u), a.err);
+    for (int i = max(tails - T, 0); i < tails; ++i) mbar_wait_inl(tail_full + i % T, i / T & 1, a.err);
   } else if (warp == kIssuer) {
     // ----------------------------------------------------------------- MMA
     // The whole warp goes through the loop, one elected lane issuing: descriptors
@@ -646,6 +655,8 @@ __global__ void __launch_bounds__(col_threads<KIND, N, TWO>(), TWO ? 2 : 1)
         mma_commit_if(leader, pv_done);
         if (kLat && ok && i + 1 < nn) qk(i + 1);
       }
+      mma_commit_if(leader, drain);  // nor a product, also after a wait that was given up
+      waited(drain, 0);
     }
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
@@ -1016,7 +1027,8 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
   uint64_t* s_full = empty + 2 * S;         // [2 tiles]
   uint64_t* p_full = s_full + 2;            // [2]
   uint64_t* o_done = p_full + 2;            // [2] the last P.V
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+  uint64_t* drain = o_done + 2;             // every product issued is complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int32_t* n_slot = reinterpret_cast<int32_t*>(tmem_slot + 1);
   uint32_t* any = reinterpret_cast<uint32_t*>(smem + L::kAnyOff);
   int64_t* row_at = reinterpret_cast<int64_t*>(smem + L::kRowOff);
@@ -1040,6 +1052,7 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
         mbar_init(p_full + h, 8);
         mbar_init(o_done + h, 1);
       }
+      mbar_init(drain, 1);
       fence_mbar_init();
     }
     if (lane < 4) any[lane] = 0u;
@@ -1137,8 +1150,10 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
 
   if (warp == kProducer) {
     const bool leader = elect_one();
-    for (int u = started; u < 2 * n; ++u)
-      if (!produce(u, leader)) break;
+    int uses = started;
+    while (uses < 2 * n && produce(uses, leader)) ++uses;
+    for (int u = max(uses - S, 0); u < uses; ++u)  // (as in columns_kernel)
+      mbar_wait_inl(full + slot_of(u), phase_of(u), a.err);
   } else if (warp == kIssuer) {
     // ----------------------------------------------------------------- MMA
     // QK0 QK1 | PV0 QK0' PV1 QK1' | ...: one tile's softmax overlaps the other's products
@@ -1191,6 +1206,8 @@ __global__ void __launch_bounds__(row_threads<FP8>(), 1)
         }
       }
     }
+    mma_commit_if(leader, drain);
+    waited(drain, 0);
   } else if (warp < kRowSoftWarps) {
     // ------------------------------------------------------------- softmax
     // tile, half of the keys, pair; every warp of a tile goes through all n blocks

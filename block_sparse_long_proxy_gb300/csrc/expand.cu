@@ -96,12 +96,12 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const void* map, uint64
       "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
 }
-// arrives on both CTAs' barriers when the products issued so far are complete
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+// arrives on both CTAs' barriers (or those in `ctas`) when the products issued so far are complete
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t ctas = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(ctas)
       : "memory");
 }
 
@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* b_empty = b_full + kMaxStages;
   uint64_t* d_full = b_empty + kMaxStages;  // [2] accumulators
   uint64_t* d_empty = d_full + 2;           // [2] CTA 0: read, by the warps of both
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_empty + 2);
+  uint64_t* drain = d_empty + 2;            // CTA 0: every product issued is complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = cta_rank();
   if (threadIdx.x == 0) {
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 8; ++i) mbar_init(a_full + i, 1), mbar_init(a_empty + i, 1);
     for (int i = 0; i < kMaxStages; ++i) mbar_init(b_full + i, 1), mbar_init(b_empty + i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(d_full + i, 1), mbar_init(d_empty + i, 16);
+    mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -183,6 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __device__ __forceinline__ void next(int n) {
       if (++s == n) s = 0, phase ^= 1;
     }
+    __device__ __forceinline__ void back(int n) {
+      if (--s < 0) s = n - 1, phase ^= 1;
+    }
   };
   // this CTA's entry of the pair's two, and its page; none, or a page outside the
   // pool: it computes on page 0 and writes nothing
@@ -197,19 +202,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 10) {
     if (lane == 0) {
       bool ok = true, good;
+      uint32_t have = 0, odd = 0;  // chunks that were loaded, and the phase of the last time
       for (int k = 0, u = unit0; u < units && ok; ++k, u += step) {
         const int row = static_cast<int>(page_of(u, good) * 128);
         for (int i = 0, c = head_of(u, 0) % steps; i < steps && ok; ++i, c = c + 1 == steps ? 0 : c + 1) {
           if (!(ok = wait_cluster(a_empty + c, (k & 1) ^ 1, a.err))) break;
           if (rank == 0) mbar_expect_tx(a_full + c, 4 * 16384);
           for (int e = 0; e < 2; ++e) tma_load_pair(smem + (2 * c + e) * 16384, &c_map, a_full + c, (2 * c + e) * 64, row);
+          have |= 1u << c, odd = (odd & ~(1u << c)) | static_cast<uint32_t>(k & 1) << c;
         }
       }
+      // Nothing is under way to either CTA's shared memory when they leave, although a role
+      // that gave up a wait leaves loads unused.
+      for (int c = 0; rank == 0 && c < steps; ++c)
+        if (have >> c & 1u) mbar_wait_inl(a_full + c, odd >> c & 1u, a.err);
     }
   } else if (warp == 8) {
     if (lane == 0) {
       bool ok = true;
       Ring ring;
+      int loads = 0;
       for (int u = unit0; u < units && ok; u += step)
         for (int i = 0; i < heads_of(u) && ok; ++i) {
           const int h = head_of(u, i);
@@ -227,8 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_pair(dst, &wv1_map, b_full + s, x, h * D + half - kNope);
               }
             }
+            loads = min(loads + 1, a.stages);
           }
         }
+      for (; rank == 0 && loads > 0; --loads) {  // (as the latents)
+        ring.back(a.stages);
+        mbar_wait_inl(b_full + ring.s, ring.phase, a.err);
+      }
     }
   } else if (warp == 9) {
     if (rank == 0) {  // issues for both CTAs: the whole warp goes through the loop, one elected lane issuing
@@ -265,6 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && leader) commit_pair(d_full + (acc & 1));
         }
       }
+      if (leader) commit_pair(drain, 1);  // nor a product, also after a wait that was given up
+      all(mbar_wait_inl(drain, 0, a.err));
     }
   } else {
     // ------------------------------------------------------------ epilogue

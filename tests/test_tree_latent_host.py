@@ -172,3 +172,23 @@ def test_the_next_launch_starts_behind_the_tensor_memory():
             alloc = re.search(r"tmem_alloc\(|tcgen05\.alloc", body).start()
             there = body.index("__syncthreads();", alloc)
             assert body.count("pdl_trigger();") == 1 and body.index("pdl_trigger();") > there
+
+
+def test_nothing_is_under_way_when_a_cta_leaves():
+    """After a wait that was given up, too, a CTA waits (bounded) for its loads and products before
+    it frees its tensor memory: the producers for what they issued last, the issuer for a commit
+    behind all of its products."""
+    import os
+    import re
+    from tests.test_host_side import ROOT
+    for name, kernels in (("columns.cu", 2), ("expand.cu", 1)):
+        with open(os.path.join(ROOT, "block_sparse_long_proxy_gb300", "csrc", name)) as f:
+            bodies = re.split(r"__global__", f.read())[1:]
+        assert len(bodies) == kernels
+        for body in bodies:
+            commit = re.search(r"(mma_commit_if\(leader, |commit_pair\()drain", body).start()
+            waits = [m.start() for m in re.finditer(r"(?<!= )(?<!\()mbar_wait_inl\((a_|b_|tail_)?full \+ [^;]*a\.err\);", body)]
+            products = [m.start() for m in re.finditer(r"\bmma_(ss_if|ts_if|pair)\(leader", body)]
+            free = max(m.start() for m in re.finditer(r"tmem_dealloc\(|tcgen05\.dealloc", body))
+            assert max(products) < commit < body.index("drain, 0", commit) < free
+            assert len(waits) == (2 if "tail_full" in body or name == "expand.cu" else 1) and max(waits) < free
